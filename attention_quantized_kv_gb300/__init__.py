@@ -3,8 +3,8 @@
 A thin Python layer over libkvq's C ABI (include/kvq.h).  PyTorch provides
 device memory and streams; every step of the path (quantize-on-append,
 split-K decode attention with its log-sum-exp merge, chunked-prefill
-attention, the degrade ladder's re-encode, probe-scored eviction) runs in the
-library's sm_103a kernels.  The functions below only
+attention, the degrade ladder's re-encode, probe-scored eviction, rotary
+positions) runs in the library's sm_103a kernels.  The functions below only
 marshal arguments: they take torch tensors, pass their device pointers and
 raise ``KVQError`` on a non-zero status.
 """
@@ -19,6 +19,8 @@ from . import _abi
 from ._abi import (KVQ_F16, KVQ_Q8_0, KVQ_Q4_0, KVQ_TURBO4, KVQ_DEVERR_CAPACITY,
                    KVQ_DEVERR_EVICT,
                    KVQ_DEVERR_MAXLEN, KVQ_DEVERR_PAGE, KVQ_DEVERR_SEQLEN, KVQ_DEVERR_TIMEOUT,
+                   KVQ_DEVERR_POS, KVQ_DEVERR_ROWS, KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED,
+                   KVQ_ROPE_LINEAR, KVQ_ROPE_NTK, KVQ_ROPE_PARTS, KVQ_ROPE_PLAIN, KVQ_ROPE_YARN,
                    kvq_layer)
 
 __all__ = ["KVQ_F16", "KVQ_Q8_0", "KVQ_Q4_0", "KVQ_TURBO4", "CODEC_NAMES", "KVQError", "KVLayer",
@@ -26,7 +28,11 @@ __all__ = ["KVQ_F16", "KVQ_Q8_0", "KVQ_Q4_0", "KVQ_TURBO4", "CODEC_NAMES", "KVQE
            "attn_prefill_workspace", "attn_prefill_chunk", "kvq_row_bytes", "kvq_cache_bytes",
            "kvq_pool_bytes", "KVQ_DEVERR_PAGE", "kv_requantize", "degrade", "aggregate_bpv",
            "ladder_next", "default_scale", "KVQ_DEVERR_EVICT", "kv_probe_scores",
-           "kv_evict_select", "kv_compact", "evict"]
+           "kv_evict_select", "kv_compact", "evict", "KVQ_DEVERR_POS", "KVQ_DEVERR_ROWS",
+           "KVQ_ROPE_HALF", "KVQ_ROPE_INTERLEAVED", "KVQ_ROPE_PLAIN", "KVQ_ROPE_LINEAR",
+           "KVQ_ROPE_NTK", "KVQ_ROPE_PARTS", "KVQ_ROPE_YARN", "Rope", "kvq_rope_freqs",
+           "kvq_rope_table", "kvq_rope_apply", "kv_append_rope", "kv_evict_delta",
+           "kv_rope_shift", "attn_decode_append_rope"]
 
 CODEC_NAMES = {KVQ_F16: "f16", KVQ_Q8_0: "q8_0", KVQ_Q4_0: "q4_0", KVQ_TURBO4: "turbo4"}
 HEAD_DIM = 128
@@ -308,11 +314,18 @@ def kv_compact(layer: KVLayer, evict, n_evicted, k_dst, v_dst, scores=None, scor
            "kv_compact")
 
 
-def evict(layer: KVLayer, scores, n_sink: int, n_recent: int, n_evict: int, stream=None):
+def evict(layer: KVLayer, scores, n_sink: int, n_recent: int, n_evict: int, stream=None,
+          rope: "Rope | None" = None):
     """Select and remove up to n_evict tokens per sequence: new zeroed cache
     buffers (torch allocations), the layer repointed at them and at the new
-    lengths.  Returns (compacted scores, evict list, n_evicted)."""
+    lengths.  With ``rope`` the kept keys are rotated to their new positions
+    too (a token's position is its place in the cache again).  Returns
+    (compacted scores, evict list, n_evicted)."""
     dev = layer.k_cache.device
+    if rope is not None:
+        rope._check_on(dev)
+        if rope.n_pos < layer.capacity:
+            raise ValueError("evict: the rope's table must cover the layer's capacity")
     ev = torch.zeros((layer.n_seqs, max(int(n_evict), 1)), dtype=torch.int32, device=dev)
     nev = torch.zeros(layer.n_seqs, dtype=torch.int32, device=dev)
     kv_evict_select(layer, scores, n_sink, n_recent, n_evict, ev, nev, stream)
@@ -321,5 +334,240 @@ def evict(layer: KVLayer, scores, n_sink: int, n_recent: int, n_evict: int, stre
     s_dst = torch.zeros_like(scores)
     lens = torch.empty_like(layer.seq_lens)
     kv_compact(layer, ev, nev, k_dst, v_dst, scores, s_dst, lens, stream)
+    if rope is not None:
+        delta = torch.empty((layer.n_seqs, layer.capacity), dtype=torch.int32, device=dev)
+        kv_evict_delta(layer, ev, nev, delta, stream)
     layer.k_cache, layer.v_cache, layer.seq_lens = k_dst, v_dst, lens
+    if rope is not None:
+        kv_rope_shift(layer, rope, delta, stream)
     return s_dst, ev, nev
+
+
+# --------------------------------------------------------------------------- rotary positions
+
+_ROW_TYPES = {torch.float16: _abi.KVQ_T_F16, torch.bfloat16: _abi.KVQ_T_BF16,
+              torch.float32: _abi.KVQ_T_F32}
+
+
+def _need(t, dtype, shape, device, what: str):
+    """A contiguous tensor of this type and shape on this device; its pointer."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: needs a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _cuda_device(t, what: str):
+    """The device of a tensor, which has to be the current CUDA device."""
+    d = t.device
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors must be on the current CUDA device, got {d}")
+    return d
+
+
+def _layer_on(layer: KVLayer, device, what: str) -> None:
+    if layer.k_cache.device != device:
+        raise ValueError(f"{what}: the layer is on {layer.k_cache.device}, expected {device}")
+
+
+def _rows(t, n_heads: int, device, what: str):
+    """(descriptor, rows) of rows [..., n_heads, 128]: one stride for all leading dimensions."""
+    if t.dtype not in _ROW_TYPES:
+        raise ValueError(f"{what}: rows are float16, bfloat16 or float32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.dim() not in (3, 4) or t.shape[-1] != HEAD_DIM or t.shape[-2] != n_heads:
+        raise ValueError(f"{what}: needs [rows, {n_heads}, {HEAD_DIM}] or [seqs, rows, {n_heads}, "
+                         f"{HEAD_DIM}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and st[0] != t.shape[1] * st[1]:
+        raise ValueError(f"{what}: sequences must be evenly spaced rows (stride {st[0]}, expected "
+                         f"{t.shape[1] * st[1]})")
+    n = t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1]
+    row = st[0] if t.dim() == 4 and t.shape[1] == 1 else st[-3]
+    return _abi.kvq_rows(t.data_ptr(), row if n > 1 else 0, st[-2] if n_heads > 1 else 0,
+                         _ROW_TYPES[t.dtype], 0), n
+
+
+def kvq_rope_freqs(rot_dim: int = HEAD_DIM, base: float = 10000.0, scaling: int = KVQ_ROPE_PLAIN,
+                   factor: float = 1.0, orig_len: float = 0.0, low: float = 1.0,
+                   high: float | None = None) -> list:
+    """Radians per position of each of the rot_dim / 2 planes.  ``low`` and ``high`` are the
+    turns over ``orig_len`` positions between which KVQ_ROPE_PARTS and KVQ_ROPE_YARN blend the
+    scaled frequency into the plain one (``high`` defaults to 4 and 32)."""
+    if high is None:
+        high = 32.0 if scaling == KVQ_ROPE_YARN else 4.0
+    out = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    _check(_abi.load().kvq_rope_freqs(int(rot_dim), float(base), int(scaling), float(factor),
+                                      float(orig_len), float(low), float(high), out),
+           "kvq_rope_freqs")
+    return list(out)
+
+
+def kvq_rope_table(freqs, table, stream=None) -> None:
+    """(cos, sin)(p * freqs[i]) for every position p into ``table`` (fp32
+    [n_pos, len(freqs), 2], device)."""
+    dev = _cuda_device(table, "kvq_rope_table")
+    n = len(freqs)
+    ptr = _need(table, torch.float32, (table.shape[0], n, 2), dev, "kvq_rope_table: table")
+    _check(_abi.load().kvq_rope_table((ctypes.c_double * n)(*freqs), 2 * n, table.shape[0], ptr,
+                                      _stream_ptr(stream)), "kvq_rope_table")
+
+
+class Rope:
+    """Rotary positions: the angle table of ``n_pos`` positions (built on the device, or the
+    caller's fp32 [n_pos, rot_dim / 2, 2] ``table``) and the C descriptor over it.
+
+    ``layout``: KVQ_ROPE_HALF pairs (i, i + rot_dim / 2), KVQ_ROPE_INTERLEAVED (2i, 2i + 1).
+    ``magnitude`` multiplies cos and sin; None means 1, and 0.1 ln(factor) + 1 for
+    KVQ_ROPE_YARN (Peng et al. 2023).  The other arguments are kvq_rope_freqs'."""
+
+    def __init__(self, n_pos: int = 0, rot_dim: int = HEAD_DIM, base: float = 10000.0,
+                 layout: int = KVQ_ROPE_HALF, scaling: int = KVQ_ROPE_PLAIN, factor: float = 1.0,
+                 orig_len: float = 0.0, low: float = 1.0, high: float | None = None,
+                 magnitude: float | None = None, table=None, device="cuda", stream=None):
+        if magnitude is None:
+            magnitude = 0.1 * math.log(factor) + 1.0 if scaling == KVQ_ROPE_YARN else 1.0
+        if layout not in (KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED):
+            raise ValueError("layout must be KVQ_ROPE_HALF or KVQ_ROPE_INTERLEAVED")
+        if not math.isfinite(magnitude):
+            raise ValueError("magnitude must be finite")
+        if table is None:
+            freqs = kvq_rope_freqs(rot_dim, base, scaling, factor, orig_len, low, high)
+            if n_pos <= 0:
+                raise ValueError("n_pos must be positive")
+            table = torch.empty((n_pos, len(freqs), 2), dtype=torch.float32, device=device)
+            kvq_rope_table(freqs, table, stream)
+        elif table.dim() != 3 or table.shape[0] < 1 or not 1 <= table.shape[1] <= HEAD_DIM // 2:
+            raise ValueError(f"table must be [n_pos, rot_dim / 2, 2], got {tuple(table.shape)}")
+        dev = _cuda_device(table, "Rope")
+        ptr = _need(table, torch.float32, (table.shape[0], table.shape[1], 2), dev, "Rope: table")
+        self.table, self.layout, self.magnitude = table, int(layout), float(magnitude)
+        self.n_pos, self.rot_dim = int(table.shape[0]), 2 * int(table.shape[1])
+        self._desc = _abi.kvq_rope(ptr, self.n_pos, self.rot_dim, self.layout, self.magnitude)
+
+    def desc(self) -> _abi.kvq_rope:
+        return self._desc
+
+    def _check_on(self, device) -> None:
+        if self.table.device != device:
+            raise ValueError(f"the rope's table is on {self.table.device}, expected {device}")
+
+
+def kvq_rope_apply(rope: Rope, x, y, positions=None, pos0: int = 0, transpose: bool = False,
+                   err=None, stream=None) -> None:
+    """Rotate the rows ``x`` (float16, bfloat16 or float32 [rows, heads, 128], strided) into ``y``
+    (x's type or float16; may be x).  ``positions``: int32 [rows], or row r is at pos0 + r.
+    ``transpose``: the gradient with respect to x, given that with respect to y.  ``err``: int32
+    word for KVQ_DEVERR_POS."""
+    dev = _cuda_device(x, "kvq_rope_apply")
+    rope._check_on(dev)
+    if x.dim() != 3 or y.shape != x.shape:
+        raise ValueError(f"kvq_rope_apply: x {tuple(x.shape)} and y {tuple(y.shape)} must be "
+                         "[rows, heads, 128]")
+    heads = x.shape[1]
+    xd, n = _rows(x, heads, dev, "kvq_rope_apply: x")
+    yd, _ = _rows(y, heads, dev, "kvq_rope_apply: y")
+    pos = None if positions is None else _need(positions, torch.int32, (n,), dev,
+                                               "kvq_rope_apply: positions")
+    word = None if err is None else _need(err, torch.int32, (1,), dev, "kvq_rope_apply: err")
+    _check(_abi.load().kvq_rope_apply(rope.desc(), xd, yd, n, heads, pos, int(pos0),
+                                      int(bool(transpose)), word, _stream_ptr(stream)),
+           "kvq_rope_apply")
+
+
+def kv_append_rope(layer: KVLayer, rope: Rope, k, v, n_new=None, row_start=None, q=None,
+                   q_out=None, positions=None, update_lens: bool = True, stream=None) -> None:
+    """Rotate the new keys and append them with the values; rotate the queries beside them.
+
+    Packed rows: k, v [rows, n_kv, 128] and ``row_start`` int32 [n_seqs + 1] (sequence s has rows
+    row_start[s] .. row_start[s + 1] - 1; the rows behind the last are padding).  Padded rows: k,
+    v [n_seqs, max_new, n_kv, 128] and ``n_new`` int32 [n_seqs].  float16, bfloat16 or float32,
+    strided (views of a fused projection).  ``q``: rows of n_q heads, same leading shape and
+    type, rotated into ``q_out`` (float16, contiguous).  ``positions``: int32, one per row;
+    without it a row's position is its place in the cache."""
+    dev = _cuda_device(k, "kv_append_rope")
+    rope._check_on(dev)
+    _layer_on(layer, dev, "kv_append_rope")
+    if (n_new is None) == (row_start is None):
+        raise ValueError("kv_append_rope: give n_new (padded rows) or row_start (packed rows)")
+    lead = k.shape[:-2]
+    if n_new is not None:
+        if len(lead) != 2 or lead[0] != layer.n_seqs:
+            raise ValueError("kv_append_rope: padded rows are [n_seqs, max_new, n_kv, 128]")
+        n_ptr, s_ptr = _need(n_new, torch.int32, (layer.n_seqs,), dev, "kv_append_rope: n_new"), None
+    else:
+        if len(lead) != 1:
+            raise ValueError("kv_append_rope: packed rows are [rows, n_kv, 128]")
+        n_ptr, s_ptr = None, _need(row_start, torch.int32, (layer.n_seqs + 1,), dev,
+                                   "kv_append_rope: row_start")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("kv_append_rope: k and v must have one shape and type")
+    kd, n = _rows(k, layer.n_kv_heads, dev, "kv_append_rope: k")
+    vd, _ = _rows(v, layer.n_kv_heads, dev, "kv_append_rope: v")
+    qd = out = None
+    if q is not None:
+        if q_out is None or q.shape[:-2] != lead or q.dtype != k.dtype:
+            raise ValueError("kv_append_rope: q needs q_out, and k's leading shape and type")
+        qd, _ = _rows(q, layer.n_q_heads, dev, "kv_append_rope: q")
+        out = _need(q_out, torch.float16, q.shape, dev, "kv_append_rope: q_out")
+    elif q_out is not None:
+        raise ValueError("kv_append_rope: q_out without q")
+    pos = None if positions is None else _need(positions, torch.int32, lead, dev,
+                                               "kv_append_rope: positions")
+    _check(_abi.load().kv_append_rope(layer.desc(), rope.desc(), qd, kd, vd, n, n_ptr, s_ptr, pos,
+                                      out, int(bool(update_lens)), _stream_ptr(stream)),
+           "kv_append_rope")
+
+
+def kv_evict_delta(layer: KVLayer, evict, n_evicted, delta, stream=None) -> None:
+    """How far kv_compact moves each kept token (new minus old position, <= 0) into ``delta``
+    (int32 [n_seqs, capacity]); ``layer`` as it was before the eviction."""
+    dev = _cuda_device(delta, "kv_evict_delta")
+    _layer_on(layer, dev, "kv_evict_delta")
+    if evict.dim() != 2:
+        raise ValueError("kv_evict_delta: evict must be [n_seqs, max_evict]")
+    ev = _need(evict, torch.int32, (layer.n_seqs, evict.shape[1]), dev, "kv_evict_delta: evict")
+    nev = _need(n_evicted, torch.int32, (layer.n_seqs,), dev, "kv_evict_delta: n_evicted")
+    out = _need(delta, torch.int32, (layer.n_seqs, layer.capacity), dev, "kv_evict_delta: delta")
+    _check(_abi.load().kv_evict_delta(layer.desc(), ev, nev, int(evict.shape[1]), out,
+                                      _stream_ptr(stream)), "kv_evict_delta")
+
+
+def kv_rope_shift(layer: KVLayer, rope: Rope, delta, stream=None) -> None:
+    """Rotate the cached keys of token t of sequence s by ``delta[s, t]`` positions, in place
+    (int32 [n_seqs, capacity]; 0 leaves the token's bytes as they are)."""
+    dev = _cuda_device(delta, "kv_rope_shift")
+    _layer_on(layer, dev, "kv_rope_shift")
+    rope._check_on(dev)
+    d = _need(delta, torch.int32, (layer.n_seqs, layer.capacity), dev, "kv_rope_shift: delta")
+    _check(_abi.load().kv_rope_shift(layer.desc(), rope.desc(), d, _stream_ptr(stream)),
+           "kv_rope_shift")
+
+
+def attn_decode_append_rope(layer: KVLayer, rope: Rope, k_new, v_new, q, scale: float, out, lse,
+                            max_len: int, workspace, positions=None, stream=None) -> None:
+    """attn_decode_append with the rotation in it: the new keys are rotated before they are
+    encoded and q before it attends, by ``positions`` (int32 [n_seqs]) or by the lengths before
+    the step."""
+    dev = _cuda_device(q, "attn_decode_append_rope")
+    _layer_on(layer, dev, "attn_decode_append_rope")
+    rope._check_on(dev)
+    kv_shape = (layer.n_seqs, layer.n_kv_heads, HEAD_DIM)
+    q_shape = (layer.n_seqs, layer.n_q_heads, HEAD_DIM)
+    what = "attn_decode_append_rope: "
+    k_ptr = _need(k_new, torch.float16, kv_shape, dev, what + "k_new")
+    v_ptr = _need(v_new, torch.float16, kv_shape, dev, what + "v_new")
+    q_ptr = _need(q, torch.float16, q_shape, dev, what + "q")
+    o_ptr = _need(out, torch.float16, q_shape, dev, what + "out")
+    l_ptr = None if lse is None else _need(lse, torch.float32, q_shape[:2], dev, what + "lse")
+    pos = None if positions is None else _need(positions, torch.int32, (layer.n_seqs,), dev,
+                                               what + "positions")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(what + f"workspace must be contiguous on {dev}")
+    _check(_abi.load().attn_decode_append_rope(
+        layer.desc(), rope.desc(), pos, k_ptr, v_ptr, q_ptr, float(scale), o_ptr, l_ptr,
+        int(max_len), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream)), "attn_decode_append_rope")

@@ -42,7 +42,11 @@
 // the same kernel (FUSED): each sequence's new token is encoded into the
 // cache by the warp that consumes the item holding it, before that warp
 // issues any copy (so its small loads and stores go out ahead of the copy
-// flood), and the lengths advance once every CTA has read them.
+// flood), and the lengths advance once every CTA has read them.  A third one
+// (attn_decode_append_rope) rotates the new keys on that way and each
+// segment's query rows in shared memory, one warp per row, before the warps
+// read their fragments: the angles' table row comes with the query rows, a
+// segment ahead, and one barrier per segment is all it adds to the loop.
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -50,6 +54,7 @@
 #include "kvq_device.cuh"
 #include "kvq_encode.cuh"
 #include "kvq_launch.h"
+#include "kvq_rope.cuh"
 
 namespace kvq {
 namespace {
@@ -58,6 +63,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRingBytes = 84 * 1024;
 constexpr int kMaxSeqs = kDecodeMaxSeqs;
+constexpr int kPlainDecode = 0, kFusedStep = 1, kFusedRope = 2;  // MODE of the split kernel
 constexpr int kRedFloats = 36;  // per lane: o[8][4], m0, m1, l0, l1
 
 struct DecodeParams {
@@ -72,6 +78,8 @@ struct DecodeParams {
   // counted in rd_ctr (zero between calls).
   const __half *k_new;
   const __half *v_new;
+  RopeArgs rope;             // kFusedRope: the rotation and its positions
+  const int32_t *positions;  // (nullptr: the lengths before the step)
   int32_t *lens_rw;
   unsigned *rd_ctr;
   float *part_o;    // [slots][8][128]
@@ -616,7 +624,13 @@ __device__ __forceinline__ bool appends(const DecodeParams &p, int seq) {
 // Fused decode step: write sequence seq's new K and V rows of kv head kvh
 // (fp16 from k_new / v_new; all 32 lanes) into the cache at position
 // pos = seq_lens[seq] (the old length).
-template <int CK, int CV>
+// kFusedRope: the table row of sequence seq's position (its old length, or
+// the caller's), clamped to the table.
+__device__ __forceinline__ const float *step_angles(const DecodeParams &p, int seq) {
+  return rope_row(p.rope, p.positions ? p.positions[seq] : p.seq_lens[seq], p.err);
+}
+
+template <int CK, int CV, int MODE>
 __device__ __forceinline__ void write_new_rows(const DecodeParams &p, int seq, int kvh, int lane) {
   const int pos = p.seq_lens[seq];
   const int64_t row = static_cast<int64_t>(seq) * p.n_kv + kvh;
@@ -635,7 +649,16 @@ __device__ __forceinline__ void write_new_rows(const DecodeParams &p, int seq, i
     unit = row * (p.capacity / kUnitTokens) + pos / kUnitTokens;
   }
   const int r = pos % kUnitTokens;
-  encode_row_into<0>(CK, rk, const_cast<uint8_t *>(p.k_cache) + unit * unit_bytes(CK), r, lane);
+  if (MODE == kFusedRope) {
+    float x[4];
+    const LaneAngles a = lane_angles(p.rope, step_angles(p, seq), lane);
+    load4<KVQ_T_F16>(&rk, x);
+    rotate_lane(p.rope, a, lane, x);
+    encode_f32_row_into<0>(CK, x, const_cast<uint8_t *>(p.k_cache) + unit * unit_bytes(CK), r,
+                           lane);
+  } else {
+    encode_row_into<0>(CK, rk, const_cast<uint8_t *>(p.k_cache) + unit * unit_bytes(CK), r, lane);
+  }
   encode_row_into<1>(CV, rv, const_cast<uint8_t *>(p.v_cache) + unit * unit_bytes(CV), r, lane);
 }
 
@@ -655,11 +678,13 @@ __device__ __forceinline__ Geo make_geo(const DecodeParams &p, const int32_t *pf
   return geo;
 }
 
-// FUSED: the fused decode step (p.k_new set); a separate instantiation, so
-// that the plain decode loop carries none of its state.
-template <int CK, int CV, bool FUSED>
+// MODE: the plain decode, the fused decode step (p.k_new set) or that with
+// the rotation; separate instantiations, so that the plain decode loop carries
+// none of their state.
+template <int CK, int CV, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeParams p) {
   using C = DecodeCfg<CK, CV>;
+  constexpr bool FUSED = MODE != kPlainDecode, ROPE = MODE == kFusedRope;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[C::NS];
   __shared__ int32_t pfx[kMaxSeqs + 1];
@@ -668,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
   // segment ahead; the first is requested before the ring's copies)
   __shared__ __align__(128) __half q_s[2][8 * kD];
   __shared__ uint64_t q_bar[2];
+  __shared__ __align__(16) float cs_s[2][ROPE ? kD : 4];  // the segments' table rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
 
@@ -753,14 +779,27 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
   };
 
   // Query rows of the segment at cursor c into q_s[buf] (thread 0).
-  const bool q_bulk = (reinterpret_cast<uintptr_t>(p.q) & 15) == 0;
+  const bool q_bulk =
+      (reinterpret_cast<uintptr_t>(p.q) & 15) == 0 && (!ROPE || (p.rope.rot & 3) == 0);
   auto issue_q = [&](int buf, const Cursor &c) {
     const int hgc = c.sl % p.n_hg;
     const uint32_t bytes = static_cast<uint32_t>(min(8, p.G - hgc * 8)) * kD * 2;
     const __half *src =
         p.q + (static_cast<int64_t>(c.seq) * p.n_q + (c.sl / p.n_hg) * p.G + hgc * 8) * kD;
-    mbar_arrive_expect_tx(&q_bar[buf], bytes);
+    const uint32_t cs_bytes = ROPE ? p.rope.rot * 4 : 0;
+    mbar_arrive_expect_tx(&q_bar[buf], bytes + cs_bytes);
     bulk_copy_g2s(q_s[buf], src, bytes, &q_bar[buf]);
+    if (ROPE) bulk_copy_g2s(cs_s[buf], step_angles(p, c.seq), cs_bytes, &q_bar[buf]);
+  };
+
+  // kFusedRope: row `warp` of the nh query rows in dst (or from src), rotated
+  // and rounded to fp16 in place.
+  auto rotate_q = [&](__half *dst, const __half *src, const float *cs, int nh) {
+    if (warp >= nh) return;
+    float x[4];
+    load4<KVQ_T_F16>((src ? src : dst) + warp * kD + 4 * lane, x);
+    rotate_lane(p.rope, lane_angles(p.rope, cs, lane), lane, x);
+    store4<KVQ_T_F16>(dst + warp * kD + 4 * lane, x);
   };
 
   Cursor seg = cursor_at(geo, u0);
@@ -781,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
       const Cursor c = cursor_at(geo, u);
       const int64_t send = u + (c.n_s - c.j);
       if (send <= u1 && static_cast<int>(send - 1 - u0) % kWarps == warp && appends(p, c.seq)) {
-        write_new_rows<CK, CV>(p, c.seq, c.sl / p.n_hg, lane);
+        write_new_rows<CK, CV, MODE>(p, c.seq, c.sl / p.n_hg, lane);
         wrote = true;
       }
       u = send;
@@ -830,6 +869,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
         ok = false;
         k_fail = k_next;
       }
+      if (ROPE) {
+        if (ok) rotate_q(q_s[buf], nullptr, cs_s[buf], min(8, p.G - hg * 8));
+        cta_bar();
+      }
       load_q_frags_smem<CK>(q_s[buf], min(8, p.G - hg * 8), lane, qb, qlo_r);
       // The next segment's rows go out now, a whole segment ahead of their
       // use (q_s[buf ^ 1] was last read before the previous segment's
@@ -839,6 +882,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
         issue_q(buf ^ 1, cursor_at(geo, seg_end));
         ++q_iss;
       }
+    } else if (ROPE) {
+      const int nh = min(8, p.G - hg * 8);
+      rotate_q(q_s[0], p.q + (static_cast<int64_t>(seq) * p.n_q + kvh * p.G + hg * 8) * kD,
+               step_angles(p, seq), nh);
+      cta_bar();
+      load_q_frags_smem<CK>(q_s[0], nh, lane, qb, qlo_r);
     } else {
       load_q_frags<CK>(p.q, static_cast<int64_t>(seq) * p.n_q + kvh * p.G, p.n_q, p.G, hg, lane,
                        qb, qlo_r);
@@ -1149,20 +1198,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
   }
 }
 
-template <int CK, int CV, bool FUSED>
-cudaError_t launch_split_f(const DecodeParams &p, int grid, cudaStream_t stream) {
+template <int CK, int CV, int MODE>
+cudaError_t launch_split_m(const DecodeParams &p, int grid, cudaStream_t stream) {
   using C = DecodeCfg<CK, CV>;
   static std::atomic<uint64_t> optin{0};
-  const cudaError_t e = smem_optin(decode_split_kernel<CK, CV, FUSED>, C::SMEM, optin);
+  const cudaError_t e = smem_optin(decode_split_kernel<CK, CV, MODE>, C::SMEM, optin);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_split_kernel<CK, CV, FUSED>, dim3(grid), dim3(kThreads), C::SMEM,
+  return launch_pdl(decode_split_kernel<CK, CV, MODE>, dim3(grid), dim3(kThreads), C::SMEM,
                     stream, p);
 }
 
 template <int CK, int CV>
 cudaError_t launch_split(const DecodeParams &p, int grid, cudaStream_t stream) {
-  return p.k_new ? launch_split_f<CK, CV, true>(p, grid, stream)
-                 : launch_split_f<CK, CV, false>(p, grid, stream);
+  return !p.k_new        ? launch_split_m<CK, CV, kPlainDecode>(p, grid, stream)
+         : !p.rope.table ? launch_split_m<CK, CV, kFusedStep>(p, grid, stream)
+                         : launch_split_m<CK, CV, kFusedRope>(p, grid, stream);
 }
 
 template <int CK>
@@ -1204,7 +1254,8 @@ DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms) {
 
 cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *q, float scale,
                           void *out, float *lse, int max_len, void *workspace,
-                          cudaStream_t stream, const void *k_new, const void *v_new) {
+                          cudaStream_t stream, const void *k_new, const void *v_new,
+                          const kvq_rope *rope, const int32_t *positions) {
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   DecodeParams p;
   p.k_cache = static_cast<const uint8_t *>(L.k_cache);
@@ -1212,6 +1263,8 @@ cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *
   p.seq_lens = L.seq_lens;
   p.k_new = static_cast<const __half *>(k_new);
   p.v_new = static_cast<const __half *>(v_new);
+  p.rope = rope ? rope_args(*rope) : RopeArgs{};
+  p.positions = positions;
   p.lens_rw = L.seq_lens;
   p.rd_ctr = reinterpret_cast<unsigned *>(ws) + (kDecodeTicketBytes / 4 - 1);
   p.q = static_cast<const __half *>(q);

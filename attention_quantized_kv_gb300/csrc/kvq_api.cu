@@ -30,6 +30,32 @@ int device_sms() {
   return cached[dev];
 }
 
+// The fused decode step; rope: with the rotation of the new keys and q.
+int decode_append(const kvq_layer *layer, const kvq_rope *rope, const int32_t *positions,
+                  const void *k_new, const void *v_new, const void *q, float scale, void *out,
+                  float *lse, int32_t max_len, void *workspace, size_t ws_bytes, void *stream) {
+  int st = check_layer(layer);
+  if (st != KVQ_OK) return st;
+  if (!k_new || !v_new || !q || !out || max_len <= 0) return KVQ_EINVAL;
+  if (!decode_shape_ok(layer)) return KVQ_EINVAL;
+  if (max_len > layer->capacity) return KVQ_ECAPACITY;
+  if (!aligned(k_new, 8) || !aligned(v_new, 8) || !aligned(q, 8) || !aligned(out, 8) ||
+      (lse && !aligned(lse, 4)))
+    return KVQ_EALIGN;
+  if (rope && !positions && rope->n_pos < max_len) return KVQ_ECAPACITY;
+  if (!aligned(positions, 4)) return KVQ_EALIGN;
+  if (!workspace) return KVQ_EWORKSPACE;
+  if (!aligned(workspace, 16)) return KVQ_EALIGN;
+  const int sms = device_sms();
+  if (sms <= 0) return KVQ_ECUDA;
+  const kvq::DecodePlan pl = kvq::plan_decode(*layer, max_len, sms);
+  if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
+  const cudaError_t e = kvq::launch_decode(*layer, pl, q, scale, out, lse, max_len, workspace,
+                                           static_cast<cudaStream_t>(stream), k_new, v_new, rope,
+                                           positions);
+  return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -110,23 +136,18 @@ int attn_decode(const kvq_layer *layer, const void *q, float scale, void *out, f
 int attn_decode_append(const kvq_layer *layer, const void *k_new, const void *v_new,
                        const void *q, float scale, void *out, float *lse, int32_t max_len,
                        void *workspace, size_t ws_bytes, void *stream) {
-  int st = check_layer(layer);
+  return decode_append(layer, nullptr, nullptr, k_new, v_new, q, scale, out, lse, max_len,
+                       workspace, ws_bytes, stream);
+}
+
+int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope,
+                            const int32_t *positions, const void *k_new, const void *v_new,
+                            const void *q, float scale, void *out, float *lse, int32_t max_len,
+                            void *workspace, size_t ws_bytes, void *stream) {
+  const int st = kvq::check_rope(rope);
   if (st != KVQ_OK) return st;
-  if (!k_new || !v_new || !q || !out || max_len <= 0) return KVQ_EINVAL;
-  if (!decode_shape_ok(layer)) return KVQ_EINVAL;
-  if (max_len > layer->capacity) return KVQ_ECAPACITY;
-  if (!aligned(k_new, 8) || !aligned(v_new, 8) || !aligned(q, 8) || !aligned(out, 8) ||
-      (lse && !aligned(lse, 4)))
-    return KVQ_EALIGN;
-  if (!workspace) return KVQ_EWORKSPACE;
-  if (!aligned(workspace, 16)) return KVQ_EALIGN;
-  const int sms = device_sms();
-  if (sms <= 0) return KVQ_ECUDA;
-  const kvq::DecodePlan pl = kvq::plan_decode(*layer, max_len, sms);
-  if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
-  const cudaError_t e = kvq::launch_decode(*layer, pl, q, scale, out, lse, max_len, workspace,
-                                           static_cast<cudaStream_t>(stream), k_new, v_new);
-  return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  return decode_append(layer, rope, positions, k_new, v_new, q, scale, out, lse, max_len,
+                       workspace, ws_bytes, stream);
 }
 
 int attn_prefill_workspace(const kvq_layer *layer, int32_t q_start, int32_t n_q_tok,

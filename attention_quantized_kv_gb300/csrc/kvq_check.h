@@ -2,6 +2,7 @@
 // libkvq, so that all of them apply the same rules (include/kvq.h: "Errors").
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/kvq.h"
@@ -41,6 +42,15 @@ inline int check_layer(const kvq_layer *L) {
       (L->err && !aligned(L->err, 4)))
     return KVQ_EALIGN;
   return KVQ_OK;
+}
+
+// The rotary descriptor.
+inline int check_rope(const kvq_rope *r) {
+  if (!r || !r->table || r->n_pos <= 0 || r->rot_dim < 2 || r->rot_dim > kHeadDim ||
+      r->rot_dim % 2 != 0 || !isfinite(r->magnitude))
+    return KVQ_EINVAL;
+  if (r->layout != KVQ_ROPE_INTERLEAVED && r->layout != KVQ_ROPE_HALF) return KVQ_EUNSUPPORTED;
+  return aligned(r->table, 16) ? KVQ_OK : KVQ_EALIGN;
 }
 
 // Decode streams: (sequence, kv head, group of up to 8 query heads).

@@ -36,11 +36,13 @@ struct DecodePlan {
 
 DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms);
 // k_new / v_new (fused decode step, fp16 [n_seqs][n_kv][128]): append one
-// token per sequence before attending, and advance the lengths.
+// token per sequence before attending, and advance the lengths; rope: rotate
+// the new keys and q first (positions: or the lengths before the step).
 cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *q, float scale,
                           void *out, float *lse, int max_len, void *workspace,
                           cudaStream_t stream, const void *k_new = nullptr,
-                          const void *v_new = nullptr);
+                          const void *v_new = nullptr, const kvq_rope *rope = nullptr,
+                          const int32_t *positions = nullptr);
 
 struct PrefillPlan {
   int64_t kv_tokens = 0;     // keys attended by the chunk: q_start + n_q_tok
@@ -69,5 +71,28 @@ cudaError_t launch_evict_select(const kvq_layer &L, const float *scores, int n_s
 cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32_t *n_evicted,
                            int max_evict, void *k_dst, void *v_dst, const float *scores,
                            float *scores_dst, int32_t *lens_dst, cudaStream_t stream);
+
+// Rotary positions (rope.cu, append_rope.cu).
+inline int type_bytes(int type) { return type == KVQ_T_F32 ? 4 : 2; }
+
+// A frequency in [0, 2 pi) radians per position as turns in units of 2^-64,
+// rounded to nearest: f / 2 pi as the sum of two doubles (2 pi's reciprocal
+// to twice double's precision), whose high part is a whole number of 2^-64 or
+// carries 53 bits.
+uint64_t turns_of(double f);
+cudaError_t launch_rope_table(const double *freqs, int rot_dim, int n_pos, float *table,
+                              cudaStream_t stream);
+cudaError_t launch_rope_apply(const kvq_rope &rope, const kvq_rows &x, const kvq_rows &y,
+                              int64_t n_rows, int n_heads, const int32_t *positions, int pos0,
+                              int transpose, int32_t *err, cudaStream_t stream);
+cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const kvq_rows *q,
+                               const kvq_rows &k, const kvq_rows &v, int64_t n_rows,
+                               const int32_t *n_new, const int32_t *row_start,
+                               const int32_t *positions, void *q_out, int update_lens,
+                               cudaStream_t stream);
+cudaError_t launch_evict_delta(const kvq_layer &L, const int32_t *evict, const int32_t *n_evicted,
+                               int max_evict, int32_t *delta, cudaStream_t stream);
+cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const int32_t *delta,
+                              cudaStream_t stream);
 
 }  // namespace kvq

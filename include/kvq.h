@@ -9,6 +9,11 @@
  *   kv_requantize        degrade one (layer, side) tensor to another codec
  *   kvq_aggregate_bpv    aggregate bits per value of a set of tensors
  *   kvq_ladder_next      the next step of the banded classic degrade ladder
+ *   kvq_rope_table       the angles of every position (rotary position embedding)
+ *   kvq_rope_apply       rotate query rows, or the transpose (their gradient)
+ *   kv_append_rope       rotate new keys and append them, with the values
+ *   kv_rope_shift        rotate cached keys again after their positions moved
+ *   attn_decode_append_rope   one decode step with the rotation in it
  *
  * Sources.  The codecs and their sizes follow the "Codecs" table of the
  * buun-llama-cpp listing (f16 16.0, q8_0 8.5, q4_0 4.5 bits per value); the
@@ -148,6 +153,8 @@ typedef enum {
 #define KVQ_DEVERR_SEQLEN 8   /* prefill: seq_lens[seq] < q_start + n_q_tok */
 #define KVQ_DEVERR_PAGE 16    /* paged: a block-table entry outside [0, n_pages) */
 #define KVQ_DEVERR_EVICT 32   /* kv_compact: an eviction list not increasing below the length */
+#define KVQ_DEVERR_POS 64     /* rotary: a position (or shift) outside the angle table, clamped to it */
+#define KVQ_DEVERR_ROWS 128   /* kv_append_rope: row_start decreasing or outside [0, n_rows] */
 
 /* One layer's cache.  All pointers are device pointers owned by the caller.
  * k_cache / v_cache: kvq_cache_bytes() bytes each (kvq_pool_bytes() when
@@ -363,6 +370,152 @@ KVQ_API int kv_evict_select(const kvq_layer *layer, const float *scores, int32_t
 KVQ_API int kv_compact(const kvq_layer *layer, const int32_t *evict, const int32_t *n_evicted,
                        int32_t max_evict, void *k_dst, void *v_dst, const float *scores,
                        float *scores_dst, int32_t *lens_dst, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions (rotary position embedding, Su et al. 2021).  The pages
+ * name no position encoding; the definitions below are this library's.
+ *
+ * A row x of 128 values at position p has its first rot_dim values turned in
+ * rot_dim / 2 planes.  Plane i holds the elements (a, b) = (2i, 2i + 1) in
+ * the interleaved layout and (i, i + rot_dim / 2) in the half layout; the
+ * values from rot_dim on are unchanged.  With (cos, sin) = table[p][i],
+ * c = RN(cos * magnitude) and s = RN(sin * magnitude), all in fp32:
+ *     y_a = RN(RN(x_a c) - RN(x_b s))      y_b = RN(RN(x_a s) + RN(x_b c))
+ * and one more rounding to the output's type; nothing is contracted, so the
+ * rotated keys' codec bytes are reproducible bit for bit.  A position outside
+ * [0, n_pos) sets KVQ_DEVERR_POS and takes the nearest row of the table.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { KVQ_ROPE_INTERLEAVED = 0, KVQ_ROPE_HALF = 1 } kvq_rope_layout;
+
+/* How the frequencies f_i = base^(-2i / rot_dim) are scaled for a context
+ * `factor` times the original one of orig_len positions:
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor (position interpolation)
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) in the place of base
+ *           (one plane: unchanged)
+ *   PARTS   by the turns r = orig_len f_i / 2 pi that a plane makes over the
+ *           original context: keep = clamp((r - low) / (high - low), 0, 1),
+ *           f_i keep + f_i / factor (1 - keep)   (Peng et al. 2023, eq. for
+ *           the interpolation by parts)
+ *   YARN    the same blend with keep = 1 - clamp((i - l) / max(h - l, 0.001),
+ *           0, 1), where l = max(floor(at(high)), 0) and h =
+ *           min(ceil(at(low)), rot_dim / 2 - 1) bound the planes that make
+ *           `high` and `low` turns: at(r) = rot_dim ln(orig_len / (2 pi r)) /
+ *           (2 ln base)                                                     */
+typedef enum {
+    KVQ_ROPE_PLAIN = 0,
+    KVQ_ROPE_LINEAR = 1,
+    KVQ_ROPE_NTK = 2,
+    KVQ_ROPE_PARTS = 3,
+    KVQ_ROPE_YARN = 4
+} kvq_rope_scaling;
+
+/* Type of rows handed to the rotary calls. */
+typedef enum { KVQ_T_F16 = 0, KVQ_T_BF16 = 1, KVQ_T_F32 = 2 } kvq_type;
+
+/* Angles and how to use them. */
+typedef struct kvq_rope {
+    const float *table; /* device, fp32 [n_pos][rot_dim / 2][2] (cos, sin), 16-byte aligned */
+    int32_t n_pos;      /* > 0 */
+    int32_t rot_dim;    /* even, 2..128 */
+    int32_t layout;     /* kvq_rope_layout */
+    float magnitude;    /* finite; multiplies cos and sin (1 for none) */
+} kvq_rope;
+
+/* Rows of 128 contiguous values: [rows][heads][128] with strides in elements.
+ * data 16-byte aligned, both strides multiples of 16 bytes. */
+typedef struct kvq_rows {
+    void *data;
+    int64_t row_stride;
+    int64_t head_stride;
+    int32_t type; /* kvq_type */
+    int32_t reserved; /* must be 0 */
+} kvq_rows;
+
+/* The rot_dim / 2 frequencies in radians per position into freqs (host), by
+ * the formulas above in double.  base > 1; factor >= 1 and finite; PARTS and
+ * YARN: orig_len > 0 and 0 < low < high.  Host only. */
+KVQ_API int kvq_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                           double orig_len, double low, double high, double *freqs);
+
+/* table[p][i] = (cos, sin)(p * freqs[i]) for p < n_pos, i < rot_dim / 2, in
+ * fp32, each within 2^-23 of the exact value.  freqs: host, each in [0, 2 pi).  The product is reduced
+ * as a 64-bit fixed-point number of turns, so far positions lose nothing.
+ * table: device, fp32 [n_pos][rot_dim / 2][2], 16-byte aligned. */
+KVQ_API int kvq_rope_table(const double *freqs, int32_t rot_dim, int32_t n_pos, float *table,
+                           void *stream);
+
+/* Rotate n_rows x n_heads rows of x into y.  positions: device int32 [n_rows],
+ * or NULL for position pos0 + row.  transpose != 0 applies the transposed
+ * rotation (s taken as -s): the gradient with respect to x of a rotation,
+ * given the gradient with respect to y.  y has x's type or fp16; y may be x
+ * itself (same data, strides and type) and must not overlap it otherwise;
+ * x may repeat rows or heads (a stride of 0), y may not.  err: optional device word for
+ * KVQ_DEVERR_POS.  n_rows = 0 launches nothing. */
+KVQ_API int kvq_rope_apply(const kvq_rope *rope, const kvq_rows *x, const kvq_rows *y,
+                           int64_t n_rows, int32_t n_heads, const int32_t *positions,
+                           int32_t pos0, int32_t transpose, int32_t *err, void *stream);
+
+/* Quantize-on-append with the rotation applied on the way: k rows are rotated
+ * in fp32 and encoded from there with codec_k (an f16 cache rounds to fp16),
+ * v rows are encoded as they are (bf16 and fp32 rows: from fp32).
+ * Rows: k, v [n_rows][n_kv_heads][128], and optionally q
+ * [n_rows][n_q_heads][128] (NULL: none), whose rotated rows go to q_out, fp16
+ * [n_rows][n_q_heads][128] contiguous and 16-byte aligned: the query of
+ * attn_decode or attn_prefill_chunk.  q, k and v have one type.
+ * Which rows belong to which sequence, one of:
+ *   row_start (device int32 [n_seqs + 1], non-decreasing, packed rows):
+ *     sequence s has rows row_start[s] .. row_start[s + 1) - 1; rows at or
+ *     behind row_start[n_seqs] are padding: not read, and q_out not written;
+ *   n_new (device int32 [n_seqs], padded rows): sequence s has rows
+ *     s * (n_rows / n_seqs) .. + n_new[s] - 1 (n_rows a multiple of n_seqs,
+ *     n_new[s] up to n_rows / n_seqs).
+ * Row i of sequence s goes to token seq_lens[s] + i and is rotated by
+ * positions[row] (device int32 [n_rows]), or with NULL by that token index.
+ * When update_lens != 0, the lengths advance afterwards (stream-ordered).
+ * Device conditions: KVQ_DEVERR_CAPACITY, KVQ_DEVERR_PAGE (the row's k and v
+ * are skipped), KVQ_DEVERR_POS, KVQ_DEVERR_ROWS (a row_start or n_new entry out
+ * of its range: that sequence's rows are unspecified, in bounds, and its
+ * length stays).  q_out may be q itself when q is fp16 and contiguous. */
+KVQ_API int kv_append_rope(const kvq_layer *layer, const kvq_rope *rope, const kvq_rows *q,
+                           const kvq_rows *k, const kvq_rows *v, int64_t n_rows,
+                           const int32_t *n_new, const int32_t *row_start,
+                           const int32_t *positions, void *q_out, int32_t update_lens,
+                           void *stream);
+
+/* How far kv_compact moves each kept token: for w < seq_lens[s] - n_evicted[s],
+ * delta[s][w] = w - (the position that token w had).  Call it with the lengths
+ * from before the eviction; arguments as kv_compact's (evict increasing and
+ * below the length, otherwise the values are unspecified).  delta: device
+ * int32 [n_seqs][capacity]; entries behind the new length are not written. */
+KVQ_API int kv_evict_delta(const kvq_layer *layer, const int32_t *evict,
+                           const int32_t *n_evicted, int32_t max_evict, int32_t *delta,
+                           void *stream);
+
+/* Move cached keys to other positions: for every token t < seq_lens[s] with
+ * delta[s][t] != 0, its K rows are decoded exactly, rotated by delta[s][t]
+ * (sin negated for a negative one; magnitude is not applied: the rows carry
+ * it already) and encoded again in place with codec_k (f16: rounded to
+ * fp16).  Tokens with delta 0 keep their bytes.  delta: device int32
+ * [n_seqs][capacity], |delta| < n_pos (otherwise KVQ_DEVERR_POS, clamped).
+ * A page shared by two sequences is outside the contract, as for an append. */
+KVQ_API int kv_rope_shift(const kvq_layer *layer, const kvq_rope *rope, const int32_t *delta,
+                          void *stream);
+
+/* attn_decode_append with the rotation in it: the new key is rotated before
+ * it is encoded and q is rotated before it attends, both by positions[s]
+ * (device int32 [n_seqs]), or with NULL by the length before the step.  The
+ * result is that of kv_append_rope (one row per sequence, update_lens = 1, q_out)
+ * followed by attn_decode of q_out, bit for bit.  q, k_new, v_new: fp16 as
+ * attn_decode_append takes them; positions NULL needs n_pos >= max_len
+ * (KVQ_ECAPACITY).  A sequence already at capacity gets no new token
+ * and attends its keys.  Everything else as attn_decode_append. */
+KVQ_API int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope,
+                                    const int32_t *positions, const void *k_new,
+                                    const void *v_new, const void *q, float scale, void *out,
+                                    float *lse, int32_t max_len, void *workspace,
+                                    size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
