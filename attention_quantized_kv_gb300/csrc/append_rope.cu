@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kArWarps = 8;
 constexpr int kArThreads = kArWarps * 32;
-constexpr int kHeadsPerWarp = 8;  // heads of one row that share a warp's angles
+constexpr int kMaxHeads = 8;  // heads of one row that share a warp's angles
 
 struct AppendRopeParams {
   RopeArgs rope;
@@ -27,7 +27,8 @@ struct AppendRopeParams {
   int32_t *err;
   int64_t n_rows, max_new;  // max_new: padded rows per sequence
   int n_seqs, n_q, n_kv, capacity, pages_per_seq, n_pages;
-  int q_chunks, kv_chunks;  // chunks of kHeadsPerWarp heads
+  int hpw, q_chunks, kv_chunks;  // heads per warp item; items of a row's q, k (or v) heads
+  int64_t kv_blocks;             // prompts: blocks that place keys and values
 };
 
 // New rows of sequence s, 0 and KVQ_DEVERR_ROWS where the caller's entries
@@ -45,12 +46,13 @@ __device__ __forceinline__ int64_t new_rows(const AppendRopeParams &p, int s, bo
 }
 
 // The sequence of a row and its index there; false for padding.
-__device__ __forceinline__ bool find_row(const AppendRopeParams &p, int64_t row, int &s,
-                                         int64_t &i) {
+__device__ __forceinline__ bool find_row(const AppendRopeParams &p, int64_t row, int &s, int &i,
+                                         int &n) {
   if (!p.row_start) {
     s = static_cast<int>(row / p.max_new);
-    i = row - s * p.max_new;
-    return i < p.n_new[s];
+    i = static_cast<int>(row - s * p.max_new);
+    n = p.n_new[s];
+    return i < n && n <= p.max_new;
   }
   int lo = 0, hi = p.n_seqs;  // the last s with row_start[s] <= row
   while (lo + 1 < hi) {
@@ -59,24 +61,122 @@ __device__ __forceinline__ bool find_row(const AppendRopeParams &p, int64_t row,
     else hi = mid;
   }
   s = lo;
-  i = row - p.row_start[s];
-  return i >= 0 && row < p.row_start[s + 1];
+  const int a = p.row_start[s], b = p.row_start[s + 1];
+  i = static_cast<int>(row - a);
+  n = b - a;
+  return a >= 0 && row >= a && row < b && b <= p.n_rows;
 }
 
-// One warp per (row, up to eight heads of q, k or v).
+// find_row of one row by a whole warp: each round narrows the range 32 times,
+// so up to 32 sequences cost one dependent load.
+__device__ __forceinline__ bool find_row_warp(const AppendRopeParams &p, int64_t row, int lane,
+                                              int &s, int &i) {
+  if (!p.row_start) {
+    int n;
+    return find_row(p, row, s, i, n);
+  }
+  int lo = 0, n = p.n_seqs;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < n && p.row_start[lo + at] <= row);
+    const int k = max(__popc(le) - 1, 0) * step;
+    lo += k;
+    n = min(step, n - k);
+  }
+  s = lo;
+  const int a = p.row_start[s], b = p.row_start[s + 1];
+  i = static_cast<int>(row - a);
+  return a >= 0 && row >= a && row < b && b <= p.n_rows;
+}
+
+// Unit of kv head 0 that holds slot `slot` of sequence s; -1 and the error
+// bit where there is no place.
+__device__ __forceinline__ int64_t unit_of(const AppendRopeParams &p, int s, int64_t slot) {
+  if (slot < 0 || slot >= p.capacity) {
+    set_err(p.err, KVQ_DEVERR_CAPACITY);
+    return -1;
+  }
+  const int64_t j = slot / kUnitTokens;
+  if (!p.table) return static_cast<int64_t>(s) * p.n_kv * (p.capacity / kUnitTokens) + j;
+  const int pg = page_of(p.table, p.pages_per_seq, p.n_pages, s, j / kPageUnits);
+  if (pg < 0) {
+    set_err(p.err, KVQ_DEVERR_PAGE);
+    return -1;
+  }
+  return static_cast<int64_t>(pg) * p.n_kv * kPageUnits + j % kPageUnits;
+}
+// Units from one kv head to the next.
+__device__ __forceinline__ int64_t unit_step(const AppendRopeParams &p) {
+  return p.table ? kPageUnits : p.capacity / kUnitTokens;
+}
+
+__device__ __forceinline__ void check_counts(const AppendRopeParams &p) {
+  if (blockIdx.x != 0) return;
+  for (int s = threadIdx.x; s < p.n_seqs; s += kArThreads) {
+    bool bad;
+    new_rows(p, s, bad);
+    if (bad) set_err(p.err, KVQ_DEVERR_ROWS);
+  }
+}
+
+// One warp: up to hpw heads of q (which 0), k (1) or v (2) of one row, every
+// value requested before the row's place and angles are looked up.
 template <int T>
-__global__ void __launch_bounds__(kArThreads) append_rope_kernel(AppendRopeParams p) {
+__device__ __forceinline__ void row_item(const AppendRopeParams &p, int64_t row, int which,
+                                         int chunk, int lane) {
+  using Raw = typename RowType<T>::raw4;
   constexpr int S = sizeof(typename RowType<T>::type);
+  const int h0 = chunk * p.hpw, nh = min(p.hpw, (which == 0 ? p.n_q : p.n_kv) - h0);
+  const uint8_t *x = p.x[which] + row * p.row[which] + h0 * p.head[which] + 4 * lane * S;
+  Raw raw[kMaxHeads];
+#pragma unroll
+  for (int h = 0; h < kMaxHeads; ++h)
+    if (h < nh) raw[h] = *reinterpret_cast<const Raw *>(x + h * p.head[which]);
+  int s, i;
+  if (!find_row_warp(p, row, lane, s, i)) return;
+  const int64_t slot = static_cast<int64_t>(p.seq_lens[s]) + i;
+  LaneAngles a;
+  if (which < 2)
+    a = lane_angles(p.rope, rope_row(p.rope, p.positions ? p.positions[row] : slot, p.err), lane);
+  if (which == 0) {
+#pragma unroll
+    for (int h = 0; h < kMaxHeads; ++h)
+      if (h < nh) {
+        float v[4];
+        load4<T>(&raw[h], v);
+        rotate_lane(p.rope, a, lane, v);
+        store4<KVQ_T_F16>(p.q_out + (row * p.n_q + h0 + h) * kD + 4 * lane, v);
+      }
+    return;
+  }
+  const int64_t unit = unit_of(p, s, slot), step = unit_step(p);
+  if (unit < 0) return;
+  const int r = static_cast<int>(slot % kUnitTokens), codec = p.codec[which - 1];
+#pragma unroll 1
+  for (int h = 0; h < nh; ++h) {
+    float v[4];
+    Raw w = raw[0];  // (a rotating window instead of an indexed array: registers)
+    load4<T>(&w, v);
+#pragma unroll
+    for (int k = 0; k + 1 < kMaxHeads; ++k) raw[k] = raw[k + 1];
+    uint8_t *u = p.cache[which - 1] + (unit + (h0 + h) * step) * unit_bytes(codec);
+    if (which == 1) {
+      rotate_lane(p.rope, a, lane, v);
+      encode_f32_row_into<0>(codec, v, u, r, lane);
+    } else {
+      encode_f32_row_into<1>(codec, v, u, r, lane);
+    }
+  }
+}
+
+// Decode steps and other short appends: one warp per row item.
+template <int T>
+__global__ void __launch_bounds__(kArThreads)
+    append_rows_kernel(const __grid_constant__ AppendRopeParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int s = threadIdx.x; s < p.n_seqs; s += kArThreads) {
-      bool bad;
-      new_rows(p, s, bad);
-      if (bad) set_err(p.err, KVQ_DEVERR_ROWS);
-    }
-  const int per_row = p.q_chunks + 2 * p.kv_chunks;
+  check_counts(p);
+  const int lane = threadIdx.x & 31, per_row = p.q_chunks + 2 * p.kv_chunks;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kArWarps + (threadIdx.x >> 5);
   const int64_t row = item / per_row;
   if (row >= p.n_rows) return;
@@ -86,53 +186,284 @@ __global__ void __launch_bounds__(kArThreads) append_rope_kernel(AppendRopeParam
     which = 1 + chunk / p.kv_chunks;
     chunk %= p.kv_chunks;
   }
-  int s;
-  int64_t i;
-  if (!find_row(p, row, s, i)) return;
-  const int64_t slot = static_cast<int64_t>(p.seq_lens[s]) + i;
-  const int h0 = chunk * kHeadsPerWarp, h1 = min(h0 + kHeadsPerWarp, which == 0 ? p.n_q : p.n_kv);
-  const uint8_t *x = p.x[which] + row * p.row[which] + 4 * lane * S;
-  LaneAngles a;
-  if (which < 2)
-    a = lane_angles(p.rope, rope_row(p.rope, p.positions ? p.positions[row] : slot, p.err), lane);
-  if (which == 0) {
-    for (int h = h0; h < h1; ++h) {
+  row_item<T>(p, row, which, chunk, lane);
+}
+
+// ------------------------------------------------------------------ prompts
+//
+// A prompt fills whole 16-token units, whose bytes interleave their tokens
+// (include/kvq.h): written row by row the V side would go out as 2-byte
+// stores, one 32-byte sector each.  So one warp takes a whole unit of one kv
+// head: its rows are copied into shared memory (16 of them in flight), encoded
+// there row by row, and the unit is put together 16 bytes per lane from the
+// 16 rows' codes and stored as contiguous 512-byte pieces.
+//
+// Packed rows are cut into windows of 16, whatever the lengths: a window's
+// warp places the units that begin with one of its rows (at most one can be
+// complete) and, row by row, the rows that lie in incomplete units.
+
+// A staged row: the input's 128 values, replaced by 128 fp16 values, or by 128
+// one-byte codes and the block scales (4, or 1 for turbo4) behind them.
+template <int T>
+struct Stage {
+  static constexpr int S = sizeof(typename RowType<T>::type);
+  static constexpr int kPitch = kD * S + 16;  // rows 4 banks apart
+  static constexpr int kWarpBytes = kUnitTokens * kPitch;
+  static constexpr int kBytes = kArWarps * kWarpBytes;
+};
+constexpr int kScaleAt = kD;  // byte offset of a staged row's scales
+
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+}
+
+// Copy the rows of `mask` (bit j: row j of the 16 at x) into their stage slots.
+template <int T>
+__device__ __forceinline__ void stage_rows(uint8_t *stage, const uint8_t *x, int64_t row_bytes,
+                                           unsigned mask, int lane) {
+  constexpr int kLanes = kD * Stage<T>::S / 16;  // lanes that carry one row
+  constexpr int kPerPass = 32 / kLanes;
+#pragma unroll
+  for (int j0 = 0; j0 < kUnitTokens; j0 += kPerPass) {
+    const int j = j0 + lane / kLanes, off = (lane % kLanes) * 16;
+    if ((mask >> j) & 1u)
+      copy_async16(stage + j * Stage<T>::kPitch + off, x + j * row_bytes + off);
+  }
+  copy_async_wait();
+  __syncwarp();
+}
+
+// Encode the staged row at `row` in place.
+__device__ __forceinline__ void encode_staged(int codec, const float (&x)[4], uint8_t *row,
+                                              int lane) {
+  if (codec == KVQ_F16) {
+    store4<KVQ_T_F16>(row + 8 * lane, x);
+    return;
+  }
+  int q[4];
+  __half d16;
+  if (codec == KVQ_Q8_0) encode_q8(x, q, d16);
+  else if (codec == KVQ_Q4_0) encode_q4(x, lane, q, d16);
+  else encode_turbo4(x, lane, q, d16);
+  reinterpret_cast<uint32_t *>(row)[lane] = (q[0] & 0xff) | ((q[1] & 0xff) << 8) |
+                                            ((q[2] & 0xff) << 16) |
+                                            (static_cast<uint32_t>(q[3] & 0xff) << 24);
+  __half *scales = reinterpret_cast<__half *>(row + kScaleAt);
+  if (codec == KVQ_TURBO4) {
+    if (lane == 0) scales[0] = d16;
+  } else if ((lane & 7) == 0) {
+    scales[lane >> 3] = d16;
+  }
+}
+
+// 16 bytes of the unit, chunk c, from the staged rows (row r at s + r * PITCH):
+// the inverse of the placement formulas of include/kvq.h.
+template <int SIDE, int PITCH>
+__device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) {
+  auto w32 = [&](int r, int byte) {
+    return *reinterpret_cast<const uint32_t *>(s + r * PITCH + byte);
+  };
+  auto w16 = [&](int r, int byte) -> uint32_t {
+    return *reinterpret_cast<const uint16_t *>(s + r * PITCH + byte);
+  };
+  uint32_t o[4];
+  const int lo = c & 3, g = (c >> 2) & 7, hi = c >> 5;  // (w or tig, row g or gq, block piece)
+  if (codec == KVQ_F16) {
+    if (SIDE == 0) {  // hi = 2b + rh: row g + 8rh, dims 32b + 4w .. and 32b + 16 + 4w ..
+      const uint8_t *row = s + (g + 8 * (hi & 1)) * PITCH + (hi >> 1) * 64 + lo * 8;
+      const uint2 a = *reinterpret_cast<const uint2 *>(row);
+      const uint2 b = *reinterpret_cast<const uint2 *>(row + 32);
+      return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    // hi = mt: dims 16 mt + 2 gq, + 1 of rows 2 tig + par + 8 rh
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh) {
+      const uint32_t a = w32(2 * lo + 8 * rh, (16 * hi + 2 * g) * 2);
+      const uint32_t b = w32(2 * lo + 1 + 8 * rh, (16 * hi + 2 * g) * 2);
+      o[2 * rh] = __byte_perm(a, b, 0x5410);
+      o[2 * rh + 1] = __byte_perm(a, b, 0x7632);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  const int data = codec == KVQ_Q8_0 ? 128 : 64;  // chunks of codes, then of scales
+  if (c >= data) {
+    const int k = c - data;
+    if (codec == KVQ_TURBO4) {  // one scale per row, 8 rows per chunk
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ra = SIDE == 0 ? 4 * k + i : 2 * (2 * k + (i >> 1)) + 8 * (i & 1);
+        const int rb = SIDE == 0 ? ra + 8 : ra + 1;
+        o[i] = w16(ra, kScaleAt) | (w16(rb, kScaleAt) << 16);
+      }
+    } else if (SIDE == 0) {  // rows k and k + 8, blocks 0..3
+      o[0] = w32(k, kScaleAt); o[1] = w32(k, kScaleAt + 4);
+      o[2] = w32(k + 8, kScaleAt); o[3] = w32(k + 8, kScaleAt + 4);
+    } else {  // tig = k / 2, blocks 2 (k % 2), + 1; rh; par
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 2 * (k & 1) + (i >> 1), r = 2 * (k >> 1) + 8 * (i & 1);
+        o[i] = w16(r, kScaleAt + 2 * b) | (w16(r + 1, kScaleAt + 2 * b) << 16);
+      }
+    }
+  } else if (codec == KVQ_Q8_0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (SIDE == 0) {  // (rh, h): dims 32b + 16h + 4w ..
+        o[i] = w32(g + 8 * (i >> 1), 32 * hi + 16 * (i & 1) + 4 * lo);
+      } else {  // (mt & 1, rh): dims 32 hi + 16 (mt & 1) + 2 gq, + 1
+        const int d = 32 * hi + 16 * (i >> 1) + 2 * g, r = 2 * lo + 8 * (i & 1);
+        o[i] = w16(r, d) | (w16(r + 1, d) << 16);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (SIDE == 0) {  // (b & 1, rh): levels of dims 4w .. low, 16 + 4w .. high
+        const int r = g + 8 * (i & 1), d = 32 * (2 * hi + (i >> 1)) + 4 * lo;
+        o[i] = w32(r, d) | (w32(r, d + 16) << 4);
+      } else {  // mt = 4 hi + i: byte par * 2 + rh, levels of dims d low, d + 16 high
+        const int mt = 4 * hi + i, d = 32 * (mt >> 1) + 8 * (mt & 1) + g;
+        o[i] = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint8_t *row = s + (2 * lo + (b >> 1) + 8 * (b & 1)) * PITCH;
+          o[i] |= static_cast<uint32_t>(row[d] | (row[d + 16] << 4)) << (8 * b);
+        }
+      }
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int T, int SIDE>
+__device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r0, int h,
+                                            uint8_t *stage, int lane) {
+  constexpr int which = SIDE + 1, kPitch = Stage<T>::kPitch, S = Stage<T>::S;
+  const int codec = p.codec[SIDE];
+  const uint8_t *x = p.x[which] + r0 * p.row[which] + h * p.head[which];
+  // lane j: row r0 + j (a unit that begins in the window ends within 31 rows)
+  const int64_t row = r0 + lane;
+  int s = 0, i = 0, n = 0;
+  int64_t slot = 0, unit = -1, pos = 0;
+  bool full = false;
+  if (row < p.n_rows && find_row(p, row, s, i, n)) {
+    slot = static_cast<int64_t>(p.seq_lens[s]) + i;
+    pos = p.positions ? p.positions[row] : slot;
+    const int first = i - static_cast<int>(slot & (kUnitTokens - 1));
+    full = slot >= 0 && first >= 0 && first + kUnitTokens <= n;
+    if (lane < kUnitTokens) unit = unit_of(p, s, slot);
+  }
+  const int r = static_cast<int>(slot & (kUnitTokens - 1));
+  const unsigned window = (1u << kUnitTokens) - 1;
+  const unsigned single = __ballot_sync(0xffffffffu, unit >= 0 && !full) & window;
+  const unsigned whole = __ballot_sync(0xffffffffu, unit >= 0 && full && r == 0) & window;
+  unit += h * unit_step(p);
+
+  auto angles = [&](int j) {  // of the row of lane j
+    return lane_angles(p.rope, rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j), p.err), lane);
+  };
+  if (single) {
+    stage_rows<T>(stage, x, p.row[which], single, lane);
+#pragma unroll 1
+    for (unsigned m = single; m; m &= m - 1) {
+      const int j = __ffs(m) - 1;
       float v[4];
-      load4<T>(x + h * p.head[0], v);
-      rotate_lane(p.rope, a, lane, v);
-      store4<KVQ_T_F16>(p.q_out + (row * p.n_q + h) * kD + 4 * lane, v);
+      load4<T>(stage + j * kPitch + 4 * lane * S, v);
+      if (SIDE == 0) rotate_lane(p.rope, angles(j), lane, v);
+      encode_f32_row_into<SIDE>(
+          codec, v, p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j) * unit_bytes(codec),
+          __shfl_sync(0xffffffffu, r, j), lane);
     }
-    return;
+    __syncwarp();
   }
-  if (slot < 0 || slot >= p.capacity) {
-    if (lane == 0) set_err(p.err, KVQ_DEVERR_CAPACITY);
-    return;
-  }
-  const int side = which - 1, codec = p.codec[side];
-  int64_t unit = static_cast<int64_t>(s) * p.n_kv * (p.capacity / kUnitTokens) + slot / kUnitTokens;
-  int64_t step = p.capacity / kUnitTokens;  // units from one kv head to the next
-  if (p.table) {
-    const int pg =
-        page_of(p.table, p.pages_per_seq, p.n_pages, s, slot / (kUnitTokens * kPageUnits));
-    if (pg < 0) {
-      if (lane == 0) set_err(p.err, KVQ_DEVERR_PAGE);
-      return;
+  if (whole) {
+    const int j0 = __ffs(whole) - 1;
+    stage_rows<T>(stage, x + j0 * p.row[which], p.row[which], window, lane);
+    if (SIDE == 0 || codec != KVQ_F16 || T != KVQ_T_F16) {  // else the rows are the codes
+      LaneAngles next;
+      if (SIDE == 0) next = angles(j0);
+#pragma unroll 1
+      for (int j = 0; j < kUnitTokens; ++j) {
+        float v[4];
+        load4<T>(stage + j * kPitch + 4 * lane * S, v);
+        if (SIDE == 0) {
+          const LaneAngles a = next;
+          next = angles((j0 + j + 1) & 31);  // requested a row ahead
+          rotate_lane(p.rope, a, lane, v);
+        }
+        __syncwarp();  // every lane has read its part before the codes replace it
+        encode_staged(codec, v, stage + j * kPitch, lane);
+      }
+      __syncwarp();
     }
-    unit = static_cast<int64_t>(pg) * p.n_kv * kPageUnits + (slot / kUnitTokens) % kPageUnits;
-    step = kPageUnits;
+    uint4 *dst = reinterpret_cast<uint4 *>(
+        p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
+    const int chunks = unit_bytes(codec) / 16;
+    for (int c = lane; c < chunks; c += 32) dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
   }
-  const int r = static_cast<int>(slot % kUnitTokens);
-  for (int h = h0; h < h1; ++h) {
-    float v[4];
-    load4<T>(x + h * p.head[which], v);
-    uint8_t *u = p.cache[side] + (unit + h * step) * unit_bytes(codec);
-    if (side == 0) {
-      rotate_lane(p.rope, a, lane, v);
-      encode_f32_row_into<0>(codec, v, u, r, lane);
-    } else {
-      encode_f32_row_into<1>(codec, v, u, r, lane);
-    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(kArThreads)
+    append_prompt_kernel(const __grid_constant__ AppendRopeParams p) {
+  extern __shared__ __align__(16) uint8_t stage[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  check_counts(p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x < p.kv_blocks) {  // (window, side, kv head), heads innermost
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kArWarps + warp;
+    const int h = static_cast<int>(item % p.n_kv), side = static_cast<int>(item / p.n_kv) & 1;
+    const int64_t r0 = item / (2 * p.n_kv) * kUnitTokens;
+    if (r0 >= p.n_rows) return;
+    uint8_t *mine = stage + warp * Stage<T>::kWarpBytes;
+    if (side == 0) window_item<T, 0>(p, r0, h, mine, lane);
+    else window_item<T, 1>(p, r0, h, mine, lane);
+  } else {
+    const int64_t item = (static_cast<int64_t>(blockIdx.x) - p.kv_blocks) * kArWarps + warp;
+    const int64_t row = item / p.q_chunks;
+    if (row < p.n_rows) row_item<T>(p, row, 0, static_cast<int>(item % p.q_chunks), lane);
   }
+}
+
+template <int T>
+cudaError_t launch_rows(AppendRopeParams &p, int num_sms, cudaStream_t stream) {
+  // A row's heads go to one warp each while the grid is small (the encoder's
+  // latency is paid once), to up to eight, sharing the angles, when it is not.
+  const int64_t slots = p.n_rows * (p.n_q * (p.q_chunks > 0) + 2 * p.n_kv);
+  while (p.hpw < kMaxHeads && slots / p.hpw > static_cast<int64_t>(num_sms) * 16) p.hpw *= 2;
+  if (p.q_chunks) p.q_chunks = (p.n_q + p.hpw - 1) / p.hpw;
+  p.kv_chunks = (p.n_kv + p.hpw - 1) / p.hpw;
+  const int64_t items = p.n_rows * (p.q_chunks + 2 * p.kv_chunks);
+  return launch_pdl(append_rows_kernel<T>, dim3(static_cast<unsigned>((items + kArWarps - 1) / kArWarps)),
+                    dim3(kArThreads), 0, stream, p);
+}
+
+template <int T>
+cudaError_t launch_prompt(AppendRopeParams &p, cudaStream_t stream) {
+  static std::atomic<uint64_t> optin{0};
+  const cudaError_t e = smem_optin(append_prompt_kernel<T>, Stage<T>::kBytes, optin);
+  if (e != cudaSuccess) return e;
+  p.hpw = kMaxHeads;
+  if (p.q_chunks) p.q_chunks = (p.n_q + p.hpw - 1) / p.hpw;
+  const int64_t windows = (p.n_rows + kUnitTokens - 1) / kUnitTokens;
+  p.kv_blocks = (windows * 2 * p.n_kv + kArWarps - 1) / kArWarps;
+  const int64_t blocks = p.kv_blocks + (p.n_rows * p.q_chunks + kArWarps - 1) / kArWarps;
+  return launch_pdl(append_prompt_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kArThreads),
+                    Stage<T>::kBytes, stream, p);
+}
+
+template <int T>
+cudaError_t launch_append_t(AppendRopeParams &p, int num_sms, cudaStream_t stream) {
+  // Whole units are worth their shared-memory pass where sequences bring half
+  // a unit of tokens or more on average.
+  return p.n_rows >= static_cast<int64_t>(p.n_seqs) * (kUnitTokens / 2)
+             ? launch_prompt<T>(p, stream)
+             : launch_rows<T>(p, num_sms, stream);
 }
 
 // Advance the lengths once every row has been placed.
@@ -152,7 +483,7 @@ cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const k
                                const kvq_rows &k, const kvq_rows &v, int64_t n_rows,
                                const int32_t *n_new, const int32_t *row_start,
                                const int32_t *positions, void *q_out, int update_lens,
-                               cudaStream_t stream) {
+                               int num_sms, cudaStream_t stream) {
   AppendRopeParams p;
   p.rope = rope_args(rope);
   const kvq_rows *rows[3] = {q ? q : &k, &k, &v};
@@ -180,15 +511,12 @@ cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const k
   p.capacity = L.capacity;
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
-  p.q_chunks = q ? (p.n_q + kHeadsPerWarp - 1) / kHeadsPerWarp : 0;
-  p.kv_chunks = (p.n_kv + kHeadsPerWarp - 1) / kHeadsPerWarp;
+  p.hpw = 1;
+  p.q_chunks = q ? 1 : 0;
   if (n_rows > 0) {
-    const int64_t items = n_rows * (p.q_chunks + 2 * p.kv_chunks);
-    const dim3 grid(static_cast<unsigned>((items + kArWarps - 1) / kArWarps)), block(kArThreads);
-    const cudaError_t e =
-        k.type == KVQ_T_F16    ? launch_pdl(append_rope_kernel<KVQ_T_F16>, grid, block, 0, stream, p)
-        : k.type == KVQ_T_BF16 ? launch_pdl(append_rope_kernel<KVQ_T_BF16>, grid, block, 0, stream, p)
-                               : launch_pdl(append_rope_kernel<KVQ_T_F32>, grid, block, 0, stream, p);
+    const cudaError_t e = k.type == KVQ_T_F16    ? launch_append_t<KVQ_T_F16>(p, num_sms, stream)
+                          : k.type == KVQ_T_BF16 ? launch_append_t<KVQ_T_BF16>(p, num_sms, stream)
+                                                 : launch_append_t<KVQ_T_F32>(p, num_sms, stream);
     if (e != cudaSuccess) return e;
   }
   if (!update_lens || n_rows == 0) return cudaSuccess;

@@ -9,13 +9,7 @@
 #include "kvq_check.h"
 #include "kvq_launch.h"
 
-namespace {
-
-using kvq::aligned;
-using kvq::check_layer;
-using kvq::decode_shape_ok;
-using kvq::kHeadDim;
-using kvq::valid_codec;
+namespace kvq {
 
 int device_sms() {
   static int cached[64] = {0};
@@ -29,6 +23,17 @@ int device_sms() {
   }
   return cached[dev];
 }
+
+}  // namespace kvq
+
+namespace {
+
+using kvq::aligned;
+using kvq::check_layer;
+using kvq::decode_shape_ok;
+using kvq::device_sms;
+using kvq::kHeadDim;
+using kvq::valid_codec;
 
 // The fused decode step; rope: with the rotation of the new keys and q.
 int decode_append(const kvq_layer *layer, const kvq_rope *rope, const int32_t *positions,

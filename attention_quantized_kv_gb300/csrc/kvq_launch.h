@@ -9,6 +9,9 @@
 
 namespace kvq {
 
+// SMs of the current device; 0 on an error.
+int device_sms();
+
 cudaError_t launch_append(const kvq_layer &L, const void *k_new, const void *v_new,
                           const int32_t *n_new, int max_new, int update_lens,
                           cudaStream_t stream);
@@ -89,7 +92,7 @@ cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const k
                                const kvq_rows &k, const kvq_rows &v, int64_t n_rows,
                                const int32_t *n_new, const int32_t *row_start,
                                const int32_t *positions, void *q_out, int update_lens,
-                               cudaStream_t stream);
+                               int num_sms, cudaStream_t stream);
 cudaError_t launch_evict_delta(const kvq_layer &L, const int32_t *evict, const int32_t *n_evicted,
                                int max_evict, int32_t *delta, cudaStream_t stream);
 cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const int32_t *delta,

@@ -126,15 +126,16 @@ __device__ __forceinline__ void rotate_lane(const RopeArgs &p, const LaneAngles 
 }
 
 // ------------------------------------------------------------- row types
+// (raw4: four consecutive values as they lie in memory)
 
 template <int T>
 struct RowType;
 template <>
-struct RowType<KVQ_T_F16> { using type = __half; };
+struct RowType<KVQ_T_F16> { using type = __half; using raw4 = uint2; };
 template <>
-struct RowType<KVQ_T_BF16> { using type = __nv_bfloat16; };
+struct RowType<KVQ_T_BF16> { using type = __nv_bfloat16; using raw4 = uint2; };
 template <>
-struct RowType<KVQ_T_F32> { using type = float; };
+struct RowType<KVQ_T_F32> { using type = float; using raw4 = float4; };
 
 // Four consecutive values as fp32 (p aligned to their size).
 template <int T>

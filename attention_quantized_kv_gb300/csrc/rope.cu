@@ -13,31 +13,76 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
+constexpr int64_t kTableBlocks = 152 * 8;  // every SM full
 
 // ------------------------------------------------------------------ table
 
 struct TableParams {
-  float2 *table;
-  int64_t n;             // n_pos * pairs
-  int pairs;
+  float *table;
+  int64_t n_pos;
+  int pairs, cols;         // planes; columns of one thread's planes
   uint64_t turns[kD / 2];  // frequency in units of 2^-64 turns per position
 };
 
-// One (position, plane) per thread.  pos * turns mod 2^64 is the angle as an
-// exact fraction of a turn; the nearest quarter turn is taken off as an
-// integer, so the remainder in [-1/8, 1/8] turns is exact too and rounds once
-// to fp32 whatever the position.
-__global__ void __launch_bounds__(kRopeThreads) table_kernel(TableParams p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  if (i >= p.n) return;
-  const uint64_t pos = static_cast<uint64_t>(i / p.pairs);
-  const uint64_t u = pos * p.turns[i % p.pairs];
+// Terms of the Taylor series of sin and cos in turns: (2 pi)^n / n!.
+constexpr double kTurn = 6.283185307179586477;  // 2 pi
+__host__ __device__ constexpr double turn_term(int n) {
+  return n == 0 ? 1.0 : turn_term(n - 1) * kTurn / n;
+}
+
+// (cos, sin) of u * 2^-64 turns.  The nearest quarter turn is taken off as an
+// integer, so the remainder t in [-1/8, 1/8] turns is exact and rounds once
+// to fp32 whatever the position (2^-24 of at most pi / 4 rad).  The series
+// end at t^9 and t^10, what is left out being below 2e-9; 2 pi t is taken
+// with 2 pi as the sum of two floats, so that the last addition's rounding is
+// the only other one of its size.  In all within 1.4 * 2^-24 (measured on the
+// host over 2M values), inside the documented 2^-23.
+__device__ __forceinline__ float2 cos_sin_turns(uint64_t u) {
+  constexpr float k1 = static_cast<float>(kTurn), k1lo = static_cast<float>(kTurn - k1);
+  constexpr float k2 = turn_term(2), k3 = turn_term(3), k4 = turn_term(4), k5 = turn_term(5),
+                  k6 = turn_term(6), k7 = turn_term(7), k8 = turn_term(8), k9 = turn_term(9),
+                  k10 = turn_term(10);
   const uint32_t quarter = static_cast<uint32_t>((u + (1ull << 61)) >> 62);
   const int64_t r = static_cast<int64_t>(u - (static_cast<uint64_t>(quarter) << 62));
-  float s, c;
-  sincospif(static_cast<float>(r) * 0x1p-63f, &s, &c);
+  const float t = static_cast<float>(r) * 0x1p-64f, t2 = t * t;
+  float s = fmaf(t2, fmaf(t2, fmaf(t2, k9, -k7), k5), -k3);
+  s = fmaf(t, k1, fmaf(t * t2, s, t * k1lo));
+  float c = fmaf(t2, fmaf(t2, fmaf(t2, fmaf(t2, -k10, k8), -k6), k4), -k2);
+  c = fmaf(t2, c, 1.0f);
   const float co = (quarter & 1) ? s : c, si = (quarter & 1) ? c : s;
-  p.table[i] = make_float2((quarter + 1) & 2 ? -co : co, quarter & 2 ? -si : si);
+  return make_float2((quarter + 1) & 2 ? -co : co, quarter & 2 ? -si : si);
+}
+
+// Thread (column, row lane): P planes of every (rows-per-pass)-th position.
+// The angle's fraction of a turn advances by a whole number of 2^-64 turns
+// per step, modulo 2^64, so the running sum is exact.  P = 2 stores 16 bytes
+// (P = 1: an odd number of planes).
+template <int P>
+__global__ void __launch_bounds__(kRopeThreads) table_kernel(const __grid_constant__ TableParams p) {
+  const int rows = kRopeThreads / p.cols;  // positions per block and pass
+  const int col = threadIdx.x % p.cols, row = threadIdx.x / p.cols;
+  if (row >= rows) return;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  int64_t pos = static_cast<int64_t>(blockIdx.x) * rows + row;
+  uint64_t u[P], du[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const uint64_t t = p.turns[col * P + k];
+    u[k] = t * static_cast<uint64_t>(pos);
+    du[k] = t * static_cast<uint64_t>(step);
+  }
+  float *out = p.table + (pos * p.pairs + col * P) * 2;
+  for (; pos < p.n_pos; pos += step, out += step * p.pairs * 2) {
+    const float2 a = cos_sin_turns(u[0]);
+    if (P == 2) {
+      const float2 b = cos_sin_turns(u[P - 1]);
+      *reinterpret_cast<float4 *>(out) = make_float4(a.x, a.y, b.x, b.y);
+    } else {
+      *reinterpret_cast<float2 *>(out) = a;
+    }
+#pragma unroll
+    for (int k = 0; k < P; ++k) u[k] += du[k];
+  }
 }
 
 // ------------------------------------------------------------------ apply
@@ -56,24 +101,35 @@ struct ApplyParams {
 
 constexpr int kHeadsPerWarp = 8;  // heads of one row that share a warp's angles
 
+// One warp per (row, up to eight heads): the angles are read once, and all
+// the heads' values are requested before the first is used.
 template <int TI, int TO>
 __global__ void __launch_bounds__(kRopeThreads) apply_kernel(ApplyParams p) {
   constexpr int SI = sizeof(typename RowType<TI>::type), SO = sizeof(typename RowType<TO>::type);
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
   const int64_t row = item / p.chunks;
   if (row >= p.n_rows) return;
   const int h0 = static_cast<int>(item % p.chunks) * kHeadsPerWarp;
+  const uint8_t *x = p.x + row * p.x_row + h0 * p.x_head + 4 * lane * SI;
+  uint8_t *y = p.y + row * p.y_row + h0 * p.y_head + 4 * lane * SO;
+  const int nh = min(kHeadsPerWarp, p.n_heads - h0);
+  typename RowType<TI>::raw4 raw[kHeadsPerWarp];
+#pragma unroll
+  for (int h = 0; h < kHeadsPerWarp; ++h)
+    if (h < nh) raw[h] = *reinterpret_cast<const typename RowType<TI>::raw4 *>(x + h * p.x_head);
   const int64_t pos = p.positions ? p.positions[row] : p.pos0 + row;
   const LaneAngles a = lane_angles(p.rope, rope_row(p.rope, pos, p.err), lane, p.sign);
-  const uint8_t *x = p.x + row * p.x_row + 4 * lane * SI;
-  uint8_t *y = p.y + row * p.y_row + 4 * lane * SO;
-  for (int h = h0; h < p.n_heads && h < h0 + kHeadsPerWarp; ++h) {
-    float v[4];
-    load4<TI>(x + h * p.x_head, v);
-    rotate_lane(p.rope, a, lane, v);
-    store4<TO>(y + h * p.y_head, v);
-  }
+#pragma unroll
+  for (int h = 0; h < kHeadsPerWarp; ++h)
+    if (h < nh) {
+      float v[4];
+      load4<TI>(&raw[h], v);
+      rotate_lane(p.rope, a, lane, v);
+      store4<TO>(y + h * p.y_head, v);
+    }
 }
 
 // ------------------------------------------------------------------ shift
@@ -147,8 +203,8 @@ __global__ void __launch_bounds__(kRopeThreads) shift_kernel(ShiftParams p) {
 template <int TI, int TO>
 cudaError_t launch_apply_t(const ApplyParams &p, cudaStream_t stream) {
   const int64_t blocks = (p.n_rows * p.chunks + kRopeWarps - 1) / kRopeWarps;
-  apply_kernel<TI, TO><<<static_cast<unsigned>(blocks), kRopeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(apply_kernel<TI, TO>, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads),
+                    0, stream, p);
 }
 
 }  // namespace
@@ -156,12 +212,17 @@ cudaError_t launch_apply_t(const ApplyParams &p, cudaStream_t stream) {
 cudaError_t launch_rope_table(const double *freqs, int rot_dim, int n_pos, float *table,
                               cudaStream_t stream) {
   TableParams p;
-  p.table = reinterpret_cast<float2 *>(table);
+  p.table = table;
+  p.n_pos = n_pos;
   p.pairs = rot_dim / 2;
-  p.n = static_cast<int64_t>(n_pos) * p.pairs;
   for (int i = 0; i < p.pairs; ++i) p.turns[i] = turns_of(freqs[i]);
-  const int64_t blocks = (p.n + kRopeThreads - 1) / kRopeThreads;
-  table_kernel<<<static_cast<unsigned>(blocks), kRopeThreads, 0, stream>>>(p);
+  const int planes = p.pairs % 2 == 0 ? 2 : 1;
+  p.cols = p.pairs / planes;
+  const int rows = kRopeThreads / p.cols;
+  const int64_t passes = (p.n_pos + rows - 1) / rows;
+  const unsigned grid = static_cast<unsigned>(passes < kTableBlocks ? passes : kTableBlocks);
+  if (planes == 2) table_kernel<2><<<grid, kRopeThreads, 0, stream>>>(p);
+  else table_kernel<1><<<grid, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

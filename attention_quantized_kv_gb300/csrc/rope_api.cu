@@ -155,8 +155,10 @@ int kv_append_rope(const kvq_layer *layer, const kvq_rope *rope, const kvq_rows 
         kvq::overlap(v->data, kvq::span_bytes(*v, n_rows, layer->n_kv_heads), q_out, nb))
       return KVQ_EINVAL;
   }
+  const int sms = kvq::device_sms();
+  if (sms <= 0) return KVQ_ECUDA;
   const cudaError_t e = kvq::launch_append_rope(*layer, *rope, q, *k, *v, n_rows, n_new, row_start,
-                                                positions, q_out, update_lens,
+                                                positions, q_out, update_lens, sms,
                                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
 }

@@ -466,8 +466,8 @@ KVQ_API int kvq_rope_apply(const kvq_rope *rope, const kvq_rows *x, const kvq_ro
  * attn_decode or attn_prefill_chunk.  q, k and v have one type.
  * Which rows belong to which sequence, one of:
  *   row_start (device int32 [n_seqs + 1], non-decreasing, packed rows):
- *     sequence s has rows row_start[s] .. row_start[s + 1) - 1; rows at or
- *     behind row_start[n_seqs] are padding: not read, and q_out not written;
+ *     sequence s has rows row_start[s] .. row_start[s + 1] - 1; rows from
+ *     row_start[n_seqs] on are padding: nothing is written for them;
  *   n_new (device int32 [n_seqs], padded rows): sequence s has rows
  *     s * (n_rows / n_seqs) .. + n_new[s] - 1 (n_rows a multiple of n_seqs,
  *     n_new[s] up to n_rows / n_seqs).
