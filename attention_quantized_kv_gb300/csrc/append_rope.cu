@@ -6,7 +6,7 @@
 
 #include "kvq_encode.cuh"
 #include "kvq_launch.h"
-#include "kvq_rope.cuh"
+#include "kvq_quad.cuh"
 
 namespace kvq {
 namespace {
@@ -29,6 +29,7 @@ struct AppendRopeParams {
   int n_seqs, n_q, n_kv, capacity, pages_per_seq, n_pages;
   int hpw, q_chunks, kv_chunks;  // heads per warp item; items of a row's q, k (or v) heads
   int64_t kv_blocks;             // prompts: blocks that place keys and values
+  int kind;                      // quad_kind
 };
 
 // New rows of sequence s, 0 and KVQ_DEVERR_ROWS where the caller's entries
@@ -194,9 +195,12 @@ __global__ void __launch_bounds__(kArThreads)
 // A prompt fills whole 16-token units, whose bytes interleave their tokens
 // (include/kvq.h): written row by row the V side would go out as 2-byte
 // stores, one 32-byte sector each.  So one warp takes a whole unit of one kv
-// head: its rows are copied into shared memory (16 of them in flight), encoded
-// there row by row, and the unit is put together 16 bytes per lane from the
-// 16 rows' codes and stored as contiguous 512-byte pieces.
+// head, and stores it as contiguous 512-byte pieces.
+//   K: every quad of lanes reads its two rows in the unit's own order, rotates
+//      and encodes them in registers (kvq_quad.cuh).
+//   V: the rows are copied into shared memory, 16 of them in flight; two lanes
+//      per row encode its four blocks; the unit is put together 16 bytes per
+//      lane from the 16 rows' codes.
 //
 // Packed rows are cut into windows of 16, whatever the lengths: a window's
 // warp places the units that begin with one of its rows (at most one can be
@@ -339,6 +343,97 @@ __device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Encode the staged rows' four 32-value blocks in place, lane l blocks
+// 2 (l / 16) and + 1 of row l % 16, each in registers: one division per block
+// and no exchange between lanes (q8_0 and q4_0).
+template <int T, int DC>
+__device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
+  uint8_t *row = stage + (lane & 15) * Stage<T>::kPitch;
+  const int b0 = 2 * (lane >> 4);
+  uint32_t code[2][8];
+  __half d16[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32 * Stage<T>::S / 16; ++i) {
+      const uint4 raw =
+          *reinterpret_cast<const uint4 *>(row + (b0 + k) * 32 * Stage<T>::S + 16 * i);
+      if (T == KVQ_T_F32) {
+        load4<T>(&raw, reinterpret_cast<float(&)[4]>(x[4 * i]));
+      } else {
+        load4<T>(&raw, reinterpret_cast<float(&)[4]>(x[8 * i]));
+        load4<T>(&raw.z, reinterpret_cast<float(&)[4]>(x[8 * i + 4]));
+      }
+    }
+    float d;
+    if (DC == KVQ_Q8_0) {
+      float a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a = fmaxf(a, fabsf(x[i]));
+      d = __fdiv_rn(a, 127.0f);
+    } else {
+      float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        hi = fmaxf(hi, x[i]);
+        lo = fminf(lo, x[i]);
+      }
+      float m = hi > -lo ? hi : lo;
+      if (hi == -lo) {  // the first of them
+#pragma unroll
+        for (int i = 31; i >= 0; --i)
+          if (fabsf(x[i]) == hi) m = x[i];
+      }
+      d = __fdiv_rn(m, -8.0f);
+    }
+    d16[k] = __float2half_rn(d);
+    const float rcp = d != 0.0f ? __frcp_rn(d) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      const uint2 c = quad_codes8<DC>(reinterpret_cast<const float(&)[8]>(x[i]), d, rcp);
+      code[k][i / 4] = DC == KVQ_Q8_0 ? c.x : clamp15x4(c.x);
+      code[k][i / 4 + 1] = DC == KVQ_Q8_0 ? c.y : clamp15x4(c.y);
+    }
+  }
+  __syncwarp();  // both lanes of a row have read it before its codes replace it
+  uint4 *out = reinterpret_cast<uint4 *>(row + 32 * b0);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    out[2 * k] = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+    out[2 * k + 1] = make_uint4(code[k][4], code[k][5], code[k][6], code[k][7]);
+  }
+  *reinterpret_cast<__half2 *>(row + kScaleAt + 2 * b0) = __halves2half2(d16[0], d16[1]);
+}
+
+// A whole unit of K: lane 4g + w reads rows g and g + 8 of the 16 at x, whose
+// positions the lanes j0 .. j0 + 15 hold.
+template <int T, int CODEC>
+__device__ __forceinline__ void quad_unit(const AppendRopeParams &p, const uint8_t *x, int j0,
+                                          int64_t pos, uint8_t *unit, int lane) {
+  using Raw = typename RowType<T>::raw4;
+  constexpr int S = Stage<T>::S;
+  const int g = lane >> 2, w = lane & 3;
+  QuadCodes<CODEC> q[2];
+  Raw raw[2][8];
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh)
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      raw[rh][c] = *reinterpret_cast<const Raw *>(x + (g + 8 * rh) * p.row[1] + (16 * c + 4 * w) * S);
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh) {
+    float v[8][4];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) load4<T>(&raw[rh][c], v[c]);
+    const float *row =
+        rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j0 + g + 8 * rh), p.err);
+    quad_rotate(p.rope, p.kind, row, w, 1.0f, v);
+    quad_encode<CODEC>(v, w, q[rh]);
+  }
+  quad_store<CODEC>(unit, lane, q);
+}
+
 template <int T, int SIDE>
 __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r0, int h,
                                             uint8_t *stage, int lane) {
@@ -382,33 +477,39 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
   }
   if (whole) {
     const int j0 = __ffs(whole) - 1;
-    stage_rows<T>(stage, x + j0 * p.row[which], p.row[which], window, lane);
-    if (SIDE == 0 || codec != KVQ_F16 || T != KVQ_T_F16) {  // else the rows are the codes
-      LaneAngles next;
-      if (SIDE == 0) next = angles(j0);
+    uint8_t *to = p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec);
+    const uint8_t *xu = x + j0 * p.row[which];
+    if (SIDE == 0 && p.kind != kQuadNone) {
+      if (codec == KVQ_F16) quad_unit<T, KVQ_F16>(p, xu, j0, pos, to, lane);
+      else if (codec == KVQ_Q8_0) quad_unit<T, KVQ_Q8_0>(p, xu, j0, pos, to, lane);
+      else if (codec == KVQ_Q4_0) quad_unit<T, KVQ_Q4_0>(p, xu, j0, pos, to, lane);
+      else quad_unit<T, KVQ_TURBO4>(p, xu, j0, pos, to, lane);
+      return;
+    }
+    stage_rows<T>(stage, xu, p.row[which], window, lane);
+    if (SIDE == 1 && codec == KVQ_Q8_0) {
+      encode_staged_blocks<T, KVQ_Q8_0>(stage, lane);
+    } else if (SIDE == 1 && codec == KVQ_Q4_0) {
+      encode_staged_blocks<T, KVQ_Q4_0>(stage, lane);
+    } else if (SIDE == 0 || codec != KVQ_F16 || T != KVQ_T_F16) {  // else the rows are the codes
 #pragma unroll 1
       for (int j = 0; j < kUnitTokens; ++j) {
         float v[4];
         load4<T>(stage + j * kPitch + 4 * lane * S, v);
-        if (SIDE == 0) {
-          const LaneAngles a = next;
-          next = angles((j0 + j + 1) & 31);  // requested a row ahead
-          rotate_lane(p.rope, a, lane, v);
-        }
+        if (SIDE == 0) rotate_lane(p.rope, angles(j0 + j), lane, v);
         __syncwarp();  // every lane has read its part before the codes replace it
         encode_staged(codec, v, stage + j * kPitch, lane);
       }
-      __syncwarp();
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(
-        p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
+    __syncwarp();
+    uint4 *dst = reinterpret_cast<uint4 *>(to);
     const int chunks = unit_bytes(codec) / 16;
     for (int c = lane; c < chunks; c += 32) dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
   }
 }
 
 template <int T>
-__global__ void __launch_bounds__(kArThreads)
+__global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
     append_prompt_kernel(const __grid_constant__ AppendRopeParams p) {
   extern __shared__ __align__(16) uint8_t stage[];
   grid_dependency_wait();
@@ -511,6 +612,7 @@ cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const k
   p.capacity = L.capacity;
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
+  p.kind = quad_kind(p.rope);
   p.hpw = 1;
   p.q_chunks = q ? 1 : 0;
   if (n_rows > 0) {

@@ -52,6 +52,53 @@ __device__ __forceinline__ int q4_from_quotient(float x, float d, float rcp) {
   return v > 15 ? 15 : v;
 }
 
+// Bytes 0 of a, b, c, d as one word (a in the lowest byte).
+__device__ __forceinline__ uint32_t low_bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// Four byte lanes holding 0..16, each clamped to 15 (16 - (16 >> 4)).
+__device__ __forceinline__ uint32_t clamp15x4(uint32_t w) { return w - ((w >> 4) & 0x01010101u); }
+
+// The quotient path of q8_from_quotient / q4_from_quotient on one chunk, two
+// values per instruction: k[v] gets the fast path's code (its lowest byte;
+// q4_0: the level before the clamp), and lo / hi collect the chunk's
+// distances from the rounding boundaries (q8_0: hi = the largest distance
+// to the nearest integer; q4_0: lo, hi = the range of u - floor(u)), which
+// say whether the fast path is the exact one for every value.
+template <int DC>
+__device__ __forceinline__ void rq_codes_fast(const float (&x)[8], float rcp, uint32_t (&k)[8],
+                                              float &lo, float &hi) {
+  const float2 r2 = make_float2(rcp, rcp), m2 = make_float2(kRoundMagic, kRoundMagic);
+  const float2 nm2 = make_float2(-kRoundMagic, -kRoundMagic), n1 = make_float2(-1.0f, -1.0f);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    if (DC == KVQ_Q8_0) {
+      const float2 t = __fmul2_rn(make_float2(x[j], x[j + 1]), r2);
+      const float2 tm = __fadd2_rn(t, m2);
+      const float2 fr = __ffma2_rn(__fadd2_rn(tm, nm2), n1, t);  // t - round(t)
+      hi = fmaxf(hi, fmaxf(fabsf(fr.x), fabsf(fr.y)));
+      k[j] = __float_as_uint(tm.x);
+      k[j + 1] = __float_as_uint(tm.y);
+    } else {
+      const float2 u =
+          __fadd2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), r2), make_float2(8.5f, 8.5f));
+      const float2 fm = __fadd2_rn(__fadd2_rn(u, make_float2(-0.5f, -0.5f)), m2);
+      const float2 fr = __ffma2_rn(__fadd2_rn(fm, nm2), n1, u);  // u - floor(u)
+      lo = fminf(lo, fminf(fr.x, fr.y));
+      hi = fmaxf(hi, fmaxf(fr.x, fr.y));
+      k[j] = __float_as_uint(fm.x);
+      k[j + 1] = __float_as_uint(fm.y);
+    }
+  }
+}
+
+// Whether the codes that rq_codes_fast gave a block (lo, hi over all its
+// chunks) are the exact path's.
+template <int DC>
+__device__ __forceinline__ bool codes_exact(float lo, float hi) {
+  return DC == KVQ_Q8_0 ? hi < 0.5f - 0x1p-14f : (lo > 0x1p-17f && hi < 1.0f - 0x1p-17f);
+}
+
 // q8_0: amax over the 8 lanes of the block, d = amax/127, q = round(x/d).
 __device__ __forceinline__ void encode_q8(const float (&x)[4], int (&q)[4], __half &d16) {
   float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));

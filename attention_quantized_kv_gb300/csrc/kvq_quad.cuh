@@ -1,0 +1,364 @@
+// kvq_quad.cuh -- rows of a K-side unit held by quads of lanes, in the order
+// in which the unit stores them (include/kvq.h): lane 4g + w of a warp holds,
+// of row g (or g + 8), the dims 16c + 4w + i as v[c][i] (c < 8, i < 4).  In
+// every codec those are the bytes of whole 16-byte pieces at 16 * lane of each
+// 512 bytes, so a warp loads and stores a unit as contiguous 512-byte pieces,
+// with no exchange between lanes but a block's maximum (two shuffles).  The
+// planes of a rotation lie inside a lane too, for the interleaved layout and
+// for half layouts whose rot_dim is a multiple of 32.
+#pragma once
+
+#include "kvq_encode.cuh"
+#include "kvq_rope.cuh"
+
+namespace kvq {
+namespace {
+
+// How a rotation's planes lie: kQuadInterleaved, or N = 1..4 for the planes
+// ((c, i), (c + N, i)) of a half layout with rot_dim 32 N.
+constexpr int kQuadInterleaved = 0;
+constexpr int kQuadNone = -1;  // planes cross lanes: rows go one by one
+
+inline int quad_kind(const RopeArgs &p) {
+  if (p.layout == KVQ_ROPE_INTERLEAVED) return kQuadInterleaved;
+  return p.rot % 32 == 0 ? p.rot / 32 : kQuadNone;
+}
+
+// (a, b) -> (a c - b s, a s + b c), every operation rounded (see kvq_rope.cuh).
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
+  const float x = __fadd_rn(__fmul_rn(a, c), __fmul_rn(b, -s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+template <int N>
+__device__ __forceinline__ void quad_rotate_half(const RopeArgs &p, const float *row, int w,
+                                                 float sign, float (&v)[8][4]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float4 t = *reinterpret_cast<const float4 *>(row + 2 * (16 * c + 4 * w));
+    const float4 u = *reinterpret_cast<const float4 *>(row + 2 * (16 * c + 4 * w) + 4);
+    const float co[4] = {t.x, t.z, u.x, u.z}, si[4] = {t.y, t.w, u.y, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      turn(v[c][i], v[c + N][i], __fmul_rn(co[i], p.magnitude),
+           sign * __fmul_rn(si[i], p.magnitude));
+  }
+}
+
+// Rotate the quad's row by the table row `row` (kind: quad_kind's, not
+// kQuadNone).
+__device__ __forceinline__ void quad_rotate(const RopeArgs &p, int kind, const float *row, int w,
+                                            float sign, float (&v)[8][4]) {
+  if (kind == 4) quad_rotate_half<4>(p, row, w, sign, v);
+  else if (kind == 3) quad_rotate_half<3>(p, row, w, sign, v);
+  else if (kind == 2) quad_rotate_half<2>(p, row, w, sign, v);
+  else if (kind == 1) quad_rotate_half<1>(p, row, w, sign, v);
+  else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int d = 16 * c + 4 * w;
+      if (d >= p.rot) continue;
+      float4 t;
+      if ((p.rot & 3) == 0) {
+        t = *reinterpret_cast<const float4 *>(row + d);
+      } else {  // table rows on 8-byte boundaries; the last plane may stand alone
+        const float2 a = *reinterpret_cast<const float2 *>(row + d);
+        float2 b = make_float2(0.0f, 0.0f);
+        if (d + 2 < p.rot) b = *reinterpret_cast<const float2 *>(row + d + 2);
+        t = make_float4(a.x, a.y, b.x, b.y);
+      }
+      turn(v[c][0], v[c][1], __fmul_rn(t.x, p.magnitude), sign * __fmul_rn(t.y, p.magnitude));
+      if (d + 2 < p.rot)
+        turn(v[c][2], v[c][3], __fmul_rn(t.z, p.magnitude), sign * __fmul_rn(t.w, p.magnitude));
+    }
+  }
+}
+
+// ------------------------------------------------------------- turbo4 rows
+
+__device__ __forceinline__ void quad_signs(float (&v)[8][4], int w) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t bits = turbo_signs(c >> 1) >> (16 * (c & 1) + 4 * w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((bits >> i) & 1u) v[c][i] = -v[c][i];
+  }
+}
+
+// Unnormalised Sylvester-order FWHT, stages 1, 2 (i), 4, 8 (lanes), 16, 32, 64
+// (c), each output one fp32 addition or subtraction, as fwht128_warp's.
+__device__ __forceinline__ void quad_fwht(float (&v)[8][4], int w) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float a0 = __fadd_rn(v[c][0], v[c][1]), a1 = __fsub_rn(v[c][0], v[c][1]);
+    const float a2 = __fadd_rn(v[c][2], v[c][3]), a3 = __fsub_rn(v[c][2], v[c][3]);
+    v[c][0] = __fadd_rn(a0, a2); v[c][2] = __fsub_rn(a0, a2);
+    v[c][1] = __fadd_rn(a1, a3); v[c][3] = __fsub_rn(a1, a3);
+  }
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1) {
+    const bool upper = (w & m) != 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float o = __shfl_xor_sync(0xffffffffu, v[c][i], m);
+        v[c][i] = upper ? __fsub_rn(o, v[c][i]) : __fadd_rn(v[c][i], o);
+      }
+  }
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if ((c & h) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = v[c][i], b = v[c + h][i];
+          v[c][i] = __fadd_rn(a, b);
+          v[c + h][i] = __fsub_rn(a, b);
+        }
+      }
+}
+
+// ------------------------------------------------------------- codes
+
+// A lane's codes of one row: f16 words 2c, 2c + 1 = v[c]; q8_0 word c = v[c];
+// nibble codecs word b = levels v[2b] low, v[2b + 1] high.  scale: of block w
+// of the row (turbo4: the row's).
+template <int CODEC>
+struct QuadCodes {
+  static constexpr int N = CODEC == KVQ_F16 ? 16 : CODEC == KVQ_Q8_0 ? 8 : 4;
+  uint32_t w[N];
+  uint16_t scale;
+};
+
+// Both rows (g, g + 8) of the lane, from and to the unit.
+template <int CODEC>
+__device__ __forceinline__ void quad_load(const uint8_t *unit, int lane,
+                                          QuadCodes<CODEC> (&q)[2]) {
+  const uint4 *u = reinterpret_cast<const uint4 *>(unit) + lane;
+  const int g = lane >> 2, w = lane & 3;
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // piece 2b + rh
+      const uint4 x = u[k * 32];
+      uint32_t *d = &q[k & 1].w[4 * (k >> 1)];
+      d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+    }
+    return;
+  }
+  const uint16_t *sc = reinterpret_cast<const uint16_t *>(unit + unit_scale_offset(CODEC));
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh)
+    q[rh].scale = CODEC == KVQ_TURBO4 ? sc[2 * g + rh] : sc[8 * g + 4 * rh + w];
+  if (CODEC == KVQ_Q8_0) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint4 x = u[b * 32];
+      q[0].w[2 * b] = x.x; q[0].w[2 * b + 1] = x.y;
+      q[1].w[2 * b] = x.z; q[1].w[2 * b + 1] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 x = u[j * 32];
+      q[0].w[2 * j] = x.x; q[1].w[2 * j] = x.y;
+      q[0].w[2 * j + 1] = x.z; q[1].w[2 * j + 1] = x.w;
+    }
+  }
+}
+
+template <int CODEC>
+__device__ __forceinline__ void quad_store(uint8_t *unit, int lane,
+                                           const QuadCodes<CODEC> (&q)[2]) {
+  uint4 *u = reinterpret_cast<uint4 *>(unit) + lane;
+  const int g = lane >> 2, w = lane & 3;
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t *d = &q[k & 1].w[4 * (k >> 1)];
+      u[k * 32] = make_uint4(d[0], d[1], d[2], d[3]);
+    }
+    return;
+  }
+  uint16_t *sc = reinterpret_cast<uint16_t *>(unit + unit_scale_offset(CODEC));
+  if (CODEC == KVQ_TURBO4) {
+    if (w < 2) sc[2 * g + w] = w == 0 ? q[0].scale : q[1].scale;
+  } else {
+    sc[8 * g + w] = q[0].scale;
+    sc[8 * g + 4 + w] = q[1].scale;
+  }
+  if (CODEC == KVQ_Q8_0) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      u[b * 32] = make_uint4(q[0].w[2 * b], q[0].w[2 * b + 1], q[1].w[2 * b], q[1].w[2 * b + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      u[j * 32] = make_uint4(q[0].w[2 * j], q[1].w[2 * j], q[0].w[2 * j + 1], q[1].w[2 * j + 1]);
+  }
+}
+
+__device__ __forceinline__ float half_bits(uint32_t b) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+}
+
+// The row's values, exact in fp32 (all 32 lanes).
+template <int CODEC>
+__device__ __forceinline__ void quad_decode(const QuadCodes<CODEC> &q, int w, float (&v)[8][4]) {
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&q.w[2 * c]));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&q.w[2 * c + 1]));
+      v[c][0] = a.x; v[c][1] = a.y; v[c][2] = b.x; v[c][3] = b.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float d = half_bits(CODEC == KVQ_TURBO4
+                                  ? q.scale
+                                  : __shfl_sync(0xffffffffu, static_cast<uint32_t>(q.scale), b, 4));
+    if (CODEC == KVQ_Q8_0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[2 * b + h][i] =
+              d * static_cast<float>(static_cast<int8_t>(q.w[2 * b + h] >> (8 * i)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = q.w[b] >> (8 * i);
+        v[2 * b][i] = d * static_cast<float>(static_cast<int>(x & 15u) - 8);
+        v[2 * b + 1][i] = d * static_cast<float>(static_cast<int>((x >> 4) & 15u) - 8);
+      }
+    }
+  }
+  if (CODEC == KVQ_TURBO4) {
+    quad_fwht(v, w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[c][i] *= 0.0625f;
+    quad_signs(v, w);
+  }
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// The codes of 8 values of one block by its scale (rq_codes_fast, and value
+// by value where one lies too near a rounding boundary), as two words of
+// bytes; levels of the nibble codecs not yet clamped.
+template <int DC>
+__device__ __forceinline__ uint2 quad_codes8(const float (&x)[8], float d, float rcp) {
+  uint32_t k[8];
+  if (d != 0.0f) {
+    float lo = 1.0f, hi = 0.0f;
+    rq_codes_fast<DC>(x, rcp, k, lo, hi);
+    if (!codes_exact<DC>(lo, hi)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        k[i] = static_cast<uint32_t>(DC == KVQ_Q8_0 ? q8_from_quotient(x[i], d, rcp)
+                                                    : q4_from_quotient(x[i], d, rcp));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = DC == KVQ_Q8_0 ? 0u : 8u;
+  }
+  return make_uint2(low_bytes4(k[0], k[1], k[2], k[3]), low_bytes4(k[4], k[5], k[6], k[7]));
+}
+
+// The scale's numerator for the 4-bit rule over the values of N planes groups
+// of the quad: the signed value of largest magnitude, the lowest dim on ties
+// (all 32 lanes; c0 .. c0 + N - 1).
+template <int N>
+__device__ __forceinline__ float quad_signed_max(const float (&v)[8][4], int c0, int w) {
+  float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi = fmaxf(hi, v[c0 + c][i]);
+      lo = fminf(lo, v[c0 + c][i]);
+    }
+  hi = quad_max(hi);
+  lo = -quad_max(-lo);
+  const bool tie = hi == -lo;
+  if (__any_sync(0xffffffffu, tie)) {  // the first of the dims that hold +-hi
+    int best = 1 << 20;
+#pragma unroll
+    for (int c = N - 1; c >= 0; --c)
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        const float x = v[c0 + c][i];
+        if (fabsf(x) == hi) best = (16 * c + 4 * w + i) * 2 + (__float_as_uint(x) >> 31);
+      }
+    best = min(best, __shfl_xor_sync(0xffffffffu, best, 1));
+    best = min(best, __shfl_xor_sync(0xffffffffu, best, 2));
+    if (tie) return (best & 1) ? -fabsf(hi) : fabsf(hi);  // (+-0 keeps its sign)
+  }
+  return hi > -lo ? hi : lo;
+}
+
+// Encode the quad's row (all 32 lanes).
+template <int CODEC>
+__device__ __forceinline__ void quad_encode(float (&v)[8][4], int w, QuadCodes<CODEC> &q) {
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      q.w[2 * c] = pack_half2(v[c][0], v[c][1]);
+      q.w[2 * c + 1] = pack_half2(v[c][2], v[c][3]);
+    }
+    return;
+  }
+  if (CODEC == KVQ_TURBO4) {
+    quad_signs(v, w);
+    quad_fwht(v, w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[c][i] *= 0.125f;
+  }
+  // Lane w takes block w's division (turbo4: all the row's), the quad shares it.
+  float num[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (CODEC == KVQ_Q8_0) {
+      float a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(v[2 * b][i]), fabsf(v[2 * b + 1][i])));
+      num[b] = quad_max(a);
+    } else {
+      num[b] = CODEC == KVQ_Q4_0 ? quad_signed_max<2>(v, 2 * b, w)
+               : b == 0          ? quad_signed_max<8>(v, 0, w)
+                                 : num[0];
+    }
+  }
+  const float mine = w == 0 ? num[0] : w == 1 ? num[1] : w == 2 ? num[2] : num[3];
+  const float dw = CODEC == KVQ_Q8_0 ? __fdiv_rn(mine, 127.0f) : __fdiv_rn(mine, -8.0f);
+  const float rw = dw != 0.0f ? __frcp_rn(dw) : 0.0f;
+  q.scale = __half_as_ushort(__float2half_rn(dw));
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float d = __shfl_sync(0xffffffffu, dw, b, 4), rcp = __shfl_sync(0xffffffffu, rw, b, 4);
+    const float x[8] = {v[2 * b][0],     v[2 * b][1],     v[2 * b][2],     v[2 * b][3],
+                        v[2 * b + 1][0], v[2 * b + 1][1], v[2 * b + 1][2], v[2 * b + 1][3]};
+    const uint2 k = quad_codes8<CODEC == KVQ_Q8_0 ? KVQ_Q8_0 : KVQ_Q4_0>(x, d, rcp);
+    if (CODEC == KVQ_Q8_0) {
+      q.w[2 * b] = k.x;
+      q.w[2 * b + 1] = k.y;
+    } else {
+      q.w[b] = clamp15x4(k.x) | (clamp15x4(k.y) << 4);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace kvq

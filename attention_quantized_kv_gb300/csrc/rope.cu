@@ -6,7 +6,7 @@
 
 #include "kvq_encode.cuh"
 #include "kvq_launch.h"
-#include "kvq_rope.cuh"
+#include "kvq_quad.cuh"
 
 namespace kvq {
 namespace {
@@ -166,10 +166,58 @@ struct ShiftParams {
   const int32_t *seq_lens, *delta, *table;
   int32_t *err;
   int codec, n_kv, capacity, pages_per_seq, n_pages;
+  int kind;  // quad_kind
 };
 
-// One warp per (sequence, token): its K rows of every kv head.
-__global__ void __launch_bounds__(kRopeThreads) shift_kernel(ShiftParams p) {
+// One warp per (sequence, 16-token unit, kv head): both rows of every quad are
+// read as they lie, turned by their tokens' shifts, encoded again and stored
+// as they lay; rows that do not move keep their codes.  The unit's bytes are
+// requested beside the shifts, which in an eviction's wake are seldom all
+// zero.
+template <int CODEC>
+__global__ void __launch_bounds__(kRopeThreads) shift_units_kernel(ShiftParams p) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, g = lane >> 2, w = lane & 3, s = blockIdx.y;
+  const int item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int j = item / p.n_kv, h = item % p.n_kv;  // unit of the sequence, kv head
+  const int len = min(p.seq_lens[s], p.capacity);
+  if (j * kUnitTokens >= len) return;
+  int64_t unit = (static_cast<int64_t>(s) * p.n_kv + h) * (p.capacity / kUnitTokens) + j;
+  if (p.table) {
+    const int pg = page_of(p.table, p.pages_per_seq, p.n_pages, s, j / kPageUnits);
+    if (pg < 0) {
+      if (lane == 0) set_err(p.err, KVQ_DEVERR_PAGE);
+      return;
+    }
+    unit = (static_cast<int64_t>(pg) * p.n_kv + h) * kPageUnits + j % kPageUnits;
+  }
+  uint8_t *u = p.k + unit * unit_bytes(CODEC);
+  QuadCodes<CODEC> q[2];
+  quad_load<CODEC>(u, lane, q);
+  int d[2];
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh) {
+    const int t = j * kUnitTokens + g + 8 * rh;
+    d[rh] = t < len ? p.delta[static_cast<int64_t>(s) * p.capacity + t] : 0;
+  }
+  if (!__any_sync(0xffffffffu, d[0] != 0 || d[1] != 0)) return;
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh) {
+    float v[8][4];
+    quad_decode<CODEC>(q[rh], w, v);
+    const int64_t by = d[rh];
+    const float *row = rope_row(p.rope, by < 0 ? -by : by, p.err);
+    quad_rotate(p.rope, p.kind, row, w, by < 0 ? -1.0f : 1.0f, v);
+    QuadCodes<CODEC> e;
+    quad_encode<CODEC>(v, w, e);
+    if (by != 0) q[rh] = e;
+  }
+  quad_store<CODEC>(u, lane, q);
+}
+
+// Planes that cross lanes: one warp per (sequence, token), its K rows of every
+// kv head one by one.
+__global__ void __launch_bounds__(kRopeThreads) shift_rows_kernel(ShiftParams p) {
   grid_dependency_wait();
   const int s = blockIdx.y, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
@@ -274,8 +322,18 @@ cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const in
   p.capacity = L.capacity;
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
-  const dim3 grid((L.capacity + kRopeWarps - 1) / kRopeWarps, L.n_seqs);
-  return launch_pdl(shift_kernel, grid, dim3(kRopeThreads), 0, stream, p);
+  p.kind = quad_kind(p.rope);
+  if (p.kind == kQuadNone) {
+    const dim3 grid((L.capacity + kRopeWarps - 1) / kRopeWarps, L.n_seqs);
+    return launch_pdl(shift_rows_kernel, grid, dim3(kRopeThreads), 0, stream, p);
+  }
+  const int64_t items = static_cast<int64_t>(L.capacity / kUnitTokens) * L.n_kv_heads;
+  const dim3 grid(static_cast<unsigned>((items + kRopeWarps - 1) / kRopeWarps), L.n_seqs);
+  const auto kernel = L.codec_k == KVQ_F16    ? shift_units_kernel<KVQ_F16>
+                      : L.codec_k == KVQ_Q8_0 ? shift_units_kernel<KVQ_Q8_0>
+                      : L.codec_k == KVQ_Q4_0 ? shift_units_kernel<KVQ_Q4_0>
+                                              : shift_units_kernel<KVQ_TURBO4>;
+  return launch_pdl(kernel, grid, dim3(kRopeThreads), 0, stream, p);
 }
 
 }  // namespace kvq
