@@ -140,14 +140,16 @@ __device__ __forceinline__ void row_item(const AppendRopeParams &p, int64_t row,
   if (which < 2)
     a = lane_angles(p.rope, rope_row(p.rope, p.positions ? p.positions[row] : slot, p.err), lane);
   if (which == 0) {
+    with_lanes(p.rope, [&](auto lanes) {
 #pragma unroll
-    for (int h = 0; h < kMaxHeads; ++h)
-      if (h < nh) {
-        float v[4];
-        load4<T>(&raw[h], v);
-        rotate_lane(p.rope, a, lane, v);
-        store4<KVQ_T_F16>(p.q_out + (row * p.n_q + h0 + h) * kD + 4 * lane, v);
-      }
+      for (int h = 0; h < kMaxHeads; ++h)
+        if (h < nh) {
+          float v[4];
+          load4<T>(&raw[h], v);
+          rotate_lane<decltype(lanes)::value>(p.rope, a, lane, v);
+          store4<KVQ_T_F16>(p.q_out + (row * p.n_q + h0 + h) * kD + 4 * lane, v);
+        }
+    });
     return;
   }
   const int64_t unit = unit_of(p, s, slot), step = unit_step(p);

@@ -253,26 +253,33 @@ __device__ __forceinline__ float quad_max(float x) {
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
-// The codes of 8 values of one block by its scale (rq_codes_fast, and value
-// by value where one lies too near a rounding boundary), as two words of
-// bytes; levels of the nibble codecs not yet clamped.
+// The codes of 8 values value by value: where rq_codes_fast's distances say
+// that one lies too near a rounding boundary (of random values one group of
+// eight in 2^10 for q8_0, in 2^13 for 4 bits).  A call, so that its length stays out of the callers.
+template <int DC>
+__device__ __noinline__ uint2 codes8_exact(float x0, float x1, float x2, float x3, float x4,
+                                           float x5, float x6, float x7, float d, float rcp) {
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+  uint32_t k[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    k[i] = static_cast<uint32_t>(DC == KVQ_Q8_0 ? q8_from_quotient(x[i], d, rcp)
+                                                : q4_from_quotient(x[i], d, rcp));
+  return make_uint2(low_bytes4(k[0], k[1], k[2], k[3]), low_bytes4(k[4], k[5], k[6], k[7]));
+}
+
+// The codes of 8 values of one block by its scale, as two words of bytes;
+// levels of the nibble codecs not yet clamped.
 template <int DC>
 __device__ __forceinline__ uint2 quad_codes8(const float (&x)[8], float d, float rcp) {
   uint32_t k[8];
-  if (d != 0.0f) {
-    float lo = 1.0f, hi = 0.0f;
-    rq_codes_fast<DC>(x, rcp, k, lo, hi);
-    if (!codes_exact<DC>(lo, hi)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        k[i] = static_cast<uint32_t>(DC == KVQ_Q8_0 ? q8_from_quotient(x[i], d, rcp)
-                                                    : q4_from_quotient(x[i], d, rcp));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = DC == KVQ_Q8_0 ? 0u : 8u;
-  }
-  return make_uint2(low_bytes4(k[0], k[1], k[2], k[3]), low_bytes4(k[4], k[5], k[6], k[7]));
+  float lo = 1.0f, hi = 0.0f;
+  rq_codes_fast<DC>(x, rcp, k, lo, hi);
+  uint2 c = make_uint2(low_bytes4(k[0], k[1], k[2], k[3]), low_bytes4(k[4], k[5], k[6], k[7]));
+  if (d == 0.0f) c = DC == KVQ_Q8_0 ? make_uint2(0u, 0u) : make_uint2(0x08080808u, 0x08080808u);
+  else if (!codes_exact<DC>(lo, hi))
+    c = codes8_exact<DC>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], d, rcp);
+  return c;
 }
 
 // The scale's numerator for the 4-bit rule over the values of N planes groups

@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kvq_device.cuh"
 
 namespace kvq {
@@ -96,14 +98,19 @@ __device__ __forceinline__ LaneAngles lane_angles(const RopeArgs &p, const float
   return a;
 }
 
+// How a row's partners lie, a kernel's uniform branch outside its loop over
+// rows: in the lane, in another lane's same element, or anywhere.
+enum class Lanes { kInterleaved, kHalf, kAny };
+
 // Rotate the row that the warp holds (all 32 lanes).
+template <Lanes L>
 __device__ __forceinline__ void rotate_lane(const RopeArgs &p, const LaneAngles &a, int lane,
                                             float (&x)[4]) {
   const int h = p.rot >> 1, d0 = 4 * lane;
   float o[4];  // the partners
-  if (p.layout == KVQ_ROPE_INTERLEAVED) {
+  if (L == Lanes::kInterleaved) {
     o[0] = x[1]; o[1] = x[0]; o[2] = x[3]; o[3] = x[2];
-  } else if ((h & 3) == 0) {
+  } else if (L == Lanes::kHalf) {
     const int src = d0 < h ? lane + (h >> 2) : lane - (h >> 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], src & 31);
@@ -123,6 +130,19 @@ __device__ __forceinline__ void rotate_lane(const RopeArgs &p, const LaneAngles 
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (d0 + i < p.rot) x[i] = __fadd_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(o[i], a.s[i]));
+}
+
+// f(the rope's Lanes as a constant).
+template <typename F>
+__device__ __forceinline__ void with_lanes(const RopeArgs &p, F f) {
+  if (p.layout == KVQ_ROPE_INTERLEAVED) f(std::integral_constant<Lanes, Lanes::kInterleaved>());
+  else if ((p.rot & 7) == 0) f(std::integral_constant<Lanes, Lanes::kHalf>());
+  else f(std::integral_constant<Lanes, Lanes::kAny>());
+}
+
+__device__ __forceinline__ void rotate_lane(const RopeArgs &p, const LaneAngles &a, int lane,
+                                            float (&x)[4]) {
+  with_lanes(p, [&](auto lanes) { rotate_lane<decltype(lanes)::value>(p, a, lane, x); });
 }
 
 // ------------------------------------------------------------- row types

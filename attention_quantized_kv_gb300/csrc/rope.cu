@@ -122,14 +122,16 @@ __global__ void __launch_bounds__(kRopeThreads) apply_kernel(ApplyParams p) {
     if (h < nh) raw[h] = *reinterpret_cast<const typename RowType<TI>::raw4 *>(x + h * p.x_head);
   const int64_t pos = p.positions ? p.positions[row] : p.pos0 + row;
   const LaneAngles a = lane_angles(p.rope, rope_row(p.rope, pos, p.err), lane, p.sign);
+  with_lanes(p.rope, [&](auto lanes) {
 #pragma unroll
-  for (int h = 0; h < kHeadsPerWarp; ++h)
-    if (h < nh) {
-      float v[4];
-      load4<TI>(&raw[h], v);
-      rotate_lane(p.rope, a, lane, v);
-      store4<TO>(y + h * p.y_head, v);
-    }
+    for (int h = 0; h < kHeadsPerWarp; ++h)
+      if (h < nh) {
+        float v[4];
+        load4<TI>(&raw[h], v);
+        rotate_lane<decltype(lanes)::value>(p.rope, a, lane, v);
+        store4<TO>(y + h * p.y_head, v);
+      }
+  });
 }
 
 // ------------------------------------------------------------------ shift
@@ -175,7 +177,7 @@ struct ShiftParams {
 // requested beside the shifts, which in an eviction's wake are seldom all
 // zero.
 template <int CODEC>
-__global__ void __launch_bounds__(kRopeThreads) shift_units_kernel(ShiftParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) shift_units_kernel(ShiftParams p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, g = lane >> 2, w = lane & 3, s = blockIdx.y;
   const int item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
