@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from array import array
 
 import torch
 
@@ -125,8 +126,10 @@ class KVLayer:
 
     def desc(self) -> kvq_layer:
         """The C descriptor (rebuilt only when a buffer was replaced)."""
-        key = (_ptr(self.k_cache), _ptr(self.v_cache), _ptr(self.seq_lens), _ptr(self.err),
-               self.codec_k, self.codec_v, _ptr(self.block_table), self.n_pages)
+        table = self.block_table
+        key = (self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.seq_lens.data_ptr(),
+               self.err.data_ptr(), self.codec_k, self.codec_v,
+               None if table is None else table.data_ptr(), self.n_pages)
         if self._desc is None or self._desc_key != key:
             d = kvq_layer()
             d.n_seqs, d.n_kv_heads, d.n_q_heads = self.n_seqs, self.n_kv_heads, self.n_q_heads
@@ -406,11 +409,11 @@ def kvq_rope_freqs(rot_dim: int = HEAD_DIM, base: float = 10000.0, scaling: int 
     scaled frequency into the plain one (``high`` defaults to 4 and 32)."""
     if high is None:
         high = 32.0 if scaling == KVQ_ROPE_YARN else 4.0
-    out = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    out = array("d", bytes(8 * max(1, int(rot_dim) // 2)))
     _check(_abi.load().kvq_rope_freqs(int(rot_dim), float(base), int(scaling), float(factor),
-                                      float(orig_len), float(low), float(high), out),
-           "kvq_rope_freqs")
-    return list(out)
+                                      float(orig_len), float(low), float(high),
+                                      out.buffer_info()[0]), "kvq_rope_freqs")
+    return out.tolist()
 
 
 def kvq_rope_table(freqs, table, stream=None) -> None:
@@ -419,7 +422,8 @@ def kvq_rope_table(freqs, table, stream=None) -> None:
     dev = _cuda_device(table, "kvq_rope_table")
     n = len(freqs)
     ptr = _need(table, torch.float32, (table.shape[0], n, 2), dev, "kvq_rope_table: table")
-    _check(_abi.load().kvq_rope_table((ctypes.c_double * n)(*freqs), 2 * n, table.shape[0], ptr,
+    f = array("d", freqs)
+    _check(_abi.load().kvq_rope_table(f.buffer_info()[0], 2 * n, table.shape[0], ptr,
                                       _stream_ptr(stream)), "kvq_rope_table")
 
 

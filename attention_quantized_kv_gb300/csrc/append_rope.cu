@@ -27,9 +27,11 @@ struct AppendRopeParams {
   int32_t *err;
   int64_t n_rows, max_new;  // max_new: padded rows per sequence
   int n_seqs, n_q, n_kv, capacity, pages_per_seq, n_pages;
-  int hpw, q_chunks, kv_chunks;  // heads per warp item; items of a row's q, k (or v) heads
+  int q_hpw, hpw;           // heads per warp item, of q and of k or v
+  int q_chunks, kv_chunks;  // items of a row's q, of its k (or v) heads
   int64_t kv_blocks;             // prompts: blocks that place keys and values
   int kind;                      // quad_kind
+  bool eight;                    // eight_lanes
 };
 
 // New rows of sequence s, 0 and KVQ_DEVERR_ROWS where the caller's entries
@@ -120,6 +122,24 @@ __device__ __forceinline__ void check_counts(const AppendRopeParams &p) {
   }
 }
 
+// One warp: up to 16 heads of q of one row (planes that eight lanes hold).
+template <int T>
+__device__ __forceinline__ void q_item(const AppendRopeParams &p, int64_t row, int chunk,
+                                       int lane) {
+  constexpr int N = T == KVQ_T_F32 ? 2 : 4;
+  const int h0 = chunk * p.q_hpw;
+  rotate_heads_eight<T, KVQ_T_F16, N>(
+      p.rope, p.x[0] + row * p.row[0] + h0 * p.head[0], p.head[0],
+      reinterpret_cast<uint8_t *>(p.q_out + (row * p.n_q + h0) * kD), 2 * kD,
+      min(p.q_hpw, p.n_q - h0), 1.0f, lane, [&]() -> const float * {
+        int s, i;
+        if (!find_row_warp(p, row, lane, s, i)) return nullptr;
+        return rope_row(
+            p.rope, p.positions ? p.positions[row] : static_cast<int64_t>(p.seq_lens[s]) + i,
+            p.err);
+      });
+}
+
 // One warp: up to hpw heads of q (which 0), k (1) or v (2) of one row, every
 // value requested before the row's place and angles are looked up.
 template <int T>
@@ -127,7 +147,8 @@ __device__ __forceinline__ void row_item(const AppendRopeParams &p, int64_t row,
                                          int chunk, int lane) {
   using Raw = typename RowType<T>::raw4;
   constexpr int S = sizeof(typename RowType<T>::type);
-  const int h0 = chunk * p.hpw, nh = min(p.hpw, (which == 0 ? p.n_q : p.n_kv) - h0);
+  const int per = which == 0 ? p.q_hpw : p.hpw;
+  const int h0 = chunk * per, nh = min(per, (which == 0 ? p.n_q : p.n_kv) - h0);
   const uint8_t *x = p.x[which] + row * p.row[which] + h0 * p.head[which] + 4 * lane * S;
   Raw raw[kMaxHeads];
 #pragma unroll
@@ -189,7 +210,8 @@ __global__ void __launch_bounds__(kArThreads)
     which = 1 + chunk / p.kv_chunks;
     chunk %= p.kv_chunks;
   }
-  row_item<T>(p, row, which, chunk, lane);
+  if (which == 0 && p.eight) q_item<T>(p, row, chunk, lane);
+  else row_item<T>(p, row, which, chunk, lane);
 }
 
 // ------------------------------------------------------------------ prompts
@@ -198,15 +220,17 @@ __global__ void __launch_bounds__(kArThreads)
 // (include/kvq.h): written row by row the V side would go out as 2-byte
 // stores, one 32-byte sector each.  So one warp takes a whole unit of one kv
 // head, and stores it as contiguous 512-byte pieces.
-//   K: every quad of lanes reads its two rows in the unit's own order, rotates
-//      and encodes them in registers (kvq_quad.cuh).
+//   K: every quad of lanes reads two rows of the window in the unit's own
+//      order, rotates and encodes them in registers (kvq_quad.cuh), whatever
+//      units they belong to.
 //   V: the rows are copied into shared memory, 16 of them in flight; two lanes
 //      per row encode its four blocks; the unit is put together 16 bytes per
 //      lane from the 16 rows' codes.
 //
-// Packed rows are cut into windows of 16, whatever the lengths: a window's
-// warp places the units that begin with one of its rows (at most one can be
-// complete) and, row by row, the rows that lie in incomplete units.
+// Packed rows are cut into windows of 16, whatever the lengths: for V a
+// window's warp places the unit that begins with one of its rows and is
+// complete (there is one at most) and, row by row, the rows of incomplete
+// units; K rows whose planes cross lanes take that way too.
 
 // A staged row: the input's 128 values, replaced by 128 fp16 values, or by 128
 // one-byte codes and the block scales (4, or 1 for turbo4) behind them.
@@ -264,6 +288,24 @@ __device__ __forceinline__ void encode_staged(int codec, const float (&x)[4], ui
   } else if ((lane & 7) == 0) {
     scales[lane >> 3] = d16;
   }
+}
+
+// Store a staged row's codes as token row r of a unit.
+template <int SIDE>
+__device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint8_t *unit, int r,
+                                             int lane) {
+  uint2 raw = make_uint2(0u, 0u);
+  int q[4] = {0, 0, 0, 0};
+  __half d16 = __float2half_rn(0.0f);
+  if (codec == KVQ_F16) {
+    raw = reinterpret_cast<const uint2 *>(row)[lane];
+  } else {
+    const uint32_t w = reinterpret_cast<const uint32_t *>(row)[lane];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = (w >> (8 * i)) & 0xff;
+    d16 = reinterpret_cast<const __half *>(row + kScaleAt)[codec == KVQ_TURBO4 ? 0 : lane >> 3];
+  }
+  store_row<SIDE>(codec, unit, r, lane, raw, q, d16);
 }
 
 // 16 bytes of the unit, chunk c, from the staged rows (row r at s + r * PITCH):
@@ -408,32 +450,52 @@ __device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
   *reinterpret_cast<__half2 *>(row + kScaleAt + 2 * b0) = __halves2half2(d16[0], d16[1]);
 }
 
-// A whole unit of K: lane 4g + w reads rows g and g + 8 of the 16 at x, whose
-// positions the lanes j0 .. j0 + 15 hold.
+// A window's 16 rows of K: lane 4g + w reads rows g and g + 8 of the 16 at x,
+// which may lie in any units: lane j knows row j's position, unit (-1: none)
+// and row there.
 template <int T, int CODEC>
-__device__ __forceinline__ void quad_unit(const AppendRopeParams &p, const uint8_t *x, int j0,
-                                          int64_t pos, uint8_t *unit, int lane) {
+__device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uint8_t *x,
+                                            int64_t pos, int64_t unit, int r, int lane) {
   using Raw = typename RowType<T>::raw4;
   constexpr int S = Stage<T>::S;
   const int g = lane >> 2, w = lane & 3;
+  int64_t at[2];
+  int64_t ps[2];
+  int rr[2];
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh) {
+    at[rh] = __shfl_sync(0xffffffffu, unit, g + 8 * rh);
+    ps[rh] = __shfl_sync(0xffffffffu, pos, g + 8 * rh);
+    rr[rh] = __shfl_sync(0xffffffffu, r, g + 8 * rh);
+  }
   QuadCodes<CODEC> q[2];
   Raw raw[2][8];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh)
+    if (at[rh] >= 0) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      raw[rh][c] = *reinterpret_cast<const Raw *>(x + (g + 8 * rh) * p.row[1] + (16 * c + 4 * w) * S);
+      for (int c = 0; c < 8; ++c)
+        raw[rh][c] =
+            *reinterpret_cast<const Raw *>(x + (g + 8 * rh) * p.row[1] + (16 * c + 4 * w) * S);
+    }
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
     float v[8][4];
 #pragma unroll
     for (int c = 0; c < 8; ++c) load4<T>(&raw[rh][c], v[c]);
-    const float *row =
-        rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j0 + g + 8 * rh), p.err);
+    const float *row = at[rh] >= 0 ? rope_row(p.rope, ps[rh], p.err) : p.rope.table;
     quad_rotate(p.rope, p.kind, row, w, 1.0f, v);
     quad_encode<CODEC>(v, w, q[rh]);
   }
-  quad_store<CODEC>(unit, lane, q);
+  uint8_t *const cache = p.cache[0];
+  if (at[0] >= 0 && at[0] == at[1] && rr[1] == rr[0] + 8) {  // a unit's rows r and r + 8
+    quad_store<CODEC>(cache + at[0] * unit_bytes(CODEC), 4 * rr[0] + w, q);
+  } else {
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh)
+      if (at[rh] >= 0)
+        quad_store_row<CODEC>(cache + at[rh] * unit_bytes(CODEC), rr[rh], w, q[rh]);
+  }
 }
 
 template <int T, int SIDE>
@@ -455,58 +517,60 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
     if (lane < kUnitTokens) unit = unit_of(p, s, slot);
   }
   const int r = static_cast<int>(slot & (kUnitTokens - 1));
+  if (unit >= 0) unit += h * unit_step(p);
+
+  if (SIDE == 0 && p.kind != kQuadNone) {
+    if (lane >= kUnitTokens) unit = -1;
+    if (codec == KVQ_F16) quad_window<T, KVQ_F16>(p, x, pos, unit, r, lane);
+    else if (codec == KVQ_Q8_0) quad_window<T, KVQ_Q8_0>(p, x, pos, unit, r, lane);
+    else if (codec == KVQ_Q4_0) quad_window<T, KVQ_Q4_0>(p, x, pos, unit, r, lane);
+    else quad_window<T, KVQ_TURBO4>(p, x, pos, unit, r, lane);
+    return;
+  }
+  // Incomplete units first, then the complete one.
   const unsigned window = (1u << kUnitTokens) - 1;
   const unsigned single = __ballot_sync(0xffffffffu, unit >= 0 && !full) & window;
   const unsigned whole = __ballot_sync(0xffffffffu, unit >= 0 && full && r == 0) & window;
-  unit += h * unit_step(p);
-
-  auto angles = [&](int j) {  // of the row of lane j
-    return lane_angles(p.rope, rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j), p.err), lane);
-  };
-  if (single) {
-    stage_rows<T>(stage, x, p.row[which], single, lane);
 #pragma unroll 1
-    for (unsigned m = single; m; m &= m - 1) {
-      const int j = __ffs(m) - 1;
-      float v[4];
-      load4<T>(stage + j * kPitch + 4 * lane * S, v);
-      if (SIDE == 0) rotate_lane(p.rope, angles(j), lane, v);
-      encode_f32_row_into<SIDE>(
-          codec, v, p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j) * unit_bytes(codec),
-          __shfl_sync(0xffffffffu, r, j), lane);
-    }
-    __syncwarp();
-  }
-  if (whole) {
-    const int j0 = __ffs(whole) - 1;
-    uint8_t *to = p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec);
-    const uint8_t *xu = x + j0 * p.row[which];
-    if (SIDE == 0 && p.kind != kQuadNone) {
-      if (codec == KVQ_F16) quad_unit<T, KVQ_F16>(p, xu, j0, pos, to, lane);
-      else if (codec == KVQ_Q8_0) quad_unit<T, KVQ_Q8_0>(p, xu, j0, pos, to, lane);
-      else if (codec == KVQ_Q4_0) quad_unit<T, KVQ_Q4_0>(p, xu, j0, pos, to, lane);
-      else quad_unit<T, KVQ_TURBO4>(p, xu, j0, pos, to, lane);
-      return;
-    }
-    stage_rows<T>(stage, xu, p.row[which], window, lane);
+  for (int pass = 0; pass < 2; ++pass) {
+    if ((pass ? whole : single) == 0) continue;
+    const int j0 = pass ? __ffs(whole) - 1 : 0;  // row r0 + j0 is in slot 0
+    const unsigned rows = pass ? window : single;
+    stage_rows<T>(stage, x + j0 * p.row[which], p.row[which], rows, lane);
     if (SIDE == 1 && codec == KVQ_Q8_0) {
       encode_staged_blocks<T, KVQ_Q8_0>(stage, lane);
     } else if (SIDE == 1 && codec == KVQ_Q4_0) {
       encode_staged_blocks<T, KVQ_Q4_0>(stage, lane);
     } else if (SIDE == 0 || codec != KVQ_F16 || T != KVQ_T_F16) {  // else the rows are the codes
 #pragma unroll 1
-      for (int j = 0; j < kUnitTokens; ++j) {
+      for (unsigned m = rows; m; m &= m - 1) {
+        const int j = __ffs(m) - 1;
         float v[4];
         load4<T>(stage + j * kPitch + 4 * lane * S, v);
-        if (SIDE == 0) rotate_lane(p.rope, angles(j0 + j), lane, v);
+        if (SIDE == 0) {
+          const float *row = rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j0 + j), p.err);
+          rotate_lane(p.rope, lane_angles(p.rope, row, lane), lane, v);
+        }
         __syncwarp();  // every lane has read its part before the codes replace it
         encode_staged(codec, v, stage + j * kPitch, lane);
       }
     }
     __syncwarp();
-    uint4 *dst = reinterpret_cast<uint4 *>(to);
-    const int chunks = unit_bytes(codec) / 16;
-    for (int c = lane; c < chunks; c += 32) dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
+    if (pass) {
+      uint4 *dst = reinterpret_cast<uint4 *>(
+          p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
+      const int chunks = unit_bytes(codec) / 16;
+      for (int c = lane; c < chunks; c += 32) dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
+    } else {
+#pragma unroll 1
+      for (unsigned m = rows; m; m &= m - 1) {
+        const int j = __ffs(m) - 1;
+        store_staged<SIDE>(codec, stage + j * kPitch,
+                           p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j) * unit_bytes(codec),
+                           __shfl_sync(0xffffffffu, r, j), lane);
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -529,17 +593,27 @@ __global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
   } else {
     const int64_t item = (static_cast<int64_t>(blockIdx.x) - p.kv_blocks) * kArWarps + warp;
     const int64_t row = item / p.q_chunks;
-    if (row < p.n_rows) row_item<T>(p, row, 0, static_cast<int>(item % p.q_chunks), lane);
+    if (row >= p.n_rows) return;
+    if (p.eight) q_item<T>(p, row, static_cast<int>(item % p.q_chunks), lane);
+    else row_item<T>(p, row, 0, static_cast<int>(item % p.q_chunks), lane);
   }
+}
+
+// Heads per item of q: 16 (8 of fp32) where eight lanes hold a row.
+template <int T>
+void set_q_items(AppendRopeParams &p, int hpw) {
+  p.q_hpw = hpw;
+  if (p.q_chunks) p.q_chunks = (p.n_q + hpw - 1) / hpw;
 }
 
 template <int T>
 cudaError_t launch_rows(AppendRopeParams &p, int num_sms, cudaStream_t stream) {
-  // A row's heads go to one warp each while the grid is small (the encoder's
-  // latency is paid once), to up to eight, sharing the angles, when it is not.
+  // A row's k and v heads go to one warp each while the grid is small (the
+  // encoder's latency is paid once), to up to eight, sharing the angles, when
+  // it is not; q heads four at a time where eight lanes hold a row.
   const int64_t slots = p.n_rows * (p.n_q * (p.q_chunks > 0) + 2 * p.n_kv);
   while (p.hpw < kMaxHeads && slots / p.hpw > static_cast<int64_t>(num_sms) * 16) p.hpw *= 2;
-  if (p.q_chunks) p.q_chunks = (p.n_q + p.hpw - 1) / p.hpw;
+  set_q_items<T>(p, p.eight ? (p.hpw > 4 ? p.hpw : 4) : p.hpw);
   p.kv_chunks = (p.n_kv + p.hpw - 1) / p.hpw;
   const int64_t items = p.n_rows * (p.q_chunks + 2 * p.kv_chunks);
   return launch_pdl(append_rows_kernel<T>, dim3(static_cast<unsigned>((items + kArWarps - 1) / kArWarps)),
@@ -551,8 +625,7 @@ cudaError_t launch_prompt(AppendRopeParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> optin{0};
   const cudaError_t e = smem_optin(append_prompt_kernel<T>, Stage<T>::kBytes, optin);
   if (e != cudaSuccess) return e;
-  p.hpw = kMaxHeads;
-  if (p.q_chunks) p.q_chunks = (p.n_q + p.hpw - 1) / p.hpw;
+  set_q_items<T>(p, !p.eight ? kMaxHeads : T == KVQ_T_F32 ? 8 : 16);
   const int64_t windows = (p.n_rows + kUnitTokens - 1) / kUnitTokens;
   p.kv_blocks = (windows * 2 * p.n_kv + kArWarps - 1) / kArWarps;
   const int64_t blocks = p.kv_blocks + (p.n_rows * p.q_chunks + kArWarps - 1) / kArWarps;
@@ -615,7 +688,8 @@ cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const k
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
   p.kind = quad_kind(p.rope);
-  p.hpw = 1;
+  p.eight = eight_lanes(p.rope);
+  p.q_hpw = p.hpw = 1;
   p.q_chunks = q ? 1 : 0;
   if (n_rows > 0) {
     const cudaError_t e = k.type == KVQ_T_F16    ? launch_append_t<KVQ_T_F16>(p, num_sms, stream)

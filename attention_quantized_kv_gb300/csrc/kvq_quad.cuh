@@ -24,13 +24,6 @@ inline int quad_kind(const RopeArgs &p) {
   return p.rot % 32 == 0 ? p.rot / 32 : kQuadNone;
 }
 
-// (a, b) -> (a c - b s, a s + b c), every operation rounded (see kvq_rope.cuh).
-__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
-  const float x = __fadd_rn(__fmul_rn(a, c), __fmul_rn(b, -s));
-  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-  a = x;
-}
-
 template <int N>
 __device__ __forceinline__ void quad_rotate_half(const RopeArgs &p, const float *row, int w,
                                                  float sign, float (&v)[8][4]) {
@@ -198,6 +191,33 @@ __device__ __forceinline__ void quad_store(uint8_t *unit, int lane,
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       u[j * 32] = make_uint4(q[0].w[2 * j], q[1].w[2 * j], q[0].w[2 * j + 1], q[1].w[2 * j + 1]);
+  }
+}
+
+// One row's codes (this lane's part of token row r).
+template <int CODEC>
+__device__ __forceinline__ void quad_store_row(uint8_t *unit, int r, int w,
+                                               const QuadCodes<CODEC> &q) {
+  const int g = r & 7, rh = r >> 3;
+  uint8_t *u = unit + (4 * g + w) * 16;
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      *reinterpret_cast<uint4 *>(u + (2 * b + rh) * 512) =
+          make_uint4(q.w[4 * b], q.w[4 * b + 1], q.w[4 * b + 2], q.w[4 * b + 3]);
+    return;
+  }
+  uint16_t *sc = reinterpret_cast<uint16_t *>(unit + unit_scale_offset(CODEC));
+  if (CODEC != KVQ_TURBO4) sc[8 * g + 4 * rh + w] = q.scale;
+  else if (w == 0) sc[2 * g + rh] = q.scale;
+  if (CODEC == KVQ_Q8_0) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      *reinterpret_cast<uint2 *>(u + b * 512 + rh * 8) = make_uint2(q.w[2 * b], q.w[2 * b + 1]);
+  } else {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      *reinterpret_cast<uint32_t *>(u + (b >> 1) * 512 + ((b & 1) * 2 + rh) * 4) = q.w[b];
   }
 }
 

@@ -18,6 +18,15 @@
 
 namespace kvq {
 
+// (a, b) -> (a c - b s, a s + b c), every operation rounded.  (The packed pair
+// __fmul2_rn, __fadd2_rn would be shorter, but the compiler contracts it: of
+// 8M random sums 46% came out as a fused multiply-add's.)
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
+  const float x = __fadd_rn(__fmul_rn(a, c), __fmul_rn(b, -s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
 // What a kernel needs of kvq_rope.
 struct RopeArgs {
   const float *table;
@@ -190,6 +199,159 @@ __device__ __forceinline__ void store4(void *p, const float (&x)[4]) {
     *static_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
                                           *reinterpret_cast<const uint32_t *>(&b));
   }
+}
+
+// ------------------------------------------------------------- eight lanes per row
+//
+// Where the planes allow it a row is held by eight lanes, 16 values each: for
+// a half layout lane l takes dims 8l .. and rot/2 + 8l .., both elements of its
+// planes, so nothing crosses lanes, loads and stores are 16 bytes and a warp
+// moves four heads at once.  Lanes behind the planes take what passes
+// through.  Either way lane l needs the table's entries 8l .. 8l + 7.
+
+__host__ __device__ inline bool eight_lanes(const RopeArgs &p) {
+  return p.layout == KVQ_ROPE_INTERLEAVED ? p.rot % 8 == 0 : p.rot % 16 == 0;
+}
+
+struct EightLanes {
+  int a, b;           // first dims of the lane's two groups of eight
+  bool turn_a, turn_b;  // whether they are rotated (half layouts: together)
+};
+
+__device__ __forceinline__ EightLanes eight_lanes_of(const RopeArgs &p, int l) {
+  EightLanes m;
+  const int h = p.rot >> 1;
+  if (p.layout == KVQ_ROPE_INTERLEAVED) {
+    m.a = 16 * l;
+    m.b = 16 * l + 8;
+    m.turn_a = m.a < p.rot;
+    m.turn_b = m.b < p.rot;
+  } else {
+    m.turn_a = m.turn_b = 8 * l < h;
+    m.a = m.turn_a ? 8 * l : p.rot + 16 * (l - (h >> 3));
+    m.b = m.turn_a ? h + 8 * l : m.a + 8;
+  }
+  return m;
+}
+
+struct EightAngles {
+  float c[8], s[8];
+};
+
+__device__ __forceinline__ EightAngles eight_angles(const RopeArgs &p, const EightLanes &m,
+                                                    const float *row, int l, float sign = 1.0f) {
+  EightAngles a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // entries 8l + 2i, + 1 (a table row ends inside group b where only a turns)
+    float4 t = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    const bool live = p.layout == KVQ_ROPE_INTERLEAVED && i >= 2 ? m.turn_b : m.turn_a;
+    if (live) t = *reinterpret_cast<const float4 *>(row + 16 * l + 4 * i);
+    a.c[2 * i] = __fmul_rn(t.x, p.magnitude);
+    a.s[2 * i] = sign * __fmul_rn(t.y, p.magnitude);
+    a.c[2 * i + 1] = __fmul_rn(t.z, p.magnitude);
+    a.s[2 * i + 1] = sign * __fmul_rn(t.w, p.magnitude);
+  }
+  return a;
+}
+
+// Rotate the lane's groups xa, xb.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate_eight(const EightLanes &m, const EightAngles &g,
+                                             float (&xa)[8], float (&xb)[8]) {
+  if (INTERLEAVED) {
+    if (m.turn_a) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) turn(xa[2 * k], xa[2 * k + 1], g.c[k], g.s[k]);
+    }
+    if (m.turn_b) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) turn(xb[2 * k], xb[2 * k + 1], g.c[4 + k], g.s[4 + k]);
+    }
+  } else if (m.turn_a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(xa[i], xb[i], g.c[i], g.s[i]);
+  }
+}
+
+// Eight consecutive values as they lie in memory, as fp32, and back.
+template <int T>
+struct Eight {
+  uint4 w[T == KVQ_T_F32 ? 2 : 1];
+};
+template <int T>
+__device__ __forceinline__ Eight<T> load_eight(const uint8_t *p) {
+  Eight<T> r;
+  r.w[0] = *reinterpret_cast<const uint4 *>(p);
+  if (T == KVQ_T_F32) r.w[T == KVQ_T_F32] = *reinterpret_cast<const uint4 *>(p + 16);
+  return r;
+}
+template <int T>
+__device__ __forceinline__ void eight_values(const Eight<T> &r, float (&x)[8]) {
+  constexpr int kSecond = T == KVQ_T_F32 ? 1 : 0;
+  float lo[4], hi[4];
+  load4<T>(&r.w[0], lo);
+  load4<T>(T == KVQ_T_F32 ? reinterpret_cast<const uint2 *>(&r.w[kSecond])
+                          : reinterpret_cast<const uint2 *>(&r.w[0]) + 1,
+           hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lo[i];
+    x[4 + i] = hi[i];
+  }
+}
+template <int T>
+__device__ __forceinline__ void store_eight(uint8_t *p, const float (&x)[8]) {
+  const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
+  uint4 w[T == KVQ_T_F32 ? 2 : 1];
+  if (T == KVQ_T_F32) {
+    store4<T>(&w[0], lo);
+    store4<T>(&w[T == KVQ_T_F32], hi);
+    reinterpret_cast<uint4 *>(p)[1] = w[T == KVQ_T_F32];
+  } else {
+    store4<T>(&w[0], lo);
+    store4<T>(reinterpret_cast<uint2 *>(&w[0]) + 1, hi);
+  }
+  *reinterpret_cast<uint4 *>(p) = w[0];
+}
+
+// Heads of one row by one warp, four at a time: x + h * x_head to
+// y + h * y_head for h < nh <= 4 * N, all of them requested before the angles.
+template <int TI, int TO, int N, typename Row>
+__device__ __forceinline__ void rotate_heads_eight(const RopeArgs &p, const uint8_t *x,
+                                                   int64_t x_head, uint8_t *y, int64_t y_head,
+                                                   int nh, float sign, int lane, Row table_row) {
+  constexpr int SI = TI == KVQ_T_F32 ? 4 : 2, SO = TO == KVQ_T_F32 ? 4 : 2;
+  const int l = lane & 7, sub = lane >> 3;
+  const EightLanes m = eight_lanes_of(p, l);
+  Eight<TI> ra[N], rb[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int h = 4 * k + sub;
+    if (h < nh) {
+      ra[k] = load_eight<TI>(x + h * x_head + m.a * SI);
+      rb[k] = load_eight<TI>(x + h * x_head + m.b * SI);
+    }
+  }
+  const float *row = table_row();
+  if (!row) return;
+  const EightAngles g = eight_angles(p, m, row, l, sign);
+  auto all = [&](auto interleaved) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int h = 4 * k + sub;
+      if (h < nh) {
+        float a[8], b[8];
+        eight_values<TI>(ra[k], a);
+        eight_values<TI>(rb[k], b);
+        rotate_eight<decltype(interleaved)::value>(m, g, a, b);
+        store_eight<TO>(y + h * y_head + m.a * SO, a);
+        store_eight<TO>(y + h * y_head + m.b * SO, b);
+      }
+    }
+  };
+  if (p.layout == KVQ_ROPE_INTERLEAVED) all(std::true_type());
+  else all(std::false_type());
 }
 
 }  // namespace kvq

@@ -14,6 +14,7 @@ namespace {
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
 constexpr int64_t kTableBlocks = 152 * 8;  // every SM full
+constexpr int64_t kSmallGrid = 152 * 8;    // warps: eight per SM
 
 // ------------------------------------------------------------------ table
 
@@ -95,16 +96,36 @@ struct ApplyParams {
   int64_t n_rows;
   const int32_t *positions;
   int32_t *err;
-  int n_heads, pos0, chunks;
+  int n_heads, pos0, hpw, chunks;  // heads per warp, and such groups in a row
   float sign;
 };
 
-constexpr int kHeadsPerWarp = 8;  // heads of one row that share a warp's angles
+constexpr int kAnyHeads = 8;  // heads per warp of the general kernel
 
-// One warp per (row, up to eight heads): the angles are read once, and all
+// One warp per (row, up to sixteen heads): the angles are read once, and all
 // the heads' values are requested before the first is used.
 template <int TI, int TO>
-__global__ void __launch_bounds__(kRopeThreads) apply_kernel(ApplyParams p) {
+__global__ void __launch_bounds__(kRopeThreads) apply_kernel(const __grid_constant__ ApplyParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+  const int64_t row = item / p.chunks;
+  if (row >= p.n_rows) return;
+  const int h0 = static_cast<int>(item % p.chunks) * p.hpw;
+  const uint8_t *x = p.x + row * p.x_row + h0 * p.x_head;
+  uint8_t *y = p.y + row * p.y_row + h0 * p.y_head;
+  rotate_heads_eight<TI, TO, 4 / (TI == KVQ_T_F32 ? 2 : 1)>(
+      p.rope, x, p.x_head, y, p.y_head, min(p.hpw, p.n_heads - h0), p.sign, lane, [&] {
+        return rope_row(p.rope, p.positions ? p.positions[row] : p.pos0 + row, p.err);
+      });
+}
+
+// Planes that eight lanes cannot hold: one head at a time, 4 values per lane.
+template <int TI, int TO>
+__global__ void __launch_bounds__(kRopeThreads)
+    apply_any_kernel(const __grid_constant__ ApplyParams p) {
+  using Raw = typename RowType<TI>::raw4;
   constexpr int SI = sizeof(typename RowType<TI>::type), SO = sizeof(typename RowType<TO>::type);
   grid_dependency_wait();
   grid_launch_dependents();
@@ -112,19 +133,18 @@ __global__ void __launch_bounds__(kRopeThreads) apply_kernel(ApplyParams p) {
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
   const int64_t row = item / p.chunks;
   if (row >= p.n_rows) return;
-  const int h0 = static_cast<int>(item % p.chunks) * kHeadsPerWarp;
+  const int h0 = static_cast<int>(item % p.chunks) * p.hpw, nh = min(p.hpw, p.n_heads - h0);
   const uint8_t *x = p.x + row * p.x_row + h0 * p.x_head + 4 * lane * SI;
   uint8_t *y = p.y + row * p.y_row + h0 * p.y_head + 4 * lane * SO;
-  const int nh = min(kHeadsPerWarp, p.n_heads - h0);
-  typename RowType<TI>::raw4 raw[kHeadsPerWarp];
+  Raw raw[kAnyHeads];
 #pragma unroll
-  for (int h = 0; h < kHeadsPerWarp; ++h)
-    if (h < nh) raw[h] = *reinterpret_cast<const typename RowType<TI>::raw4 *>(x + h * p.x_head);
+  for (int h = 0; h < kAnyHeads; ++h)
+    if (h < nh) raw[h] = *reinterpret_cast<const Raw *>(x + h * p.x_head);
   const int64_t pos = p.positions ? p.positions[row] : p.pos0 + row;
   const LaneAngles a = lane_angles(p.rope, rope_row(p.rope, pos, p.err), lane, p.sign);
   with_lanes(p.rope, [&](auto lanes) {
 #pragma unroll
-    for (int h = 0; h < kHeadsPerWarp; ++h)
+    for (int h = 0; h < kAnyHeads; ++h)
       if (h < nh) {
         float v[4];
         load4<TI>(&raw[h], v);
@@ -171,31 +191,38 @@ struct ShiftParams {
   int kind;  // quad_kind
 };
 
-// One warp per (sequence, 16-token unit, kv head): both rows of every quad are
-// read as they lie, turned by their tokens' shifts, encoded again and stored
-// as they lay; rows that do not move keep their codes.  The unit's bytes are
-// requested beside the shifts, which in an eviction's wake are seldom all
-// zero.
+// One warp per (sequence, 16-token unit, up to kShiftHeads kv heads): both rows
+// of every quad are read as they lie, turned by their tokens' shifts, encoded
+// again and stored as they lay; rows that do not move keep their codes.  The
+// next head's unit is requested before the current one is worked on, and the
+// first beside the shifts, which in an eviction's wake are seldom all zero.
+constexpr int kShiftHeads = 4;
+
 template <int CODEC>
-__global__ void __launch_bounds__(kRopeThreads, 3) shift_units_kernel(ShiftParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2)
+    shift_units_kernel(const __grid_constant__ ShiftParams p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, g = lane >> 2, w = lane & 3, s = blockIdx.y;
   const int item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int j = item / p.n_kv, h = item % p.n_kv;  // unit of the sequence, kv head
+  const int groups = (p.n_kv + kShiftHeads - 1) / kShiftHeads;
+  const int j = item / groups, h0 = item % groups * kShiftHeads;  // unit, first kv head
   const int len = min(p.seq_lens[s], p.capacity);
   if (j * kUnitTokens >= len) return;
-  int64_t unit = (static_cast<int64_t>(s) * p.n_kv + h) * (p.capacity / kUnitTokens) + j;
+  int64_t unit = (static_cast<int64_t>(s) * p.n_kv + h0) * (p.capacity / kUnitTokens) + j;
+  int64_t step = p.capacity / kUnitTokens;
   if (p.table) {
     const int pg = page_of(p.table, p.pages_per_seq, p.n_pages, s, j / kPageUnits);
     if (pg < 0) {
       if (lane == 0) set_err(p.err, KVQ_DEVERR_PAGE);
       return;
     }
-    unit = (static_cast<int64_t>(pg) * p.n_kv + h) * kPageUnits + j % kPageUnits;
+    unit = (static_cast<int64_t>(pg) * p.n_kv + h0) * kPageUnits + j % kPageUnits;
+    step = kPageUnits;
   }
   uint8_t *u = p.k + unit * unit_bytes(CODEC);
-  QuadCodes<CODEC> q[2];
-  quad_load<CODEC>(u, lane, q);
+  step *= unit_bytes(CODEC);
+  QuadCodes<CODEC> q[2], next[2];
+  quad_load<CODEC>(u, lane, next);
   int d[2];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
@@ -203,18 +230,29 @@ __global__ void __launch_bounds__(kRopeThreads, 3) shift_units_kernel(ShiftParam
     d[rh] = t < len ? p.delta[static_cast<int64_t>(s) * p.capacity + t] : 0;
   }
   if (!__any_sync(0xffffffffu, d[0] != 0 || d[1] != 0)) return;
+  const float *row[2];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
-    float v[8][4];
-    quad_decode<CODEC>(q[rh], w, v);
     const int64_t by = d[rh];
-    const float *row = rope_row(p.rope, by < 0 ? -by : by, p.err);
-    quad_rotate(p.rope, p.kind, row, w, by < 0 ? -1.0f : 1.0f, v);
-    QuadCodes<CODEC> e;
-    quad_encode<CODEC>(v, w, e);
-    if (by != 0) q[rh] = e;
+    row[rh] = rope_row(p.rope, by < 0 ? -by : by, p.err);
   }
-  quad_store<CODEC>(u, lane, q);
+  const int heads = min(kShiftHeads, p.n_kv - h0);
+#pragma unroll 1
+  for (int h = 0; h < heads; ++h, u += step) {
+    q[0] = next[0];
+    q[1] = next[1];
+    if (h + 1 < heads) quad_load<CODEC>(u + step, lane, next);
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh) {
+      float v[8][4];
+      quad_decode<CODEC>(q[rh], w, v);
+      quad_rotate(p.rope, p.kind, row[rh], w, d[rh] < 0 ? -1.0f : 1.0f, v);
+      QuadCodes<CODEC> e;
+      quad_encode<CODEC>(v, w, e);
+      if (d[rh] != 0) q[rh] = e;
+    }
+    quad_store<CODEC>(u, lane, q);
+  }
 }
 
 // Planes that cross lanes: one warp per (sequence, token), its K rows of every
@@ -251,10 +289,15 @@ __global__ void __launch_bounds__(kRopeThreads) shift_rows_kernel(ShiftParams p)
 }
 
 template <int TI, int TO>
-cudaError_t launch_apply_t(const ApplyParams &p, cudaStream_t stream) {
+cudaError_t launch_apply_t(ApplyParams &p, cudaStream_t stream) {
+  const bool eight = eight_lanes(p.rope);
+  p.hpw = eight ? (TI == KVQ_T_F32 ? 8 : 16) : kAnyHeads;
+  // few rows: spread the heads over more warps (four are one step of eight lanes)
+  while (p.hpw > 4 && p.n_rows * ((p.n_heads + p.hpw - 1) / p.hpw) < kSmallGrid) p.hpw /= 2;
+  p.chunks = (p.n_heads + p.hpw - 1) / p.hpw;
   const int64_t blocks = (p.n_rows * p.chunks + kRopeWarps - 1) / kRopeWarps;
-  return launch_pdl(apply_kernel<TI, TO>, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads),
-                    0, stream, p);
+  return launch_pdl(eight ? apply_kernel<TI, TO> : apply_any_kernel<TI, TO>,
+                    dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), 0, stream, p);
 }
 
 }  // namespace
@@ -292,7 +335,6 @@ cudaError_t launch_rope_apply(const kvq_rope &rope, const kvq_rows &x, const kvq
   p.err = err;
   p.n_heads = n_heads;
   p.pos0 = pos0;
-  p.chunks = (n_heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
   p.sign = transpose ? -1.0f : 1.0f;
   if (x.type == KVQ_T_F16) return launch_apply_t<KVQ_T_F16, KVQ_T_F16>(p, stream);
   if (x.type == KVQ_T_BF16)
@@ -329,7 +371,8 @@ cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const in
     const dim3 grid((L.capacity + kRopeWarps - 1) / kRopeWarps, L.n_seqs);
     return launch_pdl(shift_rows_kernel, grid, dim3(kRopeThreads), 0, stream, p);
   }
-  const int64_t items = static_cast<int64_t>(L.capacity / kUnitTokens) * L.n_kv_heads;
+  const int64_t items = static_cast<int64_t>(L.capacity / kUnitTokens) *
+                        ((L.n_kv_heads + kShiftHeads - 1) / kShiftHeads);
   const dim3 grid(static_cast<unsigned>((items + kRopeWarps - 1) / kRopeWarps), L.n_seqs);
   const auto kernel = L.codec_k == KVQ_F16    ? shift_units_kernel<KVQ_F16>
                       : L.codec_k == KVQ_Q8_0 ? shift_units_kernel<KVQ_Q8_0>
