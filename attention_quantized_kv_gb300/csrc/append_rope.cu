@@ -227,10 +227,12 @@ __global__ void __launch_bounds__(kArThreads)
 //      per row encode its four blocks; the unit is put together 16 bytes per
 //      lane from the 16 rows' codes.
 //
-// Packed rows are cut into windows of 16, whatever the lengths: for V a
-// window's warp places the unit that begins with one of its rows and is
-// complete (there is one at most) and, row by row, the rows of incomplete
-// units; K rows whose planes cross lanes take that way too.
+// Packed rows are cut into windows of 16, whatever the lengths.  For V a
+// window's warp places the rows of every unit whose first new row lies in the
+// window: no other warp writes that unit, so an incomplete one is put together
+// over its old bytes.  (As 2-byte stores 13 rows of one f16 unit took 10 us.)
+// One or two rows are not worth that and are stored by themselves.  K rows
+// whose planes cross lanes take the same way.
 
 // A staged row: the input's 128 values, replaced by 128 fp16 values, or by 128
 // one-byte codes and the block scales (4, or 1 for turbo4) behind them.
@@ -241,6 +243,7 @@ struct Stage {
   static constexpr int kWarpBytes = kUnitTokens * kPitch;
   static constexpr int kBytes = kArWarps * kWarpBytes;
 };
+constexpr int kGroupRows = 3;  // new rows of a unit that are worth its 16-byte pieces
 constexpr int kScaleAt = kD;  // byte offset of a staged row's scales
 
 __device__ __forceinline__ void copy_async16(void *dst, const void *src) {
@@ -306,6 +309,42 @@ __device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint
     d16 = reinterpret_cast<const __half *>(row + kScaleAt)[codec == KVQ_TURBO4 ? 0 : lane >> 3];
   }
   store_row<SIDE>(codec, unit, r, lane, raw, q, d16);
+}
+
+// The bytes of a unit's chunk c that belong to the token rows of the mask.
+template <int SIDE>
+__device__ __forceinline__ uint4 chunk_mask(int codec, int c, unsigned rows) {
+  const int data = codec == KVQ_F16 ? 256 : codec == KVQ_Q8_0 ? 128 : 64, k = c - data;
+  const int lo = c & 3, g = (c >> 2) & 7;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int ra, rb;  // token rows of the word's halves
+    if (c < data) {
+      if (SIDE == 0) {
+        const int rh = codec == KVQ_F16 ? (c >> 5) & 1 : codec == KVQ_Q8_0 ? i >> 1 : i & 1;
+        ra = rb = g + 8 * rh;
+      } else {
+        ra = 2 * lo + 8 * (codec == KVQ_F16 ? i >> 1 : i & 1);
+        rb = ra + 1;
+      }
+    } else if (codec == KVQ_TURBO4) {
+      ra = SIDE == 0 ? 4 * k + i : 2 * (2 * k + (i >> 1)) + 8 * (i & 1);
+      rb = SIDE == 0 ? ra + 8 : ra + 1;
+    } else {
+      ra = SIDE == 0 ? k + 8 * (i >> 1) : 2 * (k >> 1) + 8 * (i & 1);
+      rb = SIDE == 0 ? ra : ra + 1;
+    }
+    if (SIDE == 1 && c < data && nibble_codec(codec)) {  // byte par * 2 + rh
+      o[i] = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if ((rows >> (2 * lo + (b >> 1) + 8 * (b & 1))) & 1u) o[i] |= 0xffu << (8 * b);
+    } else {
+      o[i] = ((rows >> ra) & 1u ? 0x0000ffffu : 0u) | ((rows >> rb) & 1u ? 0xffff0000u : 0u);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // 16 bytes of the unit, chunk c, from the staged rows (row r at s + r * PITCH):
@@ -379,7 +418,8 @@ __device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) 
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint8_t *row = s + (2 * lo + (b >> 1) + 8 * (b & 1)) * PITCH;
-          o[i] |= static_cast<uint32_t>(row[d] | (row[d + 16] << 4)) << (8 * b);
+          // (a slot without a row holds anything: it must not reach other bytes)
+          o[i] |= ((row[d] | (static_cast<uint32_t>(row[d + 16]) << 4)) & 0xffu) << (8 * b);
         }
       }
     }
@@ -504,16 +544,14 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
   constexpr int which = SIDE + 1, kPitch = Stage<T>::kPitch, S = Stage<T>::S;
   const int codec = p.codec[SIDE];
   const uint8_t *x = p.x[which] + r0 * p.row[which] + h * p.head[which];
-  // lane j: row r0 + j (a unit that begins in the window ends within 31 rows)
+  // lane j: row r0 + j (the new rows of a unit whose first lies in the window
+  // end within 31 rows)
   const int64_t row = r0 + lane;
   int s = 0, i = 0, n = 0;
   int64_t slot = 0, unit = -1, pos = 0;
-  bool full = false;
   if (row < p.n_rows && find_row(p, row, s, i, n)) {
     slot = static_cast<int64_t>(p.seq_lens[s]) + i;
     pos = p.positions ? p.positions[row] : slot;
-    const int first = i - static_cast<int>(slot & (kUnitTokens - 1));
-    full = slot >= 0 && first >= 0 && first + kUnitTokens <= n;
     if (lane < kUnitTokens) unit = unit_of(p, s, slot);
   }
   const int r = static_cast<int>(slot & (kUnitTokens - 1));
@@ -527,50 +565,64 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
     else quad_window<T, KVQ_TURBO4>(p, x, pos, unit, r, lane);
     return;
   }
-  // Incomplete units first, then the complete one.
-  const unsigned window = (1u << kUnitTokens) - 1;
-  const unsigned single = __ballot_sync(0xffffffffu, unit >= 0 && !full) & window;
-  const unsigned whole = __ballot_sync(0xffffffffu, unit >= 0 && full && r == 0) & window;
+  // The new rows of this row's unit: how many, and whether this is the first.
+  const int before = min(r, i), count = before + min(kUnitTokens - r, n - i);
+  const unsigned few = __ballot_sync(0xffffffffu, unit >= 0 && count < kGroupRows);
+  unsigned first = __ballot_sync(0xffffffffu, unit >= 0 && before == 0 && count >= kGroupRows);
+  // Stage slots: token rows of a unit, or (few) rows of the window.
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if ((pass ? whole : single) == 0) continue;
-    const int j0 = pass ? __ffs(whole) - 1 : 0;  // row r0 + j0 is in slot 0
-    const unsigned rows = pass ? window : single;
-    stage_rows<T>(stage, x + j0 * p.row[which], p.row[which], rows, lane);
+  for (bool group = few == 0; !group || first; group = true) {
+    const int j0 = group ? __ffs(first) - 1 : 0;  // row r0 + j0 goes to slot k0
+    const int k0 = group ? __shfl_sync(0xffffffffu, r, j0) : 0;
+    const unsigned slots =
+        group ? ((1u << __shfl_sync(0xffffffffu, count, j0)) - 1) << k0 : few;
+    if (group) first &= first - 1;
+    stage_rows<T>(stage, x + (j0 - k0) * p.row[which], p.row[which], slots, lane);
     if (SIDE == 1 && codec == KVQ_Q8_0) {
       encode_staged_blocks<T, KVQ_Q8_0>(stage, lane);
     } else if (SIDE == 1 && codec == KVQ_Q4_0) {
       encode_staged_blocks<T, KVQ_Q4_0>(stage, lane);
     } else if (SIDE == 0 || codec != KVQ_F16 || T != KVQ_T_F16) {  // else the rows are the codes
 #pragma unroll 1
-      for (unsigned m = rows; m; m &= m - 1) {
-        const int j = __ffs(m) - 1;
+      for (unsigned m = slots; m; m &= m - 1) {
+        const int k = __ffs(m) - 1;
         float v[4];
-        load4<T>(stage + j * kPitch + 4 * lane * S, v);
+        load4<T>(stage + k * kPitch + 4 * lane * S, v);
         if (SIDE == 0) {
-          const float *row = rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j0 + j), p.err);
+          const float *row = rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j0 + k - k0), p.err);
           rotate_lane(p.rope, lane_angles(p.rope, row, lane), lane, v);
         }
         __syncwarp();  // every lane has read its part before the codes replace it
-        encode_staged(codec, v, stage + j * kPitch, lane);
+        encode_staged(codec, v, stage + k * kPitch, lane);
       }
     }
     __syncwarp();
-    if (pass) {
+    if (group) {
       uint4 *dst = reinterpret_cast<uint4 *>(
           p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
       const int chunks = unit_bytes(codec) / 16;
-      for (int c = lane; c < chunks; c += 32) dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
+      if (slots == (1u << kUnitTokens) - 1) {
+        for (int c = lane; c < chunks; c += 32)
+          dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
+      } else {
+        for (int c = lane; c < chunks; c += 32) {
+          const uint4 m = chunk_mask<SIDE>(codec, c, slots);
+          if (!(m.x | m.y | m.z | m.w)) continue;
+          const uint4 a = unit_chunk<SIDE, kPitch>(codec, stage, c), b = dst[c];
+          dst[c] = make_uint4((a.x & m.x) | (b.x & ~m.x), (a.y & m.y) | (b.y & ~m.y),
+                              (a.z & m.z) | (b.z & ~m.z), (a.w & m.w) | (b.w & ~m.w));
+        }
+      }
     } else {
 #pragma unroll 1
-      for (unsigned m = rows; m; m &= m - 1) {
-        const int j = __ffs(m) - 1;
-        store_staged<SIDE>(codec, stage + j * kPitch,
-                           p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j) * unit_bytes(codec),
-                           __shfl_sync(0xffffffffu, r, j), lane);
+      for (unsigned m = slots; m; m &= m - 1) {
+        const int k = __ffs(m) - 1;
+        store_staged<SIDE>(codec, stage + k * kPitch,
+                           p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, k) * unit_bytes(codec),
+                           __shfl_sync(0xffffffffu, r, k), lane);
       }
-      __syncwarp();
     }
+    __syncwarp();  // the slots are free again
   }
 }
 

@@ -206,8 +206,8 @@ __device__ __forceinline__ void store4(void *p, const float (&x)[4]) {
 // Where the planes allow it a row is held by eight lanes, 16 values each: for
 // a half layout lane l takes dims 8l .. and rot/2 + 8l .., both elements of its
 // planes, so nothing crosses lanes, loads and stores are 16 bytes and a warp
-// moves four heads at once.  Lanes behind the planes take what passes
-// through.  Either way lane l needs the table's entries 8l .. 8l + 7.
+// moves four heads at once (lanes behind the planes take what passes
+// through).  An interleaved layout takes dims 8l .. and 64 + 8l ..
 
 __host__ __device__ inline bool eight_lanes(const RopeArgs &p) {
   return p.layout == KVQ_ROPE_INTERLEAVED ? p.rot % 8 == 0 : p.rot % 16 == 0;
@@ -222,8 +222,8 @@ __device__ __forceinline__ EightLanes eight_lanes_of(const RopeArgs &p, int l) {
   EightLanes m;
   const int h = p.rot >> 1;
   if (p.layout == KVQ_ROPE_INTERLEAVED) {
-    m.a = 16 * l;
-    m.b = 16 * l + 8;
+    m.a = 8 * l;
+    m.b = 64 + 8 * l;
     m.turn_a = m.a < p.rot;
     m.turn_b = m.b < p.rot;
   } else {
@@ -241,12 +241,13 @@ struct EightAngles {
 __device__ __forceinline__ EightAngles eight_angles(const RopeArgs &p, const EightLanes &m,
                                                     const float *row, int l, float sign = 1.0f) {
   EightAngles a;
+  const bool inter = p.layout == KVQ_ROPE_INTERLEAVED;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // entries 8l + 2i, + 1 (a table row ends inside group b where only a turns)
+    // half: entries 8l + 2i, + 1; interleaved: 4l + .. of group a, 32 + 4l + .. of b
+    const int at = !inter ? 16 * l + 4 * i : i < 2 ? 8 * l + 4 * i : 64 + 8 * l + 4 * (i - 2);
     float4 t = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-    const bool live = p.layout == KVQ_ROPE_INTERLEAVED && i >= 2 ? m.turn_b : m.turn_a;
-    if (live) t = *reinterpret_cast<const float4 *>(row + 16 * l + 4 * i);
+    if (inter && i >= 2 ? m.turn_b : m.turn_a) t = *reinterpret_cast<const float4 *>(row + at);
     a.c[2 * i] = __fmul_rn(t.x, p.magnitude);
     a.s[2 * i] = sign * __fmul_rn(t.y, p.magnitude);
     a.c[2 * i + 1] = __fmul_rn(t.z, p.magnitude);
