@@ -524,7 +524,7 @@ __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uin
 #pragma unroll
     for (int c = 0; c < 8; ++c) load4<T>(&raw[rh][c], v[c]);
     const float *row = at[rh] >= 0 ? rope_row(p.rope, ps[rh], p.err) : p.rope.table;
-    quad_rotate(p.rope, p.kind, row, w, 1.0f, v);
+    quad_rotate<false>(p.rope, p.kind, row, w, 1.0f, v);
     quad_encode<CODEC>(v, w, q[rh]);
   }
   uint8_t *const cache = p.cache[0];
@@ -634,14 +634,18 @@ __global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
   grid_launch_dependents();
   check_counts(p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x < p.kv_blocks) {  // (window, side, kv head), heads innermost
+  // First every (window, kv head) of K, then of V, then the q rows: the blocks
+  // of an SM run mostly one of the three codes.
+  if (blockIdx.x < p.kv_blocks) {
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kArWarps + warp;
-    const int h = static_cast<int>(item % p.n_kv), side = static_cast<int>(item / p.n_kv) & 1;
-    const int64_t r0 = item / (2 * p.n_kv) * kUnitTokens;
-    if (r0 >= p.n_rows) return;
+    const int64_t per_side = (p.n_rows + kUnitTokens - 1) / kUnitTokens * p.n_kv;
+    if (item >= 2 * per_side) return;
     uint8_t *mine = stage + warp * Stage<T>::kWarpBytes;
-    if (side == 0) window_item<T, 0>(p, r0, h, mine, lane);
-    else window_item<T, 1>(p, r0, h, mine, lane);
+    if (item < per_side)
+      window_item<T, 0>(p, item / p.n_kv * kUnitTokens, static_cast<int>(item % p.n_kv), mine, lane);
+    else
+      window_item<T, 1>(p, (item - per_side) / p.n_kv * kUnitTokens,
+                        static_cast<int>((item - per_side) % p.n_kv), mine, lane);
   } else {
     const int64_t item = (static_cast<int64_t>(blockIdx.x) - p.kv_blocks) * kArWarps + warp;
     const int64_t row = item / p.q_chunks;

@@ -24,7 +24,15 @@ inline int quad_kind(const RopeArgs &p) {
   return p.rot % 32 == 0 ? p.rot / 32 : kQuadNone;
 }
 
-template <int N>
+// PURE: no magnitude (kv_rope_shift); otherwise no sign.
+template <bool PURE>
+__device__ __forceinline__ void quad_turn(const RopeArgs &p, float &a, float &b, float co, float si,
+                                          float sign) {
+  if (PURE) turn(a, b, co, sign * si);
+  else turn(a, b, __fmul_rn(co, p.magnitude), __fmul_rn(si, p.magnitude));
+}
+
+template <int N, bool PURE>
 __device__ __forceinline__ void quad_rotate_half(const RopeArgs &p, const float *row, int w,
                                                  float sign, float (&v)[8][4]) {
 #pragma unroll
@@ -34,19 +42,19 @@ __device__ __forceinline__ void quad_rotate_half(const RopeArgs &p, const float 
     const float co[4] = {t.x, t.z, u.x, u.z}, si[4] = {t.y, t.w, u.y, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      turn(v[c][i], v[c + N][i], __fmul_rn(co[i], p.magnitude),
-           sign * __fmul_rn(si[i], p.magnitude));
+      quad_turn<PURE>(p, v[c][i], v[c + N][i], co[i], si[i], sign);
   }
 }
 
 // Rotate the quad's row by the table row `row` (kind: quad_kind's, not
 // kQuadNone).
+template <bool PURE>
 __device__ __forceinline__ void quad_rotate(const RopeArgs &p, int kind, const float *row, int w,
                                             float sign, float (&v)[8][4]) {
-  if (kind == 4) quad_rotate_half<4>(p, row, w, sign, v);
-  else if (kind == 3) quad_rotate_half<3>(p, row, w, sign, v);
-  else if (kind == 2) quad_rotate_half<2>(p, row, w, sign, v);
-  else if (kind == 1) quad_rotate_half<1>(p, row, w, sign, v);
+  if (kind == 4) quad_rotate_half<4, PURE>(p, row, w, sign, v);
+  else if (kind == 3) quad_rotate_half<3, PURE>(p, row, w, sign, v);
+  else if (kind == 2) quad_rotate_half<2, PURE>(p, row, w, sign, v);
+  else if (kind == 1) quad_rotate_half<1, PURE>(p, row, w, sign, v);
   else {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -61,9 +69,8 @@ __device__ __forceinline__ void quad_rotate(const RopeArgs &p, int kind, const f
         if (d + 2 < p.rot) b = *reinterpret_cast<const float2 *>(row + d + 2);
         t = make_float4(a.x, a.y, b.x, b.y);
       }
-      turn(v[c][0], v[c][1], __fmul_rn(t.x, p.magnitude), sign * __fmul_rn(t.y, p.magnitude));
-      if (d + 2 < p.rot)
-        turn(v[c][2], v[c][3], __fmul_rn(t.z, p.magnitude), sign * __fmul_rn(t.w, p.magnitude));
+      quad_turn<PURE>(p, v[c][0], v[c][1], t.x, t.y, sign);
+      if (d + 2 < p.rot) quad_turn<PURE>(p, v[c][2], v[c][3], t.z, t.w, sign);
     }
   }
 }
@@ -237,24 +244,30 @@ __device__ __forceinline__ void quad_decode(const QuadCodes<CODEC> &q, int w, fl
     }
     return;
   }
+  // An unsigned byte or nibble n in the mantissa of 2^23 is 2^23 + n; taking
+  // off 2^23 and the code's offset (q8_0: 128, after flipping the sign bit;
+  // nibbles: 8) leaves the code exactly.
+  const uint32_t magic = 0x4B000000u;
+  const float off = CODEC == KVQ_Q8_0 ? -8388736.0f : -8388616.0f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const float d = half_bits(CODEC == KVQ_TURBO4
                                   ? q.scale
                                   : __shfl_sync(0xffffffffu, static_cast<uint32_t>(q.scale), b, 4));
-    if (CODEC == KVQ_Q8_0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      uint32_t x;  // four bytes: the codes of v[2b + h]
+      if (CODEC == KVQ_Q8_0) x = q.w[2 * b + h] ^ 0x80808080u;
+      else x = (h ? q.w[b] >> 4 : q.w[b]) & 0x0f0f0f0fu;
+      float *y = v[2 * b + h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[2 * b + h][i] =
-              d * static_cast<float>(static_cast<int8_t>(q.w[2 * b + h] >> (8 * i)));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = q.w[b] >> (8 * i);
-        v[2 * b][i] = d * static_cast<float>(static_cast<int>(x & 15u) - 8);
-        v[2 * b + 1][i] = d * static_cast<float>(static_cast<int>((x >> 4) & 15u) - 8);
+      for (int i = 0; i < 4; i += 2) {
+        const float2 n = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(x, magic, 0x7440 + i)),
+                                                __uint_as_float(__byte_perm(x, magic, 0x7441 + i))),
+                                    make_float2(off, off));
+        const float2 z = __fmul2_rn(n, make_float2(d, d));
+        y[i] = z.x;
+        y[i + 1] = z.y;
       }
     }
   }

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     for (int rh = 0; rh < 2; ++rh) {
       float v[8][4];
       quad_decode<CODEC>(q[rh], w, v);
-      quad_rotate(p.rope, p.kind, row[rh], w, d[rh] < 0 ? -1.0f : 1.0f, v);
+      quad_rotate<true>(p.rope, p.kind, row[rh], w, d[rh] < 0 ? -1.0f : 1.0f, v);
       QuadCodes<CODEC> e;
       quad_encode<CODEC>(v, w, e);
       if (d[rh] != 0) q[rh] = e;
