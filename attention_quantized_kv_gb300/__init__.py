@@ -215,10 +215,13 @@ def attn_prefill_chunk(layer: KVLayer, seq: int, q_start: int, q, scale: float, 
 
 # --------------------------------------------------------------------------- degrade ladder
 
+_ROW_BYTES = {KVQ_F16: 256, KVQ_Q8_0: 136, KVQ_Q4_0: 72, KVQ_TURBO4: 66}
+
+
 def _side_bytes(layer: KVLayer, codec: int) -> int:
-    if layer.n_pages > 0:
-        return kvq_pool_bytes(codec, layer.n_pages, layer.n_kv_heads, layer.head_dim)
-    return kvq_cache_bytes(codec, layer.n_seqs, layer.n_kv_heads, layer.capacity, layer.head_dim)
+    """kvq_pool_bytes / kvq_cache_bytes of a side of this layer in a codec (-1: no such codec)."""
+    tokens = layer.n_pages * 256 if layer.n_pages > 0 else layer.n_seqs * layer.capacity
+    return _ROW_BYTES[codec] * layer.n_kv_heads * tokens if codec in _ROW_BYTES else -1
 
 
 def kv_requantize(layer: KVLayer, side: int, dst_codec: int, dst_cache, stream=None) -> None:

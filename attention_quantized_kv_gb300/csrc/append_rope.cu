@@ -43,6 +43,7 @@ __device__ __forceinline__ int64_t new_rows(const AppendRopeParams &p, int s, bo
     bad = a < 0 || b < a || b > p.n_rows;
     return bad ? 0 : b - a;
   }
+  if (!p.n_new) return 1;  // one row per sequence
   const int n = p.n_new[s];
   bad = n < 0 || n > p.max_new;
   return bad ? 0 : n;
@@ -54,7 +55,7 @@ __device__ __forceinline__ bool find_row(const AppendRopeParams &p, int64_t row,
   if (!p.row_start) {
     s = static_cast<int>(row / p.max_new);
     i = static_cast<int>(row - s * p.max_new);
-    n = p.n_new[s];
+    n = p.n_new ? p.n_new[s] : 1;
     return i < n && n <= p.max_new;
   }
   int lo = 0, hi = p.n_seqs;  // the last s with row_start[s] <= row
@@ -293,15 +294,19 @@ __device__ __forceinline__ void encode_staged(int codec, const float (&x)[4], ui
   }
 }
 
-// Store a staged row's codes as token row r of a unit.
-template <int SIDE>
+// Store a staged row's codes as token row r of a unit.  An f16 side's row of V
+// is still the input's values, of type T (K: T = KVQ_T_F16, what its rotation
+// left).
+template <int T, int SIDE>
 __device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint8_t *unit, int r,
                                              int lane) {
   uint2 raw = make_uint2(0u, 0u);
   int q[4] = {0, 0, 0, 0};
   __half d16 = __float2half_rn(0.0f);
   if (codec == KVQ_F16) {
-    raw = reinterpret_cast<const uint2 *>(row)[lane];
+    float v[4];
+    load4<T>(row + 4 * lane * Stage<T>::S, v);
+    store4<KVQ_T_F16>(&raw, v);
   } else {
     const uint32_t w = reinterpret_cast<const uint32_t *>(row)[lane];
 #pragma unroll
@@ -349,7 +354,8 @@ __device__ __forceinline__ uint4 chunk_mask(int codec, int c, unsigned rows) {
 
 // 16 bytes of the unit, chunk c, from the staged rows (row r at s + r * PITCH):
 // the inverse of the placement formulas of include/kvq.h.
-template <int SIDE, int PITCH>
+// (T as in store_staged.)
+template <int T, int SIDE, int PITCH>
 __device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) {
   auto w32 = [&](int r, int byte) {
     return *reinterpret_cast<const uint32_t *>(s + r * PITCH + byte);
@@ -369,8 +375,21 @@ __device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) 
     // hi = mt: dims 16 mt + 2 gq, + 1 of rows 2 tig + par + 8 rh
 #pragma unroll
     for (int rh = 0; rh < 2; ++rh) {
-      const uint32_t a = w32(2 * lo + 8 * rh, (16 * hi + 2 * g) * 2);
-      const uint32_t b = w32(2 * lo + 1 + 8 * rh, (16 * hi + 2 * g) * 2);
+      uint32_t a, b;
+      const int d = (16 * hi + 2 * g) * Stage<T>::S;
+      if (T == KVQ_T_F32) {
+        const float2 x = *reinterpret_cast<const float2 *>(s + (2 * lo + 8 * rh) * PITCH + d);
+        const float2 y = *reinterpret_cast<const float2 *>(s + (2 * lo + 1 + 8 * rh) * PITCH + d);
+        a = pack_half2(x.x, x.y);
+        b = pack_half2(y.x, y.y);
+      } else {
+        a = w32(2 * lo + 8 * rh, d);
+        b = w32(2 * lo + 1 + 8 * rh, d);
+        if (T == KVQ_T_BF16) {
+          a = pack_half2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+          b = pack_half2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+        }
+      }
       o[2 * rh] = __byte_perm(a, b, 0x5410);
       o[2 * rh + 1] = __byte_perm(a, b, 0x7632);
     }
@@ -542,6 +561,7 @@ template <int T, int SIDE>
 __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r0, int h,
                                             uint8_t *stage, int lane) {
   constexpr int which = SIDE + 1, kPitch = Stage<T>::kPitch, S = Stage<T>::S;
+  constexpr int TS = SIDE == 0 ? static_cast<int>(KVQ_T_F16) : T;  // f16 rows in the stage
   const int codec = p.codec[SIDE];
   const uint8_t *x = p.x[which] + r0 * p.row[which] + h * p.head[which];
   // lane j: row r0 + j (the new rows of a unit whose first lies in the window
@@ -576,13 +596,21 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
     const int k0 = group ? __shfl_sync(0xffffffffu, r, j0) : 0;
     const unsigned slots =
         group ? ((1u << __shfl_sync(0xffffffffu, count, j0)) - 1) << k0 : few;
-    if (group) first &= first - 1;
+    uint4 *dst = nullptr;
+    if (group) {
+      first &= first - 1;
+      dst = reinterpret_cast<uint4 *>(p.cache[SIDE] +
+                                      __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
+      // an incomplete unit's old bytes, asked for beside the rows
+      if (slots != (1u << kUnitTokens) - 1 && lane * 128 < unit_bytes(codec))
+        asm volatile("prefetch.global.L1 [%0];\n" ::"l"(reinterpret_cast<uint8_t *>(dst) + lane * 128));
+    }
     stage_rows<T>(stage, x + (j0 - k0) * p.row[which], p.row[which], slots, lane);
     if (SIDE == 1 && codec == KVQ_Q8_0) {
       encode_staged_blocks<T, KVQ_Q8_0>(stage, lane);
     } else if (SIDE == 1 && codec == KVQ_Q4_0) {
       encode_staged_blocks<T, KVQ_Q4_0>(stage, lane);
-    } else if (SIDE == 0 || codec != KVQ_F16 || T != KVQ_T_F16) {  // else the rows are the codes
+    } else if (SIDE == 0 || codec != KVQ_F16) {  // (f16 V: converted on the way out)
 #pragma unroll 1
       for (unsigned m = slots; m; m &= m - 1) {
         const int k = __ffs(m) - 1;
@@ -598,17 +626,15 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
     }
     __syncwarp();
     if (group) {
-      uint4 *dst = reinterpret_cast<uint4 *>(
-          p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
       const int chunks = unit_bytes(codec) / 16;
       if (slots == (1u << kUnitTokens) - 1) {
         for (int c = lane; c < chunks; c += 32)
-          dst[c] = unit_chunk<SIDE, kPitch>(codec, stage, c);
+          dst[c] = unit_chunk<TS, SIDE, kPitch>(codec, stage, c);
       } else {
         for (int c = lane; c < chunks; c += 32) {
           const uint4 m = chunk_mask<SIDE>(codec, c, slots);
           if (!(m.x | m.y | m.z | m.w)) continue;
-          const uint4 a = unit_chunk<SIDE, kPitch>(codec, stage, c), b = dst[c];
+          const uint4 a = unit_chunk<TS, SIDE, kPitch>(codec, stage, c), b = dst[c];
           dst[c] = make_uint4((a.x & m.x) | (b.x & ~m.x), (a.y & m.y) | (b.y & ~m.y),
                               (a.z & m.z) | (b.z & ~m.z), (a.w & m.w) | (b.w & ~m.w));
         }
@@ -617,7 +643,7 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
 #pragma unroll 1
       for (unsigned m = slots; m; m &= m - 1) {
         const int k = __ffs(m) - 1;
-        store_staged<SIDE>(codec, stage + k * kPitch,
+        store_staged<TS, SIDE>(codec, stage + k * kPitch,
                            p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, k) * unit_bytes(codec),
                            __shfl_sync(0xffffffffu, r, k), lane);
       }
@@ -705,8 +731,8 @@ __global__ void advance_lens_kernel(AppendRopeParams p, int32_t *seq_lens) {
   const int s = blockIdx.x * blockDim.x + threadIdx.x;
   if (s >= p.n_seqs) return;
   bool bad;
-  const int64_t v = seq_lens[s] + new_rows(p, s, bad);
-  if (!bad) seq_lens[s] = static_cast<int32_t>(v > p.capacity ? p.capacity : v);
+  const int64_t old = seq_lens[s], v = old + new_rows(p, s, bad);
+  if (!bad && old >= 0) seq_lens[s] = static_cast<int32_t>(v > p.capacity ? p.capacity : v);
 }
 
 }  // namespace

@@ -55,9 +55,31 @@ int decode_append(const kvq_layer *layer, const kvq_rope *rope, const int32_t *p
   if (sms <= 0) return KVQ_ECUDA;
   const kvq::DecodePlan pl = kvq::plan_decode(*layer, max_len, sms);
   if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
-  const cudaError_t e = kvq::launch_decode(*layer, pl, q, scale, out, lse, max_len, workspace,
-                                           static_cast<cudaStream_t>(stream), k_new, v_new, rope,
-                                           positions);
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  // Many sequences: their new rows are placed faster by a grid of their own
+  // than by the split kernel's CTAs before their first copy, and the rotated
+  // queries wait in `out`, whose rows the merge kernel writes last.  500 / 4000
+  // f16 keys, 32 q / 8 kv heads: 16 sequences 21.1 -> 19.2 / 52.8 -> 53.2 us,
+  // 64 sequences 59.1 -> 49.4 / 180 -> 172 us; but 8 sequences 17.8 -> 17.1 /
+  // 32.8 -> 34.6 us and 2 sequences 11.7 -> 13.2 us.  Same bits either way.
+  const int64_t d = kHeadDim, q_bytes = layer->n_seqs * (layer->n_q_heads * d * 2);
+  const int64_t kv_bytes = layer->n_seqs * (layer->n_kv_heads * d * 2);
+  if (rope && layer->n_seqs >= kvq::kSplitStepSeqs && aligned(q, 16) && aligned(k_new, 16) &&
+      aligned(v_new, 16) && aligned(out, 16) &&
+      (q == out || !kvq::overlap(q, q_bytes, out, q_bytes)) &&
+      !kvq::overlap(k_new, kv_bytes, out, q_bytes) &&
+      !kvq::overlap(v_new, kv_bytes, out, q_bytes)) {
+    const kvq_rows qr = {const_cast<void *>(q), layer->n_q_heads * d, d, KVQ_T_F16, 0};
+    const kvq_rows kr = {const_cast<void *>(k_new), layer->n_kv_heads * d, d, KVQ_T_F16, 0};
+    const kvq_rows vr = {const_cast<void *>(v_new), layer->n_kv_heads * d, d, KVQ_T_F16, 0};
+    cudaError_t e = kvq::launch_append_rope(*layer, *rope, &qr, kr, vr, layer->n_seqs, nullptr,
+                                            nullptr, positions, out, 1, sms, st_);
+    if (e == cudaSuccess)
+      e = kvq::launch_decode(*layer, pl, out, scale, out, lse, max_len, workspace, st_);
+    return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  }
+  const cudaError_t e = kvq::launch_decode(*layer, pl, q, scale, out, lse, max_len, workspace, st_,
+                                           k_new, v_new, rope, positions);
   return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
 }
 
@@ -214,11 +236,6 @@ int kv_requantize(const kvq_layer *layer, int32_t side, int32_t dst_codec, void 
   return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
 }
 
-static bool overlaps(const void *a, int64_t na, const void *b, int64_t nb) {
-  const uint8_t *x = static_cast<const uint8_t *>(a), *y = static_cast<const uint8_t *>(b);
-  return x < y + nb && y < x + na;
-}
-
 // Bytes of one side's cache (or pool, for a paged layer).
 static int64_t side_bytes(const kvq_layer *L, int codec) {
   return L->pages_per_seq > 0
@@ -263,13 +280,13 @@ int kv_compact(const kvq_layer *layer, const int32_t *evict, const int32_t *n_ev
       (scores_dst && !aligned(scores_dst, 4)) || (lens_dst && !aligned(lens_dst, 4)))
     return KVQ_EALIGN;
   const int64_t kb = side_bytes(layer, layer->codec_k), vb = side_bytes(layer, layer->codec_v);
-  if (overlaps(k_dst, kb, layer->k_cache, kb) || overlaps(k_dst, kb, layer->v_cache, vb) ||
-      overlaps(v_dst, vb, layer->k_cache, kb) || overlaps(v_dst, vb, layer->v_cache, vb) ||
-      overlaps(k_dst, kb, v_dst, vb))
+  if (kvq::overlap(k_dst, kb, layer->k_cache, kb) || kvq::overlap(k_dst, kb, layer->v_cache, vb) ||
+      kvq::overlap(v_dst, vb, layer->k_cache, kb) || kvq::overlap(v_dst, vb, layer->v_cache, vb) ||
+      kvq::overlap(k_dst, kb, v_dst, vb))
     return KVQ_EINVAL;
   const int64_t sb = static_cast<int64_t>(layer->n_seqs) * layer->capacity * 4;
-  if (scores && overlaps(scores, sb, scores_dst, sb)) return KVQ_EINVAL;
-  if (lens_dst && overlaps(lens_dst, 4 * layer->n_seqs, layer->seq_lens, 4 * layer->n_seqs))
+  if (scores && kvq::overlap(scores, sb, scores_dst, sb)) return KVQ_EINVAL;
+  if (lens_dst && kvq::overlap(lens_dst, 4 * layer->n_seqs, layer->seq_lens, 4 * layer->n_seqs))
     return KVQ_EINVAL;
   const cudaError_t e =
       kvq::launch_compact(*layer, evict, n_evicted, max_evict, k_dst, v_dst, scores, scores_dst,

@@ -20,6 +20,12 @@ inline bool aligned(const void *p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uint8_t *x = static_cast<const uint8_t *>(a), *y = static_cast<const uint8_t *>(b);
+  return x < y + nb && y < x + na;
+}
+
 // The layer descriptor: geometry, codecs, cache pointers and their
 // alignment, and (paged layers) the block table.
 inline int check_layer(const kvq_layer *L) {

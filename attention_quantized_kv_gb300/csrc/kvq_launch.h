@@ -76,6 +76,12 @@ cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32
                            float *scores_dst, int32_t *lens_dst, cudaStream_t stream);
 
 // Rotary positions (rope.cu, append_rope.cu).
+
+// Sequences from which a rotary decode step appends in a launch of its own
+// (kvq_api.cu: decode_append).
+constexpr int kSplitStepSeqs = 16;
+constexpr int kShiftMaxSeqs = 65535;  // sequences of a key shift: a grid's second dimension
+
 inline int type_bytes(int type) { return type == KVQ_T_F32 ? 4 : 2; }
 
 // A frequency in [0, 2 pi) radians per position as turns in units of 2^-64,
@@ -88,6 +94,7 @@ cudaError_t launch_rope_table(const double *freqs, int rot_dim, int n_pos, float
 cudaError_t launch_rope_apply(const kvq_rope &rope, const kvq_rows &x, const kvq_rows &y,
                               int64_t n_rows, int n_heads, const int32_t *positions, int pos0,
                               int transpose, int32_t *err, cudaStream_t stream);
+// n_new and row_start both null: one row per sequence.
 cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const kvq_rows *q,
                                const kvq_rows &k, const kvq_rows &v, int64_t n_rows,
                                const int32_t *n_new, const int32_t *row_start,

@@ -31,33 +31,45 @@ __host__ __device__ constexpr double turn_term(int n) {
   return n == 0 ? 1.0 : turn_term(n - 1) * kTurn / n;
 }
 
-// (cos, sin) of u * 2^-64 turns.  The nearest quarter turn is taken off as an
+// (cos, sin) of u * 2^-64 turns for two angles at once (one polynomial
+// instruction serves both).  The nearest quarter turn is taken off as an
 // integer, so the remainder t in [-1/8, 1/8] turns is exact and rounds once
 // to fp32 whatever the position (2^-24 of at most pi / 4 rad).  The series
 // end at t^9 and t^10, what is left out being below 2e-9; 2 pi t is taken
 // with 2 pi as the sum of two floats, so that the last addition's rounding is
-// the only other one of its size.  In all within 1.4 * 2^-24 (measured on the
+// the only other one of its size.  In all within 1.3 * 2^-24 (measured on the
 // host over 2M values), inside the documented 2^-23.
-__device__ __forceinline__ float2 cos_sin_turns(uint64_t u) {
+__device__ __forceinline__ float2 both(float k) { return make_float2(k, k); }
+__device__ __forceinline__ void cos_sin_turns(uint64_t u0, uint64_t u1, float2 &first,
+                                              float2 &second) {
   constexpr float k1 = static_cast<float>(kTurn), k1lo = static_cast<float>(kTurn - k1);
   constexpr float k2 = turn_term(2), k3 = turn_term(3), k4 = turn_term(4), k5 = turn_term(5),
                   k6 = turn_term(6), k7 = turn_term(7), k8 = turn_term(8), k9 = turn_term(9),
                   k10 = turn_term(10);
-  const uint32_t quarter = static_cast<uint32_t>((u + (1ull << 61)) >> 62);
-  const int64_t r = static_cast<int64_t>(u - (static_cast<uint64_t>(quarter) << 62));
-  const float t = static_cast<float>(r) * 0x1p-64f, t2 = t * t;
-  float s = fmaf(t2, fmaf(t2, fmaf(t2, k9, -k7), k5), -k3);
-  s = fmaf(t, k1, fmaf(t * t2, s, t * k1lo));
-  float c = fmaf(t2, fmaf(t2, fmaf(t2, fmaf(t2, -k10, k8), -k6), k4), -k2);
-  c = fmaf(t2, c, 1.0f);
-  const float co = (quarter & 1) ? s : c, si = (quarter & 1) ? c : s;
-  return make_float2((quarter + 1) & 2 ? -co : co, quarter & 2 ? -si : si);
+  const uint32_t q0 = static_cast<uint32_t>((u0 + (1ull << 61)) >> 62);
+  const uint32_t q1 = static_cast<uint32_t>((u1 + (1ull << 61)) >> 62);
+  const int64_t r0 = static_cast<int64_t>(u0 - (static_cast<uint64_t>(q0) << 62));
+  const int64_t r1 = static_cast<int64_t>(u1 - (static_cast<uint64_t>(q1) << 62));
+  const float2 t = make_float2(static_cast<float>(r0) * 0x1p-64f, static_cast<float>(r1) * 0x1p-64f);
+  const float2 t2 = __fmul2_rn(t, t);
+  float2 s = __ffma2_rn(t2, __ffma2_rn(t2, __ffma2_rn(t2, both(k9), both(-k7)), both(k5)), both(-k3));
+  s = __ffma2_rn(t, both(k1), __ffma2_rn(__fmul2_rn(t, t2), s, __fmul2_rn(t, both(k1lo))));
+  float2 c = __ffma2_rn(t2, __ffma2_rn(t2, __ffma2_rn(t2, __ffma2_rn(t2, both(-k10), both(k8)),
+                                                      both(-k6)), both(k4)), both(-k2));
+  c = __ffma2_rn(t2, c, both(1.0f));
+  auto place = [](uint32_t q, float co, float si) {  // a quarter turn swaps them, a half negates
+    const float a = (q & 1) ? si : co, b = (q & 1) ? co : si;
+    return make_float2(__uint_as_float(__float_as_uint(a) ^ (((q + 1) & 2) << 30)),
+                       __uint_as_float(__float_as_uint(b) ^ ((q & 2) << 30)));
+  };
+  first = place(q0, c.x, s.x);
+  second = place(q1, c.y, s.y);
 }
 
-// Thread (column, row lane): P planes of every (rows-per-pass)-th position.
-// The angle's fraction of a turn advances by a whole number of 2^-64 turns
-// per step, modulo 2^64, so the running sum is exact.  P = 2 stores 16 bytes
-// (P = 1: an odd number of planes).
+// Thread (column, row lane): two planes of every (rows-per-pass)-th position
+// (P = 1, an odd number of planes: one plane of two such positions).  The
+// angle's fraction of a turn advances by a whole number of 2^-64 turns per
+// step, modulo 2^64, so the running sum is exact.
 template <int P>
 __global__ void __launch_bounds__(kRopeThreads) table_kernel(const __grid_constant__ TableParams p) {
   const int rows = kRopeThreads / p.cols;  // positions per block and pass
@@ -65,24 +77,23 @@ __global__ void __launch_bounds__(kRopeThreads) table_kernel(const __grid_consta
   if (row >= rows) return;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   int64_t pos = static_cast<int64_t>(blockIdx.x) * rows + row;
-  uint64_t u[P], du[P];
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    const uint64_t t = p.turns[col * P + k];
-    u[k] = t * static_cast<uint64_t>(pos);
-    du[k] = t * static_cast<uint64_t>(step);
-  }
+  const uint64_t t0 = p.turns[col * P], t1 = p.turns[col * P + P - 1];
+  const uint64_t d0 = t0 * static_cast<uint64_t>(step), d1 = t1 * static_cast<uint64_t>(step);
+  uint64_t u0 = t0 * static_cast<uint64_t>(pos), u1 = t1 * static_cast<uint64_t>(pos);
   float *out = p.table + (pos * p.pairs + col * P) * 2;
-  for (; pos < p.n_pos; pos += step, out += step * p.pairs * 2) {
-    const float2 a = cos_sin_turns(u[0]);
-    if (P == 2) {
-      const float2 b = cos_sin_turns(u[P - 1]);
+  const int64_t stride = step * p.pairs * 2;
+  float2 a, b;
+  if (P == 2) {
+    for (; pos < p.n_pos; pos += step, out += stride, u0 += d0, u1 += d1) {
+      cos_sin_turns(u0, u1, a, b);
       *reinterpret_cast<float4 *>(out) = make_float4(a.x, a.y, b.x, b.y);
-    } else {
-      *reinterpret_cast<float2 *>(out) = a;
     }
-#pragma unroll
-    for (int k = 0; k < P; ++k) u[k] += du[k];
+  } else {
+    for (; pos < p.n_pos; pos += 2 * step, out += 2 * stride, u0 += 2 * d0) {
+      cos_sin_turns(u0, u0 + d0, a, b);
+      *reinterpret_cast<float2 *>(out) = a;
+      if (pos + step < p.n_pos) *reinterpret_cast<float2 *>(out + stride) = b;
+    }
   }
 }
 

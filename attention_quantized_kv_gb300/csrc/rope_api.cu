@@ -43,11 +43,6 @@ int64_t span_bytes(const kvq_rows &r, int64_t n, int32_t heads) {
   return ((n - 1) * r.row_stride + (heads - 1) * r.head_stride + kHeadDim) * type_bytes(r.type);
 }
 
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-  const uint8_t *x = static_cast<const uint8_t *>(a), *y = static_cast<const uint8_t *>(b);
-  return x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace kvq
 
@@ -168,6 +163,7 @@ int kv_evict_delta(const kvq_layer *layer, const int32_t *evict, const int32_t *
   const int st = check_layer(layer);
   if (st != KVQ_OK) return st;
   if (!evict || !n_evicted || max_evict < 0 || !delta) return KVQ_EINVAL;
+  if (layer->n_seqs > kvq::kShiftMaxSeqs) return KVQ_EINVAL;
   if (!aligned(evict, 4) || !aligned(n_evicted, 4) || !aligned(delta, 4)) return KVQ_EALIGN;
   const cudaError_t e = kvq::launch_evict_delta(*layer, evict, n_evicted, max_evict, delta,
                                                 static_cast<cudaStream_t>(stream));
@@ -179,7 +175,7 @@ int kv_rope_shift(const kvq_layer *layer, const kvq_rope *rope, const int32_t *d
   int st = check_layer(layer);
   if (st != KVQ_OK) return st;
   if ((st = check_rope(rope)) != KVQ_OK) return st;
-  if (!delta) return KVQ_EINVAL;
+  if (!delta || layer->n_seqs > kvq::kShiftMaxSeqs) return KVQ_EINVAL;
   if (!aligned(delta, 4)) return KVQ_EALIGN;
   const cudaError_t e =
       kvq::launch_rope_shift(*layer, *rope, delta, static_cast<cudaStream_t>(stream));

@@ -488,7 +488,8 @@ KVQ_API int kv_append_rope(const kvq_layer *layer, const kvq_rope *rope, const k
  * delta[s][w] = w - (the position that token w had).  Call it with the lengths
  * from before the eviction; arguments as kv_compact's (evict increasing and
  * below the length, otherwise the values are unspecified).  delta: device
- * int32 [n_seqs][capacity]; entries behind the new length are not written. */
+ * int32 [n_seqs][capacity]; entries behind the new length are not written.
+ * At most 65535 sequences, as kv_rope_shift. */
 KVQ_API int kv_evict_delta(const kvq_layer *layer, const int32_t *evict,
                            const int32_t *n_evicted, int32_t max_evict, int32_t *delta,
                            void *stream);
@@ -510,7 +511,9 @@ KVQ_API int kv_rope_shift(const kvq_layer *layer, const kvq_rope *rope, const in
  * followed by attn_decode of q_out, bit for bit.  q, k_new, v_new: fp16 as
  * attn_decode_append takes them; positions NULL needs n_pos >= max_len
  * (KVQ_ECAPACITY).  A sequence already at capacity gets no new token
- * and attends its keys.  Everything else as attn_decode_append. */
+ * and attends its keys.  From 16 sequences on the append is a launch of its
+ * own and `out` holds the rotated queries until the results replace them.
+ * Everything else as attn_decode_append. */
 KVQ_API int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope,
                                     const int32_t *positions, const void *k_new,
                                     const void *v_new, const void *q, float scale, void *out,

@@ -575,6 +575,35 @@ def test_decode_step_is_append_then_decode(ck, cv, paged):
     assert not ws[:65536].any()
 
 
+@pytest.mark.parametrize("n_seqs,ck,cv,paged", [(16, F16, Q8, True), (33, Q4, F16, False),
+                                                (70, T4, T4, True)])
+def test_decode_step_of_many_sequences(n_seqs, ck, cv, paged):
+    """From 16 sequences on the step appends in a launch of its own: the bits
+    of a step that cannot (a query on an 8-byte boundary), in place too."""
+    n_kv, n_q, cap = 2, 6, 512
+    lens = [(s * 37) % 511 for s in range(n_seqs)]
+    lens[3], lens[5] = 512, 0
+    rope, _ = _rope(96, R.HALF, cap, 1.1)
+    L, table = _random_layer(n_seqs, n_kv, n_q, cap, ck, cv, paged, lens, 40)
+    M, N = _twin(L, table), _twin(L, table)
+    ws = torch.zeros(kvq.attn_decode_workspace(L, cap), dtype=torch.uint8, device="cuda")
+    buf = torch.randn(n_seqs * n_q * 128 + 4, device="cuda").half()
+    q_odd = buf[4:].view(n_seqs, n_q, 128)
+    q = q_odd.clone()
+    k, v = (torch.randn((n_seqs, n_kv, 128), device="cuda").half() for _ in "kv")
+    outs = [torch.empty_like(q) for _ in "ab"]
+    lses = [torch.empty((n_seqs, n_q), device="cuda") for _ in "abc"]
+    kvq.attn_decode_append_rope(L, rope, k, v, q, SCALE, outs[0], lses[0], cap, ws)
+    kvq.attn_decode_append_rope(M, rope, k, v, q_odd, SCALE, outs[1], lses[1], cap, ws)
+    kvq.attn_decode_append_rope(N, rope, k, v, q, SCALE, q, lses[2], cap, ws)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], q)
+    for X, lse in ((M, lses[1]), (N, lses[2])):
+        assert torch.equal(lses[0], lse) and L.seq_lens.tolist() == X.seq_lens.tolist()
+        assert torch.equal(L.k_cache, X.k_cache) and torch.equal(L.v_cache, X.v_cache)
+        assert X.err.item() == L.err.item() == kvq.KVQ_DEVERR_CAPACITY | kvq.KVQ_DEVERR_POS
+    assert not ws[:65536].any()
+
+
 def test_decode_step_odd_pointers():
     """q on an 8-byte boundary (rows read without the bulk copy)."""
     L, table = _random_layer(3, 2, 8, 512, F16, Q8, False, [300, 17, 0], 3)

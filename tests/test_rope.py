@@ -238,6 +238,9 @@ def test_shift_and_delta_refusals():
     assert lib.kv_evict_delta(L, 0x100, 0x100, -1, 0x200, None) == EINVAL
     assert lib.kv_evict_delta(L, 0x100, 0x100, 4, None, None) == EINVAL
     assert lib.kv_evict_delta(L, 0x102, 0x100, 4, 0x200, None) == EALIGN
+    many = _layer(n_seqs=65536)
+    assert lib.kv_rope_shift(many, r, 0x100, None) == EINVAL
+    assert lib.kv_evict_delta(many, 0x100, 0x100, 4, 0x200, None) == EINVAL
 
 
 def test_decode_refusals():
