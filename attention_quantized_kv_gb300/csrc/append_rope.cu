@@ -698,8 +698,10 @@ cudaError_t launch_rows(AppendRopeParams &p, int num_sms, cudaStream_t stream) {
   set_q_items<T>(p, p.eight ? (p.hpw > 4 ? p.hpw : 4) : p.hpw);
   p.kv_chunks = (p.n_kv + p.hpw - 1) / p.hpw;
   const int64_t items = p.n_rows * (p.q_chunks + 2 * p.kv_chunks);
-  return launch_pdl(append_rows_kernel<T>, dim3(static_cast<unsigned>((items + kArWarps - 1) / kArWarps)),
-                    dim3(kArThreads), 0, stream, p);
+  const int64_t blocks = (items + kArWarps - 1) / kArWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_pdl(append_rows_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kArThreads), 0,
+                    stream, p);
 }
 
 template <int T>
@@ -711,6 +713,7 @@ cudaError_t launch_prompt(AppendRopeParams &p, cudaStream_t stream) {
   const int64_t windows = (p.n_rows + kUnitTokens - 1) / kUnitTokens;
   p.kv_blocks = (windows * 2 * p.n_kv + kArWarps - 1) / kArWarps;
   const int64_t blocks = p.kv_blocks + (p.n_rows * p.q_chunks + kArWarps - 1) / kArWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch_pdl(append_prompt_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kArThreads),
                     Stage<T>::kBytes, stream, p);
 }

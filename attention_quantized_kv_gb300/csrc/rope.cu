@@ -33,8 +33,8 @@ __host__ __device__ constexpr double turn_term(int n) {
 
 // (cos, sin) of u * 2^-64 turns for two angles at once (one polynomial
 // instruction serves both).  The nearest quarter turn is taken off as an
-// integer, so the remainder t in [-1/8, 1/8] turns is exact and rounds once
-// to fp32 whatever the position (2^-24 of at most pi / 4 rad).  The series
+// integer, so the remainder t in [-1/8, 1/8] turns is exact (its 56 upper
+// bits are used) and rounds once to fp32 whatever the position (2^-24 of at most pi / 4 rad).  The series
 // end at t^9 and t^10, what is left out being below 2e-9; 2 pi t is taken
 // with 2 pi as the sum of two floats, so that the last addition's rounding is
 // the only other one of its size.  In all within 1.3 * 2^-24 (measured on the
@@ -46,11 +46,18 @@ __device__ __forceinline__ void cos_sin_turns(uint64_t u0, uint64_t u1, float2 &
   constexpr float k2 = turn_term(2), k3 = turn_term(3), k4 = turn_term(4), k5 = turn_term(5),
                   k6 = turn_term(6), k7 = turn_term(7), k8 = turn_term(8), k9 = turn_term(9),
                   k10 = turn_term(10);
-  const uint32_t q0 = static_cast<uint32_t>((u0 + (1ull << 61)) >> 62);
-  const uint32_t q1 = static_cast<uint32_t>((u1 + (1ull << 61)) >> 62);
-  const int64_t r0 = static_cast<int64_t>(u0 - (static_cast<uint64_t>(q0) << 62));
-  const int64_t r1 = static_cast<int64_t>(u1 - (static_cast<uint64_t>(q1) << 62));
-  const float2 t = make_float2(static_cast<float>(r0) * 0x1p-64f, static_cast<float>(r1) * 0x1p-64f);
+  // the quarter and the remainder's upper word: the lower word stays
+  const uint32_t h0 = static_cast<uint32_t>(u0 >> 32), h1 = static_cast<uint32_t>(u1 >> 32);
+  const uint32_t q0 = (h0 + (1u << 29)) >> 30, q1 = (h1 + (1u << 29)) >> 30;
+  // turns of a remainder: its top 24 bits exactly, the 32 below them added
+  // with one rounding
+  auto turns = [](uint32_t h, uint32_t lo) {
+    const float top = static_cast<float>(static_cast<int32_t>(h & ~0xffu));
+    const float rest = static_cast<float>(__funnelshift_l(lo, h, 24));
+    return fmaf(rest, 0x1p-56f, top * 0x1p-32f);
+  };
+  const float2 t = make_float2(turns(h0 - (q0 << 30), static_cast<uint32_t>(u0)),
+                               turns(h1 - (q1 << 30), static_cast<uint32_t>(u1)));
   const float2 t2 = __fmul2_rn(t, t);
   float2 s = __ffma2_rn(t2, __ffma2_rn(t2, __ffma2_rn(t2, both(k9), both(-k7)), both(k5)), both(-k3));
   s = __ffma2_rn(t, both(k1), __ffma2_rn(__fmul2_rn(t, t2), s, __fmul2_rn(t, both(k1lo))));
@@ -214,9 +221,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     shift_units_kernel(const __grid_constant__ ShiftParams p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, g = lane >> 2, w = lane & 3, s = blockIdx.y;
-  const int item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
   const int groups = (p.n_kv + kShiftHeads - 1) / kShiftHeads;
-  const int j = item / groups, h0 = item % groups * kShiftHeads;  // unit, first kv head
+  const int j = static_cast<int>(item / groups);  // unit
+  const int h0 = static_cast<int>(item % groups) * kShiftHeads;  // first kv head
   const int len = min(p.seq_lens[s], p.capacity);
   if (j * kUnitTokens >= len) return;
   int64_t unit = (static_cast<int64_t>(s) * p.n_kv + h0) * (p.capacity / kUnitTokens) + j;
@@ -307,6 +315,7 @@ cudaError_t launch_apply_t(ApplyParams &p, cudaStream_t stream) {
   while (p.hpw > 4 && p.n_rows * ((p.n_heads + p.hpw - 1) / p.hpw) < kSmallGrid) p.hpw /= 2;
   p.chunks = (p.n_heads + p.hpw - 1) / p.hpw;
   const int64_t blocks = (p.n_rows * p.chunks + kRopeWarps - 1) / kRopeWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch_pdl(eight ? apply_kernel<TI, TO> : apply_any_kernel<TI, TO>,
                     dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), 0, stream, p);
 }
@@ -384,7 +393,9 @@ cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const in
   }
   const int64_t items = static_cast<int64_t>(L.capacity / kUnitTokens) *
                         ((L.n_kv_heads + kShiftHeads - 1) / kShiftHeads);
-  const dim3 grid(static_cast<unsigned>((items + kRopeWarps - 1) / kRopeWarps), L.n_seqs);
+  const int64_t blocks = (items + kRopeWarps - 1) / kRopeWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks), L.n_seqs);
   const auto kernel = L.codec_k == KVQ_F16    ? shift_units_kernel<KVQ_F16>
                       : L.codec_k == KVQ_Q8_0 ? shift_units_kernel<KVQ_Q8_0>
                       : L.codec_k == KVQ_Q4_0 ? shift_units_kernel<KVQ_Q4_0>

@@ -651,6 +651,54 @@ def test_decode_step_positions_outside_the_table():
     assert L.err.item() == kvq.KVQ_DEVERR_POS and M.err.item() == 0
 
 
+# ------------------------------------------------------------------ far offsets
+
+def test_offsets_past_32_bits():
+    """A K side of over 4 GiB (bytes past 2^32) and rows whose strides pass 2^32
+    bytes: the last sequence's keys appended, shifted and attended."""
+    n_seqs, n_kv, cap = 9, 8, 262144
+    L = kvq.KVLayer(n_seqs, n_kv, n_kv, cap, F16, Q4)
+    assert L.k_cache.numel() > 2 ** 32
+    rope, t = _rope(128, R.HALF, cap)
+    at, n, s = cap - 50, 40, n_seqs - 1
+    per = cap * 256                                           # one stream's bytes
+    L.seq_lens[s] = at
+    wide = torch.empty((n, 2 ** 26), dtype=torch.float16, device="cuda")   # 128 MiB between rows
+    x = torch.randn((n, n_kv, 128), device="cuda").half()
+    wide[:, :n_kv * 128] = x.view(n, -1)
+    rows = wide[:, :n_kv * 128].unflatten(1, (n_kv, 128))
+    assert rows.stride(0) * 2 * (n - 1) > 2 ** 32
+    start = _i32([0] * n_seqs + [n])
+    kvq.kv_append_rope(L, rope, rows, rows, row_start=start)
+    y = torch.empty_like(x)
+    kvq.kvq_rope_apply(rope, rows, y, pos0=at)
+    assert L.seq_lens.tolist() == [0] * s + [at + n]
+
+    def stream(h):
+        c = L.k_cache[(s * n_kv + h) * per:(s * n_kv + h + 1) * per]
+        return c[(at // 16) * 4096:].cpu().numpy()
+
+    base = at // 16 * 16                                      # the first unit's token
+    def keys(h):
+        return oracle.dequant_stream(F16, 0, np.resize(stream(h), 256 * 256), 1, 256, 0, 0,
+                                     at + n - base)[at - base:]
+
+    ref = _rounded(R.rotate(_host(x), t[at:at + n], 128, R.HALF), torch.float16)
+    _same(y, ref)
+    for h in (0, n_kv - 1):
+        assert (keys(h) == ref[:, h].double().numpy()).all()
+    delta = torch.zeros((n_seqs, cap), dtype=torch.int32, device="cuda")
+    delta[s, at:at + n] = -cap // 2
+    kvq.kv_rope_shift(L, rope, delta)
+    d = np.full(n, cap // 2)
+    ref2 = R.rotate(ref.float().numpy(), t[d], 128, R.HALF, transpose=True).astype(np.float16)
+    for h in (0, n_kv - 1):
+        assert (keys(h) == ref2[:, h].astype(np.float64)).all()
+    assert L.err.item() == 0
+    del L, wide, rows
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ together
 
 def _prompt(L, rope, counts, seed, ti=torch.float16):
