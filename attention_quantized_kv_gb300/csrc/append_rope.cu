@@ -300,13 +300,25 @@ __device__ __forceinline__ void encode_staged(int codec, const float (&x)[4], ui
 template <int T, int SIDE>
 __device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint8_t *unit, int r,
                                              int lane) {
+  if (SIDE == 1 && codec == KVQ_F16) {
+    // One value per lane, dim 32 j + lane: a token's values lie four to a
+    // 128-byte line of V, so each store touches 8 lines (four values per lane
+    // touched 32 each time, and a window of 16 single tokens took 8 us).
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = 32 * j + lane;
+      const typename RowType<T>::type v = reinterpret_cast<const typename RowType<T>::type *>(row)[d];
+      const int mt = d >> 4, gq = (d & 15) >> 1, s = d & 1, tig = (r & 7) >> 1;
+      st_u16(unit + mt * 512 + (4 * gq + tig) * 16 + ((r >> 3) * 4 + s * 2 + (r & 1)) * 2,
+             __half_as_ushort(__float2half_rn(static_cast<float>(v))));
+    }
+    return;
+  }
   uint2 raw = make_uint2(0u, 0u);
   int q[4] = {0, 0, 0, 0};
   __half d16 = __float2half_rn(0.0f);
   if (codec == KVQ_F16) {
-    float v[4];
-    load4<T>(row + 4 * lane * Stage<T>::S, v);
-    store4<KVQ_T_F16>(&raw, v);
+    raw = reinterpret_cast<const uint2 *>(row)[lane];  // (K: T is KVQ_T_F16)
   } else {
     const uint32_t w = reinterpret_cast<const uint32_t *>(row)[lane];
 #pragma unroll
@@ -631,12 +643,21 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
         for (int c = lane; c < chunks; c += 32)
           dst[c] = unit_chunk<TS, SIDE, kPitch>(codec, stage, c);
       } else {
-        for (int c = lane; c < chunks; c += 32) {
-          const uint4 m = chunk_mask<SIDE>(codec, c, slots);
-          if (!(m.x | m.y | m.z | m.w)) continue;
-          const uint4 a = unit_chunk<TS, SIDE, kPitch>(codec, stage, c), b = dst[c];
-          dst[c] = make_uint4((a.x & m.x) | (b.x & ~m.x), (a.y & m.y) | (b.y & ~m.y),
-                              (a.z & m.z) | (b.z & ~m.z), (a.w & m.w) | (b.w & ~m.w));
+        constexpr int kAhead = 4;  // old pieces requested at once
+        for (int c0 = lane; c0 < chunks; c0 += 32 * kAhead) {
+          uint4 old[kAhead];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            if (c0 + 32 * i < chunks) old[i] = dst[c0 + 32 * i];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int c = c0 + 32 * i;
+            if (c >= chunks) break;
+            const uint4 m = chunk_mask<SIDE>(codec, c, slots), b = old[i];
+            const uint4 a = unit_chunk<TS, SIDE, kPitch>(codec, stage, c);
+            dst[c] = make_uint4((a.x & m.x) | (b.x & ~m.x), (a.y & m.y) | (b.y & ~m.y),
+                                (a.z & m.z) | (b.z & ~m.z), (a.w & m.w) | (b.w & ~m.w));
+          }
         }
       }
     } else {
