@@ -123,6 +123,16 @@ __device__ __forceinline__ void check_counts(const AppendRopeParams &p) {
   }
 }
 
+// Where dim d of token row r lies in an f16 unit of V.  A token's values lie
+// four to a 128-byte line there, so a row is stored one value per lane, dims
+// 32 j + lane: 8 lines per store.  (Four consecutive dims per lane, as the
+// encoders hold them, touch 32 each time; a window of 16 single tokens took
+// 8 us longer that way.)
+__device__ __forceinline__ uint8_t *v_f16_place(uint8_t *unit, int r, int d) {
+  return unit + (d >> 4) * 512 + (4 * ((d & 15) >> 1) + ((r & 7) >> 1)) * 16 +
+         ((r >> 3) * 4 + (d & 1) * 2 + (r & 1)) * 2;
+}
+
 // One warp: up to 16 heads of q of one row (planes that eight lanes hold).
 template <int T>
 __device__ __forceinline__ void q_item(const AppendRopeParams &p, int64_t row, int chunk,
@@ -188,6 +198,14 @@ __device__ __forceinline__ void row_item(const AppendRopeParams &p, int64_t row,
     if (which == 1) {
       rotate_lane(p.rope, a, lane, v);
       encode_f32_row_into<0>(codec, v, u, r, lane);
+    } else if (codec == KVQ_F16) {
+      const uint32_t lo = pack_half2(v[0], v[1]), hi = pack_half2(v[2], v[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // dim 32 j + lane: of lane 8 j + lane / 4
+        const uint32_t a = __shfl_sync(0xffffffffu, lo, 8 * j + (lane >> 2));
+        const uint32_t b = __shfl_sync(0xffffffffu, hi, 8 * j + (lane >> 2));
+        st_u16(v_f16_place(u, r, 32 * j + lane), ((lane & 2) ? b : a) >> (16 * (lane & 1)));
+      }
     } else {
       encode_f32_row_into<1>(codec, v, u, r, lane);
     }
@@ -301,15 +319,10 @@ template <int T, int SIDE>
 __device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint8_t *unit, int r,
                                              int lane) {
   if (SIDE == 1 && codec == KVQ_F16) {
-    // One value per lane, dim 32 j + lane: a token's values lie four to a
-    // 128-byte line of V, so each store touches 8 lines (four values per lane
-    // touched 32 each time, and a window of 16 single tokens took 8 us).
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int d = 32 * j + lane;
-      const typename RowType<T>::type v = reinterpret_cast<const typename RowType<T>::type *>(row)[d];
-      const int mt = d >> 4, gq = (d & 15) >> 1, s = d & 1, tig = (r & 7) >> 1;
-      st_u16(unit + mt * 512 + (4 * gq + tig) * 16 + ((r >> 3) * 4 + s * 2 + (r & 1)) * 2,
+      const auto v = reinterpret_cast<const typename RowType<T>::type *>(row)[32 * j + lane];
+      st_u16(v_f16_place(unit, r, 32 * j + lane),
              __half_as_ushort(__float2half_rn(static_cast<float>(v))));
     }
     return;
