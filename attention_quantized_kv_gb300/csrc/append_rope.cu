@@ -14,6 +14,7 @@ namespace {
 constexpr int kArWarps = 8;
 constexpr int kArThreads = kArWarps * 32;
 constexpr int kMaxHeads = 8;  // heads of one row that share a warp's angles
+constexpr int kRowSlotsPerSm = 128;  // rows x heads per SM up to which an append goes by rows
 
 struct AppendRopeParams {
   RopeArgs rope;
@@ -248,10 +249,9 @@ __global__ void __launch_bounds__(kArThreads)
 //
 // Packed rows are cut into windows of 16, whatever the lengths.  For V a
 // window's warp places the rows of every unit whose first new row lies in the
-// window: no other warp writes that unit, so an incomplete one is put together
-// over its old bytes.  (As 2-byte stores 13 rows of one f16 unit took 10 us.)
-// One or two rows are not worth that and are stored by themselves.  K rows
-// whose planes cross lanes take the same way.
+// window: no other warp writes that unit, so an incomplete one with enough new
+// rows is put together over its old bytes; rows of others are stored one by
+// one.  K rows whose planes cross lanes take the same way.
 
 // A staged row: the input's 128 values, replaced by 128 fp16 values, or by 128
 // one-byte codes and the block scales (4, or 1 for turbo4) behind them.
@@ -262,7 +262,10 @@ struct Stage {
   static constexpr int kWarpBytes = kUnitTokens * kPitch;
   static constexpr int kBytes = kArWarps * kWarpBytes;
 };
-constexpr int kGroupRows = 3;  // new rows of a unit that are worth its 16-byte pieces
+// New rows of a unit that are worth putting it together over its old bytes; 3,
+// 8, 12 or 16: a prompt of 2047 rows 11.4, 11.4, 11.4, 13.3 us, 16 prompts of
+// 16 rows 10.9, 9.3, 9.4, 9.4 us, 64 of 16 rows 19.7, 14.9, 14.0, 13.4 us.
+constexpr int kGroupRows = 12;
 constexpr int kScaleAt = kD;  // byte offset of a staged row's scales
 
 __device__ __forceinline__ void copy_async16(void *dst, const void *src) {
@@ -754,9 +757,13 @@ cudaError_t launch_prompt(AppendRopeParams &p, cudaStream_t stream) {
 
 template <int T>
 cudaError_t launch_append_t(AppendRopeParams &p, int num_sms, cudaStream_t stream) {
-  // Whole units are worth their shared-memory pass where sequences bring half
-  // a unit of tokens or more on average.
-  return p.n_rows >= static_cast<int64_t>(p.n_seqs) * (kUnitTokens / 2)
+  // Short appends go row by row, whatever their sequences: the chain of one
+  // row is 3 us, of a window 6 to 10.  With 40 q / 8 kv heads and f16 caches
+  // 256 rows take 5.7 us by rows and 6.6 (one sequence) to 9.7 us (64) by
+  // windows, 512 rows 9.7 and 7.7 to 10.7 us, 2048 rows 31 and 11.4 to 18 us;
+  // q8_0 caches cross at the same sizes.
+  const int64_t slots = p.n_rows * (p.n_q * (p.q_chunks > 0) + 2 * p.n_kv);
+  return slots > static_cast<int64_t>(num_sms) * kRowSlotsPerSm
              ? launch_prompt<T>(p, stream)
              : launch_rows<T>(p, num_sms, stream);
 }

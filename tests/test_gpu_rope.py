@@ -332,6 +332,86 @@ def test_append_padded_with_positions(ck, cv, layout, rot, update):
     assert L.err.item() == 0
 
 
+WINDOW_COUNTS = [1, 0, 300, 17, 1, 2, 1, 13, 12, 11, 16, 250, 1, 3]
+WINDOW_LENS = [255, 9, 247, 0, 16, 510, 31, 3, 4, 5, 240, 77, 0, 254]
+
+
+@pytest.mark.parametrize("ck", [F16, Q8, Q4, T4])
+@pytest.mark.parametrize("cv", [F16, Q8, Q4, T4])
+@pytest.mark.parametrize("paged", [False, True])
+def test_append_windows(ck, cv, paged):
+    """Appends long enough to go by 16-row windows: whole units, incomplete ones
+    with few and with many new rows, several sequences in a window, every kind
+    of plane and row type, explicit positions, a padded tail."""
+    n_kv, n_q, cap, i = 2, 32, 768, ck + 4 * cv + 16 * paged
+    layout, rot = [(R.HALF, 128), (R.INTERLEAVED, 96), (R.HALF, 40), (R.HALF, 64), (R.INTERLEAVED, 6),
+                   (R.HALF, 32), (R.HALF, 96), (R.HALF, 126), (R.INTERLEAVED, 128)][i % 9]
+    ti = [torch.float16, torch.bfloat16, torch.float32][i % 3]
+    n_seqs, total = len(WINDOW_COUNTS), sum(WINDOW_COUNTS)
+    assert total * (n_q + 2 * n_kv) > 152 * 128               # (the kernel's rule)
+    rope, t = _rope(rot, layout, cap, 1.25)
+    L, table = _layer(n_seqs, n_kv, n_q, cap, ck, cv, paged, 4)
+    L.seq_lens.copy_(_i32(WINDOW_LENS))
+    images = _images(L, table)
+    start = np.r_[0, np.cumsum(WINDOW_COUNTS)]
+    g = torch.Generator().manual_seed(100 + i)
+    qkv = torch.randn((total + 21, n_q + 2 * n_kv, 128), generator=g).to(ti)
+    q, k, v = qkv.cuda().split([n_q, n_kv, n_kv], dim=1)
+    q_out = torch.full((total + 21, n_q, 128), 2.0, dtype=torch.float16, device="cuda")
+    pos = None
+    if i % 2:
+        pos = torch.randint(0, cap, (total + 21,), generator=g, dtype=torch.int32)
+    kvq.kv_append_rope(L, rope, k, v, row_start=_i32(start), q=q, q_out=q_out,
+                       positions=None if pos is None else pos.cuda())
+    rows = [(start[s] + j, s, j) for s in range(n_seqs) for j in range(WINDOW_COUNTS[s])]
+    p = np.array([WINDOW_LENS[s] + j for _, s, j in rows]) if pos is None else pos.numpy()[:total]
+    x = qkv.float().numpy()
+    _append_ref(images, rows, WINDOW_LENS, x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:], t[p], rot, layout, 1.25)
+    _check_caches(L, images)
+    _same(q_out[:total], _rounded(R.rotate(x[:total, :n_q], t[p], rot, layout, 1.25), torch.float16))
+    assert (q_out[total:] == 2.0).all()
+    assert L.seq_lens.tolist() == [a + b for a, b in zip(WINDOW_LENS, WINDOW_COUNTS)]
+    assert L.err.item() == 0
+
+
+@pytest.mark.parametrize("ck,cv,rot", [(F16, F16, 128), (Q8, Q4, 40), (T4, Q8, 64)])
+def test_append_windows_device_conditions(ck, cv, rot):
+    """By windows too: rows past the capacity, on an unmapped page and behind
+    bad row starts are skipped, the padded form leaves gaps alone."""
+    n_kv, n_q, cap, max_new = 2, 32, 512, 200
+    rope, t = _rope(rot, R.HALF, cap)
+    lens, counts = [400, 250, 33], [200, 180, 77]
+    L, table = _layer(3, n_kv, n_q, cap, ck, cv, True, 3, unmapped=[(1, 1)])
+    L.seq_lens.copy_(_i32(lens))
+    images = _images(L, table)
+    g = torch.Generator().manual_seed(rot)
+    k, v = (torch.randn((3, max_new, n_kv, 128), generator=g).half() for _ in "kv")
+    q = torch.randn((3, max_new, n_q, 128), generator=g).half()
+    q_out = torch.full((3, max_new, n_q, 128), 2.0, dtype=torch.float16, device="cuda")
+    assert 3 * max_new * (n_q + 2 * n_kv) > 152 * 128
+    kvq.kv_append_rope(L, rope, k.cuda(), v.cuda(), n_new=_i32(counts), q=q.cuda(), q_out=q_out)
+    rows = [(s * max_new + i, s, i) for s in range(3) for i in range(counts[s])
+            if lens[s] + i < cap and not (s == 1 and lens[s] + i >= 256)]
+    pos = np.array([lens[s] + i for _, s, i in rows])
+    _append_ref(images, rows, lens, k.float().numpy().reshape(-1, n_kv, 128),
+                v.float().numpy().reshape(-1, n_kv, 128), t[pos], rot, R.HALF, 1.0)
+    _check_caches(L, images)
+    for s in range(3):
+        p = np.minimum(cap - 1, lens[s] + np.arange(counts[s]))
+        _same(q_out[s, :counts[s]], _rounded(R.rotate(q[s, :counts[s]].float().numpy(), t[p], rot, R.HALF),
+                                             torch.float16))
+        assert (q_out[s, counts[s]:] == 2.0).all()
+    # (positions of the rows past the capacity leave the table too)
+    assert L.err.item() == kvq.KVQ_DEVERR_CAPACITY | kvq.KVQ_DEVERR_PAGE | kvq.KVQ_DEVERR_POS
+    assert L.seq_lens.tolist() == [512, 430, 110]
+    M, _ = _layer(3, n_kv, n_q, cap, ck, cv, True, 3)
+    before = [M.k_cache.clone(), M.v_cache.clone()]
+    kvq.kv_append_rope(M, rope, k.cuda().view(600, n_kv, 128), v.cuda().view(600, n_kv, 128),
+                       row_start=_i32([0, 601, -5, 700]), q=q.cuda().view(600, n_q, 128),
+                       q_out=q_out.view(600, n_q, 128))
+    assert M.err.item() & kvq.KVQ_DEVERR_ROWS and M.seq_lens.tolist() == [0, 0, 0]
+
+
 def test_append_long_prompt_many_heads():
     """A prompt of several thousand rows with more query heads than one warp
     takes, q rotated in place."""
