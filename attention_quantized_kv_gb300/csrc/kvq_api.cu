@@ -56,12 +56,13 @@ int decode_append(const kvq_layer *layer, const kvq_rope *rope, const int32_t *p
   const kvq::DecodePlan pl = kvq::plan_decode(*layer, max_len, sms);
   if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
-  // Many sequences: their new rows are placed faster by a grid of their own
+  // Several sequences: their new rows are placed faster by a grid of their own
   // than by the split kernel's CTAs before their first copy, and the rotated
-  // queries wait in `out`, whose rows the merge kernel writes last.  500 / 4000
-  // f16 keys, 32 q / 8 kv heads: 16 sequences 21.1 -> 19.2 / 52.8 -> 53.2 us,
-  // 64 sequences 59.1 -> 49.4 / 180 -> 172 us; but 8 sequences 17.8 -> 17.1 /
-  // 32.8 -> 34.6 us and 2 sequences 11.7 -> 13.2 us.  Same bits either way.
+  // queries wait in `out`, whose rows the merge kernel writes last.  In the
+  // split kernel -> in two steps, 32 q / 8 kv heads, 500 and 4000 keys: 4
+  // sequences 13.0 -> 13.5 and 18.9 -> 19.0 us (f16), 14.3 -> 14.5 and 21.0 ->
+  // 20.9 us (q8_0); 8 sequences 17.8 -> 16.3 and 33.0 -> 33.8 us, 19.7 -> 17.4
+  // and 26.6 -> 25.2 us; 64 sequences 59.1 -> 49.3 and 180 -> 172 us.  Same bits.
   const int64_t d = kHeadDim, q_bytes = layer->n_seqs * (layer->n_q_heads * d * 2);
   const int64_t kv_bytes = layer->n_seqs * (layer->n_kv_heads * d * 2);
   if (rope && layer->n_seqs >= kvq::kSplitStepSeqs && aligned(q, 16) && aligned(k_new, 16) &&

@@ -79,7 +79,7 @@ cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32
 
 // Sequences from which a rotary decode step appends in a launch of its own
 // (kvq_api.cu: decode_append).
-constexpr int kSplitStepSeqs = 16;
+constexpr int kSplitStepSeqs = 8;
 constexpr int kShiftMaxSeqs = 65535;  // sequences of a key shift: a grid's second dimension
 
 inline int type_bytes(int type) { return type == KVQ_T_F32 ? 4 : 2; }

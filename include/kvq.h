@@ -511,7 +511,7 @@ KVQ_API int kv_rope_shift(const kvq_layer *layer, const kvq_rope *rope, const in
  * followed by attn_decode of q_out, bit for bit.  q, k_new, v_new: fp16 as
  * attn_decode_append takes them; positions NULL needs n_pos >= max_len
  * (KVQ_ECAPACITY).  A sequence already at capacity gets no new token
- * and attends its keys.  From 16 sequences on the append is a launch of its
+ * and attends its keys.  From 8 sequences on the append is a launch of its
  * own and `out` holds the rotated queries until the results replace them.
  * Everything else as attn_decode_append. */
 KVQ_API int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope,

@@ -405,7 +405,6 @@ def test_append_windows_device_conditions(ck, cv, rot):
     assert L.err.item() == kvq.KVQ_DEVERR_CAPACITY | kvq.KVQ_DEVERR_PAGE | kvq.KVQ_DEVERR_POS
     assert L.seq_lens.tolist() == [512, 430, 110]
     M, _ = _layer(3, n_kv, n_q, cap, ck, cv, True, 3)
-    before = [M.k_cache.clone(), M.v_cache.clone()]
     kvq.kv_append_rope(M, rope, k.cuda().view(600, n_kv, 128), v.cuda().view(600, n_kv, 128),
                        row_start=_i32([0, 601, -5, 700]), q=q.cuda().view(600, n_q, 128),
                        q_out=q_out.view(600, n_q, 128))
@@ -655,10 +654,10 @@ def test_decode_step_is_append_then_decode(ck, cv, paged):
     assert not ws[:65536].any()
 
 
-@pytest.mark.parametrize("n_seqs,ck,cv,paged", [(16, F16, Q8, True), (33, Q4, F16, False),
+@pytest.mark.parametrize("n_seqs,ck,cv,paged", [(8, F16, Q8, True), (33, Q4, F16, False),
                                                 (70, T4, T4, True)])
 def test_decode_step_of_many_sequences(n_seqs, ck, cv, paged):
-    """From 16 sequences on the step appends in a launch of its own: the bits
+    """From 8 sequences on the step appends in a launch of its own: the bits
     of a step that cannot (a query on an 8-byte boundary), in place too."""
     n_kv, n_q, cap = 2, 6, 512
     lens = [(s * 37) % 511 for s in range(n_seqs)]
