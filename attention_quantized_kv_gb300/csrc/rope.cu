@@ -79,12 +79,18 @@ __device__ __forceinline__ void cos_sin_turns(uint64_t u0, uint64_t u1, float2 &
 // step, modulo 2^64, so the running sum is exact.
 template <int P>
 __global__ void __launch_bounds__(kRopeThreads) table_kernel(const __grid_constant__ TableParams p) {
+  // (from shared memory: parameters indexed by lane are read one at a time)
+  __shared__ uint64_t turns[kD / 2];
+  if (threadIdx.x < p.pairs) turns[threadIdx.x] = p.turns[threadIdx.x];
+  __syncthreads();
   const int rows = kRopeThreads / p.cols;  // positions per block and pass
   const int col = threadIdx.x % p.cols, row = threadIdx.x / p.cols;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (row >= rows) return;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   int64_t pos = static_cast<int64_t>(blockIdx.x) * rows + row;
-  const uint64_t t0 = p.turns[col * P], t1 = p.turns[col * P + P - 1];
+  const uint64_t t0 = turns[col * P], t1 = turns[col * P + P - 1];
   const uint64_t d0 = t0 * static_cast<uint64_t>(step), d1 = t1 * static_cast<uint64_t>(step);
   uint64_t u0 = t0 * static_cast<uint64_t>(pos), u1 = t1 * static_cast<uint64_t>(pos);
   float *out = p.table + (pos * p.pairs + col * P) * 2;
@@ -180,22 +186,58 @@ struct DeltaParams {
   int capacity, max_evict;
 };
 
+// Of the block's n items, how many does the predicate hold for (it holds for a
+// first part of them), by probing them 256 at a time: one dependent load per
+// round, two rounds up to 65536 items.
+template <typename Pred>
+__device__ __forceinline__ int block_partition(int n, Pred pred) {
+  int lo = 0;
+  while (n > 0) {
+    const int step = (n + kRopeThreads - 1) / kRopeThreads, at = threadIdx.x * step;
+    const int k = __syncthreads_count(at < n && pred(lo + at));
+    if (k == 0) break;
+    if (step == 1) return lo + k;
+    lo += (k - 1) * step + 1;  // probe k - 1 holds; the answer lies before probe k
+    n = min(step - 1, n - (k - 1) * step - 1);
+  }
+  return lo;
+}
+
 // delta[s][w] = -(evicted tokens before the one that moves to w).  evict[j] - j
 // kept tokens lie before evicted token j, a non-decreasing count, so that
-// number is the count of j with evict[j] - j <= w: a binary search.
+// number is the count of j with evict[j] - j <= w.  A block takes 256
+// consecutive w: it finds the first of them together, keeps the next 256
+// counts in shared memory, and each thread searches those.  (A binary search
+// by each thread over 2048 evicted tokens is eleven dependent loads, 6 us.)
 __global__ void __launch_bounds__(kRopeThreads) delta_kernel(DeltaParams p) {
+  __shared__ int key[kRopeThreads];
   grid_dependency_wait();
+  grid_launch_dependents();
   const int s = blockIdx.y;
-  const int w = blockIdx.x * kRopeThreads + threadIdx.x;
+  const int w0 = blockIdx.x * kRopeThreads, w = w0 + threadIdx.x;
   const int len = min(p.seq_lens[s], p.capacity);
   const int n = max(0, min(p.n_evicted[s], p.max_evict));
-  if (w >= len - n) return;
+  if (w0 >= len - n) return;  // (the whole block)
   const int32_t *e = p.evict + static_cast<int64_t>(s) * p.max_evict;
-  int lo = 0, hi = n;
+  const int first = block_partition(n, [&](int j) { return e[j] - j < w0; });
+  const int m = min(kRopeThreads, n - first);
+  if (threadIdx.x < m) key[threadIdx.x] = e[first + threadIdx.x] - (first + threadIdx.x);
+  __syncthreads();
+  if (w >= len - n) return;
+  int lo = 0, hi = m;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (e[mid] - mid <= w) lo = mid + 1;
+    if (key[mid] <= w) lo = mid + 1;
     else hi = mid;
+  }
+  lo += first;
+  if (lo == first + kRopeThreads) {  // many evicted tokens in a row: search the rest
+    hi = n;
+    while (lo < hi) {
+      const int mid = lo + ((hi - lo) >> 1);
+      if (e[mid] - mid <= w) lo = mid + 1;
+      else hi = mid;
+    }
   }
   p.delta[static_cast<int64_t>(s) * p.capacity + w] = -lo;
 }
@@ -334,9 +376,8 @@ cudaError_t launch_rope_table(const double *freqs, int rot_dim, int n_pos, float
   const int rows = kRopeThreads / p.cols;
   const int64_t passes = (p.n_pos + rows - 1) / rows;
   const unsigned grid = static_cast<unsigned>(passes < kTableBlocks ? passes : kTableBlocks);
-  if (planes == 2) table_kernel<2><<<grid, kRopeThreads, 0, stream>>>(p);
-  else table_kernel<1><<<grid, kRopeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(planes == 2 ? table_kernel<2> : table_kernel<1>, dim3(grid),
+                    dim3(kRopeThreads), 0, stream, p);
 }
 
 cudaError_t launch_rope_apply(const kvq_rope &rope, const kvq_rows &x, const kvq_rows &y,

@@ -601,6 +601,27 @@ def test_delta():
         assert (got[s, len(left):] == 99).all()
 
 
+def test_delta_of_long_lists():
+    """Lists longer than a block takes at once: scattered, all in a row, at
+    both ends, and exactly a block's number of tokens."""
+    n, cap = 70000, 70144
+    rng = np.random.default_rng(14)
+    ev = [np.sort(rng.permutation(n)[:30000]), np.arange(1000, 3500), np.r_[0:700, n - 900:n],
+          np.sort(rng.permutation(n)[:256]), np.arange(5, 5 + 257), np.sort(rng.permutation(n)[:69999])]
+    L = kvq.KVLayer(len(ev), 1, 1, cap, Q4, Q4)
+    L.seq_lens.fill_(n)
+    e = np.zeros((len(ev), 70000), np.int32)
+    for s, row in enumerate(ev):
+        e[s, :len(row)] = row
+    delta = torch.full((len(ev), cap), 99, dtype=torch.int32, device="cuda")
+    kvq.kv_evict_delta(L, torch.from_numpy(e).cuda(), _i32([len(r) for r in ev]), delta)
+    got = delta.cpu().numpy()
+    for s in range(len(ev)):
+        left = np.setdiff1d(np.arange(n), ev[s])
+        assert (got[s, :len(left)] == np.arange(len(left)) - left).all()
+        assert (got[s, len(left):] == 99).all()
+
+
 # ------------------------------------------------------------------ decode step
 
 def _twin(L, table):
