@@ -2,6 +2,15 @@
 // the way: new keys are rotated in fp32 and encoded from there, values are
 // encoded as they come, and the queries of the same rows are rotated to fp16
 // beside them.
+//
+// One launch reads each value once and writes each code once.  Device times on
+// one GB300 against the bytes at the measured 6.78 TB/s: 32768 prompt tokens of
+// 32 q / 4 kv heads into f16 caches 109 us (0.93), K f16 / V q8_0 112 us (0.88),
+// q8_0 118 us (0.82), q4_0 127 us (0.74), turbo4 151 us (0.62): HBM bounds the
+// first, the encoders' instructions the last.  2048 tokens into q8_0 caches
+// 12.8 us (0.55) and a mixed batch of 1821 rows 14.5 us (0.54): two waves of
+// blocks, each a chain of dependent loads (row -> length -> page -> rows).  16
+// single tokens of 40 q / 8 kv heads 3.4 us, the same chain once.
 #include <cuda_runtime.h>
 
 #include "kvq_encode.cuh"

@@ -1,5 +1,8 @@
 // rope.cu -- rotary positions: the angle table, the rotation of rows, and the
 // re-rotation of cached keys after an eviction moved them.
+//
+// All three move bytes: what they cannot do without, at the measured copy rate
+// of 6.78 TB/s, is the floor of the figures below (device times on one GB300).
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -73,6 +76,11 @@ __device__ __forceinline__ void cos_sin_turns(uint64_t u0, uint64_t u1, float2 &
   second = place(q1, c.y, s.y);
 }
 
+// Writes 4 rot_dim bytes per position and reads nothing: 200704 positions x 64
+// planes 15.9 us, 0.95 of the floor (a thread per plane with 64-bit division
+// and conversion 92 us, with running sums 24 us); 32768 positions 4.3 us, of
+// which the launch is half.
+//
 // Thread (column, row lane): two planes of every (rows-per-pass)-th position
 // (P = 1, an odd number of planes: one plane of two such positions).  The
 // angle's fraction of a turn advances by a whole number of 2^-64 turns per
@@ -127,7 +135,10 @@ struct ApplyParams {
 constexpr int kAnyHeads = 8;  // heads per warp of the general kernel
 
 // One warp per (row, up to sixteen heads): the angles are read once, and all
-// the heads' values are requested before the first is used.
+// the heads' values are requested before the first is used (up to 4 KB per
+// warp in flight).  Bound by HBM: 8191 rows x 40 bf16 heads, 64 interleaved
+// dims, 27.4 us, 0.92 of the floor; by lanes of four values 31 us, with one
+// head at a time 51 us.  16 rows x 40 heads take 2.0 us, a launch's length.
 template <int TI, int TO>
 __global__ void __launch_bounds__(kRopeThreads) apply_kernel(const __grid_constant__ ApplyParams p) {
   grid_dependency_wait();
@@ -145,7 +156,8 @@ __global__ void __launch_bounds__(kRopeThreads) apply_kernel(const __grid_consta
       });
 }
 
-// Planes that eight lanes cannot hold: one head at a time, 4 values per lane.
+// Planes that eight lanes cannot hold: one head at a time, 4 values per lane,
+// eight heads requested at once.
 template <int TI, int TO>
 __global__ void __launch_bounds__(kRopeThreads)
     apply_any_kernel(const __grid_constant__ ApplyParams p) {
@@ -256,6 +268,12 @@ struct ShiftParams {
 // again and stored as they lay; rows that do not move keep their codes.  The
 // next head's unit is requested before the current one is worked on, and the
 // first beside the shifts, which in an eviction's wake are seldom all zero.
+//
+// 74k tokens x 8 heads in four sequences, the deltas (2.5 us) included: f16
+// 57 us, 0.78 of the floor, bound by the latency of the loads at the 16 warps
+// that 128 registers leave an SM (row by row 166 us, a head per warp 69 us,
+// eight heads per warp 61 us); q8_0 64 us, 4-bit 73 us, turbo4 139 us, bound by
+// instruction issue: 17, 20 and 50 instructions per value.
 constexpr int kShiftHeads = 4;
 
 template <int CODEC>
@@ -317,7 +335,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 }
 
 // Planes that cross lanes: one warp per (sequence, token), its K rows of every
-// kv head one by one.
+// kv head one by one (166 us where shift_units_kernel takes 57).
 __global__ void __launch_bounds__(kRopeThreads) shift_rows_kernel(ShiftParams p) {
   grid_dependency_wait();
   const int s = blockIdx.y, lane = threadIdx.x & 31;
