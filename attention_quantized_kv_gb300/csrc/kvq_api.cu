@@ -60,9 +60,9 @@ int decode_append(const kvq_layer *layer, const kvq_rope *rope, const int32_t *p
   // than by the split kernel's CTAs before their first copy, and the rotated
   // queries wait in `out`, whose rows the merge kernel writes last.  In the
   // split kernel -> in two steps, 32 q / 8 kv heads, 500 and 4000 keys: 4
-  // sequences 13.0 -> 13.5 and 18.9 -> 19.0 us (f16), 14.3 -> 14.5 and 21.0 ->
-  // 20.9 us (q8_0); 8 sequences 17.8 -> 16.3 and 33.0 -> 33.8 us, 19.7 -> 17.4
-  // and 26.6 -> 25.2 us; 64 sequences 59.1 -> 49.3 and 180 -> 172 us.  Same bits.
+  // sequences 13.0 -> 13.7 and 19.1 -> 19.0 us (f16), 14.3 -> 14.5 and 20.8 ->
+  // 20.9 us (q8_0); 8 sequences 17.8 -> 16.2 and 33.0 -> 33.4 us, 19.7 -> 17.3
+  // and 26.6 -> 25.1 us; 64 sequences 59.1 -> 49.3 and 180 -> 172 us.  Same bits.
   const int64_t d = kHeadDim, q_bytes = layer->n_seqs * (layer->n_q_heads * d * 2);
   const int64_t kv_bytes = layer->n_seqs * (layer->n_kv_heads * d * 2);
   if (rope && layer->n_seqs >= kvq::kSplitStepSeqs && aligned(q, 16) && aligned(k_new, 16) &&

@@ -60,8 +60,8 @@ def _rope(rot, layout, n_pos, magnitude=1.0, base=500000.0):
 
 # ------------------------------------------------------------------ table
 
-# The fraction of a turn is off by pos * 2^-65 + 2^-66 turns (below 2^-46 rad
-# here); its conversion to fp32 by half an ulp of at most pi / 4 rad, 0.79 *
+# The fraction of a turn is off by pos * 2^-65 turns (below 2^-42 rad up to
+# position 2^20); its conversion to fp32 by half an ulp of at most pi / 4 rad, 0.79 *
 # 2^-24; cos and sin by at most an ulp of a value up to 1, 2^-24; the
 # reference by 2^-50.  In all below 2^-23.
 TABLE_TOL = 2.0 ** -23
