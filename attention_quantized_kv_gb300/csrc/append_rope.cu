@@ -5,10 +5,10 @@
 //
 // One launch reads each value once and writes each code once.  Device times on
 // one GB300 against the bytes at the measured 6.78 TB/s: 32768 prompt tokens of
-// 32 q / 4 kv heads into f16 caches 109 us (0.93), K f16 / V q8_0 112 us (0.88),
-// q8_0 118 us (0.82), q4_0 127 us (0.74), turbo4 151 us (0.62): HBM bounds the
+// 32 q / 4 kv heads into f16 caches 106 us (0.96), K f16 / V q8_0 108 us (0.92),
+// q8_0 111 us (0.87), q4_0 118 us (0.80), turbo4 146 us (0.65): HBM bounds the
 // first, the encoders' instructions the last.  2048 tokens into q8_0 caches
-// 12.8 us (0.55) and a mixed batch of 1821 rows 14.5 us (0.54): two waves of
+// 13.0 us (0.54) and a mixed batch of 1821 rows 14.5 us (0.54): two waves of
 // blocks, each a chain of dependent loads (row -> length -> page -> rows).  16
 // single tokens of 40 q / 8 kv heads 3.4 us, the same chain once.
 #include <cuda_runtime.h>
@@ -706,10 +706,16 @@ __global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
   grid_launch_dependents();
   check_counts(p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // First every (window, kv head) of K, then of V, then the q rows: the blocks
-  // of an SM run mostly one of the three codes.
-  if (blockIdx.x < p.kv_blocks) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kArWarps + warp;
+  // Blocks of keys and values (first every (window, kv head) of K, then of V)
+  // alternate with blocks of q rows while there are both: the encoders'
+  // instructions and the q rows' bytes share an SM (32768 rows, q8_0: 111 us;
+  // all of K and V first 118, spread over the whole grid 116; 2048 rows 13.0,
+  // 12.8, 14.7 us).
+  const int64_t b = blockIdx.x, pairs = min(p.kv_blocks, static_cast<int64_t>(gridDim.x) - p.kv_blocks);
+  const bool kv = b < 2 * pairs ? b % 2 == 0 : b - pairs < p.kv_blocks;
+  const int64_t at = b < 2 * pairs ? b / 2 : kv ? b - pairs : b - p.kv_blocks;
+  if (kv) {
+    const int64_t item = at * kArWarps + warp;
     const int64_t per_side = (p.n_rows + kUnitTokens - 1) / kUnitTokens * p.n_kv;
     if (item >= 2 * per_side) return;
     uint8_t *mine = stage + warp * Stage<T>::kWarpBytes;
@@ -719,7 +725,7 @@ __global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
       window_item<T, 1>(p, (item - per_side) / p.n_kv * kUnitTokens,
                         static_cast<int>((item - per_side) % p.n_kv), mine, lane);
   } else {
-    const int64_t item = (static_cast<int64_t>(blockIdx.x) - p.kv_blocks) * kArWarps + warp;
+    const int64_t item = at * kArWarps + warp;
     const int64_t row = item / p.q_chunks;
     if (row >= p.n_rows) return;
     if (p.eight) q_item<T>(p, row, static_cast<int>(item % p.q_chunks), lane);
@@ -727,7 +733,6 @@ __global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
   }
 }
 
-// Heads per item of q: 16 (8 of fp32) where eight lanes hold a row.
 template <int T>
 void set_q_items(AppendRopeParams &p, int hpw) {
   p.q_hpw = hpw;
