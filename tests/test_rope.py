@@ -166,7 +166,7 @@ def test_table_refusals():
     assert call(f, 130, 16, 0x1000, None) == EINVAL
     assert call(f, 128, 0, 0x1000, None) == EINVAL
     assert call(f, 128, 16, 0x1008, None) == EALIGN
-    for bad in (-1e-9, 6.2831853072, math.nan, math.inf):
+    for bad in (-1e-9, 6.28318531, math.nan, math.inf):
         f[63] = bad
         assert call(f, 128, 16, 0x1000, None) == EINVAL, bad
 
