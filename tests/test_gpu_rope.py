@@ -720,6 +720,23 @@ def test_decode_step_odd_pointers():
     assert torch.equal(out, ref) and torch.equal(L.k_cache, M.k_cache)
 
 
+@pytest.mark.parametrize("n_seqs", [3, 9])
+def test_decode_step_every_pointer_odd(n_seqs):
+    """q, out, k and v on 8-byte boundaries, few sequences and several."""
+    lens = [(300 * s + 17) % 512 for s in range(n_seqs)]
+    L, table = _random_layer(n_seqs, 2, 8, 512, F16, Q8, False, lens, 4)
+    M = _twin(L, table)
+    rope, _ = _rope(128, R.HALF, 512)
+    ws = torch.zeros(kvq.attn_decode_workspace(L, 512), dtype=torch.uint8, device="cuda")
+    q, k, v, out = (torch.randn(n_seqs * h * 128 + 4, device="cuda").half()[4:].view(n_seqs, h, 128)
+                    for h in (8, 2, 2, 8))
+    ref = torch.empty((n_seqs, 8, 128), device="cuda").half()
+    kvq.attn_decode_append_rope(L, rope, k, v, q, SCALE, out, None, 512, ws)
+    kvq.attn_decode_append_rope(M, rope, k.clone(), v.clone(), q.clone(), SCALE, ref, None, 512, ws)
+    assert torch.equal(out, ref) and torch.equal(L.k_cache, M.k_cache)
+    assert torch.equal(L.v_cache, M.v_cache) and L.seq_lens.tolist() == [n + 1 for n in lens]
+
+
 def test_decode_step_against_the_oracle():
     """fp64 attention over the cache's own decoded rows, by the rotated query."""
     lens = [1500, 40]
