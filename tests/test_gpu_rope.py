@@ -622,6 +622,40 @@ def test_delta_of_long_lists():
         assert (got[s, len(left):] == 99).all()
 
 
+@pytest.mark.parametrize("layout", [R.INTERLEAVED, R.HALF])
+@pytest.mark.parametrize("rot", [40, 128])
+def test_append_and_shift_against_64_bits(layout, rot):
+    """f16 keys against the fp64 rotation by exact angles.  A key is rounded to
+    fp16 once (half a step, 2^-11 of it, 2^-25 below 2^-14) after a rotation
+    that is off by (|a| + |b|)(2^-23 + 3 * 2^-24), as in the rows' test."""
+    n, cap, at = 700, 1024, 300
+    freqs = kvq.kvq_rope_freqs(rot, 10000.0)
+    rope = kvq.Rope(n_pos=2048, rot_dim=rot, layout=layout)
+    L, _ = _layer(1, 2, 32, cap, F16, F16, False, 0, fill=0)
+    L.seq_lens.fill_(at)
+    x = torch.randn((n, 2, 128), device="cuda").half()
+    q = torch.zeros((n, 32, 128), dtype=torch.float16, device="cuda")
+    kvq.kv_append_rope(L, rope, x, x, row_start=_i32([0, n]), q=q, q_out=q)
+
+    def keys():
+        c = L.k_cache.cpu().numpy()
+        return np.stack([oracle.dequant_stream(F16, 0, c, 2, cap, 0, h, at + n)[at:] for h in (0, 1)], 1)
+
+    def check(x64, pos, transpose=False):
+        c, s = R.angles64(freqs, pos)
+        ref = R.rotate(x64, np.stack([c, s], -1), rot, layout, transpose=transpose)
+        size = np.zeros_like(ref)
+        a, b = R.planes(rot, layout)
+        size[..., a] = size[..., b] = np.abs(x64[..., a]) + np.abs(x64[..., b])
+        got = keys()
+        assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -11 + size * 6 * 2.0 ** -24 + 2.0 ** -25).all()
+        return got
+
+    got = check(x.double().cpu().numpy(), np.arange(at, at + n))
+    kvq.kv_rope_shift(L, rope, torch.full((1, cap), -977, dtype=torch.int32, device="cuda"))
+    check(got, np.full(n, 977), transpose=True)
+
+
 # ------------------------------------------------------------------ decode step
 
 def _twin(L, table):
@@ -956,3 +990,43 @@ def test_captured_and_on_another_stream():
     assert torch.equal(L.k_cache, M.k_cache) and torch.equal(L.v_cache, M.v_cache)
     for a, b in zip(outs[id(L)], outs[id(M)]):
         assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Appends and decode steps of two layers issued in turn on two streams,
+    with nothing between them, against the same calls one after the other."""
+    rope = kvq.Rope(n_pos=1024)
+    layers = [_random_layer(2, 2, 8, 1024, Q8, F16, i == 1, [400, 33], 50 + i) for i in range(2)]
+    pairs = [(L, _twin(L, t)) for L, t in layers]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xs = [torch.randn((90, 12, 128), generator=g, device="cuda").half() for _ in range(2)]
+    start = _i32([0, 60, 90])
+
+    def calls(L, x, ws, res):
+        q, k, v = x.split([8, 2, 2], dim=1)
+        kvq.kv_append_rope(L, rope, k, v, row_start=start, q=q, q_out=res[0])
+        kvq.attn_decode_append_rope(L, rope, k[:2].contiguous(), v[:2].contiguous(), q[:2].contiguous(),
+                                    SCALE, res[1], res[2], 1024, ws)
+
+    def room(L):
+        return (torch.zeros(kvq.attn_decode_workspace(L, 1024), dtype=torch.uint8, device="cuda"),
+                (torch.empty((90, 8, 128), dtype=torch.float16, device="cuda"),
+                 torch.empty((2, 8, 128), dtype=torch.float16, device="cuda"),
+                 torch.empty((2, 8), device="cuda")))
+
+    rooms = [[room(L) for L in p] for p in pairs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                calls(pairs[i][0], xs[i], *rooms[i][0])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for _ in range(6):
+            calls(pairs[i][1], xs[i], *rooms[i][1])
+        a, b = pairs[i]
+        assert a.seq_lens.tolist() == b.seq_lens.tolist() == [400 + 6 * 61, 33 + 6 * 31]
+        assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.v_cache, b.v_cache)
+        for t, u in zip(rooms[i][0][1], rooms[i][1][1]):
+            assert torch.equal(t, u)
