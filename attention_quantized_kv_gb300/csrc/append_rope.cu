@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(kArThreads)
 // window's warp places the rows of every unit whose first new row lies in the
 // window: no other warp writes that unit, so an incomplete one with enough new
 // rows is put together over its old bytes; rows of others are stored one by
-// one.  K rows whose planes cross lanes take the same way.
+// one.
 
-// A staged row: the input's 128 values, replaced by 128 fp16 values, or by 128
-// one-byte codes and the block scales (4, or 1 for turbo4) behind them.
+// A staged row: the input's 128 values, replaced (but for f16) by 128 one-byte
+// codes and the block scales (4, or 1 for turbo4) behind them.
 template <int T>
 struct Stage {
   static constexpr int S = sizeof(typename RowType<T>::type);
@@ -301,36 +301,23 @@ __device__ __forceinline__ void stage_rows(uint8_t *stage, const uint8_t *x, int
   __syncwarp();
 }
 
-// Encode the staged row at `row` in place.
-__device__ __forceinline__ void encode_staged(int codec, const float (&x)[4], uint8_t *row,
-                                              int lane) {
-  if (codec == KVQ_F16) {
-    store4<KVQ_T_F16>(row + 8 * lane, x);
-    return;
-  }
+// Encode the staged row at `row`, of which the lane holds x, in place (turbo4).
+__device__ __forceinline__ void encode_staged_turbo4(const float (&x)[4], uint8_t *row, int lane) {
   int q[4];
   __half d16;
-  if (codec == KVQ_Q8_0) encode_q8(x, q, d16);
-  else if (codec == KVQ_Q4_0) encode_q4(x, lane, q, d16);
-  else encode_turbo4(x, lane, q, d16);
+  encode_turbo4(x, lane, q, d16);
   reinterpret_cast<uint32_t *>(row)[lane] = (q[0] & 0xff) | ((q[1] & 0xff) << 8) |
                                             ((q[2] & 0xff) << 16) |
                                             (static_cast<uint32_t>(q[3] & 0xff) << 24);
-  __half *scales = reinterpret_cast<__half *>(row + kScaleAt);
-  if (codec == KVQ_TURBO4) {
-    if (lane == 0) scales[0] = d16;
-  } else if ((lane & 7) == 0) {
-    scales[lane >> 3] = d16;
-  }
+  if (lane == 0) *reinterpret_cast<__half *>(row + kScaleAt) = d16;
 }
 
-// Store a staged row's codes as token row r of a unit.  An f16 side's row of V
-// is still the input's values, of type T (K: T = KVQ_T_F16, what its rotation
-// left).
-template <int T, int SIDE>
+// Store a staged row as token row r of a unit of V (f16: the input's values, of
+// type T, still).
+template <int T>
 __device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint8_t *unit, int r,
                                              int lane) {
-  if (SIDE == 1 && codec == KVQ_F16) {
+  if (codec == KVQ_F16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const auto v = reinterpret_cast<const typename RowType<T>::type *>(row)[32 * j + lane];
@@ -339,144 +326,89 @@ __device__ __forceinline__ void store_staged(int codec, const uint8_t *row, uint
     }
     return;
   }
-  uint2 raw = make_uint2(0u, 0u);
-  int q[4] = {0, 0, 0, 0};
-  __half d16 = __float2half_rn(0.0f);
-  if (codec == KVQ_F16) {
-    raw = reinterpret_cast<const uint2 *>(row)[lane];  // (K: T is KVQ_T_F16)
-  } else {
-    const uint32_t w = reinterpret_cast<const uint32_t *>(row)[lane];
+  const uint32_t w = reinterpret_cast<const uint32_t *>(row)[lane];
+  int q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = (w >> (8 * i)) & 0xff;
-    d16 = reinterpret_cast<const __half *>(row + kScaleAt)[codec == KVQ_TURBO4 ? 0 : lane >> 3];
-  }
-  store_row<SIDE>(codec, unit, r, lane, raw, q, d16);
+  for (int i = 0; i < 4; ++i) q[i] = (w >> (8 * i)) & 0xff;
+  const __half d16 =
+      reinterpret_cast<const __half *>(row + kScaleAt)[codec == KVQ_TURBO4 ? 0 : lane >> 3];
+  store_row<1>(codec, unit, r, lane, make_uint2(0u, 0u), q, d16);
 }
 
-// The bytes of a unit's chunk c that belong to the token rows of the mask.
-template <int SIDE>
+// The bytes of a V unit's chunk c that belong to the token rows of the mask.
 __device__ __forceinline__ uint4 chunk_mask(int codec, int c, unsigned rows) {
   const int data = codec == KVQ_F16 ? 256 : codec == KVQ_Q8_0 ? 128 : 64, k = c - data;
-  const int lo = c & 3, g = (c >> 2) & 7;
+  const int tig = c & 3;
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    int ra, rb;  // token rows of the word's halves
-    if (c < data) {
-      if (SIDE == 0) {
-        const int rh = codec == KVQ_F16 ? (c >> 5) & 1 : codec == KVQ_Q8_0 ? i >> 1 : i & 1;
-        ra = rb = g + 8 * rh;
-      } else {
-        ra = 2 * lo + 8 * (codec == KVQ_F16 ? i >> 1 : i & 1);
-        rb = ra + 1;
-      }
-    } else if (codec == KVQ_TURBO4) {
-      ra = SIDE == 0 ? 4 * k + i : 2 * (2 * k + (i >> 1)) + 8 * (i & 1);
-      rb = SIDE == 0 ? ra + 8 : ra + 1;
-    } else {
-      ra = SIDE == 0 ? k + 8 * (i >> 1) : 2 * (k >> 1) + 8 * (i & 1);
-      rb = SIDE == 0 ? ra : ra + 1;
-    }
-    if (SIDE == 1 && c < data && nibble_codec(codec)) {  // byte par * 2 + rh
+    if (c < data && nibble_codec(codec)) {  // byte par * 2 + rh: row 2 tig + par + 8 rh
       o[i] = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b)
-        if ((rows >> (2 * lo + (b >> 1) + 8 * (b & 1))) & 1u) o[i] |= 0xffu << (8 * b);
-    } else {
-      o[i] = ((rows >> ra) & 1u ? 0x0000ffffu : 0u) | ((rows >> rb) & 1u ? 0xffff0000u : 0u);
+        if ((rows >> (2 * tig + (b >> 1) + 8 * (b & 1))) & 1u) o[i] |= 0xffu << (8 * b);
+    } else {  // halves par of rows 2 tig + par + 8 rh
+      const int r = c < data              ? 2 * tig + 8 * (codec == KVQ_F16 ? i >> 1 : i & 1)
+                    : codec == KVQ_TURBO4 ? 2 * (2 * k + (i >> 1)) + 8 * (i & 1)
+                                          : 2 * (k >> 1) + 8 * (i & 1);
+      o[i] = ((rows >> r) & 1u ? 0x0000ffffu : 0u) | ((rows >> (r + 1)) & 1u ? 0xffff0000u : 0u);
     }
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 16 bytes of the unit, chunk c, from the staged rows (row r at s + r * PITCH):
-// the inverse of the placement formulas of include/kvq.h.
-// (T as in store_staged.)
-template <int T, int SIDE, int PITCH>
+// 16 bytes of a V unit, chunk c, from the staged rows: the inverse of the
+// placement formulas of include/kvq.h.
+template <int T>
 __device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) {
-  auto w32 = [&](int r, int byte) {
-    return *reinterpret_cast<const uint32_t *>(s + r * PITCH + byte);
-  };
+  constexpr int kPitch = Stage<T>::kPitch;
   auto w16 = [&](int r, int byte) -> uint32_t {
-    return *reinterpret_cast<const uint16_t *>(s + r * PITCH + byte);
+    return *reinterpret_cast<const uint16_t *>(s + r * kPitch + byte);
   };
   uint32_t o[4];
-  const int lo = c & 3, g = (c >> 2) & 7, hi = c >> 5;  // (w or tig, row g or gq, block piece)
-  if (codec == KVQ_F16) {
-    if (SIDE == 0) {  // hi = 2b + rh: row g + 8rh, dims 32b + 4w .. and 32b + 16 + 4w ..
-      const uint8_t *row = s + (g + 8 * (hi & 1)) * PITCH + (hi >> 1) * 64 + lo * 8;
-      const uint2 a = *reinterpret_cast<const uint2 *>(row);
-      const uint2 b = *reinterpret_cast<const uint2 *>(row + 32);
-      return make_uint4(a.x, a.y, b.x, b.y);
-    }
-    // hi = mt: dims 16 mt + 2 gq, + 1 of rows 2 tig + par + 8 rh
+  const int tig = c & 3, gq = (c >> 2) & 7, hi = c >> 5;
+  if (codec == KVQ_F16) {  // hi = mt: dims 16 mt + 2 gq, + 1 of rows 2 tig + par + 8 rh
 #pragma unroll
     for (int rh = 0; rh < 2; ++rh) {
-      uint32_t a, b;
-      const int d = (16 * hi + 2 * g) * Stage<T>::S;
-      if (T == KVQ_T_F32) {
-        const float2 x = *reinterpret_cast<const float2 *>(s + (2 * lo + 8 * rh) * PITCH + d);
-        const float2 y = *reinterpret_cast<const float2 *>(s + (2 * lo + 1 + 8 * rh) * PITCH + d);
-        a = pack_half2(x.x, x.y);
-        b = pack_half2(y.x, y.y);
-      } else {
-        a = w32(2 * lo + 8 * rh, d);
-        b = w32(2 * lo + 1 + 8 * rh, d);
-        if (T == KVQ_T_BF16) {
-          a = pack_half2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
-          b = pack_half2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+      uint32_t h[2];  // par: the row's two values as fp16
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const uint8_t *at = s + (2 * tig + par + 8 * rh) * kPitch + (16 * hi + 2 * gq) * Stage<T>::S;
+        if (T == KVQ_T_F32) {
+          const float2 x = *reinterpret_cast<const float2 *>(at);
+          h[par] = pack_half2(x.x, x.y);
+        } else {
+          h[par] = *reinterpret_cast<const uint32_t *>(at);
+          if (T == KVQ_T_BF16)
+            h[par] = pack_half2(__uint_as_float(h[par] << 16), __uint_as_float(h[par] & 0xffff0000u));
         }
       }
-      o[2 * rh] = __byte_perm(a, b, 0x5410);
-      o[2 * rh + 1] = __byte_perm(a, b, 0x7632);
+      o[2 * rh] = __byte_perm(h[0], h[1], 0x5410);
+      o[2 * rh + 1] = __byte_perm(h[0], h[1], 0x7632);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
   }
   const int data = codec == KVQ_Q8_0 ? 128 : 64;  // chunks of codes, then of scales
-  if (c >= data) {
-    const int k = c - data;
-    if (codec == KVQ_TURBO4) {  // one scale per row, 8 rows per chunk
+  const int k = c - data;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ra = SIDE == 0 ? 4 * k + i : 2 * (2 * k + (i >> 1)) + 8 * (i & 1);
-        const int rb = SIDE == 0 ? ra + 8 : ra + 1;
-        o[i] = w16(ra, kScaleAt) | (w16(rb, kScaleAt) << 16);
-      }
-    } else if (SIDE == 0) {  // rows k and k + 8, blocks 0..3
-      o[0] = w32(k, kScaleAt); o[1] = w32(k, kScaleAt + 4);
-      o[2] = w32(k + 8, kScaleAt); o[3] = w32(k + 8, kScaleAt + 4);
-    } else {  // tig = k / 2, blocks 2 (k % 2), + 1; rh; par
+  for (int i = 0; i < 4; ++i) {
+    if (c >= data) {
+      // turbo4: one scale per row, tig 2k and 2k + 1; else tig = k / 2, blocks
+      // 2 (k % 2) and + 1; rh; par
+      const int r = (codec == KVQ_TURBO4 ? 2 * (2 * k + (i >> 1)) : 2 * (k >> 1)) + 8 * (i & 1);
+      const int at = kScaleAt + (codec == KVQ_TURBO4 ? 0 : 2 * (2 * (k & 1) + (i >> 1)));
+      o[i] = w16(r, at) | (w16(r + 1, at) << 16);
+    } else if (codec == KVQ_Q8_0) {  // (mt & 1, rh): dims 32 hi + 16 (mt & 1) + 2 gq, + 1
+      const int d = 32 * hi + 16 * (i >> 1) + 2 * gq, r = 2 * tig + 8 * (i & 1);
+      o[i] = w16(r, d) | (w16(r + 1, d) << 16);
+    } else {  // mt = 4 hi + i: byte par * 2 + rh, levels of dims d low, d + 16 high
+      const int mt = 4 * hi + i, d = 32 * (mt >> 1) + 8 * (mt & 1) + gq;
+      o[i] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = 2 * (k & 1) + (i >> 1), r = 2 * (k >> 1) + 8 * (i & 1);
-        o[i] = w16(r, kScaleAt + 2 * b) | (w16(r + 1, kScaleAt + 2 * b) << 16);
-      }
-    }
-  } else if (codec == KVQ_Q8_0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (SIDE == 0) {  // (rh, h): dims 32b + 16h + 4w ..
-        o[i] = w32(g + 8 * (i >> 1), 32 * hi + 16 * (i & 1) + 4 * lo);
-      } else {  // (mt & 1, rh): dims 32 hi + 16 (mt & 1) + 2 gq, + 1
-        const int d = 32 * hi + 16 * (i >> 1) + 2 * g, r = 2 * lo + 8 * (i & 1);
-        o[i] = w16(r, d) | (w16(r + 1, d) << 16);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (SIDE == 0) {  // (b & 1, rh): levels of dims 4w .. low, 16 + 4w .. high
-        const int r = g + 8 * (i & 1), d = 32 * (2 * hi + (i >> 1)) + 4 * lo;
-        o[i] = w32(r, d) | (w32(r, d + 16) << 4);
-      } else {  // mt = 4 hi + i: byte par * 2 + rh, levels of dims d low, d + 16 high
-        const int mt = 4 * hi + i, d = 32 * (mt >> 1) + 8 * (mt & 1) + g;
-        o[i] = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint8_t *row = s + (2 * lo + (b >> 1) + 8 * (b & 1)) * PITCH;
-          // (a slot without a row holds anything: it must not reach other bytes)
-          o[i] |= ((row[d] | (static_cast<uint32_t>(row[d + 16]) << 4)) & 0xffu) << (8 * b);
-        }
+      for (int b = 0; b < 4; ++b) {
+        const uint8_t *row = s + (2 * tig + (b >> 1) + 8 * (b & 1)) * kPitch;
+        // (a slot without a row holds anything: it must not reach other bytes)
+        o[i] |= ((row[d] | (static_cast<uint32_t>(row[d + 16]) << 4)) & 0xffu) << (8 * b);
       }
     }
   }
@@ -551,7 +483,8 @@ __device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
 // and row there.
 template <int T, int CODEC>
 __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uint8_t *x,
-                                            int64_t pos, int64_t unit, int r, int lane) {
+                                            int64_t pos, int64_t unit, int r, float *copy,
+                                            int lane) {
   using Raw = typename RowType<T>::raw4;
   constexpr int S = Stage<T>::S;
   const int g = lane >> 2, w = lane & 3;
@@ -580,7 +513,8 @@ __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uin
 #pragma unroll
     for (int c = 0; c < 8; ++c) load4<T>(&raw[rh][c], v[c]);
     const float *row = at[rh] >= 0 ? rope_row(p.rope, ps[rh], p.err) : p.rope.table;
-    quad_rotate<false>(p.rope, p.kind, row, w, 1.0f, v);
+    if (p.kind == kQuadAny) quad_rotate_any<false>(p.rope, row, lane, 1.0f, copy, v);
+    else quad_rotate<false>(p.rope, p.kind, row, w, 1.0f, v);
     quad_encode<CODEC>(v, w, q[rh]);
   }
   uint8_t *const cache = p.cache[0];
@@ -594,36 +528,54 @@ __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uin
   }
 }
 
-template <int T, int SIDE>
-__device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r0, int h,
-                                            uint8_t *stage, int lane) {
-  constexpr int which = SIDE + 1, kPitch = Stage<T>::kPitch, S = Stage<T>::S;
-  constexpr int TS = SIDE == 0 ? static_cast<int>(KVQ_T_F16) : T;  // f16 rows in the stage
-  const int codec = p.codec[SIDE];
-  const uint8_t *x = p.x[which] + r0 * p.row[which] + h * p.head[which];
-  // lane j: row r0 + j (the new rows of a unit whose first lies in the window
-  // end within 31 rows)
+// Lane j's row r0 + j of a window: its sequence's new rows n, its index i among
+// them, its position, its unit of kv head 0 (lanes below 16; -1: no place) and
+// its row there.  (The new rows of a unit whose first lies in the window end
+// within 31 rows.)
+struct WindowRow {
+  int64_t pos = 0, unit = -1;
+  int i = 0, n = 0, r = 0;
+};
+__device__ __forceinline__ WindowRow window_row(const AppendRopeParams &p, int64_t r0, int lane) {
+  WindowRow w;
   const int64_t row = r0 + lane;
-  int s = 0, i = 0, n = 0;
-  int64_t slot = 0, unit = -1, pos = 0;
-  if (row < p.n_rows && find_row(p, row, s, i, n)) {
-    slot = static_cast<int64_t>(p.seq_lens[s]) + i;
-    pos = p.positions ? p.positions[row] : slot;
-    if (lane < kUnitTokens) unit = unit_of(p, s, slot);
+  int s = 0;
+  if (row < p.n_rows && find_row(p, row, s, w.i, w.n)) {
+    const int64_t slot = static_cast<int64_t>(p.seq_lens[s]) + w.i;
+    w.pos = p.positions ? p.positions[row] : slot;
+    w.r = static_cast<int>(slot & (kUnitTokens - 1));
+    if (lane < kUnitTokens) w.unit = unit_of(p, s, slot);
   }
-  const int r = static_cast<int>(slot & (kUnitTokens - 1));
-  if (unit >= 0) unit += h * unit_step(p);
+  return w;
+}
 
-  if (SIDE == 0 && p.kind != kQuadNone) {
-    if (lane >= kUnitTokens) unit = -1;
-    if (codec == KVQ_F16) quad_window<T, KVQ_F16>(p, x, pos, unit, r, lane);
-    else if (codec == KVQ_Q8_0) quad_window<T, KVQ_Q8_0>(p, x, pos, unit, r, lane);
-    else if (codec == KVQ_Q4_0) quad_window<T, KVQ_Q4_0>(p, x, pos, unit, r, lane);
-    else quad_window<T, KVQ_TURBO4>(p, x, pos, unit, r, lane);
-    return;
+template <int T>
+__device__ __forceinline__ void k_window(const AppendRopeParams &p, int64_t r0, int h,
+                                         uint8_t *stage, int lane) {
+  static_assert(Stage<T>::kWarpBytes >= kQuadBytes, "the quads' copy takes the stage's place");
+  const WindowRow w = window_row(p, r0, lane);
+  const uint8_t *x = p.x[1] + r0 * p.row[1] + h * p.head[1];
+  const int64_t unit = w.unit < 0 ? -1 : w.unit + h * unit_step(p);
+  float *copy = reinterpret_cast<float *>(stage);
+  switch (p.codec[0]) {
+    case KVQ_F16: quad_window<T, KVQ_F16>(p, x, w.pos, unit, w.r, copy, lane); break;
+    case KVQ_Q8_0: quad_window<T, KVQ_Q8_0>(p, x, w.pos, unit, w.r, copy, lane); break;
+    case KVQ_Q4_0: quad_window<T, KVQ_Q4_0>(p, x, w.pos, unit, w.r, copy, lane); break;
+    default: quad_window<T, KVQ_TURBO4>(p, x, w.pos, unit, w.r, copy, lane); break;
   }
+}
+
+template <int T>
+__device__ __forceinline__ void v_window(const AppendRopeParams &p, int64_t r0, int h,
+                                         uint8_t *stage, int lane) {
+  constexpr int kPitch = Stage<T>::kPitch, S = Stage<T>::S;
+  const int codec = p.codec[1];
+  const WindowRow w = window_row(p, r0, lane);
+  const uint8_t *x = p.x[2] + r0 * p.row[2] + h * p.head[2];
+  const int64_t unit = w.unit < 0 ? -1 : w.unit + h * unit_step(p);
+  const int r = w.r;
   // The new rows of this row's unit: how many, and whether this is the first.
-  const int before = min(r, i), count = before + min(kUnitTokens - r, n - i);
+  const int before = min(r, w.i), count = before + min(kUnitTokens - r, w.n - w.i);
   const unsigned few = __ballot_sync(0xffffffffu, unit >= 0 && count < kGroupRows);
   unsigned first = __ballot_sync(0xffffffffu, unit >= 0 && before == 0 && count >= kGroupRows);
   // Stage slots: token rows of a unit, or (few) rows of the window.
@@ -636,37 +588,32 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
     uint4 *dst = nullptr;
     if (group) {
       first &= first - 1;
-      dst = reinterpret_cast<uint4 *>(p.cache[SIDE] +
+      dst = reinterpret_cast<uint4 *>(p.cache[1] +
                                       __shfl_sync(0xffffffffu, unit, j0) * unit_bytes(codec));
       // an incomplete unit's old bytes, asked for beside the rows
       if (slots != (1u << kUnitTokens) - 1 && lane * 128 < unit_bytes(codec))
         asm volatile("prefetch.global.L1 [%0];\n" ::"l"(reinterpret_cast<uint8_t *>(dst) + lane * 128));
     }
-    stage_rows<T>(stage, x + (j0 - k0) * p.row[which], p.row[which], slots, lane);
-    if (SIDE == 1 && codec == KVQ_Q8_0) {
+    stage_rows<T>(stage, x + (j0 - k0) * p.row[2], p.row[2], slots, lane);
+    if (codec == KVQ_Q8_0) {
       encode_staged_blocks<T, KVQ_Q8_0>(stage, lane);
-    } else if (SIDE == 1 && codec == KVQ_Q4_0) {
+    } else if (codec == KVQ_Q4_0) {
       encode_staged_blocks<T, KVQ_Q4_0>(stage, lane);
-    } else if (SIDE == 0 || codec != KVQ_F16) {  // (f16 V: converted on the way out)
+    } else if (codec == KVQ_TURBO4) {  // (f16: converted on the way out)
 #pragma unroll 1
       for (unsigned m = slots; m; m &= m - 1) {
-        const int k = __ffs(m) - 1;
+        uint8_t *row = stage + (__ffs(m) - 1) * kPitch;
         float v[4];
-        load4<T>(stage + k * kPitch + 4 * lane * S, v);
-        if (SIDE == 0) {
-          const float *row = rope_row(p.rope, __shfl_sync(0xffffffffu, pos, j0 + k - k0), p.err);
-          rotate_lane(p.rope, lane_angles(p.rope, row, lane), lane, v);
-        }
+        load4<T>(row + 4 * lane * S, v);
         __syncwarp();  // every lane has read its part before the codes replace it
-        encode_staged(codec, v, stage + k * kPitch, lane);
+        encode_staged_turbo4(v, row, lane);
       }
     }
     __syncwarp();
     if (group) {
       const int chunks = unit_bytes(codec) / 16;
       if (slots == (1u << kUnitTokens) - 1) {
-        for (int c = lane; c < chunks; c += 32)
-          dst[c] = unit_chunk<TS, SIDE, kPitch>(codec, stage, c);
+        for (int c = lane; c < chunks; c += 32) dst[c] = unit_chunk<T>(codec, stage, c);
       } else {
         constexpr int kAhead = 4;  // old pieces requested at once
         for (int c0 = lane; c0 < chunks; c0 += 32 * kAhead) {
@@ -678,8 +625,8 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
           for (int i = 0; i < kAhead; ++i) {
             const int c = c0 + 32 * i;
             if (c >= chunks) break;
-            const uint4 m = chunk_mask<SIDE>(codec, c, slots), b = old[i];
-            const uint4 a = unit_chunk<TS, SIDE, kPitch>(codec, stage, c);
+            const uint4 m = chunk_mask(codec, c, slots), b = old[i];
+            const uint4 a = unit_chunk<T>(codec, stage, c);
             dst[c] = make_uint4((a.x & m.x) | (b.x & ~m.x), (a.y & m.y) | (b.y & ~m.y),
                                 (a.z & m.z) | (b.z & ~m.z), (a.w & m.w) | (b.w & ~m.w));
           }
@@ -689,9 +636,9 @@ __device__ __forceinline__ void window_item(const AppendRopeParams &p, int64_t r
 #pragma unroll 1
       for (unsigned m = slots; m; m &= m - 1) {
         const int k = __ffs(m) - 1;
-        store_staged<TS, SIDE>(codec, stage + k * kPitch,
-                           p.cache[SIDE] + __shfl_sync(0xffffffffu, unit, k) * unit_bytes(codec),
-                           __shfl_sync(0xffffffffu, r, k), lane);
+        store_staged<T>(codec, stage + k * kPitch,
+                        p.cache[1] + __shfl_sync(0xffffffffu, unit, k) * unit_bytes(codec),
+                        __shfl_sync(0xffffffffu, r, k), lane);
       }
     }
     __syncwarp();  // the slots are free again
@@ -720,10 +667,10 @@ __global__ void __launch_bounds__(kArThreads, T == KVQ_T_F32 ? 2 : 3)
     if (item >= 2 * per_side) return;
     uint8_t *mine = stage + warp * Stage<T>::kWarpBytes;
     if (item < per_side)
-      window_item<T, 0>(p, item / p.n_kv * kUnitTokens, static_cast<int>(item % p.n_kv), mine, lane);
+      k_window<T>(p, item / p.n_kv * kUnitTokens, static_cast<int>(item % p.n_kv), mine, lane);
     else
-      window_item<T, 1>(p, (item - per_side) / p.n_kv * kUnitTokens,
-                        static_cast<int>((item - per_side) % p.n_kv), mine, lane);
+      v_window<T>(p, (item - per_side) / p.n_kv * kUnitTokens,
+                  static_cast<int>((item - per_side) % p.n_kv), mine, lane);
   } else {
     const int64_t item = at * kArWarps + warp;
     const int64_t row = item / p.q_chunks;

@@ -249,91 +249,6 @@ __device__ __forceinline__ void store_row(int codec, uint8_t *unit, int r, int l
   }
 }
 
-// Read one row (token row r of `unit`) into the lane-held form of store_row:
-// lane l gets dims 4l..4l+3 as fp32, the decoded values x^ = d16 * q (q8_0),
-// d16 * (n - 8) (q4_0), s * H (d16 * (n - 8)) / 16 (turbo4) or the fp16
-// values, all exact in fp32.
-template <int SIDE>
-__device__ __forceinline__ void load_row(int codec, const uint8_t *unit, int r, int lane,
-                                         float (&x)[4]) {
-  const int g = r & 7, rh = r >> 3, tig = (r & 7) >> 1, par = r & 1;
-  const int b = lane >> 3, lb = lane & 7;
-  if (codec == KVQ_F16) {
-    if (SIDE == 0) {
-      const int h = (lane >> 2) & 1, w = lane & 3;
-      const uint2 raw =
-          *reinterpret_cast<const uint2 *>(unit + (2 * b + rh) * 512 + (4 * g + w) * 16 + h * 8);
-      const __half2 h01 = *reinterpret_cast<const __half2 *>(&raw.x);
-      const __half2 h23 = *reinterpret_cast<const __half2 *>(&raw.y);
-      x[0] = __low2float(h01); x[1] = __high2float(h01);
-      x[2] = __low2float(h23); x[3] = __high2float(h23);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = 4 * lane + i, mt = d >> 4, gq = (d & 15) >> 1, sb = d & 1;
-        x[i] = __half2float(*reinterpret_cast<const __half *>(
-            unit + mt * 512 + (4 * gq + tig) * 16 + (rh * 4 + sb * 2 + par) * 2));
-      }
-    }
-    return;
-  }
-  if (codec == KVQ_Q8_0) {
-    int q[4];
-    int soff;
-    if (SIDE == 0) {
-      const int h = lb >> 2, w = lane & 3;
-      const uint32_t word =
-          *reinterpret_cast<const uint32_t *>(unit + b * 512 + (4 * g + w) * 16 + (2 * rh + h) * 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = static_cast<int8_t>((word >> (8 * i)) & 0xffu);
-      soff = 2048 + g * 16 + rh * 8 + b * 2;
-    } else {
-#pragma unroll
-      for (int pp = 0; pp < 2; ++pp) {
-        const int d = 4 * lane + 2 * pp, mt = d >> 4, gq = (d & 15) >> 1;
-        const uint32_t v = *reinterpret_cast<const uint16_t *>(
-            unit + (mt >> 1) * 512 + (4 * gq + tig) * 16 + ((mt & 1) * 2 + rh) * 4 + par * 2);
-        q[2 * pp] = static_cast<int8_t>(v & 0xffu);
-        q[2 * pp + 1] = static_cast<int8_t>(v >> 8);
-      }
-      soff = 2048 + tig * 32 + b * 8 + rh * 4 + par * 2;
-    }
-    const float d = __half2float(*reinterpret_cast<const __half *>(unit + soff));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = d * static_cast<float>(q[i]);
-    return;
-  }
-  if (codec == KVQ_TURBO4) {
-    turbo4_row_rotated<SIDE>(unit, r, lane, x);
-    turbo_unrotate_lane(x, lane);
-    return;
-  }
-  // q4_0: lanes lb < 4 hold canonical bytes jc = 4lb..4lb+3 (low nibbles),
-  // lanes lb + 4 the same bytes' high nibbles.
-  const int l4 = lb & 3, hi = lb >> 2;
-  uint32_t bytes[4];
-  if (SIDE == 0) {
-    const uint32_t word = *reinterpret_cast<const uint32_t *>(
-        unit + (b >> 1) * 512 + (4 * g + l4) * 16 + ((b & 1) * 2 + rh) * 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bytes[i] = (word >> (8 * i)) & 0xffu;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int jc = 4 * l4 + i, mt = 2 * b + (jc >> 3), gq = jc & 7;
-      bytes[i] = unit[(mt >> 2) * 512 + (4 * gq + tig) * 16 + (mt & 3) * 4 + par * 2 + rh];
-    }
-  }
-  const int soff = SIDE == 0 ? 1024 + g * 16 + rh * 8 + b * 2
-                             : 1024 + tig * 32 + b * 8 + rh * 4 + par * 2;
-  const float d = __half2float(*reinterpret_cast<const __half *>(unit + soff));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = hi ? static_cast<int>(bytes[i] >> 4) : static_cast<int>(bytes[i] & 0xfu);
-    x[i] = d * static_cast<float>(n - 8);
-  }
-}
-
 // Encode one fp32 row (lane l holds its dims 4l..4l+3) with `codec` into token
 // row r of `unit` (all 32 lanes of the warp); an f16 target rounds to fp16.
 template <int SIDE>

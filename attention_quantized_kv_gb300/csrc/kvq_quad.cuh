@@ -5,7 +5,8 @@
 // 512 bytes, so a warp loads and stores a unit as contiguous 512-byte pieces,
 // with no exchange between lanes but a block's maximum (two shuffles).  The
 // planes of a rotation lie inside a lane too, for the interleaved layout and
-// for half layouts whose rot_dim is a multiple of 32.
+// for half layouts whose rot_dim is a multiple of 32; otherwise the partners
+// are read from a copy of the rows in shared memory.
 #pragma once
 
 #include "kvq_encode.cuh"
@@ -17,11 +18,13 @@ namespace {
 // How a rotation's planes lie: kQuadInterleaved, or N = 1..4 for the planes
 // ((c, i), (c + N, i)) of a half layout with rot_dim 32 N.
 constexpr int kQuadInterleaved = 0;
-constexpr int kQuadNone = -1;  // planes cross lanes: rows go one by one
+constexpr int kQuadAny = -1;        // planes cross lanes
+constexpr int kQuadPitch = kD + 4;  // floats from row to row of the copy: four banks apart
+constexpr int kQuadBytes = 8 * kQuadPitch * 4;  // a warp's copy: one row per quad
 
 inline int quad_kind(const RopeArgs &p) {
   if (p.layout == KVQ_ROPE_INTERLEAVED) return kQuadInterleaved;
-  return p.rot % 32 == 0 ? p.rot / 32 : kQuadNone;
+  return p.rot % 32 == 0 ? p.rot / 32 : kQuadAny;
 }
 
 // PURE: no magnitude (kv_rope_shift); otherwise no sign.
@@ -46,8 +49,53 @@ __device__ __forceinline__ void quad_rotate_half(const RopeArgs &p, const float 
   }
 }
 
-// Rotate the quad's row by the table row `row` (kind: quad_kind's, not
-// kQuadNone).
+// Planes anywhere: every lane's values go to shared memory, and each lane reads
+// its values' partners there (all 32 lanes).
+template <bool PURE>
+__device__ __forceinline__ void quad_rotate_any(const RopeArgs &p, const float *row, int lane,
+                                                float sign, float *copy, float (&v)[8][4]) {
+  const int w = lane & 3, h = p.rot >> 1;
+  float *mine = copy + (lane >> 2) * kQuadPitch;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4 *>(mine + 16 * c + 4 * w) =
+        make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int d0 = 16 * c + 4 * w;
+    if (d0 >= p.rot) continue;
+    float o[4], co[4], si[4];
+    if ((h & 3) == 0) {  // the four values lie in one half, their partners together
+      const int e = d0 < h ? d0 : d0 - h;
+      const float4 x = *reinterpret_cast<const float4 *>(mine + (d0 < h ? d0 + h : e));
+      const float4 t = *reinterpret_cast<const float4 *>(row + 2 * e);
+      const float4 u = *reinterpret_cast<const float4 *>(row + 2 * e + 4);
+      o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+      co[0] = t.x; co[1] = t.z; co[2] = u.x; co[3] = u.z;
+      si[0] = t.y; si[1] = t.w; si[2] = u.y; si[3] = u.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = d0 + i < p.rot ? d0 + i : 0, e = d < h ? d : d - h;
+        const float2 t = *reinterpret_cast<const float2 *>(row + 2 * e);
+        o[i] = mine[d < h ? d + h : e];
+        co[i] = t.x;
+        si[i] = t.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float cc = PURE ? co[i] : __fmul_rn(co[i], p.magnitude);
+      const float ss = PURE ? sign * si[i] : __fmul_rn(si[i], p.magnitude);
+      if (d0 + i < p.rot)
+        v[c][i] = __fadd_rn(__fmul_rn(v[c][i], cc), __fmul_rn(o[i], d0 + i < h ? -ss : ss));
+    }
+  }
+  __syncwarp();  // the copy may be written again
+}
+
+// Rotate the quad's row by the table row `row` (kind: quad_kind's, not kQuadAny).
 template <bool PURE>
 __device__ __forceinline__ void quad_rotate(const RopeArgs &p, int kind, const float *row, int w,
                                             float sign, float (&v)[8][4]) {

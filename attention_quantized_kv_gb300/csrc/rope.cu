@@ -7,7 +7,6 @@
 
 #include <math.h>
 
-#include "kvq_encode.cuh"
 #include "kvq_launch.h"
 #include "kvq_quad.cuh"
 
@@ -37,11 +36,12 @@ __host__ __device__ constexpr double turn_term(int n) {
 // (cos, sin) of u * 2^-64 turns for two angles at once (one polynomial
 // instruction serves both).  The nearest quarter turn is taken off as an
 // integer, so the remainder t in [-1/8, 1/8] turns is exact (its 56 upper
-// bits are used) and rounds once to fp32 whatever the position (2^-24 of at most pi / 4 rad).  The series
-// end at t^9 and t^10, what is left out being below 2e-9; 2 pi t is taken
-// with 2 pi as the sum of two floats, so that the last addition's rounding is
-// the only other one of its size.  In all within 1.3 * 2^-24 (measured on the
-// host over 2M values), inside the documented 2^-23.
+// bits are used) and rounds once to fp32 whatever the position (2^-24 of at
+// most pi / 4 rad).  The Taylor series end at t^9 and t^10, what is left out
+// being below 2e-9; 2 pi t is taken with 2 pi as the sum of two floats, so that
+// the last addition's rounding is the only other one of its size.  In all
+// within 1.3 * 2^-24 (measured on the host over 4M values), inside the
+// documented 2^-23.
 __device__ __forceinline__ float2 both(float k) { return make_float2(k, k); }
 __device__ __forceinline__ void cos_sin_turns(uint64_t u0, uint64_t u1, float2 &first,
                                               float2 &second) {
@@ -276,10 +276,13 @@ struct ShiftParams {
 // instruction issue: 17, 20 and 50 instructions per value.
 constexpr int kShiftHeads = 4;
 
-template <int CODEC>
+// ANY: planes that cross lanes (a kernel of its own, so that its registers are
+// not the others'): f16 with 40 dims in halves 67 us (row by row 166 us).
+template <int CODEC, bool ANY>
 __global__ void __launch_bounds__(kRopeThreads, 2)
     shift_units_kernel(const __grid_constant__ ShiftParams p) {
   grid_dependency_wait();
+  __shared__ __align__(16) float copies[ANY ? kRopeWarps : 1][ANY ? kQuadBytes / 4 : 4];
   const int lane = threadIdx.x & 31, g = lane >> 2, w = lane & 3, s = blockIdx.y;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
   const int groups = (p.n_kv + kShiftHeads - 1) / kShiftHeads;
@@ -325,7 +328,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     for (int rh = 0; rh < 2; ++rh) {
       float v[8][4];
       quad_decode<CODEC>(q[rh], w, v);
-      quad_rotate<true>(p.rope, p.kind, row[rh], w, d[rh] < 0 ? -1.0f : 1.0f, v);
+      const float sign = d[rh] < 0 ? -1.0f : 1.0f;
+      if (ANY)
+        quad_rotate_any<true>(p.rope, row[rh], lane, sign, copies[ANY ? threadIdx.x >> 5 : 0], v);
+      else
+        quad_rotate<true>(p.rope, p.kind, row[rh], w, sign, v);
       QuadCodes<CODEC> e;
       quad_encode<CODEC>(v, w, e);
       if (d[rh] != 0) q[rh] = e;
@@ -334,37 +341,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   }
 }
 
-// Planes that cross lanes: one warp per (sequence, token), its K rows of every
-// kv head one by one (166 us where shift_units_kernel takes 57).
-__global__ void __launch_bounds__(kRopeThreads) shift_rows_kernel(ShiftParams p) {
-  grid_dependency_wait();
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  if (t >= min(p.seq_lens[s], p.capacity)) return;
-  const int d = p.delta[static_cast<int64_t>(s) * p.capacity + t];
-  if (d == 0) return;
-  int64_t unit = static_cast<int64_t>(s) * p.n_kv * (p.capacity / kUnitTokens) + t / kUnitTokens;
-  int64_t step = p.capacity / kUnitTokens;
-  if (p.table) {
-    const int pg = page_of(p.table, p.pages_per_seq, p.n_pages, s, t / (kUnitTokens * kPageUnits));
-    if (pg < 0) {
-      if (lane == 0) set_err(p.err, KVQ_DEVERR_PAGE);
-      return;
-    }
-    unit = static_cast<int64_t>(pg) * p.n_kv * kPageUnits + (t / kUnitTokens) % kPageUnits;
-    step = kPageUnits;
-  }
-  const int64_t by = d;
-  const LaneAngles a =
-      lane_angles(p.rope, rope_row(p.rope, by < 0 ? -by : by, p.err), lane, d < 0 ? -1.0f : 1.0f);
-  for (int h = 0; h < p.n_kv; ++h) {
-    uint8_t *u = p.k + (unit + h * step) * unit_bytes(p.codec);
-    float x[4];
-    load_row<0>(p.codec, u, t % kUnitTokens, lane, x);
-    rotate_lane(p.rope, a, lane, x);
-    __syncwarp();  // every lane has read its part before any is written
-    encode_f32_row_into<0>(p.codec, x, u, t % kUnitTokens, lane);
-  }
+template <bool ANY>
+auto shift_kernel_of(int codec) {
+  return codec == KVQ_F16    ? shift_units_kernel<KVQ_F16, ANY>
+         : codec == KVQ_Q8_0 ? shift_units_kernel<KVQ_Q8_0, ANY>
+         : codec == KVQ_Q4_0 ? shift_units_kernel<KVQ_Q4_0, ANY>
+                             : shift_units_kernel<KVQ_TURBO4, ANY>;
 }
 
 template <int TI, int TO>
@@ -446,19 +428,13 @@ cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const in
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
   p.kind = quad_kind(p.rope);
-  if (p.kind == kQuadNone) {
-    const dim3 grid((L.capacity + kRopeWarps - 1) / kRopeWarps, L.n_seqs);
-    return launch_pdl(shift_rows_kernel, grid, dim3(kRopeThreads), 0, stream, p);
-  }
   const int64_t items = static_cast<int64_t>(L.capacity / kUnitTokens) *
                         ((L.n_kv_heads + kShiftHeads - 1) / kShiftHeads);
   const int64_t blocks = (items + kRopeWarps - 1) / kRopeWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks), L.n_seqs);
-  const auto kernel = L.codec_k == KVQ_F16    ? shift_units_kernel<KVQ_F16>
-                      : L.codec_k == KVQ_Q8_0 ? shift_units_kernel<KVQ_Q8_0>
-                      : L.codec_k == KVQ_Q4_0 ? shift_units_kernel<KVQ_Q4_0>
-                                              : shift_units_kernel<KVQ_TURBO4>;
+  const auto kernel = p.kind == kQuadAny ? shift_kernel_of<true>(L.codec_k)
+                                         : shift_kernel_of<false>(L.codec_k);
   return launch_pdl(kernel, grid, dim3(kRopeThreads), 0, stream, p);
 }
 
