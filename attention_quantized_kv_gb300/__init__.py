@@ -126,9 +126,9 @@ class KVLayer:
 
     def desc(self) -> kvq_layer:
         """The C descriptor (rebuilt only when a buffer was replaced)."""
-        table = self.block_table
+        table, err = self.block_table, self.err
         key = (self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.seq_lens.data_ptr(),
-               self.err.data_ptr(), self.codec_k, self.codec_v,
+               None if err is None else err.data_ptr(), self.codec_k, self.codec_v,
                None if table is None else table.data_ptr(), self.n_pages)
         if self._desc is None or self._desc_key != key:
             d = kvq_layer()

@@ -300,3 +300,22 @@ def test_row_descriptors():
                 torch.zeros((3, 9, 12, 128))[:, :4]):
         with pytest.raises(ValueError):
             kvq._rows(bad, 12, dev, "x")
+
+
+def test_layer_without_an_error_word():
+    """err is optional in the C descriptor: a layer may drop or replace its word."""
+    L = kvq.KVLayer(1, 1, 1, 256, kvq.KVQ_F16, kvq.KVQ_F16, device="cpu")
+    word = L.err
+    assert L.desc().err == word.data_ptr()
+    L.err = None
+    assert not L.desc().err
+    L.err = word
+    assert L.desc().err == word.data_ptr()
+
+
+@pytest.mark.parametrize("codec", [kvq.KVQ_F16, kvq.KVQ_Q8_0, kvq.KVQ_Q4_0, kvq.KVQ_TURBO4, 9])
+def test_side_bytes_are_the_librarys(codec):
+    flat = kvq.KVLayer(3, 2, 4, 512, kvq.KVQ_F16, kvq.KVQ_F16, device="cpu")
+    paged = kvq.KVLayer(1, 2, 4, 512, kvq.KVQ_F16, kvq.KVQ_F16, device="cpu", n_pages=7)
+    assert kvq._side_bytes(flat, codec) == kvq.kvq_cache_bytes(codec, 3, 2, 512)
+    assert kvq._side_bytes(paged, codec) == kvq.kvq_pool_bytes(codec, 7, 2)
