@@ -59,6 +59,19 @@ def _stream_ptr(stream) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _hand_over(stream, *tensors) -> None:
+    """Tensors of the current stream's are used on another one next: that stream waits for what
+    fills them, and their memory is given to nothing else before its work on them is done."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(tensors[0].device)
+    if stream == current:
+        return
+    stream.wait_stream(current)
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else int(t.data_ptr())
 
@@ -328,8 +341,9 @@ def evict(layer: KVLayer, scores, n_sink: int, n_recent: int, n_evict: int, stre
     """Select and remove up to n_evict tokens per sequence: new zeroed cache
     buffers (torch allocations), the layer repointed at them and at the new
     lengths.  With ``rope`` the kept keys are rotated to their new positions
-    too (a token's position is its place in the cache again).  Returns
-    (compacted scores, evict list, n_evicted)."""
+    too (a token's position is its place in the cache again).  On another
+    stream than the current one the work starts behind the current stream's.
+    Returns (compacted scores, evict list, n_evicted)."""
     dev = layer.k_cache.device
     if rope is not None:
         rope._check_on(dev)
@@ -337,14 +351,17 @@ def evict(layer: KVLayer, scores, n_sink: int, n_recent: int, n_evict: int, stre
             raise ValueError("evict: the rope's table must cover the layer's capacity")
     ev = torch.zeros((layer.n_seqs, max(int(n_evict), 1)), dtype=torch.int32, device=dev)
     nev = torch.zeros(layer.n_seqs, dtype=torch.int32, device=dev)
-    kv_evict_select(layer, scores, n_sink, n_recent, n_evict, ev, nev, stream)
     k_dst = torch.zeros_like(layer.k_cache)
     v_dst = torch.zeros_like(layer.v_cache)
     s_dst = torch.zeros_like(scores)
     lens = torch.empty_like(layer.seq_lens)
+    delta = torch.empty((layer.n_seqs, layer.capacity if rope is not None else 0),
+                        dtype=torch.int32, device=dev)
+    _hand_over(stream, ev, nev, k_dst, v_dst, s_dst, lens, delta, scores, layer.k_cache,
+               layer.v_cache, layer.seq_lens)
+    kv_evict_select(layer, scores, n_sink, n_recent, n_evict, ev, nev, stream)
     kv_compact(layer, ev, nev, k_dst, v_dst, scores, s_dst, lens, stream)
     if rope is not None:
-        delta = torch.empty((layer.n_seqs, layer.capacity), dtype=torch.int32, device=dev)
         kv_evict_delta(layer, ev, nev, delta, stream)
     layer.k_cache, layer.v_cache, layer.seq_lens = k_dst, v_dst, lens
     if rope is not None:
@@ -453,6 +470,8 @@ class Rope:
             if n_pos <= 0:
                 raise ValueError("n_pos must be positive")
             table = torch.empty((n_pos, len(freqs), 2), dtype=torch.float32, device=device)
+            if table.is_cuda:
+                _hand_over(stream, table)
             kvq_rope_table(freqs, table, stream)
         elif table.dim() != 3 or table.shape[0] < 1 or not 1 <= table.shape[1] <= HEAD_DIM // 2:
             raise ValueError(f"table must be [n_pos, rot_dim / 2, 2], got {tuple(table.shape)}")

@@ -621,15 +621,15 @@ __device__ __forceinline__ bool appends(const DecodeParams &p, int seq) {
   return p.k_new && len >= 0 && len < p.capacity;
 }
 
-// Fused decode step: write sequence seq's new K and V rows of kv head kvh
-// (fp16 from k_new / v_new; all 32 lanes) into the cache at position
-// pos = seq_lens[seq] (the old length).
 // kFusedRope: the table row of sequence seq's position (its old length, or
 // the caller's), clamped to the table.
 __device__ __forceinline__ const float *step_angles(const DecodeParams &p, int seq) {
   return rope_row(p.rope, p.positions ? p.positions[seq] : p.seq_lens[seq], p.err);
 }
 
+// Fused decode step: write sequence seq's new K and V rows of kv head kvh
+// (fp16 from k_new / v_new; all 32 lanes) into the cache at position
+// pos = seq_lens[seq] (the old length).
 template <int CK, int CV, int MODE>
 __device__ __forceinline__ void write_new_rows(const DecodeParams &p, int seq, int kvh, int lane) {
   const int pos = p.seq_lens[seq];

@@ -440,8 +440,9 @@ KVQ_API int kvq_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double
                            double orig_len, double low, double high, double *freqs);
 
 /* table[p][i] = (cos, sin)(p * freqs[i]) for p < n_pos, i < rot_dim / 2, in
- * fp32, each within 2^-23 of the exact value.  freqs: host, each in [0, 2 pi).  The product is reduced
- * as a 64-bit fixed-point number of turns, so far positions lose nothing.
+ * fp32, each within 2^-23 of the exact value.  freqs: host, each in [0, 2 pi).
+ * The product is reduced as a 64-bit fixed-point number of turns, so far
+ * positions lose nothing.
  * table: device, fp32 [n_pos][rot_dim / 2][2], 16-byte aligned. */
 KVQ_API int kvq_rope_table(const double *freqs, int32_t rot_dim, int32_t n_pos, float *table,
                            void *stream);
@@ -450,9 +451,10 @@ KVQ_API int kvq_rope_table(const double *freqs, int32_t rot_dim, int32_t n_pos, 
  * or NULL for position pos0 + row.  transpose != 0 applies the transposed
  * rotation (s taken as -s): the gradient with respect to x of a rotation,
  * given the gradient with respect to y.  y has x's type or fp16; y may be x
- * itself (same data, strides and type) and must not overlap it otherwise;
- * x may repeat rows or heads (a stride of 0), y may not.  err: optional device word for
- * KVQ_DEVERR_POS.  n_rows = 0 launches nothing. */
+ * itself (same data, strides and type); otherwise the ranges from the first to
+ * the last byte of x and of y must not meet.  x may repeat rows or heads (a
+ * stride of 0), y may not.  err: optional device word for KVQ_DEVERR_POS.
+ * n_rows = 0 launches nothing. */
 KVQ_API int kvq_rope_apply(const kvq_rope *rope, const kvq_rows *x, const kvq_rows *y,
                            int64_t n_rows, int32_t n_heads, const int32_t *positions,
                            int32_t pos0, int32_t transpose, int32_t *err, void *stream);
@@ -477,7 +479,8 @@ KVQ_API int kvq_rope_apply(const kvq_rope *rope, const kvq_rows *x, const kvq_ro
  * Device conditions: KVQ_DEVERR_CAPACITY, KVQ_DEVERR_PAGE (the row's k and v
  * are skipped), KVQ_DEVERR_POS, KVQ_DEVERR_ROWS (a row_start or n_new entry out
  * of its range: that sequence's rows are unspecified, in bounds, and its
- * length stays).  q_out may be q itself when q is fp16 and contiguous. */
+ * length stays).  q_out may be q itself when q is fp16 and contiguous;
+ * otherwise it must not meet the ranges of q, k and v. */
 KVQ_API int kv_append_rope(const kvq_layer *layer, const kvq_rope *rope, const kvq_rows *q,
                            const kvq_rows *k, const kvq_rows *v, int64_t n_rows,
                            const int32_t *n_new, const int32_t *row_start,

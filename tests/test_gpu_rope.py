@@ -1030,3 +1030,33 @@ def test_two_streams_at_once():
         assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.v_cache, b.v_cache)
         for t, u in zip(rooms[i][0][1], rooms[i][1][1]):
             assert torch.equal(t, u)
+
+
+def test_evict_and_table_on_another_stream():
+    """evict (with and without rope) and a table on a busy stream that is not
+    the current one, which goes on to allocate and fill memory of the sizes
+    that the call let go of: the results of the same calls made in order."""
+    side = torch.cuda.Stream()
+    for with_rope in (False, True):
+        base, table = _random_layer(2, 2, 4, 1024, Q8, F16, False, [900, 640], 21)
+        M = _twin(base, table)
+        L = _twin(base, table)
+        g = torch.Generator(device="cuda").manual_seed(3)
+        scores = torch.rand((2, 1024), generator=g, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        rope = kvq.Rope(n_pos=1024, rot_dim=96, stream=side)
+        got = kvq.evict(L, scores, 4, 32, 200, stream=side, rope=rope if with_rope else None)
+        sizes = [(t.numel(), t.dtype) for t in (M.k_cache, M.v_cache, M.seq_lens)]
+        sizes.append((2 * 1024, torch.int32))
+        junk = [torch.full((n,), 77, dtype=t, device="cuda") for n, t in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all((t == 77).all() for t in junk)
+        same = kvq.Rope(n_pos=1024, rot_dim=96)
+        want = kvq.evict(M, scores, 4, 32, 200, rope=same if with_rope else None)
+        assert torch.equal(rope.table, same.table)
+        for a, b in zip((*got, L.k_cache, L.v_cache, L.seq_lens),
+                        (*want, M.k_cache, M.v_cache, M.seq_lens)):
+            assert torch.equal(a, b)
+        assert L.err.item() == 0
