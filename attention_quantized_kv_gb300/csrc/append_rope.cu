@@ -277,14 +277,6 @@ struct Stage {
 constexpr int kGroupRows = 12;
 constexpr int kScaleAt = kD;  // byte offset of a staged row's scales
 
-__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_all;\n" ::: "memory");
-}
-
 // Copy the rows of `mask` (bit j: row j of the 16 at x) into their stage slots.
 template <int T>
 __device__ __forceinline__ void stage_rows(uint8_t *stage, const uint8_t *x, int64_t row_bytes,
@@ -297,7 +289,7 @@ __device__ __forceinline__ void stage_rows(uint8_t *stage, const uint8_t *x, int
     if ((mask >> j) & 1u)
       copy_async16(stage + j * Stage<T>::kPitch + off, x + j * row_bytes + off);
   }
-  copy_async_wait();
+  copy_async_wait_all();
   __syncwarp();
 }
 

@@ -15,6 +15,22 @@
 namespace kvq {
 namespace {
 
+// 16 bytes from global to shared memory behind the thread's back, in groups.
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+template <int N>  // all but the newest N groups have landed (this thread's)
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() {
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+}
+
 // How a rotation's planes lie: kQuadInterleaved, or N = 1..4 for the planes
 // ((c, i), (c + N, i)) of a half layout with rot_dim 32 N.
 constexpr int kQuadInterleaved = 0;
@@ -182,42 +198,34 @@ struct QuadCodes {
   uint16_t scale;
 };
 
-// Both rows (g, g + 8) of the lane, from and to the unit.
+// One row's codes (this lane's part of token row r).
 template <int CODEC>
-__device__ __forceinline__ void quad_load(const uint8_t *unit, int lane,
-                                          QuadCodes<CODEC> (&q)[2]) {
-  const uint4 *u = reinterpret_cast<const uint4 *>(unit) + lane;
-  const int g = lane >> 2, w = lane & 3;
+__device__ __forceinline__ void quad_load_row(const uint8_t *unit, int r, int w,
+                                              QuadCodes<CODEC> &q) {
+  const int g = r & 7, rh = r >> 3;
+  const uint8_t *u = unit + (4 * g + w) * 16;
   if (CODEC == KVQ_F16) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {  // piece 2b + rh
-      const uint4 x = u[k * 32];
-      uint32_t *d = &q[k & 1].w[4 * (k >> 1)];
-      d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+    for (int b = 0; b < 4; ++b) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(u + (2 * b + rh) * 512);
+      q.w[4 * b] = x.x; q.w[4 * b + 1] = x.y; q.w[4 * b + 2] = x.z; q.w[4 * b + 3] = x.w;
     }
     return;
   }
   const uint16_t *sc = reinterpret_cast<const uint16_t *>(unit + unit_scale_offset(CODEC));
+  q.scale = CODEC == KVQ_TURBO4 ? sc[2 * g + rh] : sc[8 * g + 4 * rh + w];
 #pragma unroll
-  for (int rh = 0; rh < 2; ++rh)
-    q[rh].scale = CODEC == KVQ_TURBO4 ? sc[2 * g + rh] : sc[8 * g + 4 * rh + w];
-  if (CODEC == KVQ_Q8_0) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint4 x = u[b * 32];
-      q[0].w[2 * b] = x.x; q[0].w[2 * b + 1] = x.y;
-      q[1].w[2 * b] = x.z; q[1].w[2 * b + 1] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 x = u[j * 32];
-      q[0].w[2 * j] = x.x; q[1].w[2 * j] = x.y;
-      q[0].w[2 * j + 1] = x.z; q[1].w[2 * j + 1] = x.w;
+  for (int b = 0; b < 4; ++b) {
+    if (CODEC == KVQ_Q8_0) {
+      const uint2 x = *reinterpret_cast<const uint2 *>(u + b * 512 + rh * 8);
+      q.w[2 * b] = x.x; q.w[2 * b + 1] = x.y;
+    } else {
+      q.w[b] = *reinterpret_cast<const uint32_t *>(u + (b >> 1) * 512 + ((b & 1) * 2 + rh) * 4);
     }
   }
 }
 
+// Both rows (g, g + 8) of the lane, to the unit.
 template <int CODEC>
 __device__ __forceinline__ void quad_store(uint8_t *unit, int lane,
                                            const QuadCodes<CODEC> (&q)[2]) {

@@ -263,24 +263,32 @@ struct ShiftParams {
   int kind;  // quad_kind
 };
 
-// One warp per (sequence, 16-token unit, up to kShiftHeads kv heads): both rows
-// of every quad are read as they lie, turned by their tokens' shifts, encoded
-// again and stored as they lay; rows that do not move keep their codes.  The
-// next head's unit is requested before the current one is worked on, and the
-// first beside the shifts, which in an eviction's wake are seldom all zero.
+// One warp per (sequence, 16-token unit, up to kShiftHeads kv heads).  A head's
+// unit is copied to shared memory while the one before it is worked on, the
+// first ones beside the shifts, which in an eviction's wake are seldom all
+// zero; every quad turns and encodes its two rows from there and stores the ones
+// that move straight to the unit.
 //
-// 74k tokens x 8 heads in four sequences, the deltas (2.5 us) included: f16
-// 57 us, 0.78 of the floor, bound by the latency of the loads at the 16 warps
-// that 128 registers leave an SM (row by row 166 us, a head per warp 69 us,
-// eight heads per warp 61 us); q8_0 64 us, 4-bit 73 us, turbo4 139 us, bound by
-// instruction issue: 17, 20 and 50 instructions per value.
+// 74k tokens x 8 heads in four sequences, the deltas (2.5 us) included: f16 51
+// us, 0.88 of the floor (the next unit in registers 57 us, no look-ahead 74 us),
+// bound by HBM; q8_0 58 us, q4_0 68 us, turbo4 124 us, bound by instruction
+// issue, most of it the encoders'.  Tried for f16, q8_0 and q4_0: both rows
+// encoded before either is stored 52, 60, 70 us; rows encoded in the shared copy
+// and the whole unit stored 52, 62, 73 us; a third unit in the ring 51, 59, 68
+// us; a third block per SM (80 registers) 56, 63, 72 us; eight heads per warp
+// 52, 55, 66 us, but 29 instead of 17 us for 16k tokens in eight sequences
+// (q8_0).  The code of a lane's two rows is interleaved but for turbo4 (124
+// instead of 133 us; q8_0 60 instead of 58 us).
 constexpr int kShiftHeads = 4;
+constexpr int kShiftSlots = 2;  // units in a warp's ring
 
 // ANY: planes that cross lanes (a kernel of its own, so that its registers are
-// not the others'): f16 with 40 dims in halves 67 us (row by row 166 us).
+// not the others'): with 40 dims in halves f16 61 us, q8_0 78 us, turbo4 148 us
+// (by whole rows, a warp each, f16 166 us).
 template <int CODEC, bool ANY>
 __global__ void __launch_bounds__(kRopeThreads, 2)
     shift_units_kernel(const __grid_constant__ ShiftParams p) {
+  extern __shared__ __align__(16) uint8_t units[];
   grid_dependency_wait();
   __shared__ __align__(16) float copies[ANY ? kRopeWarps : 1][ANY ? kQuadBytes / 4 : 4];
   const int lane = threadIdx.x & 31, g = lane >> 2, w = lane & 3, s = blockIdx.y;
@@ -301,52 +309,68 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     unit = (static_cast<int64_t>(pg) * p.n_kv + h0) * kPageUnits + j % kPageUnits;
     step = kPageUnits;
   }
-  uint8_t *u = p.k + unit * unit_bytes(CODEC);
-  step *= unit_bytes(CODEC);
-  QuadCodes<CODEC> q[2], next[2];
-  quad_load<CODEC>(u, lane, next);
+  constexpr int kBytes = unit_bytes(CODEC);
+  uint8_t *u = p.k + unit * kBytes;
+  step *= kBytes;
+  const int heads = min(kShiftHeads, p.n_kv - h0);
+  uint8_t *const ring = units + (threadIdx.x >> 5) * kShiftSlots * kBytes;
+  auto fetch = [&](int h) {  // head h's unit (none behind the last: an empty group)
+    if (h < heads)
+      for (int c = 16 * lane; c < kBytes; c += 512)
+        copy_async16(ring + h % kShiftSlots * kBytes + c, u + h * step + c);
+    copy_async_commit();
+  };
+#pragma unroll
+  for (int h = 0; h < kShiftSlots - 1; ++h) fetch(h);
   int d[2];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
     const int t = j * kUnitTokens + g + 8 * rh;
     d[rh] = t < len ? p.delta[static_cast<int64_t>(s) * p.capacity + t] : 0;
   }
-  if (!__any_sync(0xffffffffu, d[0] != 0 || d[1] != 0)) return;
+  if (!__any_sync(0xffffffffu, d[0] != 0 || d[1] != 0)) {
+    copy_async_wait<0>();
+    return;
+  }
   const float *row[2];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
     const int64_t by = d[rh];
     row[rh] = rope_row(p.rope, by < 0 ? -by : by, p.err);
   }
-  const int heads = min(kShiftHeads, p.n_kv - h0);
 #pragma unroll 1
-  for (int h = 0; h < heads; ++h, u += step) {
-    q[0] = next[0];
-    q[1] = next[1];
-    if (h + 1 < heads) quad_load<CODEC>(u + step, lane, next);
-#pragma unroll
+  for (int h = 0; h < heads; ++h) {
+    copy_async_wait<kShiftSlots - 2>();
+    __syncwarp();  // every lane's copies of head h have landed, and head h - 1 has left
+    fetch(h + kShiftSlots - 1);
+    uint8_t *slot = ring + h % kShiftSlots * kBytes;
+#pragma unroll (ANY || CODEC == KVQ_TURBO4 ? 1 : 2)
     for (int rh = 0; rh < 2; ++rh) {
+      const int by = rh ? d[1] : d[0];
+      const float *angles = rh ? row[1] : row[0], sign = by < 0 ? -1.0f : 1.0f;
       float v[8][4];
-      quad_decode<CODEC>(q[rh], w, v);
-      const float sign = d[rh] < 0 ? -1.0f : 1.0f;
+      QuadCodes<CODEC> q;
+      quad_load_row<CODEC>(slot, g + 8 * rh, w, q);
+      quad_decode<CODEC>(q, w, v);
       if (ANY)
-        quad_rotate_any<true>(p.rope, row[rh], lane, sign, copies[ANY ? threadIdx.x >> 5 : 0], v);
+        quad_rotate_any<true>(p.rope, angles, lane, sign, copies[ANY ? threadIdx.x >> 5 : 0], v);
       else
-        quad_rotate<true>(p.rope, p.kind, row[rh], w, sign, v);
-      QuadCodes<CODEC> e;
-      quad_encode<CODEC>(v, w, e);
-      if (d[rh] != 0) q[rh] = e;
+        quad_rotate<true>(p.rope, p.kind, angles, w, sign, v);
+      quad_encode<CODEC>(v, w, q);
+      if (by != 0) quad_store_row<CODEC>(u + h * step, g + 8 * rh, w, q);
     }
-    quad_store<CODEC>(u, lane, q);
   }
 }
 
-template <bool ANY>
-auto shift_kernel_of(int codec) {
-  return codec == KVQ_F16    ? shift_units_kernel<KVQ_F16, ANY>
-         : codec == KVQ_Q8_0 ? shift_units_kernel<KVQ_Q8_0, ANY>
-         : codec == KVQ_Q4_0 ? shift_units_kernel<KVQ_Q4_0, ANY>
-                             : shift_units_kernel<KVQ_TURBO4, ANY>;
+template <int CODEC>
+cudaError_t launch_shift(const ShiftParams &p, dim3 grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> optin[2]{};
+  const bool any = p.kind == kQuadAny;
+  const auto kernel = any ? shift_units_kernel<CODEC, true> : shift_units_kernel<CODEC, false>;
+  const int bytes = kRopeWarps * kShiftSlots * unit_bytes(CODEC);
+  const cudaError_t e = smem_optin(kernel, bytes, optin[any]);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, grid, dim3(kRopeThreads), bytes, stream, p);
 }
 
 template <int TI, int TO>
@@ -433,9 +457,10 @@ cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const in
   const int64_t blocks = (items + kRopeWarps - 1) / kRopeWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks), L.n_seqs);
-  const auto kernel = p.kind == kQuadAny ? shift_kernel_of<true>(L.codec_k)
-                                         : shift_kernel_of<false>(L.codec_k);
-  return launch_pdl(kernel, grid, dim3(kRopeThreads), 0, stream, p);
+  return L.codec_k == KVQ_F16    ? launch_shift<KVQ_F16>(p, grid, stream)
+         : L.codec_k == KVQ_Q8_0 ? launch_shift<KVQ_Q8_0>(p, grid, stream)
+         : L.codec_k == KVQ_Q4_0 ? launch_shift<KVQ_Q4_0>(p, grid, stream)
+                                 : launch_shift<KVQ_TURBO4>(p, grid, stream);
 }
 
 }  // namespace kvq
