@@ -249,12 +249,13 @@ __global__ void __launch_bounds__(kArThreads)
 // (include/kvq.h): written row by row the V side would go out as 2-byte
 // stores, one 32-byte sector each.  So one warp takes a whole unit of one kv
 // head, and stores it as contiguous 512-byte pieces.
-//   K: every quad of lanes reads two rows of the window in the unit's own
-//      order, rotates and encodes them in registers (kvq_quad.cuh), whatever
-//      units they belong to.
-//   V: the rows are copied into shared memory, 16 of them in flight; two lanes
-//      per row encode its four blocks; the unit is put together 16 bytes per
-//      lane from the 16 rows' codes.
+// The window's rows are copied into shared memory, 16 of them in flight (K rows
+// read into registers instead, 32768 rows: f16 106 instead of 103 us, q8_0 112
+// instead of 110 us).
+//   K: every quad of lanes takes two rows in the unit's own order, rotates,
+//      encodes and stores them (kvq_quad.cuh), whatever units they belong to.
+//   V: two lanes per row encode its four blocks; the unit is put together 16
+//      bytes per lane from the 16 rows' codes.
 //
 // Packed rows are cut into windows of 16, whatever the lengths.  For V a
 // window's warp places the rows of every unit whose first new row lies in the
@@ -470,53 +471,36 @@ __device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
   *reinterpret_cast<__half2 *>(row + kScaleAt + 2 * b0) = __halves2half2(d16[0], d16[1]);
 }
 
-// A window's 16 rows of K: lane 4g + w reads rows g and g + 8 of the 16 at x,
-// which may lie in any units: lane j knows row j's position, unit (-1: none)
-// and row there.
+// A window's 16 rows of K, at x, which may lie in any units: lane j knows row
+// j's position, unit (-1: none) and row there.  All of them are requested at
+// once; then every quad turns, encodes and stores rows g and g + 8, one after
+// the other where the encoder's registers are many.
 template <int T, int CODEC>
 __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uint8_t *x,
-                                            int64_t pos, int64_t unit, int r, float *copy,
+                                            int64_t pos, int64_t unit, int r, uint8_t *stage,
                                             int lane) {
-  using Raw = typename RowType<T>::raw4;
   constexpr int S = Stage<T>::S;
   const int g = lane >> 2, w = lane & 3;
-  int64_t at[2];
-  int64_t ps[2];
-  int rr[2];
-#pragma unroll
+  stage_rows<T>(stage, x, p.row[1], __ballot_sync(0xffffffffu, unit >= 0), lane);
+#pragma unroll (CODEC == KVQ_F16 ? 2 : 1)
   for (int rh = 0; rh < 2; ++rh) {
-    at[rh] = __shfl_sync(0xffffffffu, unit, g + 8 * rh);
-    ps[rh] = __shfl_sync(0xffffffffu, pos, g + 8 * rh);
-    rr[rh] = __shfl_sync(0xffffffffu, r, g + 8 * rh);
-  }
-  QuadCodes<CODEC> q[2];
-  Raw raw[2][8];
-#pragma unroll
-  for (int rh = 0; rh < 2; ++rh)
-    if (at[rh] >= 0) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        raw[rh][c] =
-            *reinterpret_cast<const Raw *>(x + (g + 8 * rh) * p.row[1] + (16 * c + 4 * w) * S);
-    }
-#pragma unroll
-  for (int rh = 0; rh < 2; ++rh) {
+    const int64_t at = __shfl_sync(0xffffffffu, unit, g + 8 * rh);
+    const int64_t ps = __shfl_sync(0xffffffffu, pos, g + 8 * rh);
+    const int rr = __shfl_sync(0xffffffffu, r, g + 8 * rh);
+    const uint8_t *mine = stage + (g + 8 * rh) * Stage<T>::kPitch;
     float v[8][4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) load4<T>(&raw[rh][c], v[c]);
-    const float *row = at[rh] >= 0 ? rope_row(p.rope, ps[rh], p.err) : p.rope.table;
-    if (p.kind == kQuadAny) quad_rotate_any<false>(p.rope, row, lane, 1.0f, copy, v);
-    else quad_rotate<false>(p.rope, p.kind, row, w, 1.0f, v);
-    quad_encode<CODEC>(v, w, q[rh]);
-  }
-  uint8_t *const cache = p.cache[0];
-  if (at[0] >= 0 && at[0] == at[1] && rr[1] == rr[0] + 8) {  // a unit's rows r and r + 8
-    quad_store<CODEC>(cache + at[0] * unit_bytes(CODEC), 4 * rr[0] + w, q);
-  } else {
-#pragma unroll
-    for (int rh = 0; rh < 2; ++rh)
-      if (at[rh] >= 0)
-        quad_store_row<CODEC>(cache + at[rh] * unit_bytes(CODEC), rr[rh], w, q[rh]);
+    for (int c = 0; c < 8; ++c) load4<T>(mine + (16 * c + 4 * w) * S, v[c]);
+    const float *row = at >= 0 ? rope_row(p.rope, ps, p.err) : p.rope.table;
+    if (p.kind == kQuadAny)
+      quad_rotate_any<false>(
+          p.rope, row, w, 1.0f, [&](int d, float(&o)[4]) { load4<T>(mine + d * S, o); },
+          [&](int d) { return load1<T>(mine + d * S); }, v);
+    else
+      quad_rotate<false>(p.rope, p.kind, row, w, 1.0f, v);
+    QuadCodes<CODEC> q;
+    quad_encode<CODEC>(v, w, q);
+    if (at >= 0) quad_store_row<CODEC>(p.cache[0] + at * unit_bytes(CODEC), rr, w, q);
   }
 }
 
@@ -544,16 +528,14 @@ __device__ __forceinline__ WindowRow window_row(const AppendRopeParams &p, int64
 template <int T>
 __device__ __forceinline__ void k_window(const AppendRopeParams &p, int64_t r0, int h,
                                          uint8_t *stage, int lane) {
-  static_assert(Stage<T>::kWarpBytes >= kQuadBytes, "the quads' copy takes the stage's place");
   const WindowRow w = window_row(p, r0, lane);
   const uint8_t *x = p.x[1] + r0 * p.row[1] + h * p.head[1];
   const int64_t unit = w.unit < 0 ? -1 : w.unit + h * unit_step(p);
-  float *copy = reinterpret_cast<float *>(stage);
   switch (p.codec[0]) {
-    case KVQ_F16: quad_window<T, KVQ_F16>(p, x, w.pos, unit, w.r, copy, lane); break;
-    case KVQ_Q8_0: quad_window<T, KVQ_Q8_0>(p, x, w.pos, unit, w.r, copy, lane); break;
-    case KVQ_Q4_0: quad_window<T, KVQ_Q4_0>(p, x, w.pos, unit, w.r, copy, lane); break;
-    default: quad_window<T, KVQ_TURBO4>(p, x, w.pos, unit, w.r, copy, lane); break;
+    case KVQ_F16: quad_window<T, KVQ_F16>(p, x, w.pos, unit, w.r, stage, lane); break;
+    case KVQ_Q8_0: quad_window<T, KVQ_Q8_0>(p, x, w.pos, unit, w.r, stage, lane); break;
+    case KVQ_Q4_0: quad_window<T, KVQ_Q4_0>(p, x, w.pos, unit, w.r, stage, lane); break;
+    default: quad_window<T, KVQ_TURBO4>(p, x, w.pos, unit, w.r, stage, lane); break;
   }
 }
 

@@ -6,7 +6,7 @@
 // with no exchange between lanes but a block's maximum (two shuffles).  The
 // planes of a rotation lie inside a lane too, for the interleaved layout and
 // for half layouts whose rot_dim is a multiple of 32; otherwise the partners
-// are read from a copy of the rows in shared memory.
+// are read from the rows in shared memory.
 #pragma once
 
 #include "kvq_encode.cuh"
@@ -65,18 +65,13 @@ __device__ __forceinline__ void quad_rotate_half(const RopeArgs &p, const float 
   }
 }
 
-// Planes anywhere: every lane's values go to shared memory, and each lane reads
-// its values' partners there (all 32 lanes).
-template <bool PURE>
-__device__ __forceinline__ void quad_rotate_any(const RopeArgs &p, const float *row, int lane,
-                                                float sign, float *copy, float (&v)[8][4]) {
-  const int w = lane & 3, h = p.rot >> 1;
-  float *mine = copy + (lane >> 2) * kQuadPitch;
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<float4 *>(mine + 16 * c + 4 * w) =
-        make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
-  __syncwarp();
+// Planes anywhere, by the unrotated row: four(d, o) its values d .. d + 3 (d a
+// multiple of 4), one(d) its value d.
+template <bool PURE, typename Four, typename One>
+__device__ __forceinline__ void quad_rotate_any(const RopeArgs &p, const float *row, int w,
+                                                float sign, Four four, One one,
+                                                float (&v)[8][4]) {
+  const int h = p.rot >> 1;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const int d0 = 16 * c + 4 * w;
@@ -84,10 +79,9 @@ __device__ __forceinline__ void quad_rotate_any(const RopeArgs &p, const float *
     float o[4], co[4], si[4];
     if ((h & 3) == 0) {  // the four values lie in one half, their partners together
       const int e = d0 < h ? d0 : d0 - h;
-      const float4 x = *reinterpret_cast<const float4 *>(mine + (d0 < h ? d0 + h : e));
+      four(d0 < h ? d0 + h : e, o);
       const float4 t = *reinterpret_cast<const float4 *>(row + 2 * e);
       const float4 u = *reinterpret_cast<const float4 *>(row + 2 * e + 4);
-      o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
       co[0] = t.x; co[1] = t.z; co[2] = u.x; co[3] = u.z;
       si[0] = t.y; si[1] = t.w; si[2] = u.y; si[3] = u.w;
     } else {
@@ -95,7 +89,7 @@ __device__ __forceinline__ void quad_rotate_any(const RopeArgs &p, const float *
       for (int i = 0; i < 4; ++i) {
         const int d = d0 + i < p.rot ? d0 + i : 0, e = d < h ? d : d - h;
         const float2 t = *reinterpret_cast<const float2 *>(row + 2 * e);
-        o[i] = mine[d < h ? d + h : e];
+        o[i] = one(d < h ? d + h : e);
         co[i] = t.x;
         si[i] = t.y;
       }
@@ -108,6 +102,26 @@ __device__ __forceinline__ void quad_rotate_any(const RopeArgs &p, const float *
         v[c][i] = __fadd_rn(__fmul_rn(v[c][i], cc), __fmul_rn(o[i], d0 + i < h ? -ss : ss));
     }
   }
+}
+
+// The same by a copy of the quad's row in shared memory (all 32 lanes).
+template <bool PURE>
+__device__ __forceinline__ void quad_rotate_copied(const RopeArgs &p, const float *row, int lane,
+                                                   float sign, float *copy, float (&v)[8][4]) {
+  const int w = lane & 3;
+  float *mine = copy + (lane >> 2) * kQuadPitch;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4 *>(mine + 16 * c + 4 * w) =
+        make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+  __syncwarp();
+  quad_rotate_any<PURE>(
+      p, row, w, sign,
+      [&](int d, float(&o)[4]) {
+        const float4 x = *reinterpret_cast<const float4 *>(mine + d);
+        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+      },
+      [&](int d) { return mine[d]; }, v);
   __syncwarp();  // the copy may be written again
 }
 
@@ -222,38 +236,6 @@ __device__ __forceinline__ void quad_load_row(const uint8_t *unit, int r, int w,
     } else {
       q.w[b] = *reinterpret_cast<const uint32_t *>(u + (b >> 1) * 512 + ((b & 1) * 2 + rh) * 4);
     }
-  }
-}
-
-// Both rows (g, g + 8) of the lane, to the unit.
-template <int CODEC>
-__device__ __forceinline__ void quad_store(uint8_t *unit, int lane,
-                                           const QuadCodes<CODEC> (&q)[2]) {
-  uint4 *u = reinterpret_cast<uint4 *>(unit) + lane;
-  const int g = lane >> 2, w = lane & 3;
-  if (CODEC == KVQ_F16) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t *d = &q[k & 1].w[4 * (k >> 1)];
-      u[k * 32] = make_uint4(d[0], d[1], d[2], d[3]);
-    }
-    return;
-  }
-  uint16_t *sc = reinterpret_cast<uint16_t *>(unit + unit_scale_offset(CODEC));
-  if (CODEC == KVQ_TURBO4) {
-    if (w < 2) sc[2 * g + w] = w == 0 ? q[0].scale : q[1].scale;
-  } else {
-    sc[8 * g + w] = q[0].scale;
-    sc[8 * g + 4 + w] = q[1].scale;
-  }
-  if (CODEC == KVQ_Q8_0) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      u[b * 32] = make_uint4(q[0].w[2 * b], q[0].w[2 * b + 1], q[1].w[2 * b], q[1].w[2 * b + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      u[j * 32] = make_uint4(q[0].w[2 * j], q[1].w[2 * j], q[0].w[2 * j + 1], q[1].w[2 * j + 1]);
   }
 }
 

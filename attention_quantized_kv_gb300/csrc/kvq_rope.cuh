@@ -189,6 +189,13 @@ __device__ __forceinline__ void load4(const void *p, float (&x)[4]) {
 
 // Four consecutive values, rounded once to the type.
 template <int T>
+__device__ __forceinline__ float load1(const void *p) {
+  if (T == KVQ_T_F32) return *static_cast<const float *>(p);
+  const uint16_t v = *static_cast<const uint16_t *>(p);
+  return T == KVQ_T_F16 ? __half2float(__ushort_as_half(v))
+                        : __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+template <int T>
 __device__ __forceinline__ void store4(void *p, const float (&x)[4]) {
   if (T == KVQ_T_F32) {
     *static_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
       quad_load_row<CODEC>(slot, g + 8 * rh, w, q);
       quad_decode<CODEC>(q, w, v);
       if (ANY)
-        quad_rotate_any<true>(p.rope, angles, lane, sign, copies[ANY ? threadIdx.x >> 5 : 0], v);
+        quad_rotate_copied<true>(p.rope, angles, lane, sign, copies[ANY ? threadIdx.x >> 5 : 0], v);
       else
         quad_rotate<true>(p.rope, p.kind, angles, w, sign, v);
       quad_encode<CODEC>(v, w, q);
