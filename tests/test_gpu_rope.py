@@ -1060,3 +1060,44 @@ def test_evict_and_table_on_another_stream():
                         (*want, M.k_cache, M.v_cache, M.seq_lens)):
             assert torch.equal(a, b)
         assert L.err.item() == 0
+
+
+@pytest.mark.parametrize("n_seqs", [3, 9])
+def test_two_graphs_share_a_workspace(n_seqs):
+    """Decode steps of two layers captured in two graphs over one workspace and
+    replayed in turn, between shifts by captured deltas, against eager calls."""
+    n_kv, n_q, cap = 2, 8, 512
+    rope = kvq.Rope(n_pos=cap)
+    lens = [(s * 53) % 490 for s in range(n_seqs)]
+    layers = [_random_layer(n_seqs, n_kv, n_q, cap, Q8, F16, i == 1, lens, 70 + i) for i in range(2)]
+    pairs = [(L, _twin(L, t)) for L, t in layers]
+    ws = torch.zeros(max(kvq.attn_decode_workspace(L, cap) for L, _ in layers), dtype=torch.uint8,
+                     device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.randn((n_seqs, h, 128), generator=g, device="cuda").half() for h in (n_q, n_kv, n_kv))
+    delta = torch.randint(-3, 3, (n_seqs, cap), generator=g, device="cuda", dtype=torch.int32)
+    outs = [[torch.empty_like(q) for _ in p] for p in pairs]
+
+    def step(L, out):
+        kvq.attn_decode_append_rope(L, rope, k, v, q, SCALE, out, None, cap, ws)
+        kvq.kv_rope_shift(L, rope, delta)
+
+    warm = _twin(*layers[0])
+    step(warm, torch.empty_like(q))
+    torch.cuda.synchronize()
+    graphs = []
+    for i in (0, 1):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            step(pairs[i][0], outs[i][0])
+    for _ in range(4):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        a, b = pairs[i]
+        for _ in range(4):
+            step(b, outs[i][1])
+        assert a.seq_lens.tolist() == b.seq_lens.tolist() == [n + 4 for n in lens]
+        assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.v_cache, b.v_cache)
+        assert torch.equal(*outs[i]) and a.err.item() == b.err.item() == 0
