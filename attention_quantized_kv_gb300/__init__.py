@@ -426,7 +426,8 @@ def kvq_rope_freqs(rot_dim: int = HEAD_DIM, base: float = 10000.0, scaling: int 
                    high: float | None = None) -> list:
     """Radians per position of each of the rot_dim / 2 planes.  ``low`` and ``high`` are the
     turns over ``orig_len`` positions between which KVQ_ROPE_PARTS and KVQ_ROPE_YARN blend the
-    scaled frequency into the plain one (``high`` defaults to 4 and 32)."""
+    scaled frequency into the plain one.  ``high`` defaults to 32 for KVQ_ROPE_YARN, as Peng et
+    al. 2023 have it, and to 4 for KVQ_ROPE_PARTS (a narrower blend than their 1 to 32)."""
     if high is None:
         high = 32.0 if scaling == KVQ_ROPE_YARN else 4.0
     out = array("d", bytes(8 * max(1, int(rot_dim) // 2)))

@@ -70,7 +70,7 @@ int kvq_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
   if (scaling == KVQ_ROPE_YARN) {
     const double turn = rot_dim / (2.0 * log(base));
     l = fmax(floor(turn * log(orig_len / (high * kvq::kTwoPi))), 0.0);
-    h = fmin(ceil(turn * log(orig_len / (low * kvq::kTwoPi))), n - 1.0);
+    h = fmin(ceil(turn * log(orig_len / (low * kvq::kTwoPi))), rot_dim - 1.0);
   }
   for (int i = 0; i < n; ++i) {
     const double f = pow(base, -2.0 * i / rot_dim);

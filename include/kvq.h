@@ -396,13 +396,14 @@ typedef enum { KVQ_ROPE_INTERLEAVED = 0, KVQ_ROPE_HALF = 1 } kvq_rope_layout;
  *           (one plane: unchanged)
  *   PARTS   by the turns r = orig_len f_i / 2 pi that a plane makes over the
  *           original context: keep = clamp((r - low) / (high - low), 0, 1),
- *           f_i keep + f_i / factor (1 - keep)   (Peng et al. 2023, eq. for
- *           the interpolation by parts)
+ *           f_i keep + f_i / factor (1 - keep)   (the interpolation by parts
+ *           of Peng et al. 2023, who take low = 1 and high = 32)
  *   YARN    the same blend with keep = 1 - clamp((i - l) / max(h - l, 0.001),
- *           0, 1), where l = max(floor(at(high)), 0) and h =
- *           min(ceil(at(low)), rot_dim / 2 - 1) bound the planes that make
- *           `high` and `low` turns: at(r) = rot_dim ln(orig_len / (2 pi r)) /
- *           (2 ln base)                                                     */
+ *           0, 1) (Peng et al. 2023, as published checkpoints are run), where
+ *           l = max(floor(at(high)), 0) and h = min(ceil(at(low)), rot_dim - 1)
+ *           are the plane indexes that make `high` and `low` turns: at(r) =
+ *           rot_dim ln(orig_len / (2 pi r)) / (2 ln base).  h may lie past the
+ *           last plane, rot_dim / 2 - 1, where even that one makes `low` turns */
 typedef enum {
     KVQ_ROPE_PLAIN = 0,
     KVQ_ROPE_LINEAR = 1,
