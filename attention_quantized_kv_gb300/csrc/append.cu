@@ -562,9 +562,7 @@ __device__ __forceinline__ void rq_encode_item(const uint8_t *su, uint8_t *du, i
     }
     rq_store_chunk<SIDE, DC>(du, q, w, x, k);
   }
-  const bool exact =
-      DC == KVQ_Q8_0 ? hi < 0.5f - 0x1p-14f : (lo > 0x1p-17f && hi < 1.0f - 0x1p-17f);
-  if (d != 0.0f && !exact) {  // rare: some quotient near a boundary
+  if (d != 0.0f && !codes_exact<DC>(lo, hi)) {  // rare: some quotient near a boundary
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int w = (c + rot) & 3;

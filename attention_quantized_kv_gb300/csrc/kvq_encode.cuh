@@ -46,10 +46,28 @@ __device__ __forceinline__ int q4_from_quotient(float x, float d, float rcp) {
   const float u = __fadd_rn(__fmul_rn(x, rcp), 8.5f);
   const float fm = __fadd_rn(__fsub_rn(u, 0.5f), kRoundMagic);
   const float fr = __fsub_rn(u, __fsub_rn(fm, kRoundMagic));  // u - floor(u)
-  const int v = (fr > 0x1p-17f && fr < 1.0f - 0x1p-17f)
-                    ? __float_as_int(fm) - kRoundMagicBits
-                    : static_cast<int>(__fadd_rn(__fdiv_rn(x, d), 8.5f));  // truncation; u >= 0.5
-  return v > 15 ? 15 : v;
+  if (fr > 0x1p-17f && fr < 1.0f - 0x1p-17f) return min(__float_as_int(fm) - kRoundMagicBits, 15);
+  // truncation; u >= 0.5 but for the last steps of fp32, where d is a rounded
+  // m / -8 and a negative integer keeps its lowest 4 bits
+  return min(static_cast<int>(__fadd_rn(__fdiv_rn(x, d), 8.5f)), 15) & 15;
+}
+
+// The largest (smallest) of three values, NaN if one of them is (fmaxf and
+// fminf leave NaN out).
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {  // of magnitudes
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // Bytes 0 of a, b, c, d as one word (a in the lowest byte).
@@ -64,7 +82,9 @@ __device__ __forceinline__ uint32_t clamp15x4(uint32_t w) { return w - ((w >> 4)
 // q4_0: the level before the clamp), and lo / hi collect the chunk's
 // distances from the rounding boundaries (q8_0: hi = the largest distance
 // to the nearest integer; q4_0: lo, hi = the range of u - floor(u)), which
-// say whether the fast path is the exact one for every value.
+// say whether the fast path is the exact one for every value.  Where 1/d is
+// infinite (d below 2^-128) the quotients are infinities or NaN and so is
+// their distance: lo and hi keep a NaN, and codes_exact refuses it.
 template <int DC>
 __device__ __forceinline__ void rq_codes_fast(const float (&x)[8], float rcp, uint32_t (&k)[8],
                                               float &lo, float &hi) {
@@ -76,7 +96,7 @@ __device__ __forceinline__ void rq_codes_fast(const float (&x)[8], float rcp, ui
       const float2 t = __fmul2_rn(make_float2(x[j], x[j + 1]), r2);
       const float2 tm = __fadd2_rn(t, m2);
       const float2 fr = __ffma2_rn(__fadd2_rn(tm, nm2), n1, t);  // t - round(t)
-      hi = fmaxf(hi, fmaxf(fabsf(fr.x), fabsf(fr.y)));
+      hi = max3_abs_nan(hi, fr.x, fr.y);
       k[j] = __float_as_uint(tm.x);
       k[j + 1] = __float_as_uint(tm.y);
     } else {
@@ -84,8 +104,8 @@ __device__ __forceinline__ void rq_codes_fast(const float (&x)[8], float rcp, ui
           __fadd2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), r2), make_float2(8.5f, 8.5f));
       const float2 fm = __fadd2_rn(__fadd2_rn(u, make_float2(-0.5f, -0.5f)), m2);
       const float2 fr = __ffma2_rn(__fadd2_rn(fm, nm2), n1, u);  // u - floor(u)
-      lo = fminf(lo, fminf(fr.x, fr.y));
-      hi = fmaxf(hi, fmaxf(fr.x, fr.y));
+      lo = min3_nan(lo, fr.x, fr.y);
+      hi = max3_nan(hi, fr.x, fr.y);
       k[j] = __float_as_uint(fm.x);
       k[j + 1] = __float_as_uint(fm.y);
     }

@@ -47,7 +47,7 @@
  *   q4_0 : per block fp16 d16 + 16 bytes of nibbles.      72 bytes / row
  *          m = the signed x with the largest |x| (lowest index wins ties);
  *          d = m / -8 (fp32 RN); t = x / d (fp32 RN; 0 when d == 0);
- *          u = t + 8.5 (fp32 RN); q = min(15, trunc(u));
+ *          u = t + 8.5 (fp32 RN); q = min(15, trunc(u)), its lowest 4 bits;
  *          canonical byte j = q[j] | q[j+16] << 4; d16 = fp16_RN(d).
  *          x^ = d16 * (q - 8).
  *   turbo4: a Walsh-Hadamard-rotated 4-bit row (the turbo4 row of the
