@@ -485,7 +485,8 @@ __device__ __forceinline__ void rq_encode_item(const uint8_t *su, uint8_t *du, i
   // pass 1: amax (q8_0) or the largest and smallest value (q4_0)
   float pmax, nmin;
   if (SIDE == 0 && SC == KVQ_F16) {  // on the fp16 values themselves (exact)
-    __half2 hp = __float2half2_rn(-65504.0f), hn = __float2half2_rn(65504.0f);
+    __half2 hp = __float2half2_rn(DC == KVQ_Q8_0 ? 0.0f : -INFINITY);
+    __half2 hn = __float2half2_rn(INFINITY);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint4 raw = *reinterpret_cast<const uint4 *>(su + rq_k_off(SC, q, (c + rot) & 3));
@@ -526,7 +527,9 @@ __device__ __forceinline__ void rq_encode_item(const uint8_t *su, uint8_t *du, i
     d = __fdiv_rn(pmax, 127.0f);
   } else {
     float m = pmax > -nmin ? pmax : nmin;
-    if (pmax == -nmin) {  // both signs reach the largest magnitude (or all zero)
+    if (pmax < nmin) {  // all NaN
+      m = 0.0f;
+    } else if (pmax == -nmin) {  // both signs reach the largest magnitude (or all zero)
       float best = -1.0f;
       int idx = 32;
 #pragma unroll
@@ -547,7 +550,7 @@ __device__ __forceinline__ void rq_encode_item(const uint8_t *su, uint8_t *du, i
   *reinterpret_cast<__half *>(du + unit_scale_offset(DC) + soff) = __float2half_rn(d);
   const float rcp = d != 0.0f ? __frcp_rn(d) : 0.0f;
   // pass 2: the codes
-  float lo = 1.0f, hi = 0.0f;
+  float far = 0.0f;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int w = (c + rot) & 3;
@@ -555,14 +558,14 @@ __device__ __forceinline__ void rq_encode_item(const uint8_t *su, uint8_t *du, i
     uint32_t k[8];
     rq_load_chunk<SIDE, SC>(su, q, w, ds, x);
     if (d != 0.0f) {
-      rq_codes_fast<DC>(x, rcp, k, lo, hi);
+      rq_codes_fast<DC>(x, rcp, k, far);
     } else {
 #pragma unroll
       for (int v = 0; v < 8; ++v) k[v] = DC == KVQ_Q8_0 ? 0u : 8u;
     }
     rq_store_chunk<SIDE, DC>(du, q, w, x, k);
   }
-  if (d != 0.0f && !codes_exact<DC>(lo, hi)) {  // rare: some quotient near a boundary
+  if (d != 0.0f && !codes_exact<DC>(far)) {  // rare: some quotient near a boundary
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int w = (c + rot) & 3;

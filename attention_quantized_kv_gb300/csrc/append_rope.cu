@@ -445,7 +445,8 @@ __device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
         lo = fminf(lo, x[i]);
       }
       float m = hi > -lo ? hi : lo;
-      if (hi == -lo) {  // the first of them
+      if (hi == -lo) {  // the first of them (none: all NaN)
+        m = 0.0f;
 #pragma unroll
         for (int i = 31; i >= 0; --i)
           if (fabsf(x[i]) == hi) m = x[i];

@@ -6,7 +6,8 @@
 // rotated turbo4 rows, with the fp32 encoder formulas of include/kvq.h,
 // evaluated with explicit IEEE round-to-nearest operations so that the bytes
 // are reproducible bit for bit.  One warp encodes one 128-value row: lane l
-// holds dims 4l..4l+3.
+// holds dims 4l..4l+3.  A NaN is left out of a block's maximum and takes the
+// code of 0, as an infinity's quotient by the infinite scale does.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -35,7 +36,16 @@ __device__ __forceinline__ int q8_from_quotient(float x, float d, float rcp) {
   const float tm = __fadd_rn(t, kRoundMagic);
   const float dist = fabsf(__fsub_rn(t, __fsub_rn(tm, kRoundMagic)));  // to the nearest integer
   if (fabsf(__fsub_rn(dist, 0.5f)) > 0x1p-14f) return __float_as_int(tm) - kRoundMagicBits;
-  return static_cast<int>(roundf(__fdiv_rn(x, d)));
+  return __float2int_rz(roundf(__fdiv_rn(x, d)));  // (NaN: 0)
+}
+
+// The 4-bit rule by its division (rare; a call, as its length inline cost the
+// callers more: 2048 appended rows of 8 heads into q4_0 13.9 instead of 15.0 us
+// with the ties below).  A NaN gives 8.  u >= 0.5 but for the last steps of
+// fp32, where d is a rounded m / -8: a negative integer keeps its lowest 4 bits.
+__device__ __noinline__ int q4_exact(float x, float d) {
+  const float t = __fdiv_rn(x, d);
+  return t != t ? 8 : min(__float2int_rz(__fadd_rn(t, 8.5f)), 15) & 15;
 }
 
 // q4_0 and turbo4: q = min(15, trunc(RN(RN(x/d) + 8.5))) with |x/d| <= 8 (1 +
@@ -46,27 +56,15 @@ __device__ __forceinline__ int q4_from_quotient(float x, float d, float rcp) {
   const float u = __fadd_rn(__fmul_rn(x, rcp), 8.5f);
   const float fm = __fadd_rn(__fsub_rn(u, 0.5f), kRoundMagic);
   const float fr = __fsub_rn(u, __fsub_rn(fm, kRoundMagic));  // u - floor(u)
-  if (fr > 0x1p-17f && fr < 1.0f - 0x1p-17f) return min(__float_as_int(fm) - kRoundMagicBits, 15);
-  // truncation; u >= 0.5 but for the last steps of fp32, where d is a rounded
-  // m / -8 and a negative integer keeps its lowest 4 bits
-  return min(static_cast<int>(__fadd_rn(__fdiv_rn(x, d), 8.5f)), 15) & 15;
+  return fr > 0x1p-17f && fr < 1.0f - 0x1p-17f ? min(__float_as_int(fm) - kRoundMagicBits, 15)
+                                               : q4_exact(x, d);
 }
 
-// The largest (smallest) of three values, NaN if one of them is (fmaxf and
-// fminf leave NaN out).
-__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {  // of magnitudes
+// The largest magnitude of three values, NaN if one of them is (fmaxf leaves
+// NaN out).
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float y;
   asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ float min3_nan(float a, float b, float c) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -79,49 +77,40 @@ __device__ __forceinline__ uint32_t clamp15x4(uint32_t w) { return w - ((w >> 4)
 
 // The quotient path of q8_from_quotient / q4_from_quotient on one chunk, two
 // values per instruction: k[v] gets the fast path's code (its lowest byte;
-// q4_0: the level before the clamp), and lo / hi collect the chunk's
-// distances from the rounding boundaries (q8_0: hi = the largest distance
-// to the nearest integer; q4_0: lo, hi = the range of u - floor(u)), which
-// say whether the fast path is the exact one for every value.  Where 1/d is
+// q4_0: the level before the clamp), and far collects the chunk's largest
+// distance of t (q4_0: of u - 0.5) from the integer next to it, which says
+// whether the fast path is the exact one for every value.  Where 1/d is
 // infinite (d below 2^-128) the quotients are infinities or NaN and so is
-// their distance: lo and hi keep a NaN, and codes_exact refuses it.
+// their distance: far keeps a NaN, and codes_exact refuses it.
 template <int DC>
 __device__ __forceinline__ void rq_codes_fast(const float (&x)[8], float rcp, uint32_t (&k)[8],
-                                              float &lo, float &hi) {
+                                              float &far) {
   const float2 r2 = make_float2(rcp, rcp), m2 = make_float2(kRoundMagic, kRoundMagic);
   const float2 nm2 = make_float2(-kRoundMagic, -kRoundMagic), n1 = make_float2(-1.0f, -1.0f);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    if (DC == KVQ_Q8_0) {
-      const float2 t = __fmul2_rn(make_float2(x[j], x[j + 1]), r2);
-      const float2 tm = __fadd2_rn(t, m2);
-      const float2 fr = __ffma2_rn(__fadd2_rn(tm, nm2), n1, t);  // t - round(t)
-      hi = max3_abs_nan(hi, fr.x, fr.y);
-      k[j] = __float_as_uint(tm.x);
-      k[j + 1] = __float_as_uint(tm.y);
-    } else {
-      const float2 u =
-          __fadd2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), r2), make_float2(8.5f, 8.5f));
-      const float2 fm = __fadd2_rn(__fadd2_rn(u, make_float2(-0.5f, -0.5f)), m2);
-      const float2 fr = __ffma2_rn(__fadd2_rn(fm, nm2), n1, u);  // u - floor(u)
-      lo = min3_nan(lo, fr.x, fr.y);
-      hi = max3_nan(hi, fr.x, fr.y);
-      k[j] = __float_as_uint(fm.x);
-      k[j + 1] = __float_as_uint(fm.y);
-    }
+    float2 t = __fmul2_rn(make_float2(x[j], x[j + 1]), r2);
+    if (DC != KVQ_Q8_0)  // floor(u) = the integer next to u - 0.5
+      t = __fadd2_rn(__fadd2_rn(t, make_float2(8.5f, 8.5f)), make_float2(-0.5f, -0.5f));
+    const float2 tm = __fadd2_rn(t, m2);
+    const float2 fr = __ffma2_rn(__fadd2_rn(tm, nm2), n1, t);  // t - round(t)
+    far = max3_abs_nan(far, fr.x, fr.y);
+    k[j] = __float_as_uint(tm.x);
+    k[j + 1] = __float_as_uint(tm.y);
   }
 }
 
-// Whether the codes that rq_codes_fast gave a block (lo, hi over all its
-// chunks) are the exact path's.
+// Whether the codes that rq_codes_fast gave a block (far over all its chunks)
+// are the exact path's.
 template <int DC>
-__device__ __forceinline__ bool codes_exact(float lo, float hi) {
-  return DC == KVQ_Q8_0 ? hi < 0.5f - 0x1p-14f : (lo > 0x1p-17f && hi < 1.0f - 0x1p-17f);
+__device__ __forceinline__ bool codes_exact(float far) {
+  return far < 0.5f - (DC == KVQ_Q8_0 ? 0x1p-14f : 0x1p-17f);
 }
 
 // q8_0: amax over the 8 lanes of the block, d = amax/127, q = round(x/d).
 __device__ __forceinline__ void encode_q8(const float (&x)[4], int (&q)[4], __half &d16) {
   float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+  a = fmaxf(a, 0.0f);  // (four NaN)
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   const float d = __fdiv_rn(a, 127.0f);
@@ -131,24 +120,50 @@ __device__ __forceinline__ void encode_q8(const float (&x)[4], int (&q)[4], __ha
   for (int i = 0; i < 4; ++i) q[i] = d != 0.0f ? q8_from_quotient(x[i], d, rcp) : 0;
 }
 
-// q4_0: signed value of largest magnitude (lowest dim wins ties), d = m/-8,
+// The first of the dims of LANES lanes that hold +-hi, times 2, plus its sign
+// (all 32 lanes; 2^20: none).  A call: ties are rare.
+template <int LANES>
+__device__ __noinline__ int first_of(float x0, float x1, float x2, float x3, float hi, int lane) {
+  const float x[4] = {x0, x1, x2, x3};
+  int best = 1 << 20;
+#pragma unroll
+  for (int i = 3; i >= 0; --i)
+    if (fabsf(x[i]) == hi) best = (4 * lane + i) * 2 + (__float_as_uint(x[i]) >> 31);
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+  return best;
+}
+
+// The signed value of largest magnitude of the rows' groups of LANES lanes,
+// the lowest dim on ties, 0 where all are NaN (all 32 lanes).
+template <int LANES>
+__device__ __forceinline__ float lanes_signed_max(const float (&x)[4], int lane) {
+  float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi = fmaxf(hi, x[i]);
+    lo = fminf(lo, x[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  const bool tie = hi == -lo;
+  if (__any_sync(0xffffffffu, tie)) {
+    const int best = first_of<LANES>(x[0], x[1], x[2], x[3], hi, lane);
+    if (tie) {  // (+-0 keeps its sign; no dim at all: only NaN)
+      const float size = best == 1 << 20 ? 0.0f : fabsf(hi);
+      return (best & 1) ? -size : size;
+    }
+  }
+  return hi > -lo ? hi : lo;
+}
+
+// q4_0: m = the block's signed value of largest magnitude, d = m/-8,
 // q = min(15, trunc(x/d + 8.5)).
 __device__ __forceinline__ void encode_q4(const float (&x)[4], int lane, int (&q)[4], __half &d16) {
-  float best = fabsf(x[0]);
-  float m = x[0];
-  int idx = 4 * lane;
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    const float a = fabsf(x[i]);
-    if (a > best) { best = a; m = x[i]; idx = 4 * lane + i; }
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-    const float om = __shfl_xor_sync(0xffffffffu, m, o);
-    const int oi = __shfl_xor_sync(0xffffffffu, idx, o);
-    if (ob > best || (ob == best && oi < idx)) { best = ob; m = om; idx = oi; }
-  }
+  const float m = lanes_signed_max<8>(x, lane);
   const float d = __fdiv_rn(m, -8.0f);
   d16 = __float2half_rn(d);
   const float rcp = d != 0.0f ? __frcp_rn(d) : 0.0f;
@@ -166,21 +181,7 @@ __device__ __forceinline__ void encode_turbo4(const float (&x)[4], int lane, int
   fwht128_warp(y, lane);
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] *= 0.125f;
-  float best = fabsf(y[0]);
-  float m = y[0];
-  int idx = 4 * lane;
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    const float a = fabsf(y[i]);
-    if (a > best) { best = a; m = y[i]; idx = 4 * lane + i; }
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-    const float om = __shfl_xor_sync(0xffffffffu, m, o);
-    const int oi = __shfl_xor_sync(0xffffffffu, idx, o);
-    if (ob > best || (ob == best && oi < idx)) { best = ob; m = om; idx = oi; }
-  }
+  const float m = lanes_signed_max<32>(y, lane);
   const float d = __fdiv_rn(m, -8.0f);
   d16 = __float2half_rn(d);
   const float rcp = d != 0.0f ? __frcp_rn(d) : 0.0f;

@@ -324,7 +324,7 @@ __device__ __forceinline__ float quad_max(float x) {
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
-// The codes of 8 values value by value: where rq_codes_fast's distances say
+// The codes of 8 values value by value: where rq_codes_fast's distance says
 // that one lies too near a rounding boundary (of random values one group of
 // eight in 2^10 for q8_0, in 2^13 for 4 bits).  A call, so that its length stays out of the callers.
 template <int DC>
@@ -344,18 +344,18 @@ __device__ __noinline__ uint2 codes8_exact(float x0, float x1, float x2, float x
 template <int DC>
 __device__ __forceinline__ uint2 quad_codes8(const float (&x)[8], float d, float rcp) {
   uint32_t k[8];
-  float lo = 1.0f, hi = 0.0f;
-  rq_codes_fast<DC>(x, rcp, k, lo, hi);
+  float far = 0.0f;
+  rq_codes_fast<DC>(x, rcp, k, far);
   uint2 c = make_uint2(low_bytes4(k[0], k[1], k[2], k[3]), low_bytes4(k[4], k[5], k[6], k[7]));
   if (d == 0.0f) c = DC == KVQ_Q8_0 ? make_uint2(0u, 0u) : make_uint2(0x08080808u, 0x08080808u);
-  else if (!codes_exact<DC>(lo, hi))
+  else if (!codes_exact<DC>(far))
     c = codes8_exact<DC>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], d, rcp);
   return c;
 }
 
 // The scale's numerator for the 4-bit rule over the values of N planes groups
-// of the quad: the signed value of largest magnitude, the lowest dim on ties
-// (all 32 lanes; c0 .. c0 + N - 1).
+// of the quad: the signed value of largest magnitude, the lowest dim on ties,
+// 0 where all are NaN (all 32 lanes; c0 .. c0 + N - 1).
 template <int N>
 __device__ __forceinline__ float quad_signed_max(const float (&v)[8][4], int c0, int w) {
   float hi = -INFINITY, lo = INFINITY;
@@ -380,7 +380,10 @@ __device__ __forceinline__ float quad_signed_max(const float (&v)[8][4], int c0,
       }
     best = min(best, __shfl_xor_sync(0xffffffffu, best, 1));
     best = min(best, __shfl_xor_sync(0xffffffffu, best, 2));
-    if (tie) return (best & 1) ? -fabsf(hi) : fabsf(hi);  // (+-0 keeps its sign)
+    if (tie) {  // (+-0 keeps its sign; no dim at all: only NaN)
+      const float size = best == 1 << 20 ? 0.0f : fabsf(hi);
+      return (best & 1) ? -size : size;
+    }
   }
   return hi > -lo ? hi : lo;
 }

@@ -65,6 +65,12 @@
  *          Attention never forms x^: q . x^ = (H (s * q) / 16) . y^, so the
  *          kernels rotate the query once, accumulate V in the rotated space
  *          and rotate the output back once.
+ *   Values that are not finite: f16 keeps them (a NaN's payload may change).
+ *   In the other codecs a NaN is left out of the maximum (amax, m; 0 where a
+ *   block is all NaN) and takes the code of 0 (q = 0, level 8): it reads back
+ *   as 0, and a turbo4 row whose sums are all NaN, as one NaN makes them, as
+ *   zeros.  An infinity makes d16 infinite and every code that of 0: its block
+ *   (turbo4: its row) reads back as NaN.  The bytes are the same on every path.
  *   The canonical row is the row's four blocks end to end (d16 little-endian
  *   before each block's quants); for turbo4 the row's d16 then its 64 bytes.
  *

@@ -38,7 +38,7 @@ def _tensor(x, dtype):
     return torch.from_numpy(h.view(np.int16)).view(torch.float16).cuda()
 
 
-KINDS = [FINITE]
+KINDS = [FINITE, OTHER]
 
 
 def _specials(dtype, kind, n_kv=2):
@@ -73,7 +73,9 @@ def _same_rows(codec, got, want):
         assert (a[~nan] == b[~nan]).all()
         return
     bad = np.argwhere((got != want).any(axis=-1))
-    assert len(bad) == 0, (codec, len(bad), bad[:4].tolist())
+    first = [] if len(bad) == 0 else np.argwhere(got[tuple(bad[0])] != want[tuple(bad[0])])[:4, 0]
+    assert len(bad) == 0, (codec, len(bad), bad[:4].tolist(),
+                           [(int(i), int(got[tuple(bad[0])][i]), int(want[tuple(bad[0])][i])) for i in first])
 
 
 def _check_side(L, table, side, want, at):
