@@ -60,8 +60,8 @@ def _stream_ptr(stream) -> int:
 
 
 def _hand_over(stream, *tensors) -> None:
-    """Tensors of the current stream's are used on another one next: that stream waits for what
-    fills them, and their memory is given to nothing else before its work on them is done."""
+    """Tensors of the current stream's (or None) are used on another one next: that stream waits for
+    what fills them, and their memory is given to nothing else before its work on them is done."""
     if stream is None:
         return
     current = torch.cuda.current_stream(tensors[0].device)
@@ -69,7 +69,8 @@ def _hand_over(stream, *tensors) -> None:
         return
     stream.wait_stream(current)
     for t in tensors:
-        t.record_stream(stream)
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _ptr(t) -> int | None:
@@ -358,7 +359,8 @@ def evict(layer: KVLayer, scores, n_sink: int, n_recent: int, n_evict: int, stre
     delta = torch.empty((layer.n_seqs, layer.capacity if rope is not None else 0),
                         dtype=torch.int32, device=dev)
     _hand_over(stream, ev, nev, k_dst, v_dst, s_dst, lens, delta, scores, layer.k_cache,
-               layer.v_cache, layer.seq_lens)
+               layer.v_cache, layer.seq_lens, layer.block_table, layer.err,
+               None if rope is None else rope.table)
     kv_evict_select(layer, scores, n_sink, n_recent, n_evict, ev, nev, stream)
     kv_compact(layer, ev, nev, k_dst, v_dst, scores, s_dst, lens, stream)
     if rope is not None:
