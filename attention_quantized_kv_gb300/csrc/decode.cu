@@ -711,6 +711,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
         if (p.k_new && blockIdx.x == 0) {
           const int old = p.seq_lens[s];
           if (old < 0 || old >= p.capacity) set_err(p.err, KVQ_DEVERR_CAPACITY);
+          if (ROPE) {  // (every sequence's, as kv_append_rope: one without keys meets no other check)
+            const int at = p.positions ? p.positions[s] : old;
+            if (at < 0 || at >= p.rope.n_pos) set_err(p.err, KVQ_DEVERR_POS);
+          }
         }
         int len = attended_len(p, s);
         if (len > p.max_len) {
