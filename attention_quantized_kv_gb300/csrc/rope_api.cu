@@ -130,9 +130,9 @@ int kv_append_rope(const kvq_layer *layer, const kvq_rope *rope, const kvq_rows 
   if (!k || !v || n_rows < 0 || n_rows > INT32_MAX) return KVQ_EINVAL;
   if ((n_new == nullptr) == (row_start == nullptr)) return KVQ_EINVAL;
   if (n_new && n_rows % layer->n_seqs != 0) return KVQ_EINVAL;
-  if ((q == nullptr) != (q_out == nullptr)) return KVQ_EINVAL;
   if (!aligned(n_new, 4) || !aligned(row_start, 4) || !aligned(positions, 4)) return KVQ_EALIGN;
-  if (n_rows == 0) return KVQ_OK;
+  if (n_rows == 0) return KVQ_OK;  // (an empty batch's tensors have no address)
+  if ((q == nullptr) != (q_out == nullptr)) return KVQ_EINVAL;
   if ((st = kvq::check_rows(*k, false, n_rows, layer->n_kv_heads)) != KVQ_OK) return st;
   if ((st = kvq::check_rows(*v, false, n_rows, layer->n_kv_heads)) != KVQ_OK) return st;
   if (k->type != v->type) return KVQ_EUNSUPPORTED;

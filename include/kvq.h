@@ -483,6 +483,7 @@ KVQ_API int kvq_rope_apply(const kvq_rope *rope, const kvq_rows *x, const kvq_ro
  * Row i of sequence s goes to token seq_lens[s] + i and is rotated by
  * positions[row] (device int32 [n_rows]), or with NULL by that token index.
  * When update_lens != 0, the lengths advance afterwards (stream-ordered).
+ * n_rows = 0 launches nothing.
  * Device conditions: KVQ_DEVERR_CAPACITY, KVQ_DEVERR_PAGE (the row's k and v
  * are skipped), KVQ_DEVERR_POS, KVQ_DEVERR_ROWS (a row_start or n_new entry out
  * of its range: that sequence's rows are unspecified, in bounds, and its
