@@ -74,7 +74,7 @@ def _hand_over(stream, *tensors) -> None:
 
 
 def _ptr(t) -> int | None:
-    return None if t is None else int(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def default_scale(head_dim: int = HEAD_DIM) -> float:
@@ -140,10 +140,8 @@ class KVLayer:
 
     def desc(self) -> kvq_layer:
         """The C descriptor (rebuilt only when a buffer was replaced)."""
-        table, err = self.block_table, self.err
-        key = (self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.seq_lens.data_ptr(),
-               None if err is None else err.data_ptr(), self.codec_k, self.codec_v,
-               None if table is None else table.data_ptr(), self.n_pages)
+        key = (_ptr(self.k_cache), _ptr(self.v_cache), _ptr(self.seq_lens), _ptr(self.err),
+               self.codec_k, self.codec_v, _ptr(self.block_table), self.n_pages)
         if self._desc is None or self._desc_key != key:
             d = kvq_layer()
             d.n_seqs, d.n_kv_heads, d.n_q_heads = self.n_seqs, self.n_kv_heads, self.n_q_heads

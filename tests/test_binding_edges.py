@@ -1,4 +1,4 @@
-"""Calls at the binding's edges: batches without a row."""
+"""Calls at the binding's edges: batches without a row, layers without a buffer."""
 import pytest
 import torch
 
@@ -27,6 +27,15 @@ def test_an_append_of_no_rows_takes_queries(packed):
     # with rows the two go together, as before
     some = T._rows(row_stride=256)
     assert lib.kv_append_rope(L, r, T._rows(), some, some, 4, n_new, start, None, None, 1, None) == EINVAL
+
+
+@pytest.mark.parametrize("buffer", ["k_cache", "v_cache", "seq_lens"])
+def test_a_layer_without_a_buffer_is_refused(buffer):
+    L = kvq.KVLayer(1, 1, 1, 256, kvq.KVQ_F16, kvq.KVQ_F16, device="cpu")
+    setattr(L, buffer, None)
+    with pytest.raises(kvq.KVQError) as e:
+        kvq.attn_decode_workspace(L, 256)
+    assert e.value.status == EINVAL
 
 
 @pytest.mark.gpu
