@@ -410,9 +410,10 @@ __device__ __forceinline__ uint4 unit_chunk(int codec, const uint8_t *s, int c) 
 
 // Encode the staged rows' four 32-value blocks in place, lane l blocks
 // 2 (l / 16) and + 1 of row l % 16, each in registers: one division per block
-// and no exchange between lanes (q8_0 and q4_0).
+// and no exchange between lanes (q8_0 and q4_0).  slots: those that hold a row.
 template <int T, int DC>
-__device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
+__device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, unsigned slots, int lane) {
+  const bool live = (slots >> (lane & 15)) & 1u;
   uint8_t *row = stage + (lane & 15) * Stage<T>::kPitch;
   const int b0 = 2 * (lane >> 4);
   uint32_t code[2][8];
@@ -457,7 +458,7 @@ __device__ __forceinline__ void encode_staged_blocks(uint8_t *stage, int lane) {
     const float rcp = d != 0.0f ? __frcp_rn(d) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
-      const uint2 c = quad_codes8<DC>(reinterpret_cast<const float(&)[8]>(x[i]), d, rcp);
+      const uint2 c = quad_codes8<DC>(reinterpret_cast<const float(&)[8]>(x[i]), d, rcp, live);
       code[k][i / 4] = DC == KVQ_Q8_0 ? c.x : clamp15x4(c.x);
       code[k][i / 4 + 1] = DC == KVQ_Q8_0 ? c.y : clamp15x4(c.y);
     }
@@ -500,7 +501,7 @@ __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uin
     else
       quad_rotate<false>(p.rope, p.kind, row, w, 1.0f, v);
     QuadCodes<CODEC> q;
-    quad_encode<CODEC>(v, w, q);
+    quad_encode<CODEC>(v, w, at >= 0, q);
     if (at >= 0) quad_store_row<CODEC>(p.cache[0] + at * unit_bytes(CODEC), rr, w, q);
   }
 }
@@ -571,9 +572,9 @@ __device__ __forceinline__ void v_window(const AppendRopeParams &p, int64_t r0, 
     }
     stage_rows<T>(stage, x + (j0 - k0) * p.row[2], p.row[2], slots, lane);
     if (codec == KVQ_Q8_0) {
-      encode_staged_blocks<T, KVQ_Q8_0>(stage, lane);
+      encode_staged_blocks<T, KVQ_Q8_0>(stage, slots, lane);
     } else if (codec == KVQ_Q4_0) {
-      encode_staged_blocks<T, KVQ_Q4_0>(stage, lane);
+      encode_staged_blocks<T, KVQ_Q4_0>(stage, slots, lane);
     } else if (codec == KVQ_TURBO4) {  // (f16: converted on the way out)
 #pragma unroll 1
       for (unsigned m = slots; m; m &= m - 1) {

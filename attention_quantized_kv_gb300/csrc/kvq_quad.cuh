@@ -340,15 +340,16 @@ __device__ __noinline__ uint2 codes8_exact(float x0, float x1, float x2, float x
 }
 
 // The codes of 8 values of one block by its scale, as two words of bytes;
-// levels of the nibble codecs not yet clamped.
+// levels of the nibble codecs not yet clamped.  live: they are stored (what a
+// place without a row holds is often NaN, and not worth the divisions).
 template <int DC>
-__device__ __forceinline__ uint2 quad_codes8(const float (&x)[8], float d, float rcp) {
+__device__ __forceinline__ uint2 quad_codes8(const float (&x)[8], float d, float rcp, bool live) {
   uint32_t k[8];
   float far = 0.0f;
   rq_codes_fast<DC>(x, rcp, k, far);
   uint2 c = make_uint2(low_bytes4(k[0], k[1], k[2], k[3]), low_bytes4(k[4], k[5], k[6], k[7]));
   if (d == 0.0f) c = DC == KVQ_Q8_0 ? make_uint2(0u, 0u) : make_uint2(0x08080808u, 0x08080808u);
-  else if (!codes_exact<DC>(far))
+  else if (live && !codes_exact<DC>(far))
     c = codes8_exact<DC>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], d, rcp);
   return c;
 }
@@ -388,9 +389,10 @@ __device__ __forceinline__ float quad_signed_max(const float (&v)[8][4], int c0,
   return hi > -lo ? hi : lo;
 }
 
-// Encode the quad's row (all 32 lanes).
+// Encode the quad's row (all 32 lanes; live: its codes are stored).
 template <int CODEC>
-__device__ __forceinline__ void quad_encode(float (&v)[8][4], int w, QuadCodes<CODEC> &q) {
+__device__ __forceinline__ void quad_encode(float (&v)[8][4], int w, bool live,
+                                            QuadCodes<CODEC> &q) {
   if (CODEC == KVQ_F16) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -431,7 +433,7 @@ __device__ __forceinline__ void quad_encode(float (&v)[8][4], int w, QuadCodes<C
     const float d = __shfl_sync(0xffffffffu, dw, b, 4), rcp = __shfl_sync(0xffffffffu, rw, b, 4);
     const float x[8] = {v[2 * b][0],     v[2 * b][1],     v[2 * b][2],     v[2 * b][3],
                         v[2 * b + 1][0], v[2 * b + 1][1], v[2 * b + 1][2], v[2 * b + 1][3]};
-    const uint2 k = quad_codes8<CODEC == KVQ_Q8_0 ? KVQ_Q8_0 : KVQ_Q4_0>(x, d, rcp);
+    const uint2 k = quad_codes8<CODEC == KVQ_Q8_0 ? KVQ_Q8_0 : KVQ_Q4_0>(x, d, rcp, live);
     if (CODEC == KVQ_Q8_0) {
       q.w[2 * b] = k.x;
       q.w[2 * b + 1] = k.y;

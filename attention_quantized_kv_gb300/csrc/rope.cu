@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
         quad_rotate_copied<true>(p.rope, angles, lane, sign, copies[ANY ? threadIdx.x >> 5 : 0], v);
       else
         quad_rotate<true>(p.rope, p.kind, angles, w, sign, v);
-      quad_encode<CODEC>(v, w, q);
+      quad_encode<CODEC>(v, w, by != 0, q);
       if (by != 0) quad_store_row<CODEC>(u + h * step, g + 8 * rh, w, q);
     }
   }
