@@ -506,10 +506,9 @@ __device__ __forceinline__ void quad_window(const AppendRopeParams &p, const uin
   }
 }
 
-// Lane j's row r0 + j of a window: its sequence's new rows n, its index i among
-// them, its position, its unit of kv head 0 (lanes below 16; -1: no place) and
-// its row there.  (The new rows of a unit whose first lies in the window end
-// within 31 rows.)
+// Lane j's row r0 + j of a window (lanes below 16; the others hold none): its
+// sequence's new rows n, its index i among them, its position, its unit of kv
+// head 0 (-1: no place) and its row there.
 struct WindowRow {
   int64_t pos = 0, unit = -1;
   int i = 0, n = 0, r = 0;
@@ -518,11 +517,11 @@ __device__ __forceinline__ WindowRow window_row(const AppendRopeParams &p, int64
   WindowRow w;
   const int64_t row = r0 + lane;
   int s = 0;
-  if (row < p.n_rows && find_row(p, row, s, w.i, w.n)) {
+  if (lane < kUnitTokens && row < p.n_rows && find_row(p, row, s, w.i, w.n)) {
     const int64_t slot = static_cast<int64_t>(p.seq_lens[s]) + w.i;
     w.pos = p.positions ? p.positions[row] : slot;
     w.r = static_cast<int>(slot & (kUnitTokens - 1));
-    if (lane < kUnitTokens) w.unit = unit_of(p, s, slot);
+    w.unit = unit_of(p, s, slot);
   }
   return w;
 }

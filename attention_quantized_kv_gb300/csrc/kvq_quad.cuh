@@ -212,7 +212,7 @@ struct QuadCodes {
   uint16_t scale;
 };
 
-// One row's codes (this lane's part of token row r).
+// Token row r's codes (this lane's part of them) from a unit.
 template <int CODEC>
 __device__ __forceinline__ void quad_load_row(const uint8_t *unit, int r, int w,
                                               QuadCodes<CODEC> &q) {
@@ -239,7 +239,7 @@ __device__ __forceinline__ void quad_load_row(const uint8_t *unit, int r, int w,
   }
 }
 
-// One row's codes (this lane's part of token row r).
+// And back into a unit.
 template <int CODEC>
 __device__ __forceinline__ void quad_store_row(uint8_t *unit, int r, int w,
                                                const QuadCodes<CODEC> &q) {

@@ -187,7 +187,7 @@ __device__ __forceinline__ void load4(const void *p, float (&x)[4]) {
   }
 }
 
-// Four consecutive values, rounded once to the type.
+// One value as fp32.
 template <int T>
 __device__ __forceinline__ float load1(const void *p) {
   if (T == KVQ_T_F32) return *static_cast<const float *>(p);
@@ -195,6 +195,7 @@ __device__ __forceinline__ float load1(const void *p) {
   return T == KVQ_T_F16 ? __half2float(__ushort_as_half(v))
                         : __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
+// Four consecutive values, rounded once to the type.
 template <int T>
 __device__ __forceinline__ void store4(void *p, const float (&x)[4]) {
   if (T == KVQ_T_F32) {

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
-constexpr int64_t kTableBlocks = 152 * 8;  // every SM full
-constexpr int64_t kSmallGrid = 152 * 8;    // warps: eight per SM
+constexpr int kTableBlocks = 8;  // of the table kernel's grid per SM, of which six are resident
+constexpr int kSmallGrid = 8;    // warps per SM below which a row's heads are spread
 
 // ------------------------------------------------------------------ table
 
@@ -259,7 +259,7 @@ struct ShiftParams {
   uint8_t *k;
   const int32_t *seq_lens, *delta, *table;
   int32_t *err;
-  int codec, n_kv, capacity, pages_per_seq, n_pages;
+  int n_kv, capacity, pages_per_seq, n_pages;
   int kind;  // quad_kind
 };
 
@@ -378,7 +378,8 @@ cudaError_t launch_apply_t(ApplyParams &p, cudaStream_t stream) {
   const bool eight = eight_lanes(p.rope);
   p.hpw = eight ? (TI == KVQ_T_F32 ? 8 : 16) : kAnyHeads;
   // few rows: spread the heads over more warps (four are one step of eight lanes)
-  while (p.hpw > 4 && p.n_rows * ((p.n_heads + p.hpw - 1) / p.hpw) < kSmallGrid) p.hpw /= 2;
+  const int64_t few = static_cast<int64_t>(device_sms()) * kSmallGrid;
+  while (p.hpw > 4 && p.n_rows * ((p.n_heads + p.hpw - 1) / p.hpw) < few) p.hpw /= 2;
   p.chunks = (p.n_heads + p.hpw - 1) / p.hpw;
   const int64_t blocks = (p.n_rows * p.chunks + kRopeWarps - 1) / kRopeWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -399,7 +400,10 @@ cudaError_t launch_rope_table(const double *freqs, int rot_dim, int n_pos, float
   p.cols = p.pairs / planes;
   const int rows = kRopeThreads / p.cols;
   const int64_t passes = (p.n_pos + rows - 1) / rows;
-  const unsigned grid = static_cast<unsigned>(passes < kTableBlocks ? passes : kTableBlocks);
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int64_t most = static_cast<int64_t>(sms) * kTableBlocks;
+  const unsigned grid = static_cast<unsigned>(passes < most ? passes : most);
   return launch_pdl(planes == 2 ? table_kernel<2> : table_kernel<1>, dim3(grid),
                     dim3(kRopeThreads), 0, stream, p);
 }
@@ -446,7 +450,6 @@ cudaError_t launch_rope_shift(const kvq_layer &L, const kvq_rope &rope, const in
   p.delta = delta;
   p.table = L.pages_per_seq > 0 ? L.block_table : nullptr;
   p.err = L.err;
-  p.codec = L.codec_k;
   p.n_kv = L.n_kv_heads;
   p.capacity = L.capacity;
   p.pages_per_seq = L.pages_per_seq;
