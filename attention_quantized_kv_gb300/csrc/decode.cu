@@ -449,6 +449,18 @@ __device__ __forceinline__ void half_bar() {  // warps 0 .. kWarps/2 - 1
 // Online softmax + PV for N units at once (N = 1, 2 or 4): one max reduction and
 // at most one rescale per call.  A unit may have no valid token at all (the
 // second unit of a two-unit item past the length): it is fully masked.
+//
+// The weights p become fp16 here, an operand of the tensor-core product, and
+// with a quantized V once more with the block scale d in them (unit_pv): an
+// fp32 weight has no mma of this rate, and two fp16 parts would double the PV
+// products.  Each rounding is off by at most 2^-11 of its value or, below
+// 2^-14, by 2^-25.  Sums, maxima and l stay in fp32, l over the unrounded p.
+// So an output, before its rounding to fp16, is within
+//   (2^-11 sum p (|v| + |d c|) + 2^-25 sum (|v| + |c|)) / l
+// of exact, c being the code that d p multiplies: the 8-bit code, for 4 bits
+// the unsigned level (0 .. 15: corr takes its offset off with the unrounded
+// d p, exact in fp32), 0 for f16.  The second part grows with the keys that
+// share the weight: values below about 2^-10 in few bits lose digits there.
 template <int CK, int CV, int N>
 __device__ __forceinline__ void process_units(const uint8_t *const (&ku)[N],
                                               const uint8_t *const (&vus)[N],

@@ -228,7 +228,13 @@ KVQ_API int attn_decode_workspace(const kvq_layer *layer, int32_t max_len, size_
  * sum-exp of the scaled scores (NULL to skip).  max_len bounds every
  * seq_lens[s] (1..capacity).  workspace: device, 16-byte aligned, at least
  * attn_decode_workspace() bytes.  A sequence of length 0 gives out = 0 and
- * lse = -inf. */
+ * lse = -inf.
+ * Accuracy: softmax weights p, and their products with a quantized value's
+ * scale d, are fp16 operands.  Before its own rounding an output is within
+ * (2^-11 sum p (|v| + |d c|) + 2^-25 sum (|v| + |c|)) / sum p of softmax
+ * attention over the decoded rows, c being the q8_0 code, the 4-bit level
+ * (0..15, before its offset of 8) or 0 for f16, p relative to the largest; the
+ * other sums are fp32.  turbo4: the same in its rotated space. */
 KVQ_API int attn_decode(const kvq_layer *layer, const void *q, float scale, void *out, float *lse,
                 int32_t max_len, void *workspace, size_t ws_bytes, void *stream);
 
