@@ -495,7 +495,8 @@ def kvq_rope_apply(rope: Rope, x, y, positions=None, pos0: int = 0, transpose: b
     """Rotate the rows ``x`` (float16, bfloat16 or float32 [rows, heads, 128], strided) into ``y``
     (x's type or float16; may be x).  ``positions``: int32 [rows], or row r is at pos0 + r.
     ``transpose``: the gradient with respect to x, given that with respect to y.  ``err``: int32
-    word for KVQ_DEVERR_POS."""
+    word for KVQ_DEVERR_POS.  Like every call here it writes through pointers: autograd neither
+    records it nor sees that y (or x, in place) changed."""
     dev = _cuda_device(x, "kvq_rope_apply")
     rope._check_on(dev)
     if x.dim() != 3 or y.shape != x.shape:

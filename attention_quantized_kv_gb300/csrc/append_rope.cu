@@ -5,12 +5,14 @@
 //
 // One launch reads each value once and writes each code once.  Device times on
 // one GB300 against the bytes at the measured 6.78 TB/s: 32768 prompt tokens of
-// 32 q / 4 kv heads into f16 caches 103 us (0.98), K f16 / V q8_0 106 us (0.94),
-// q8_0 110 us (0.88), q4_0 113 us (0.84), turbo4 142 us (0.66): HBM bounds the
-// first, the encoders' instructions the last.  2048 tokens into q8_0 caches
-// 12.8 us (0.55) and a mixed batch of 1821 rows 14.1 us (0.55): two waves of
-// blocks, each a chain of dependent loads (row -> length -> page -> rows).  16
-// single tokens of 40 q / 8 kv heads 3.4 us, the same chain once.
+// 32 q / 4 kv heads into f16 caches 103 us (0.98), K f16 / V q8_0 106 us (0.93),
+// q8_0 109 us (0.88), q4_0 113 us (0.83), turbo4 138 us (0.68): HBM bounds the
+// first; the last issues 106 M warp instructions, 84 us of them at full issue,
+// and 0.61 per scheduler and cycle behind loads and dependent instructions.
+// 2048 tokens into q8_0 caches 12.8 us (0.55) and a mixed batch of 1821 rows
+// 14.4 us (0.54): two waves of blocks, each a chain of dependent loads (row ->
+// length -> page, and only then the rows).  16 single tokens of 40 q / 8 kv
+// heads 3.4 us, one such chain.
 #include <cuda_runtime.h>
 
 #include "kvq_encode.cuh"

@@ -137,7 +137,7 @@ constexpr int kAnyHeads = 8;  // heads per warp of the general kernel
 // One warp per (row, up to sixteen heads): the angles are read once, and all
 // the heads' values are requested before the first is used (up to 4 KB per
 // warp in flight).  Bound by HBM: 8191 rows x 40 bf16 heads, 64 interleaved
-// dims, 27.4 us, 0.92 of the floor; by lanes of four values 31 us, with one
+// dims, 27.6 us, 0.91 of the floor; by lanes of four values 31 us, with one
 // head at a time 51 us.  16 rows x 40 heads take 2.0 us, a launch's length.
 template <int TI, int TO>
 __global__ void __launch_bounds__(kRopeThreads) apply_kernel(const __grid_constant__ ApplyParams p) {
@@ -157,7 +157,10 @@ __global__ void __launch_bounds__(kRopeThreads) apply_kernel(const __grid_consta
 }
 
 // Planes that eight lanes cannot hold: one head at a time, 4 values per lane,
-// eight heads requested at once.
+// eight heads requested at once.  8191 rows x 40 bf16 heads: interleaved, 6 dims
+// 31 us (0.80 of the floor), halves with 40 dims 33 us (0.75); with 20 and 126
+// dims (Lanes::kAny) 48 and 49 us (0.52), bound by instruction issue (0.77 per
+// scheduler and cycle).
 template <int TI, int TO>
 __global__ void __launch_bounds__(kRopeThreads)
     apply_any_kernel(const __grid_constant__ ApplyParams p) {
@@ -271,19 +274,21 @@ struct ShiftParams {
 //
 // 74k tokens x 8 heads in four sequences, the deltas (2.5 us) included: f16 51
 // us, 0.88 of the floor (the next unit in registers 57 us, no look-ahead 74 us),
-// bound by HBM; q8_0 58 us, q4_0 68 us, turbo4 124 us, bound by instruction
-// issue, most of it the encoders'.  Tried for f16, q8_0 and q4_0: both rows
-// encoded before either is stored 52, 60, 70 us; rows encoded in the shared copy
-// and the whole unit stored 52, 62, 73 us; a third unit in the ring 51, 59, 68
-// us; a third block per SM (80 registers) 56, 63, 72 us; eight heads per warp
-// 52, 55, 66 us, but 29 instead of 17 us for 16k tokens in eight sequences
-// (q8_0).  The code of a lane's two rows is interleaved but for turbo4 (124
-// instead of 133 us; q8_0 60 instead of 58 us).
+// bound by HBM; q8_0 58 us and q4_0 67 us, bound by the latency of dependent
+// instructions (0.64 issued per scheduler and cycle by its 3.7 warps; 31 and 37
+// us at full issue); turbo4 123 us, bound by instruction issue (0.83), most of
+// it the encoder's.  Tried for f16, q8_0 and q4_0: both rows encoded before
+// either is stored 52, 60, 70 us; rows encoded in the shared copy and the whole
+// unit stored 52, 62, 73 us; a third unit in the ring 51, 59, 68 us; a third
+// block per SM (80 registers) 56, 63, 72 us; eight heads per warp 52, 55, 66 us,
+// but 29 instead of 17 us for 16k tokens in eight sequences (q8_0).  The code of
+// a lane's two rows is interleaved but for turbo4 (124 instead of 133 us; q8_0
+// 60 instead of 58 us).
 constexpr int kShiftHeads = 4;
 constexpr int kShiftSlots = 2;  // units in a warp's ring
 
 // ANY: planes that cross lanes (a kernel of its own, so that its registers are
-// not the others'): with 40 dims in halves f16 61 us, q8_0 78 us, turbo4 148 us
+// not the others'): with 40 dims in halves f16 62 us, q8_0 76 us, turbo4 145 us
 // (by whole rows, a warp each, f16 166 us).
 template <int CODEC, bool ANY>
 __global__ void __launch_bounds__(kRopeThreads, 2)
