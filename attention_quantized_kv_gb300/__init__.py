@@ -11,6 +11,7 @@ raise ``KVQError`` on a non-zero status.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from array import array
 
@@ -51,12 +52,22 @@ def _check(status: int, where: str) -> None:
         raise KVQError(status, where)
 
 
+def _private(name: str, public):
+    """torch._C's function, or the public way to the same where a version has none."""
+    return getattr(torch._C, name, None) or public
+
+
+_current_device = _private("_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = _private("_cuda_getCurrentRawStream",
+                       lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream_ptr(stream) -> int:
     """The stream's handle; without one the current stream's, read without building a
     torch.cuda.Stream object (0.2 instead of 3.0 us a call)."""
     if stream is not None:
         return int(stream.cuda_stream)
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_current_device())
 
 
 def _hand_over(stream, *tensors) -> None:
@@ -227,13 +238,16 @@ def attn_prefill_chunk(layer: KVLayer, seq: int, q_start: int, q, scale: float, 
 
 # --------------------------------------------------------------------------- degrade ladder
 
-_ROW_BYTES = {KVQ_F16: 256, KVQ_Q8_0: 136, KVQ_Q4_0: 72, KVQ_TURBO4: 66}
+@functools.lru_cache(maxsize=None)
+def _row_bytes(codec: int) -> int:
+    return kvq_row_bytes(codec)
 
 
 def _side_bytes(layer: KVLayer, codec: int) -> int:
     """kvq_pool_bytes / kvq_cache_bytes of a side of this layer in a codec (-1: no such codec)."""
     tokens = layer.n_pages * 256 if layer.n_pages > 0 else layer.n_seqs * layer.capacity
-    return _ROW_BYTES[codec] * layer.n_kv_heads * tokens if codec in _ROW_BYTES else -1
+    row = _row_bytes(codec)
+    return row * layer.n_kv_heads * tokens if row > 0 else -1
 
 
 def kv_requantize(layer: KVLayer, side: int, dst_codec: int, dst_cache, stream=None) -> None:
@@ -386,7 +400,7 @@ def _need(t, dtype, shape, device, what: str):
 def _cuda_device(t, what: str):
     """The device of a tensor, which has to be the current CUDA device."""
     d = t.device
-    if d.type != "cuda" or d.index != torch._C._cuda_getDevice():
+    if d.type != "cuda" or d.index != _current_device():
         raise ValueError(f"{what}: tensors must be on the current CUDA device, got {d}")
     return d
 

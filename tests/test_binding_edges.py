@@ -1,4 +1,5 @@
-"""Calls at the binding's edges: batches without a row, layers without a buffer."""
+"""Calls at the binding's edges: batches without a row, layers without a buffer, the current
+stream."""
 import pytest
 import torch
 
@@ -36,6 +37,18 @@ def test_a_layer_without_a_buffer_is_refused(buffer):
     with pytest.raises(kvq.KVQError) as e:
         kvq.attn_decode_workspace(L, 256)
     assert e.value.status == EINVAL
+
+
+def test_public_ways_where_torch_has_no_private_ones():
+    assert kvq._private("_no_such_name", torch.cuda.current_device) is torch.cuda.current_device
+
+
+@pytest.mark.gpu
+def test_the_current_stream_and_device():
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            assert kvq._stream_ptr(None) == kvq._stream_ptr(stream) == stream.cuda_stream
+    assert kvq._current_device() == torch.cuda.current_device()
 
 
 @pytest.mark.gpu
