@@ -36,7 +36,8 @@
 //    accumulator, then s += d * partial), so K dequantization is exact.
 //  * Online softmax in the log2 domain per head with xor-shuffle maxima; P is
 //    transposed in registers (movmatrix) into the B operand of O^T = V^T P^T
-//    (M = 16 head dims); the V block scale is folded into P.
+//    (M = 16 head dims); the V block scale is folded into P (turbo4's, one per
+//    row, in fp32 before the transpose).
 //
 // The fused decode step (attn_decode_append) is a second instantiation of
 // the same kernel (FUSED): each sequence's new token is encoded into the
@@ -220,13 +221,18 @@ __device__ __forceinline__ void unit_scores(const uint8_t *ku, int lane, const u
 // O^T (128 dims x 8 heads) += V^T (dims x 16 tokens) * P^T (16 tokens x heads).
 // FULL: all 16 tokens of the unit are valid (no masking needed).
 //
-// q4_0 V takes the nibbles n as fp16 subnormals, one AND each: rows g of an
+// Nibble codecs take the nibbles n as fp16 subnormals, one AND each: rows g of an
 // m-tile get n * 2^-24 (low nibbles), rows g+8 get 16n * 2^-24 (high nibbles
 // masked in place).  Every product with the folded P (an fp16 number) is
 // still exact in fp32.  The offset of the codec, -8 per value, is restored
 // at the end of the segment from corr, whose rows r collect
-// C_b = sum over tokens of d_b(t) p(t, h) for block b = r & 3: one MMA with
-// A rows r holding the scales d_{r&3} of the unit's tokens and B = P^T.
+// C_b = sum over tokens of the folded P of block b = r & 3 (turbo4: of the row):
+// one MMA per block with A rows r of ones where r & 3 = b and B the folded P.
+// It has to be the same folded P: a sum over d p before that rounding leaves its
+// rounding times n instead of n - 8, and an output of a 4-bit V twice as far
+// off as an f16 one's (relative error 4.1 to 5.2 instead of 2.4 to 3.0 * 10^-4;
+// the three more MMAs cost q4_0 0 to 3%: 2 x 200000 keys 50.3 -> 51.7 us).
+// B0, B1: P^T; turbo4: with the scale of the row in it.
 template <int CV, bool FULL>
 __device__ __forceinline__ void unit_pv(const uint8_t *vu, int lane, uint32_t B0, uint32_t B1,
                                         int nvalid, float (&o)[8][4], float (&corr)[4]) {
@@ -247,26 +253,22 @@ __device__ __forceinline__ void unit_pv(const uint8_t *vu, int lane, uint32_t B0
     }
   } else {
     uint32_t dp01[4], dp23[4];
-    if (CV == KVQ_TURBO4) {  // one scale per token: (2tig, 2tig+1), (2tig+8, 2tig+9)
-      const uint2 sv = lds64(vu + 1024 + tig * 8);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) { dp01[b] = sv.x; dp23[b] = sv.y; }
-    } else {
+    if (CV != KVQ_TURBO4) {
       const uint4 s01 = lds128(vu + unit_scale_offset(CV) + tig * 32);
       const uint4 s23 = lds128(vu + unit_scale_offset(CV) + tig * 32 + 16);
       dp01[0] = s01.x; dp01[1] = s01.z; dp01[2] = s23.x; dp01[3] = s23.z;
       dp23[0] = s01.y; dp23[1] = s01.w; dp23[2] = s23.y; dp23[3] = s23.w;
-    }
-    if (!FULL) {
+      if (!FULL) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) { dp01[b] &= m01; dp23[b] &= m23; }
+        for (int b = 0; b < 4; ++b) { dp01[b] &= m01; dp23[b] &= m23; }
+      }
     }
     // P^T with the V block scale folded in, one pair of B registers per block
     uint32_t bp0[4], bp1[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      bp0[b] = hmul2_bits(B0, dp01[b]);
-      bp1[b] = hmul2_bits(B1, dp23[b]);
+      bp0[b] = CV == KVQ_TURBO4 ? B0 : hmul2_bits(B0, dp01[b]);
+      bp1[b] = CV == KVQ_TURBO4 ? B1 : hmul2_bits(B1, dp23[b]);
     }
     if (CV == KVQ_Q8_0) {
 #pragma unroll
@@ -292,12 +294,12 @@ __device__ __forceinline__ void unit_pv(const uint8_t *vu, int lane, uint32_t B0
         }
       }
       const int g = lane >> 2;
-      // scales of block g & 3 for tokens (2tig, 2tig+1) and (2tig+8, 2tig+9)
-      uint2 dg = CV == KVQ_TURBO4 ? lds64(vu + 1024 + tig * 8)
-                                  : lds64(vu + unit_scale_offset(CV) + tig * 32 + (g & 3) * 8);
-      if (!FULL) { dg.x &= m01; dg.y &= m23; }
-      const uint32_t a[4] = {dg.x, dg.x, dg.y, dg.y};
-      mma16816(corr, a, B0, B1);
+#pragma unroll
+      for (int b = 0; b < (CV == KVQ_TURBO4 ? 1 : 4); ++b) {
+        const uint32_t one = CV == KVQ_TURBO4 || (g & 3) == b ? 0x3c003c00u : 0u;
+        const uint32_t a[4] = {one, one, one, one};
+        mma16816(corr, a, bp0[b], bp1[b]);
+      }
     }
   }
 }
@@ -450,17 +452,18 @@ __device__ __forceinline__ void half_bar() {  // warps 0 .. kWarps/2 - 1
 // at most one rescale per call.  A unit may have no valid token at all (the
 // second unit of a two-unit item past the length): it is fully masked.
 //
-// The weights p become fp16 here, an operand of the tensor-core product, and
-// with a quantized V once more with the block scale d in them (unit_pv): an
-// fp32 weight has no mma of this rate, and two fp16 parts would double the PV
-// products.  Each rounding is off by at most 2^-11 of its value or, below
-// 2^-14, by 2^-25.  Sums, maxima and l stay in fp32, l over the unrounded p.
-// So an output, before its rounding to fp16, is within
+// The weights p become fp16 here, an operand of the tensor-core product, with a
+// turbo4 row's scale in them, and with q8_0 and q4_0 once more with the block
+// scale d in them (unit_pv): an fp32 weight has no mma of this rate; a second
+// fp16 part of p, which takes that first rounding off, cost 2 to 8% (q4_0 50.3 ->
+// 54.3 us).  Each rounding is off by at most 2^-11 of its value or, below 2^-14,
+// by 2^-25.  Sums, maxima and l stay in fp32, l over the unrounded p.  So an
+// output, before its rounding to fp16, is within
 //   (2^-11 sum p (|v| + |d c|) + 2^-25 sum (|v| + |c|)) / l
-// of exact, c being the code that d p multiplies: the 8-bit code, for 4 bits
-// the unsigned level (0 .. 15: corr takes its offset off with the unrounded
-// d p, exact in fp32), 0 for f16.  The second part grows with the keys that
-// share the weight: values below about 2^-10 in few bits lose digits there.
+// of exact, c being the stored code (q8_0's, q4_0's n - 8; 0 for f16; turbo4 in
+// its rotated space: 2^-11 sum p |v| + 2^-25 sum |c|).  The second part grows
+// with the keys that share the weight: values below about 2^-10 in few bits lose
+// digits there.
 template <int CK, int CV, int N>
 __device__ __forceinline__ void process_units(const uint8_t *const (&ku)[N],
                                               const uint8_t *const (&vus)[N],
@@ -509,9 +512,21 @@ __device__ __forceinline__ void process_units(const uint8_t *const (&ku)[N],
     const float p2 = fast_exp2(sc[u][2] - m0), p3 = fast_exp2(sc[u][3] - m1);
     l0 += p0 + p2;
     l1 += p1 + p3;
-    const uint32_t B0 = movmatrix_trans(pack_half2(p0, p1));
-    const uint32_t B1 = movmatrix_trans(pack_half2(p2, p3));
     const uint8_t *vu = vus[u];
+    float d0 = 1.0f, d1 = 1.0f;
+    if (CV == KVQ_TURBO4) {  // the scales of tokens g and g + 8
+      const uint2 sv = lds64(vu + 1024 + (g >> 1) * 8);
+      d0 = half_bits_to_float((sv.x >> (16 * (g & 1))) & 0xffffu);
+      d1 = half_bits_to_float((sv.y >> (16 * (g & 1))) & 0xffffu);
+      if (nvalid[u] < kUnitTokens) {
+        if (g >= nvalid[u]) d0 = 0.0f;
+        if (g + 8 >= nvalid[u]) d1 = 0.0f;
+      }
+    }
+    const uint32_t B0 =
+        movmatrix_trans(CV == KVQ_TURBO4 ? pack_half2(p0 * d0, p1 * d0) : pack_half2(p0, p1));
+    const uint32_t B1 =
+        movmatrix_trans(CV == KVQ_TURBO4 ? pack_half2(p2 * d1, p3 * d1) : pack_half2(p2, p3));
     if (nvalid[u] == kUnitTokens) unit_pv<CV, true>(vu, lane, B0, B1, nvalid[u], o, corr);
     else unit_pv<CV, false>(vu, lane, B0, B1, nvalid[u], o, corr);
   }

@@ -232,9 +232,9 @@ KVQ_API int attn_decode_workspace(const kvq_layer *layer, int32_t max_len, size_
  * Accuracy: softmax weights p, and their products with a quantized value's
  * scale d, are fp16 operands.  Before its own rounding an output is within
  * (2^-11 sum p (|v| + |d c|) + 2^-25 sum (|v| + |c|)) / sum p of softmax
- * attention over the decoded rows, c being the q8_0 code, the 4-bit level
- * (0..15, before its offset of 8) or 0 for f16, p relative to the largest; the
- * other sums are fp32.  turbo4: the same in its rotated space. */
+ * attention over the decoded rows, c being the code (q8_0's, q4_0's level - 8,
+ * 0 for f16) and p relative to the largest; in turbo4's rotated space within
+ * (2^-11 sum p |v| + 2^-25 sum |c|) / sum p.  The other sums are fp32. */
 KVQ_API int attn_decode(const kvq_layer *layer, const void *q, float scale, void *out, float *lse,
                 int32_t max_len, void *workspace, size_t ws_bytes, void *stream);
 
