@@ -230,7 +230,7 @@ __device__ __forceinline__ void unit_scores(const uint8_t *ku, int lane, const u
 // one MMA per block with A rows r of ones where r & 3 = b and B the folded P.
 // It has to be the same folded P: a sum over d p before that rounding leaves its
 // rounding times n instead of n - 8, and an output of a 4-bit V twice as far
-// off as an f16 one's (relative error 4.1 to 5.2 instead of 2.4 to 3.0 * 10^-4;
+// off as an f16 one's (relative error 3.9 to 5.2 instead of 2.4 to 3.0 * 10^-4;
 // the three more MMAs cost q4_0 0 to 3%: 2 x 200000 keys 50.3 -> 51.7 us).
 // B0, B1: P^T; turbo4: with the scale of the row in it.
 template <int CV, bool FULL>
