@@ -4,7 +4,7 @@ A thin Python layer over libkvq's C ABI (include/kvq.h).  PyTorch provides
 device memory and streams; every step of the path (quantize-on-append,
 split-K decode attention with its log-sum-exp merge, chunked-prefill
 attention, the degrade ladder's re-encode, probe-scored eviction, rotary
-positions) runs in the library's sm_103a kernels.  The functions below only
+positions, cross attention, shared prefixes, rows read back) runs in the library's sm_103a kernels.  The functions below only
 marshal arguments: they take torch tensors, pass their device pointers and
 raise ``KVQError`` on a non-zero status.
 """
@@ -34,7 +34,9 @@ __all__ = ["KVQ_F16", "KVQ_Q8_0", "KVQ_Q4_0", "KVQ_TURBO4", "CODEC_NAMES", "KVQE
            "KVQ_ROPE_HALF", "KVQ_ROPE_INTERLEAVED", "KVQ_ROPE_PLAIN", "KVQ_ROPE_LINEAR",
            "KVQ_ROPE_NTK", "KVQ_ROPE_PARTS", "KVQ_ROPE_YARN", "Rope", "kvq_rope_freqs",
            "kvq_rope_table", "kvq_rope_apply", "kv_append_rope", "kv_evict_delta",
-           "kv_rope_shift", "attn_decode_append_rope"]
+           "kv_rope_shift", "attn_decode_append_rope", "kv_append_rows", "kv_read_rows",
+           "attn_cross_workspace", "attn_cross", "attn_decode_prefix_workspace",
+           "attn_decode_prefix"]
 
 CODEC_NAMES = {KVQ_F16: "f16", KVQ_Q8_0: "q8_0", KVQ_Q4_0: "q4_0", KVQ_TURBO4: "turbo4"}
 HEAD_DIM = 128
@@ -620,3 +622,132 @@ def attn_decode_append_rope(layer: KVLayer, rope: Rope, k_new, v_new, q, scale: 
         layer.desc(), rope.desc(), pos, k_ptr, v_ptr, q_ptr, float(scale), o_ptr, l_ptr,
         int(max_len), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream_ptr(stream)), "attn_decode_append_rope")
+
+
+# --------------------------------------------------------------------------- rows and their caches
+
+def _counts(layer: KVLayer, lead, n_new, row_start, dev, what: str, one_each: bool = False):
+    """(n_new, row_start) pointers for rows of leading shape ``lead``: padded, packed, or (where
+    the call has it) one row per sequence."""
+    if n_new is not None and row_start is not None:
+        raise ValueError(what + ": give n_new (padded rows) or row_start (packed rows)")
+    if n_new is not None:
+        if len(lead) != 2 or lead[0] != layer.n_seqs:
+            raise ValueError(what + ": padded rows are [n_seqs, max_new, heads, 128]")
+        return _need(n_new, torch.int32, (layer.n_seqs,), dev, what + ": counts"), None
+    if len(lead) != 1:
+        raise ValueError(what + ": packed rows are [rows, heads, 128]")
+    if row_start is not None:
+        return None, _need(row_start, torch.int32, (layer.n_seqs + 1,), dev, what + ": row_start")
+    if not one_each:
+        raise ValueError(what + ": give counts (padded rows) or row_start (packed rows)")
+    if lead[0] != layer.n_seqs:
+        raise ValueError(what + ": without row_start there is one row per sequence")
+    return None, None
+
+
+def kv_append_rows(layer: KVLayer, k, v, n_new=None, row_start=None, update_lens: bool = True,
+                   stream=None) -> None:
+    """Append new keys and values as they are: kv_append_rope's rows (float16, bfloat16 or float32,
+    strided; packed with ``row_start`` or padded with ``n_new``) without a rotation."""
+    dev = _cuda_device(k, "kv_append_rows")
+    _layer_on(layer, dev, "kv_append_rows")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("kv_append_rows: k and v must have one shape and type")
+    n_ptr, s_ptr = _counts(layer, k.shape[:-2], n_new, row_start, dev, "kv_append_rows")
+    kd, n = _rows(k, layer.n_kv_heads, dev, "kv_append_rows: k")
+    vd, _ = _rows(v, layer.n_kv_heads, dev, "kv_append_rows: v")
+    _check(_abi.load().kv_append_rows(layer.desc(), kd, vd, n, n_ptr, s_ptr,
+                                      int(bool(update_lens)), _stream_ptr(stream)),
+           "kv_append_rows")
+
+
+def kv_read_rows(layer: KVLayer, k=None, v=None, n_read=None, row_start=None, first=None,
+                 stream=None) -> None:
+    """Cached rows as values into ``k`` and ``v`` (float16, bfloat16 or float32, strided; None: that
+    side is not read): packed [rows, n_kv, 128] with ``row_start`` (int32 [n_seqs + 1]) or padded
+    [n_seqs, max, n_kv, 128] with ``n_read`` (int32 [n_seqs]).  Row i of sequence s is token
+    first[s] + i (``first``: int32 [n_seqs], default 0).  Rows of no token are left as they are."""
+    what = "kv_read_rows"
+    some = k if k is not None else v
+    if some is None:
+        raise ValueError(what + ": give k or v")
+    dev = _cuda_device(some, what)
+    _layer_on(layer, dev, what)
+    lead = some.shape[:-2]
+    if k is not None and v is not None and v.shape != k.shape:
+        raise ValueError(what + ": k and v must have one shape")
+    n_ptr, s_ptr = _counts(layer, lead, n_read, row_start, dev, what)
+    kd = vd = None
+    if k is not None:
+        kd, n = _rows(k, layer.n_kv_heads, dev, what + ": k")
+    if v is not None:
+        vd, n = _rows(v, layer.n_kv_heads, dev, what + ": v")
+    at = None if first is None else _need(first, torch.int32, (layer.n_seqs,), dev, what + ": first")
+    _check(_abi.load().kv_read_rows(layer.desc(), kd, vd, n, n_ptr, s_ptr, at,
+                                    _stream_ptr(stream)), what)
+
+
+def attn_cross_workspace(layer: KVLayer, n_rows: int, max_len: int) -> int:
+    """Bytes of attn_cross workspace (of any contents)."""
+    n = ctypes.c_size_t(0)
+    _check(_abi.load().attn_cross_workspace(layer.desc(), int(n_rows), int(max_len),
+                                            ctypes.byref(n)), "attn_cross_workspace")
+    return int(n.value)
+
+
+def attn_cross(layer: KVLayer, q, scale: float, out, lse, max_len: int, workspace, n_new=None,
+               row_start=None, stream=None) -> None:
+    """Query rows against every cached key of their sequence (no causal mask).  ``q``, ``out``:
+    float16 or bfloat16, strided, packed [rows, n_q, 128] with ``row_start``, padded [n_seqs,
+    max_new, n_q, 128] with ``n_new``, or one row per sequence; ``lse``: fp32, contiguous, the
+    leading shape and n_q, or None.  Rows of no sequence are left as they are."""
+    what = "attn_cross"
+    dev = _cuda_device(q, what)
+    _layer_on(layer, dev, what)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(what + ": q and out must have one shape and type")
+    n_ptr, s_ptr = _counts(layer, q.shape[:-2], n_new, row_start, dev, what, one_each=True)
+    qd, n = _rows(q, layer.n_q_heads, dev, what + ": q")
+    od, _ = _rows(out, layer.n_q_heads, dev, what + ": out")
+    l_ptr = None if lse is None else _need(lse, torch.float32, q.shape[:-1], dev, what + ": lse")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(what + f": workspace must be contiguous on {dev}")
+    _check(_abi.load().attn_cross(layer.desc(), qd, n, n_ptr, s_ptr, float(scale), od, l_ptr,
+                                  int(max_len), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(),
+                                  _stream_ptr(stream)), what)
+
+
+def attn_decode_prefix_workspace(layer: KVLayer, prefix: KVLayer, max_len: int,
+                                 max_prefix: int) -> int:
+    """Bytes of attn_decode_prefix workspace (of any contents)."""
+    n = ctypes.c_size_t(0)
+    _check(_abi.load().attn_decode_prefix_workspace(layer.desc(), prefix.desc(), int(max_len),
+                                                    int(max_prefix), ctypes.byref(n)),
+           "attn_decode_prefix_workspace")
+    return int(n.value)
+
+
+def attn_decode_prefix(layer: KVLayer, prefix: KVLayer, q, scale: float, out, lse, max_len: int,
+                       max_prefix: int, workspace, group_start=None, stream=None) -> None:
+    """attn_decode of sequences behind shared prefixes: sequence g of ``prefix`` is read once for
+    the sequences group_start[g] .. group_start[g + 1] - 1 of ``layer`` (int32 [prefix.n_seqs + 1];
+    None: one prefix for all), and each attends its own keys too.  q, out: fp16 [n_seqs, n_q, 128];
+    lse: fp32 [n_seqs, n_q] or None."""
+    what = "attn_decode_prefix: "
+    dev = _cuda_device(q, "attn_decode_prefix")
+    _layer_on(layer, dev, "attn_decode_prefix")
+    _layer_on(prefix, dev, "attn_decode_prefix")
+    q_shape = (layer.n_seqs, layer.n_q_heads, HEAD_DIM)
+    q_ptr = _need(q, torch.float16, q_shape, dev, what + "q")
+    o_ptr = _need(out, torch.float16, q_shape, dev, what + "out")
+    l_ptr = None if lse is None else _need(lse, torch.float32, q_shape[:2], dev, what + "lse")
+    groups = None if group_start is None else _need(
+        group_start, torch.int32, (prefix.n_seqs + 1,), dev, what + "group_start")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(what + f"workspace must be contiguous on {dev}")
+    _check(_abi.load().attn_decode_prefix(
+        layer.desc(), prefix.desc(), groups, q_ptr, float(scale), o_ptr, l_ptr, int(max_len),
+        int(max_prefix), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream)), "attn_decode_prefix")

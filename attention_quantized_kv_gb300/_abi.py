@@ -28,7 +28,9 @@ EXPORTS = ("kvq_status_str", "kvq_row_bytes", "kvq_cache_bytes", "kvq_pool_bytes
            "attn_prefill_workspace", "attn_prefill_chunk", "kv_requantize", "kvq_aggregate_bpv",
            "kvq_ladder_next", "kv_probe_scores", "kv_evict_select", "kv_compact",
            "kvq_rope_freqs", "kvq_rope_table", "kvq_rope_apply", "kv_append_rope",
-           "kv_evict_delta", "kv_rope_shift", "attn_decode_append_rope")
+           "kv_evict_delta", "kv_rope_shift", "attn_decode_append_rope", "kv_append_rows",
+           "kv_read_rows", "attn_cross_workspace", "attn_cross", "attn_decode_prefix_workspace",
+           "attn_decode_prefix")
 
 
 class kvq_layer(ctypes.Structure):
@@ -119,6 +121,13 @@ def load(path: str | None = None):
         "kv_rope_shift": (ctypes.c_int, [L, R, P, P]),
         "attn_decode_append_rope": (ctypes.c_int, [L, R, P, P, P, P, f32, P, P, i32, P,
                                                    ctypes.c_size_t, P]),
+        "kv_append_rows": (ctypes.c_int, [L, W, W, i64, P, P, i32, P]),
+        "kv_read_rows": (ctypes.c_int, [L, W, W, i64, P, P, P, P]),
+        "attn_cross_workspace": (ctypes.c_int, [L, i64, i32, sz]),
+        "attn_cross": (ctypes.c_int, [L, W, i64, P, P, f32, W, P, i32, P, ctypes.c_size_t, P]),
+        "attn_decode_prefix_workspace": (ctypes.c_int, [L, L, i32, i32, sz]),
+        "attn_decode_prefix": (ctypes.c_int, [L, L, P, P, f32, P, P, i32, i32, P,
+                                              ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

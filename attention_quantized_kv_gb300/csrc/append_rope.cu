@@ -181,7 +181,7 @@ __device__ __forceinline__ void row_item(const AppendRopeParams &p, int64_t row,
   if (!find_row_warp(p, row, lane, s, i)) return;
   const int64_t slot = static_cast<int64_t>(p.seq_lens[s]) + i;
   LaneAngles a;
-  if (which < 2)
+  if (which < 2 && p.rope.rot > 0)
     a = lane_angles(p.rope, rope_row(p.rope, p.positions ? p.positions[row] : slot, p.err), lane);
   if (which == 0) {
     with_lanes(p.rope, [&](auto lanes) {
@@ -719,13 +719,15 @@ __global__ void advance_lens_kernel(AppendRopeParams p, int32_t *seq_lens) {
 
 }  // namespace
 
-cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const kvq_rows *q,
+cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope *rope, const kvq_rows *q,
                                const kvq_rows &k, const kvq_rows &v, int64_t n_rows,
                                const int32_t *n_new, const int32_t *row_start,
                                const int32_t *positions, void *q_out, int update_lens,
                                int num_sms, cudaStream_t stream) {
   AppendRopeParams p;
-  p.rope = rope_args(rope);
+  // no rotation: no planes, so no kernel reads an angle
+  p.rope = rope ? rope_args(*rope)
+                : RopeArgs{nullptr, INT32_MAX, 0, KVQ_ROPE_INTERLEAVED, 1.0f};
   const kvq_rows *rows[3] = {q ? q : &k, &k, &v};
   for (int i = 0; i < 3; ++i) {
     p.x[i] = static_cast<const uint8_t *>(rows[i]->data);

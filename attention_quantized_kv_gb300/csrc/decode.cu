@@ -601,18 +601,34 @@ struct MergeArgs {
 };
 
 // One head's merged row: o = acc / L (rotated back for turbo4 V), fp16, and
-// its natural-log lse (M is in log2 units).
+// its natural-log lse (M is in log2 units).  xml, xo: one more part, not rotated.
 template <bool ROT>
 __device__ __forceinline__ void merge_write(const MergeArgs &p, int seq, int kvh, int hg, int h,
                                             int lane, float4 acc, float M, float L,
-                                            bool dry = false) {
+                                            float2 xml = make_float2(-INFINITY, 0.0f),
+                                            float4 xo = make_float4(0.0f, 0.0f, 0.0f, 0.0f)) {
+  float wx = 0.0f, w = 1.0f;
+  if (xml.x != -INFINITY) {
+    const float top = fmaxf(M, xml.x);
+    w = M == -INFINITY ? 0.0f : fast_exp2(M - top);
+    wx = fast_exp2(xml.x - top);
+    L = fmaf(wx, xml.y, w * L);
+    M = top;
+  }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   const int64_t row = static_cast<int64_t>(seq) * p.n_q + kvh * p.G + hg * 8 + h;
-  float ov[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  const float own = w * inv;
+  float ov[4] = {acc.x * own, acc.y * own, acc.z * own, acc.w * own};
   if (ROT) turbo_unrotate_lane(ov, lane);  // turbo4 V: back from the rotated space
+  if (wx != 0.0f) {
+    wx *= inv;
+    ov[0] = fmaf(xo.x, wx, ov[0]);
+    ov[1] = fmaf(xo.y, wx, ov[1]);
+    ov[2] = fmaf(xo.z, wx, ov[2]);
+    ov[3] = fmaf(xo.w, wx, ov[3]);
+  }
   const __half2 o01 = __floats2half2_rn(ov[0], ov[1]), o23 = __floats2half2_rn(ov[2], ov[3]);
   const float lse = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-  if (dry) return;
   __half2 *dst = reinterpret_cast<__half2 *>(p.out + row * kD) + lane * 2;
   dst[0] = o01;
   dst[1] = o23;
@@ -1093,7 +1109,13 @@ struct MergeParams {
   int ups;    // units per work item of the decode kernel's codec pair
   int grid;   // the decode kernel's CTAs
   int fused;  // the decode kernel advances the lengths (a fused decode step)
+  PrefixPart prefix;  // SHARED: one more part per row
 };
+
+// Whether sequence `seq` has a part from a shared prefix.
+__device__ __forceinline__ bool behind_prefix(const PrefixPart &p, int seq) {
+  return !p.group_start || (seq >= p.group_start[0] && seq < p.group_start[p.n_groups]);
+}
 
 // The log-sum-exp merge of every stream's partials (the second kernel of a
 // decode call), one 4-warp CTA per (stream, query head of its group):
@@ -1109,10 +1131,13 @@ struct MergeParams {
 // output does not depend on timing.  The partition is recomputed from the
 // lengths exactly as the decode kernel computed it (a fused step's lengths
 // are already advanced, which is the count it attended).
+// SHARED: one more part per row, from the keys of a shared prefix, already
+// turned back from turbo4's space (its codec may be another): joined last, in
+// fp32, where the row's own parts end.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeRows = 64 / kMergeWarps;  // rows of a warp per window
 
-template <bool ROT>
+template <bool ROT, bool SHARED>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const MergeParams p) {
   __shared__ int32_t pfx[kMaxSeqs + 1];
   __shared__ float4 accs[kMergeWarps][32];
@@ -1152,7 +1177,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
   const int kvh = sl / p.n_hg, hg = sl % p.n_hg, h = blockIdx.y;
   const int n_s = pfx[seq + 1] - pfx[seq];
   // no keys: the decode kernel wrote the rows; heads past the group: nothing
-  if (n_s == 0 || h >= min(8, p.a.G - hg * 8)) return;
+  if ((!SHARED && n_s == 0) || h >= min(8, p.a.G - hg * 8)) return;
   const int64_t U = static_cast<int64_t>(pfx[p.n_seqs]) * KH;
   const int64_t P = p.grid;
   const int64_t S = static_cast<int64_t>(pfx[seq]) * KH + static_cast<int64_t>(sl) * n_s;
@@ -1161,8 +1186,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
   // partial of the owner of item S + j (the owner of item u is
   // floor(((u + 1) P - 1) / U)).
   const bool sparse = U < P;
-  const int64_t c_first = ((S + 1) * P - 1) / U;
-  const int n_live = sparse ? n_s : static_cast<int>(((S + n_s) * P - 1) / U - c_first + 1);
+  const int64_t c_first = SHARED && U == 0 ? 0 : ((S + 1) * P - 1) / U;
+  const int n_live =
+      sparse || n_s == 0 ? n_s : static_cast<int>(((S + n_s) * P - 1) / U - c_first + 1);
   auto slot_of = [&](int j) -> int64_t {
     return (sparse ? ((S + j + 1) * P - 1) / U : c_first + j) + stream;
   };
@@ -1225,7 +1251,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
       const float4 y = accs[w][lane];
       acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
     }
-    merge_write<ROT>(p.a, seq, kvh, hg, h, lane, acc, M, L);
+    if (SHARED && behind_prefix(p.prefix, seq)) {
+      const int64_t row = static_cast<int64_t>(seq) * p.a.n_q + kvh * p.a.G + hg * 8 + h;
+      const float2 x = p.prefix.xml[row];
+      merge_write<ROT>(p.a, seq, kvh, hg, h, lane, acc, M, L, x,
+                       reinterpret_cast<const float4 *>(p.prefix.xo + row * kD)[lane]);
+    } else {
+      merge_write<ROT>(p.a, seq, kvh, hg, h, lane, acc, M, L);
+    }
   }
 }
 
@@ -1286,7 +1319,8 @@ DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms) {
 cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *q, float scale,
                           void *out, float *lse, int max_len, void *workspace,
                           cudaStream_t stream, const void *k_new, const void *v_new,
-                          const kvq_rope *rope, const int32_t *positions) {
+                          const kvq_rope *rope, const int32_t *positions,
+                          const PrefixPart *prefix) {
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   DecodeParams p;
   p.k_cache = static_cast<const uint8_t *>(L.k_cache);
@@ -1336,9 +1370,15 @@ cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *
   const dim3 mgrid(static_cast<unsigned>(p.n_seqs * p.n_kv * p.n_hg),
                    static_cast<unsigned>(p.G < 8 ? p.G : 8));
   const dim3 mblock(kMergeWarps * 32);
-  return L.codec_v == KVQ_TURBO4
-             ? launch_pdl(decode_merge_kernel<true>, mgrid, mblock, 0, stream, mp)
-             : launch_pdl(decode_merge_kernel<false>, mgrid, mblock, 0, stream, mp);
+  const bool rot = L.codec_v == KVQ_TURBO4;
+  if (prefix) {
+    mp.prefix = *prefix;
+    return rot ? launch_pdl(decode_merge_kernel<true, true>, mgrid, mblock, 0, stream, mp)
+               : launch_pdl(decode_merge_kernel<false, true>, mgrid, mblock, 0, stream, mp);
+  }
+  mp.prefix = PrefixPart{};
+  return rot ? launch_pdl(decode_merge_kernel<true, false>, mgrid, mblock, 0, stream, mp)
+             : launch_pdl(decode_merge_kernel<false, false>, mgrid, mblock, 0, stream, mp);
 }
 
 }  // namespace kvq

@@ -73,7 +73,7 @@ int decode_append(const kvq_layer *layer, const kvq_rope *rope, const int32_t *p
     const kvq_rows qr = {const_cast<void *>(q), layer->n_q_heads * d, d, KVQ_T_F16, 0};
     const kvq_rows kr = {const_cast<void *>(k_new), layer->n_kv_heads * d, d, KVQ_T_F16, 0};
     const kvq_rows vr = {const_cast<void *>(v_new), layer->n_kv_heads * d, d, KVQ_T_F16, 0};
-    cudaError_t e = kvq::launch_append_rope(*layer, *rope, &qr, kr, vr, layer->n_seqs, nullptr,
+    cudaError_t e = kvq::launch_append_rope(*layer, rope, &qr, kr, vr, layer->n_seqs, nullptr,
                                             nullptr, positions, out, 1, sms, st_);
     if (e == cudaSuccess)
       e = kvq::launch_decode(*layer, pl, out, scale, out, lse, max_len, workspace, st_);

@@ -59,6 +59,49 @@ inline int check_rope(const kvq_rope *r) {
   return aligned(r->table, 16) ? KVQ_OK : KVQ_EALIGN;
 }
 
+// Strides and pointer of a set of rows [n][heads][128].
+inline int check_rows(const kvq_rows &r, bool is_written, int64_t n, int32_t heads) {
+  if (!r.data || r.reserved != 0) return KVQ_EINVAL;
+  if (r.type != KVQ_T_F16 && r.type != KVQ_T_BF16 && r.type != KVQ_T_F32) return KVQ_EUNSUPPORTED;
+  if (r.row_stride < 0 || r.head_stride < 0) return KVQ_EINVAL;
+  const int64_t sz = type_bytes(r.type);
+  if (!aligned(r.data, 16) || r.row_stride * sz % 16 || r.head_stride * sz % 16) return KVQ_EALIGN;
+  if (is_written) {  // no two rows may share a place
+    const int64_t d = kHeadDim;
+    const bool heads_inside = (heads == 1 || r.head_stride >= d) &&
+                              (n == 1 || r.row_stride >= (heads - 1) * r.head_stride + d);
+    const bool rows_inside = (n == 1 || r.row_stride >= d) &&
+                             (heads == 1 || r.head_stride >= (n - 1) * r.row_stride + d);
+    if (!heads_inside && !rows_inside) return KVQ_EINVAL;
+  }
+  return KVQ_OK;
+}
+
+inline int64_t span_bytes(const kvq_rows &r, int64_t n, int32_t heads) {
+  return ((n - 1) * r.row_stride + (heads - 1) * r.head_stride + kHeadDim) * type_bytes(r.type);
+}
+
+// Whether a and b are disjoint parts of the same rows (views of one tensor).
+inline bool interleaved(const kvq_rows &a, const kvq_rows &b, int64_t n, int32_t heads) {
+  const int64_t pitch = a.row_stride * type_bytes(a.type);
+  if (n < 2 || pitch != b.row_stride * type_bytes(b.type)) return false;
+  const int64_t wa = span_bytes(a, 1, heads), wb = span_bytes(b, 1, heads);
+  const int64_t at = static_cast<uint8_t *>(b.data) - static_cast<uint8_t *>(a.data);
+  const int64_t d = (at % pitch + pitch) % pitch;
+  return d >= wa && d + wb <= pitch;
+}
+
+// Which rows belong to which sequence: row_start (packed), n_new (padded) or
+// neither (one row per sequence).
+inline int check_packed(const kvq_layer *L, int64_t n_rows, const int32_t *n_new,
+                        const int32_t *row_start, bool one_each) {
+  if (n_rows < 0 || n_rows > INT32_MAX) return KVQ_EINVAL;
+  if (n_new && row_start) return KVQ_EINVAL;
+  if (!n_new && !row_start && (!one_each || n_rows != L->n_seqs)) return KVQ_EINVAL;
+  if (n_new && n_rows % L->n_seqs != 0) return KVQ_EINVAL;
+  return aligned(n_new, 4) && aligned(row_start, 4) ? KVQ_OK : KVQ_EALIGN;
+}
+
 // Decode streams: (sequence, kv head, group of up to 8 query heads).
 inline bool decode_shape_ok(const kvq_layer *L) {
   const int64_t G = L->n_q_heads / L->n_kv_heads;

@@ -37,6 +37,16 @@ struct DecodePlan {
   int64_t ws_bytes = 0;
 };
 
+// What a decode step's rows have from the keys of a shared prefix: xo fp32
+// [n_seqs][n_q][128] unnormalised, xml [n_seqs][n_q] (max in log2 units, sum),
+// of sequences group_start[0] .. group_start[n_groups] - 1 (null: all).
+struct PrefixPart {
+  const float *xo;
+  const float2 *xml;
+  const int32_t *group_start;
+  int n_groups;
+};
+
 DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms);
 // k_new / v_new (fused decode step, fp16 [n_seqs][n_kv][128]): append one
 // token per sequence before attending, and advance the lengths; rope: rotate
@@ -45,7 +55,8 @@ cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *
                           void *out, float *lse, int max_len, void *workspace,
                           cudaStream_t stream, const void *k_new = nullptr,
                           const void *v_new = nullptr, const kvq_rope *rope = nullptr,
-                          const int32_t *positions = nullptr);
+                          const int32_t *positions = nullptr,
+                          const PrefixPart *prefix = nullptr);
 
 struct PrefillPlan {
   int64_t kv_tokens = 0;     // keys attended by the chunk: q_start + n_q_tok
@@ -75,6 +86,31 @@ cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32
                            int max_evict, void *k_dst, void *v_dst, const float *scores,
                            float *scores_dst, int32_t *lens_dst, cudaStream_t stream);
 
+// Query rows against every key of their sequence (cross.cu).
+constexpr int kCrossMaxSeqs = 1024;  // key sequences per call
+struct CrossPlan {
+  int64_t ws_bytes = 0;
+};
+// Where the rows go: out and lse (optional), or, for a merge, xo fp32
+// [n_rows][n_q][128] unnormalised and xml [n_rows][n_q] (max in log2 units, sum).
+struct CrossOut {
+  void *out;
+  float *lse;
+  float *xo;
+  float2 *xml;
+};
+// n_new and row_start both null: n_rows / n_seqs rows per sequence.
+CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms);
+cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows &q,
+                         int64_t n_rows, const int32_t *n_new, const int32_t *row_start,
+                         float scale, const CrossOut &out, int64_t out_row, int64_t out_head,
+                         int out_type, int max_len, void *workspace, cudaStream_t stream);
+
+// Cached rows as values (read_rows.cu).
+cudaError_t launch_read_rows(const kvq_layer &L, const kvq_rows *k, const kvq_rows *v,
+                             int64_t n_rows, const int32_t *n_read, const int32_t *row_start,
+                             const int32_t *first, cudaStream_t stream);
+
 // Rotary positions (rope.cu, append_rope.cu).
 
 // Sequences from which a rotary decode step appends in a launch of its own
@@ -94,8 +130,8 @@ cudaError_t launch_rope_table(const double *freqs, int rot_dim, int n_pos, float
 cudaError_t launch_rope_apply(const kvq_rope &rope, const kvq_rows &x, const kvq_rows &y,
                               int64_t n_rows, int n_heads, const int32_t *positions, int pos0,
                               int transpose, int32_t *err, cudaStream_t stream);
-// n_new and row_start both null: one row per sequence.
-cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope &rope, const kvq_rows *q,
+// n_new and row_start both null: one row per sequence.  rope null: no rotation.
+cudaError_t launch_append_rope(const kvq_layer &L, const kvq_rope *rope, const kvq_rows *q,
                                const kvq_rows &k, const kvq_rows &v, int64_t n_rows,
                                const int32_t *n_new, const int32_t *row_start,
                                const int32_t *positions, void *q_out, int update_lens,

@@ -21,28 +21,6 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586;
 
-// Strides and pointer of a set of rows [n][heads][128].
-int check_rows(const kvq_rows &r, bool is_written, int64_t n, int32_t heads) {
-  if (!r.data || r.reserved != 0) return KVQ_EINVAL;
-  if (r.type != KVQ_T_F16 && r.type != KVQ_T_BF16 && r.type != KVQ_T_F32) return KVQ_EUNSUPPORTED;
-  if (r.row_stride < 0 || r.head_stride < 0) return KVQ_EINVAL;
-  const int64_t sz = type_bytes(r.type);
-  if (!aligned(r.data, 16) || r.row_stride * sz % 16 || r.head_stride * sz % 16) return KVQ_EALIGN;
-  if (is_written) {  // no two rows may share a place
-    const int64_t d = kHeadDim;
-    const bool heads_inside = (heads == 1 || r.head_stride >= d) &&
-                              (n == 1 || r.row_stride >= (heads - 1) * r.head_stride + d);
-    const bool rows_inside = (n == 1 || r.row_stride >= d) &&
-                             (heads == 1 || r.head_stride >= (n - 1) * r.row_stride + d);
-    if (!heads_inside && !rows_inside) return KVQ_EINVAL;
-  }
-  return KVQ_OK;
-}
-
-int64_t span_bytes(const kvq_rows &r, int64_t n, int32_t heads) {
-  return ((n - 1) * r.row_stride + (heads - 1) * r.head_stride + kHeadDim) * type_bytes(r.type);
-}
-
 }  // namespace
 }  // namespace kvq
 
@@ -152,7 +130,7 @@ int kv_append_rope(const kvq_layer *layer, const kvq_rope *rope, const kvq_rows 
   }
   const int sms = kvq::device_sms();
   if (sms <= 0) return KVQ_ECUDA;
-  const cudaError_t e = kvq::launch_append_rope(*layer, *rope, q, *k, *v, n_rows, n_new, row_start,
+  const cudaError_t e = kvq::launch_append_rope(*layer, rope, q, *k, *v, n_rows, n_new, row_start,
                                                 positions, q_out, update_lens, sms,
                                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;

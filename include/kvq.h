@@ -14,6 +14,10 @@
  *   kv_append_rope       rotate new keys and append them, with the values
  *   kv_rope_shift        rotate cached keys again after their positions moved
  *   attn_decode_append_rope   one decode step with the rotation in it
+ *   attn_cross           query rows against every key of their sequence
+ *   attn_decode_prefix   decode attention of sequences that share a prefix
+ *   kv_append_rows       packed or padded rows appended as they are
+ *   kv_read_rows         cached rows read back as values
  *
  * Sources.  The codecs and their sizes follow the "Codecs" table of the
  * buun-llama-cpp listing (f16 16.0, q8_0 8.5, q4_0 4.5 bits per value); the
@@ -154,13 +158,14 @@ typedef enum {
 
 /* Bits OR-ed into *kvq_layer.err by the device (the word is never cleared). */
 #define KVQ_DEVERR_CAPACITY 1 /* append: seq_lens[s] + n_new[s] > capacity; rows skipped */
-#define KVQ_DEVERR_MAXLEN 2   /* decode: seq_lens[s] > max_len; keys past max_len ignored */
+#define KVQ_DEVERR_MAXLEN 2   /* decode, cross: seq_lens[s] > max_len; keys past max_len ignored */
 #define KVQ_DEVERR_TIMEOUT 4  /* a bounded wait on an async copy gave up */
-#define KVQ_DEVERR_SEQLEN 8   /* prefill: seq_lens[seq] < q_start + n_q_tok */
+#define KVQ_DEVERR_SEQLEN 8   /* prefill: seq_lens[seq] < q_start + n_q_tok; read: a token outside
+                               * the sequence */
 #define KVQ_DEVERR_PAGE 16    /* paged: a block-table entry outside [0, n_pages) */
 #define KVQ_DEVERR_EVICT 32   /* kv_compact: an eviction list not increasing below the length */
 #define KVQ_DEVERR_POS 64     /* rotary: a position (or shift) outside the angle table, clamped to it */
-#define KVQ_DEVERR_ROWS 128   /* kv_append_rope: row_start decreasing or outside [0, n_rows] */
+#define KVQ_DEVERR_ROWS 128   /* packed or padded rows: a count or row_start entry out of range */
 
 /* One layer's cache.  All pointers are device pointers owned by the caller.
  * k_cache / v_cache: kvq_cache_bytes() bytes each (kvq_pool_bytes() when
@@ -536,6 +541,76 @@ KVQ_API int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope
                                     const void *v_new, const void *q, float scale, void *out,
                                     float *lse, int32_t max_len, void *workspace,
                                     size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rows of several sequences against their caches, without a rotation and
+ * without a causal mask.  The pages name none of these; the definitions below
+ * are this library's.  Which rows belong to which sequence is said as for
+ * kv_append_rope, by row_start (packed) or n_new (padded); an entry out of
+ * range sets KVQ_DEVERR_ROWS and that sequence's rows are unspecified.
+ * ------------------------------------------------------------------------ */
+
+/* kv_append_rope without the rotation: k and v rows (one type; strided) are
+ * encoded as they are, for keys that carry no position or carry it already, an
+ * encoder's states among them.  The bytes are those of kv_append_quantize (bf16
+ * and fp32 rows: encoded from fp32). */
+KVQ_API int kv_append_rows(const kvq_layer *layer, const kvq_rows *k, const kvq_rows *v,
+                           int64_t n_rows, const int32_t *n_new, const int32_t *row_start,
+                           int32_t update_lens, void *stream);
+
+/* Cached rows as values: row i of sequence s is token first[s] + i (first:
+ * device int32 [n_seqs], or NULL for 0), decoded exactly in fp32 and rounded
+ * once to the output's type.  k, v: rows [n_rows][n_kv_heads][128] to be
+ * written, either of them NULL for a side that is not read; their types and
+ * strides may differ, their places may not meet.  n_read, row_start: as n_new
+ * and row_start of kv_append_rope.  A token outside [0, seq_lens[s]) sets
+ * KVQ_DEVERR_SEQLEN, an unmapped page KVQ_DEVERR_PAGE; such rows, and rows that
+ * belong to no sequence, are left as they were. */
+KVQ_API int kv_read_rows(const kvq_layer *layer, const kvq_rows *k, const kvq_rows *v,
+                         int64_t n_rows, const int32_t *n_read, const int32_t *row_start,
+                         const int32_t *first, void *stream);
+
+/* Workspace bytes that attn_cross needs for n_rows rows and max_len. */
+KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t max_len,
+                                 size_t *bytes);
+
+/* Attention of query rows to every key of their sequence: row r of sequence s,
+ * head h: softmax(scale q k^T) v over the tokens t < seq_lens[s] of kv head
+ * h / (n_q/n_kv); cross attention to an encoder's states, whose lengths have
+ * nothing to do with the rows'.
+ * q: rows [n_rows][n_q_heads][128], fp16 or bf16 (taken as fp16: rounded, and
+ * infinite beyond its range); out: rows of the same type, not meeting q; lse:
+ * optional fp32 [n_rows][n_q_heads], natural log.  Rows belong to sequences by
+ * n_new or row_start; both NULL: row s to sequence s (n_rows = n_seqs).  Rows
+ * that belong to no sequence are left as they were; a sequence of length 0 gives
+ * out = 0 and lse = -inf.  scale > 0.  max_len bounds every seq_lens[s].
+ * workspace: device, 16-byte aligned, of any contents; calls that may run
+ * concurrently need separate ones.  At most 1024 sequences. */
+KVQ_API int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows,
+                       const int32_t *n_new, const int32_t *row_start, float scale,
+                       const kvq_rows *out, float *lse, int32_t max_len, void *workspace,
+                       size_t ws_bytes, void *stream);
+
+/* Workspace bytes that attn_decode_prefix needs. */
+KVQ_API int attn_decode_prefix_workspace(const kvq_layer *layer, const kvq_layer *prefix,
+                                         int32_t max_len, int32_t max_prefix, size_t *bytes);
+
+/* attn_decode of sequences that share long prefixes, each prefix held and read
+ * once: sequence s of `layer` attends every key of its group's sequence of
+ * `prefix` and every key of its own, one softmax over both.  prefix: a layer of
+ * the same heads whose sequence g is the prefix of the sequences group_start[g]
+ * .. group_start[g + 1] - 1 of `layer` (device int32 [prefix n_seqs + 1],
+ * non-decreasing; NULL: the one prefix of all); sequences outside the groups
+ * attend their own keys alone.  Its codecs, capacity and pages are its own: two
+ * paged layers may be views of one pool, the prefix's block table over the shared
+ * pages, the layer's over the rest (their lengths then count those alone).
+ * q, out, lse, max_len: as attn_decode (q 16-byte aligned and not meeting out;
+ * scale > 0); max_prefix bounds the prefix's lengths.  workspace: as attn_cross.
+ * Conditions of the prefix (and of group_start) are set in its own err word. */
+KVQ_API int attn_decode_prefix(const kvq_layer *layer, const kvq_layer *prefix,
+                               const int32_t *group_start, const void *q, float scale,
+                               void *out, float *lse, int32_t max_len, int32_t max_prefix,
+                               void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
