@@ -3,112 +3,1144 @@
 // the shared part of a decode step behind a common prefix.
 //
 // o = softmax(scale q K^T) V over the keys below the sequence's length, query
-// head h reading kv head h / (n_q / n_kv).
+// head h reading kv head h / G, G = n_q / n_kv.  The G heads of a kv head read the
+// same keys, so a sequence's rows are taken as n * G rows per kv head (row R:
+// token R / G, head R % G) in tiles of 128, and two tiles (a pair) share every
+// key tile that is read; a last odd tile stands alone.
+//
+// Work.  An item is (sequence, kv head, pair or single tile): a run of key-tile
+// steps, one per 128 keys.  All items' steps are laid end to end, a pair's
+// counting twice, and the CTAs (one per SM) take equal contiguous slices: whole
+// items, and pieces of at most two more.  The rows of a piece go to a partial
+// slot (unnormalised O, max, sum), and a second kernel joins an item's pieces by
+// log-sum-exp in a fixed order.  Lengths and row counts are read on the device.
+//
+// Inside a CTA (16 warps) nothing is written to HBM but the results: codes are
+// copied in as they lie in the cache, turned into tensor-core operand tiles in
+// shared memory and used there.
+//  * Warp 12 copies the codes of 64 keys of one side at a time into a ring
+//    (1-D bulk copies); K and V tiles alternate.
+//  * Warps 8-11 turn them into fp16 operand tiles (x^ = d q rounded once; three
+//    32 KB buffers).  The cache's order is kept where the operands leave the
+//    choice, so that 16 bytes of codes become whole 8- or 16-byte pieces of a tile
+//    without an exchange between lanes: a key's place in its tile is 4 tig + 2 rh
+//    + par (include/kvq.h), the same for K's rows and V's columns, and K's dims
+//    stand in the order 32 b + 8 w + 4 h + i, as Q's do.  turbo4 stays in its
+//    rotated space: Q is rotated, O rotated back.
+//  * One thread of warp 13 issues tcgen05.mma: S = Q K^T into TMEM, O += P V with
+//    P read from TMEM.
+//  * Warps 0-3 and 4-7 are two softmax pipes, one query row per thread.  In a
+//    pair they hold the two tiles; with a single tile they take its even and odd
+//    key tiles and are joined through shared memory at the end, so that one
+//    pipe's softmax overlaps the other's products either way.
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include <math.h>
 
 #include "kvq_launch.h"
 #include "kvq_packed.cuh"
 #include "kvq_rope.cuh"
-#include "kvq_row_decode.cuh"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kCrossWarps = 8;
+constexpr int kTile = 128;                        // query rows, and keys, of a tile
+constexpr int kSlotUnits = 4;                     // units per ring slot: half a key tile
+constexpr int kBufs = 3;                          // operand tiles of K and V
+constexpr int kMaxSlots = 14;
+constexpr int kThreads = 512;
+constexpr int kDequantWarp = 8, kDequantWarps = 4, kCopyWarp = 12, kMmaWarp = 13;
+constexpr int kRingBytes = 65536;                 // four slots of f16 units
+constexpr int kSmemBytes = (2 + kBufs) * kTileBytes + kRingBytes + 1024;
+constexpr float kRaise = 8.0f;                    // log2 units, as in the prefill
+// Weights are held as 2^(s - m + 6): at most 2^14 in fp16, and 2^6 further from
+// its subnormals than 2^(s - m).
+constexpr float kLift = 6.0f;
+constexpr int kPartStride = 132;                  // floats of a partial row: 128 O, m, l, 2 pad
+constexpr int kSlotFloats = 2 * kTile * kPartStride;
 
 struct CrossParams {
   const uint8_t *cache[2];
   int codec[2];
   const uint8_t *q;
   int64_t q_row, q_head, out_row, out_head;  // strides in bytes
-  int q_type, out_type;
+  int q_bf16;                                // q and out: bf16, else fp16
   CrossOut out;
+  float *part;  // partial slots [2 per CTA][2 tiles][128][kPartStride]
   PackedRows rows;
   const int32_t *seq_lens, *table;
   int32_t *err;
-  int n_q, n_kv, G, capacity, max_len, pages_per_seq, n_pages;
+  int n_q, n_kv, G, capacity, max_len, pages_per_seq, n_pages, slots, slot_bytes;
   float scale_log2;
 };
 
-// A warp per (row, query head), one key after the other.
-__global__ void __launch_bounds__(kCrossWarps * 32)
-    cross_kernel(const __grid_constant__ CrossParams p) {
+// ------------------------------------------------------------------ work
+
+// One sequence's rows and keys.
+struct SeqWork {
+  int64_t first, R;  // first row (token); rows per kv head: tokens * G
+  int len, nt;       // keys, key tiles (0: nothing to do)
+  int blocks;        // pairs, and the single tile if there is one
+  bool odd;          // the last block is a single tile
+  __device__ __forceinline__ int weight(int blk) const { return odd && blk == blocks - 1 ? 1 : 2; }
+  __device__ __forceinline__ int64_t per_head() const {
+    return static_cast<int64_t>(nt) * (2 * static_cast<int64_t>(blocks) - (odd ? 1 : 0));
+  }
+};
+__device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
+  SeqWork w;
+  bool bad;
+  const int64_t n = packed_rows(p.rows, s, w.first, bad);
+  w.len = max(0, min(p.seq_lens[s], p.max_len));
+  w.R = n * p.G;
+  w.nt = n > 0 ? (w.len + kTile - 1) / kTile : 0;
+  const int64_t tiles = (w.R + kTile - 1) / kTile;
+  w.blocks = static_cast<int>((tiles + 1) / 2);
+  w.odd = (tiles & 1) != 0;
+  return w;
+}
+// CTAs that get a slice: each at least as long as a step, so that every CTA
+// between an item's first and last has a step of it.
+__device__ __forceinline__ int64_t cross_ctas(int64_t W, int grid) {
+  return max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), W / 2));
+}
+// The CTA whose slice [W c / P, W (c + 1) / P) holds position x.
+__device__ __forceinline__ int64_t owner_of(int64_t x, int64_t W, int64_t P) {
+  return ((x + 1) * P - 1) / W;
+}
+
+struct Segment {
+  int64_t first, R, row0;  // the sequence's first row and rows; the block's first row
+  int s, kvh, len, nt, j_lo, j_hi;
+  bool pair, inside;       // inside: the item begins in this CTA's slice
+};
+// A CTA's segments: the pieces of the items that its slice [s0, s1) holds.
+struct SegIter {
+  int64_t s0, s1, at;  // at: the current item's first position
+  SeqWork w;
+  int s, kvh, blk;
+  __device__ __forceinline__ void init(const CrossParams &p, int64_t a, int64_t b, int seq,
+                                       int64_t seq_at) {
+    s0 = a;
+    s1 = b;
+    s = seq;
+    w = seq_work(p, s);
+    const int64_t head = w.per_head(), off = a - seq_at;
+    kvh = static_cast<int>(off / head);
+    blk = static_cast<int>(min((off % head) / (2 * w.nt), static_cast<int64_t>(w.blocks - 1)));
+    at = seq_at + kvh * head + static_cast<int64_t>(blk) * 2 * w.nt;
+  }
+  __device__ __forceinline__ bool next(const CrossParams &p, Segment &g) {
+    while (at < s1) {
+      const int wt = w.weight(blk);
+      const int64_t lo = s0 <= at ? 0 : (s0 - at + wt - 1) / wt;
+      const int64_t hi = min(static_cast<int64_t>(w.nt), (s1 - at + wt - 1) / wt);
+      g.first = w.first;
+      g.R = w.R;
+      g.row0 = static_cast<int64_t>(blk) * (2 * kTile);
+      g.s = s;
+      g.kvh = kvh;
+      g.len = w.len;
+      g.nt = w.nt;
+      g.j_lo = static_cast<int>(lo);
+      g.j_hi = static_cast<int>(hi);
+      g.pair = wt == 2;
+      g.inside = at >= s0;
+      at += static_cast<int64_t>(wt) * w.nt;
+      if (++blk == w.blocks) {
+        blk = 0;
+        if (++kvh == p.n_kv) {
+          kvh = 0;
+          while (++s < p.rows.n_seqs) {
+            w = seq_work(p, s);
+            if (w.nt > 0) break;
+          }
+          if (s >= p.rows.n_seqs) at = INT64_MAX;
+        }
+      }
+      if (lo < hi) return true;
+    }
+    return false;
+  }
+};
+// The order in which a segment of n steps uses its 2 n operand tiles: K_0, then
+// K_{j+1}, V_j in turn, the last V alone.
+__device__ __forceinline__ int k_use(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_use(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+__device__ __forceinline__ void use_at(int i, int n, int &side, int &j) {
+  side = i == 0 || ((i & 1) && i < 2 * n - 1) ? 0 : 1;
+  j = side == 0 ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1;
+}
+
+// ------------------------------------------------------------------ codes to operand tiles
+
+__device__ __forceinline__ void sts128(uint8_t *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(a, b, c, d);
+}
+__device__ __forceinline__ void sts64(uint8_t *p, uint32_t a, uint32_t b) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+}
+__device__ __forceinline__ uint32_t twice(uint32_t half) { return half * 0x10001u; }
+// Four signed bytes as fp16 pairs (0, 1) and (2, 3), exact: the byte plus 128 in
+// the mantissa of 1024, less 1152.
+__device__ __forceinline__ void s8_quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t t = w ^ 0x80808080u;
+  lo = hsub2_bits(__byte_perm(t, 0x64646464u, 0x4140), 0x64806480u);
+  hi = hsub2_bits(__byte_perm(t, 0x64646464u, 0x4342), 0x64806480u);
+}
+// Four nibbles (one in each byte's low half) less 8, likewise.
+__device__ __forceinline__ void u4_quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  lo = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4140), 0x64086408u);
+  hi = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4342), 0x64086408u);
+}
+
+// One unit of K into rows 16 u .. of the tile (all 32 lanes).  A lane takes the
+// 16-byte pieces (g, w) of row g and row g + 8; the order of g over the lanes
+// keeps loads (pieces 4 g + w) and stores (piece w ^ place of g) of eight lanes on
+// distinct banks.
+template <int CODEC>
+__device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int row0, int lane) {
+  const int q8 = lane >> 2, w = lane & 3;
+  const int g = (q8 & 4) | ((0x2130 >> (4 * (q8 & 3))) & 3);
+  const int place = row0 + 4 * (g >> 1) + (g & 1);
+  uint8_t *row[2] = {tile + place * 128, tile + (place + 2) * 128};
+  const int sw[2] = {place & 7, (place + 2) & 7};
+  const uint8_t *src = u + (4 * g + w) * 16;
+  auto at = [&](int rh, int b) {
+    return row[rh] + (b >> 1) * kHalfBytes + (((4 * (b & 1) + w) ^ sw[rh]) << 4);
+  };
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh)
+        *reinterpret_cast<uint4 *>(at(rh, b)) = lds128(src + (2 * b + rh) * 512);
+    return;
+  }
+  uint32_t d[2][4];  // scales by row and block, as pairs
+  if (CODEC == KVQ_TURBO4) {
+    const uint32_t x = *reinterpret_cast<const uint32_t *>(u + 1024 + g * 4);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      d[0][b] = twice(x & 0xffffu);
+      d[1][b] = twice(x >> 16);
+    }
+  } else {
+    const uint4 x = lds128(u + unit_scale_offset(CODEC) + g * 16);
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh) {
+        const uint32_t z = y[2 * rh + (b >> 1)];
+        d[rh][b] = twice((b & 1) ? z >> 16 : z & 0xffffu);
+      }
+  }
+  if (CODEC == KVQ_Q8_0) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint4 x = lds128(src + b * 512);
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (rh, h)
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh) {
+        uint32_t o[4];
+        s8_quad(y[2 * rh], o[0], o[1]);
+        s8_quad(y[2 * rh + 1], o[2], o[3]);
+        sts128(at(rh, b), hmul2_bits(o[0], d[rh][b]), hmul2_bits(o[1], d[rh][b]),
+               hmul2_bits(o[2], d[rh][b]), hmul2_bits(o[3], d[rh][b]));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int bp = 0; bp < 2; ++bp) {
+      const uint4 x = lds128(src + bp * 512);
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (b & 1, rh)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 2 * bp + (i >> 1), rh = i & 1;
+        uint32_t o[4];
+        u4_quad(y[i] & 0x0f0f0f0fu, o[0], o[1]);
+        u4_quad((y[i] >> 4) & 0x0f0f0f0fu, o[2], o[3]);
+        sts128(at(rh, b), hmul2_bits(o[0], d[rh][b]), hmul2_bits(o[1], d[rh][b]),
+               hmul2_bits(o[2], d[rh][b]), hmul2_bits(o[3], d[rh][b]));
+      }
+    }
+  }
+}
+
+// One unit of V into columns 16 u .. of the tile, whose rows are dims (all 32
+// lanes).  A lane takes the pieces (gq, tig): two to eight dims of four tokens,
+// eight bytes in each dim's row.  TAIL: of the unit only `live` tokens (any
+// number, none and more than 16 included) are the sequence's; the others'
+// columns are zeros, whatever lies there.
+template <int CODEC, bool TAIL>
+__device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int unit, int live,
+                                          int lane) {
+  const int q8 = lane >> 2, tig = lane & 3;
+  const int gq = nibble_codec(CODEC) ? (0x65217430 >> (4 * q8)) & 7 : q8;
+  uint8_t *col = tile + (unit >> 2) * kHalfBytes + (tig & 1) * 8;
+  const int piece = 2 * (unit & 3) + (tig >> 1);
+  uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // tokens 2 tig, + 1; + 8, + 9
+  if (TAIL) {
+    auto mask = [&](int t) {
+      return (t < live ? 0x0000ffffu : 0u) | (t + 1 < live ? 0xffff0000u : 0u);
+    };
+    m0 = mask(2 * tig);
+    m1 = mask(2 * tig + 8);
+  }
+  auto put = [&](int dim, uint32_t a, uint32_t b) {
+    if (TAIL) {
+      a &= m0;
+      b &= m1;
+    }
+    sts64(col + dim * 128 + ((piece ^ (dim & 7)) << 4), a, b);
+  };
+  const uint8_t *src = u + (4 * gq + tig) * 16;
+  if (CODEC == KVQ_F16) {
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const uint4 x = lds128(src + mt * 512);  // (rh, s)
+      put(16 * mt + 2 * gq, x.x, x.z);
+      put(16 * mt + 2 * gq + 1, x.y, x.w);
+    }
+  } else if (CODEC == KVQ_Q8_0) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint2 d = lds64(u + 2048 + tig * 32 + b * 8);
+      const uint4 x = lds128(src + b * 512);
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (mt & 1, rh)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int dim = 32 * b + 16 * m + 2 * gq;
+        put(dim, hmul2_bits(s8_pair_02(y[2 * m]), d.x), hmul2_bits(s8_pair_02(y[2 * m + 1]), d.y));
+        put(dim + 1, hmul2_bits(s8_pair_13(y[2 * m]), d.x),
+            hmul2_bits(s8_pair_13(y[2 * m + 1]), d.y));
+      }
+    }
+  } else {
+    uint2 d = make_uint2(0u, 0u);
+    if (CODEC == KVQ_TURBO4) d = lds64(u + 1024 + tig * 8);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 x = lds128(src + h * 512);
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // mt = 4 h + i; bytes (par, rh)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 2 * h + (i >> 1), dim = 32 * b + 8 * (i & 1) + gq;
+        if (CODEC == KVQ_Q4_0 && (i & 1) == 0) d = lds64(u + 1024 + tig * 32 + b * 8);
+        const uint32_t z = y[i] >> 8;
+        put(dim, hmul2_bits(u4_pair_minus8(y[i]), d.x), hmul2_bits(u4_pair_minus8(z), d.y));
+        put(dim + 16, hmul2_bits(u4_pair_minus8_hi(y[i]), d.x),
+            hmul2_bits(u4_pair_minus8_hi(z), d.y));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void unit_to_tile(int side, int codec, const uint8_t *u, uint8_t *tile,
+                                             int unit, int live, int lane) {
+  if (side == 0) {  // (rows past the length: their scores are masked)
+    if (codec == KVQ_F16) unit_to_k<KVQ_F16>(u, tile, 16 * unit, lane);
+    else if (codec == KVQ_Q8_0) unit_to_k<KVQ_Q8_0>(u, tile, 16 * unit, lane);
+    else if (codec == KVQ_Q4_0) unit_to_k<KVQ_Q4_0>(u, tile, 16 * unit, lane);
+    else unit_to_k<KVQ_TURBO4>(u, tile, 16 * unit, lane);
+  } else if (live >= kUnitTokens) {
+    if (codec == KVQ_F16) unit_to_v<KVQ_F16, false>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, false>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, false>(u, tile, unit, live, lane);
+    else unit_to_v<KVQ_TURBO4, false>(u, tile, unit, live, lane);
+  } else {
+    if (codec == KVQ_F16) unit_to_v<KVQ_F16, true>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, true>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, true>(u, tile, unit, live, lane);
+    else unit_to_v<KVQ_TURBO4, true>(u, tile, unit, live, lane);
+  }
+}
+// The token, within a unit, of column c of a tile (mod 16).
+__device__ __forceinline__ constexpr int token_of(int c) {
+  return 8 * ((c >> 1) & 1) + 2 * ((c & 15) >> 2) + (c & 1);
+}
+
+// ------------------------------------------------------------------ TMEM pieces
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Unnormalised Sylvester-order FWHT of 32 values in registers.
+__device__ __forceinline__ void fwht32(float (&v)[32]) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+}
+
+// Where a finished row goes: its place in out (fp16 or bf16, normalised), or
+// fp32 (unnormalised) in xo or a partial slot.
+struct RowOut {
+  uint8_t *half;
+  float *full;
+  float inv;
+  int bf16;
+  // 8 values at dims d ..
+  __device__ __forceinline__ void put(int d, const float (&x)[8]) const {
+    if (full) {
+      reinterpret_cast<float4 *>(full + d)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4 *>(full + d)[1] = make_float4(x[4], x[5], x[6], x[7]);
+      return;
+    }
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+    if (bf16) store_eight<KVQ_T_BF16>(half + 2 * d, y);
+    else store_eight<KVQ_T_F16>(half + 2 * d, y);
+  }
+};
+
+struct __align__(8) CrossBars {
+  uint64_t raw_full[kMaxSlots], raw_empty[kMaxSlots];
+  uint64_t tile_full[kBufs], tile_empty[kBufs];
+  uint64_t sfull[2], pfull[2], odone[2], segdone[2], qready[2], ofree[2], drain;
+};
+
+// ------------------------------------------------------------------ attention
+
+// Both softmax pipes (256 threads).
+__device__ __forceinline__ void pipes_sync() {
+  asm volatile("bar.sync 1, 256;\n" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_attn_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ CrossBars bars;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag, first_seq;
+  __shared__ int64_t slice[3];  // the slice, and the first sequence's position
+  __shared__ float2 pipe1_ml[kTile];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sq = smem, *tiles = smem + 2 * kTileBytes, *ring = tiles + kBufs * kTileBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
   grid_dependency_wait();
   grid_launch_dependents();
-  if (blockIdx.x == 0) packed_check(p.rows, p.err);
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kCrossWarps + (threadIdx.x >> 5);
-  const int64_t row = item / p.n_q;
-  const int head = static_cast<int>(item % p.n_q), kvh = head / p.G;
-  if (row >= p.rows.n_rows) return;
+
+  if (warp == 0) {  // this CTA's slice, and where it begins
+    int64_t sum = 0;
+    for (int s = lane; s < p.rows.n_seqs; s += 32) {
+      if (blockIdx.x == 0) {
+        bool bad;
+        int64_t first;
+        packed_rows(p.rows, s, first, bad);
+        if (bad) set_err(p.err, KVQ_DEVERR_ROWS);
+        if (p.seq_lens[s] > p.max_len) set_err(p.err, KVQ_DEVERR_MAXLEN);
+      }
+      sum += seq_work(p, s).per_head() * p.n_kv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int64_t W = sum, P = cross_ctas(W, gridDim.x), c = blockIdx.x;
+    const int64_t s0 = c < P ? W * c / P : W, s1 = c < P ? W * (c + 1) / P : W;
+    if (s0 < s1) {
+      int64_t carry = 0;
+      for (int base = 0; base < p.rows.n_seqs; base += 32) {
+        const int s = base + lane;
+        const int64_t n = s < p.rows.n_seqs ? seq_work(p, s).per_head() * p.n_kv : 0;
+        int64_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, carry + incl > s0);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            first_seq = s;
+            slice[2] = carry + incl - n;
+          }
+          break;
+        }
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (lane == 0) {
+      slice[0] = s0;
+      slice[1] = s1;
+      abort_flag = 0;
+      for (int i = 0; i < p.slots; ++i) {
+        mbar_init(&bars.raw_full[i], 1);
+        mbar_init(&bars.raw_empty[i], kDequantWarps);
+      }
+      for (int i = 0; i < kBufs; ++i) {
+        mbar_init(&bars.tile_full[i], kDequantWarps);
+        mbar_init(&bars.tile_empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.sfull[i], 1);
+        mbar_init(&bars.pfull[i], 4);  // one arrival per softmax warp
+        mbar_init(&bars.odone[i], 1);
+        mbar_init(&bars.segdone[i], 1);
+        mbar_init(&bars.qready[i], 4);
+        mbar_init(&bars.ofree[i], 4);
+      }
+      mbar_init(&bars.drain, 1);
+      fence_mbar_init();
+    }
+  }
+  __syncthreads();
+  const int64_t s0 = slice[0], s1 = slice[1];
+  if (s0 >= s1) return;  // whole CTA: no work
+  if (warp == kMmaWarp) tmem_alloc(&tmem_base_sh, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 384};
+
+  SegIter it;
+  it.init(p, s0, s1, first_seq, slice[2]);
+  Segment sg;
+
+  if (warp == kCopyWarp) {
+    // ---------------- codes into the ring, half a tile of one side at a time
+    if (lane == 0) {
+      int t = 0;  // slots filled
+      bool ok = true;
+      while (ok && it.next(p, sg)) {
+        const int n = sg.j_hi - sg.j_lo, units = (sg.len + kUnitTokens - 1) / kUnitTokens;
+        for (int i = 0; i < 2 * n && ok; ++i) {
+          int side, j;
+          use_at(i, n, side, j);
+          const int u0 = (sg.j_lo + j) * (kTile / kUnitTokens);
+          const int ub = unit_bytes(p.codec[side]);
+          int64_t unit = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) *
+                             (p.capacity / kUnitTokens) + u0;
+          if (p.table) {  // a tile lies inside one page
+            int pg = page_of(p.table, p.pages_per_seq, p.n_pages, sg.s, u0 / kPageUnits);
+            if (pg < 0) {
+              set_err(p.err, KVQ_DEVERR_PAGE);
+              pg = 0;  // read pool page 0 in its place
+            }
+            unit = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits + u0 % kPageUnits;
+          }
+          const uint8_t *src = p.cache[side] + unit * ub;
+          for (int h = 0; h < 2; ++h, ++t) {
+            const int slot = t % p.slots;
+            if (t >= p.slots &&
+                !mbar_wait_bounded(&bars.raw_empty[slot],
+                                   static_cast<uint32_t>(t / p.slots - 1) & 1u, &abort_flag)) {
+              ok = false;
+              break;
+            }
+            const int nu = max(0, min(kSlotUnits, units - u0 - h * kSlotUnits));
+            const uint32_t bytes = static_cast<uint32_t>(nu * ub);
+            mbar_arrive_expect_tx(&bars.raw_full[slot], bytes);
+            if (bytes)
+              bulk_copy_g2s(ring + slot * p.slot_bytes, src + h * kSlotUnits * ub, bytes,
+                            &bars.raw_full[slot]);
+          }
+        }
+      }
+      // after an abort, wait (bounded) for the copies still landing in the ring
+      if (!ok || *reinterpret_cast<volatile int *>(&abort_flag))
+        for (int u = max(0, t - p.slots); u < t; ++u)
+          mbar_wait_bounded(&bars.raw_full[u % p.slots], static_cast<uint32_t>(u / p.slots) & 1u,
+                            nullptr, 100000000ull);
+    }
+  } else if (warp >= kDequantWarp && warp < kDequantWarp + kDequantWarps) {
+    // ---------------- codes into operand tiles
+    const int dw = warp - kDequantWarp;
+    int t = 0, use = 0;  // slots and tiles so far
+    bool ok = true;
+    while (ok && it.next(p, sg)) {
+      const int n = sg.j_hi - sg.j_lo;
+      for (int i = 0; i < 2 * n && ok; ++i, ++use) {
+        int side, j;
+        use_at(i, n, side, j);
+        const int buf = use % kBufs;
+        if (use >= kBufs)
+          ok = mbar_wait_bounded(&bars.tile_empty[buf], static_cast<uint32_t>(use / kBufs - 1) & 1u,
+                                 &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        for (int h = 0; h < 2 && ok; ++h, ++t) {
+          const int slot = t % p.slots;
+          ok = mbar_wait_bounded(&bars.raw_full[slot], static_cast<uint32_t>(t / p.slots) & 1u,
+                                 &abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int unit = h * kSlotUnits + dw;  // of the tile
+          const int live = sg.len - (sg.j_lo + j) * kTile - unit * kUnitTokens;
+          unit_to_tile(side, p.codec[side],
+                       ring + slot * p.slot_bytes + dw * unit_bytes(p.codec[side]),
+                       tiles + buf * kTileBytes, unit, live, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.raw_empty[slot]);
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.tile_full[buf]);
+      }
+    }
+    if (!ok && lane == 0) {
+      set_err(p.err, KVQ_DEVERR_TIMEOUT);
+      atomicExch(&abort_flag, 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- MMA issuer (one thread)
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16(0);
+      // 16 columns kk of a 128-row tile
+      auto desc = [](uint32_t base, int kk) {
+        return smem_desc(base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
+      };
+      auto wait = [&](uint64_t *bar, int phase) {
+        return mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u, &abort_flag);
+      };
+      // S_e = Q K^T of the operand tile of use u
+      auto qk = [&](int e, int qtile, int u) {
+        const uint32_t a = smem_u32(sq + qtile * kTileBytes);
+        const uint32_t b = smem_u32(tiles + (u % kBufs) * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ss(tm_s[e], desc(a, kk), desc(b, kk), idesc, kk > 0);
+        mma_commit(&bars.sfull[e]);
+      };
+      // O_e (+)= P_e V
+      auto pv = [&](int e, int u, bool first) {
+        const uint32_t b = smem_u32(tiles + (u % kBufs) * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tm_o[e], tm_s[e] + kk * 8, desc(b, kk), idesc, (!first || kk > 0) ? 1u : 0u);
+        mma_commit(&bars.odone[e]);
+      };
+      auto free_tile = [&](int u) { mma_commit(&bars.tile_empty[u % kBufs]); };
+      auto have_tile = [&](int u) { return wait(&bars.tile_full[u % kBufs], u / kBufs); };
+      int u0 = 0;         // operand tiles used by earlier segments
+      int u[2] = {0, 0};  // products P V of each pipe
+      int k[2] = {0, 0};  // segments of each pipe
+      int nq[2] = {0, 0};  // query tiles taken
+      bool ok = true;
+      while (ok && it.next(p, sg)) {
+        const int n = sg.j_hi - sg.j_lo;
+        ok = wait(&bars.qready[0], nq[0]) && (!sg.pair || wait(&bars.qready[1], nq[1])) &&
+             have_tile(u0 + k_use(0));
+        if (!ok) break;
+        ++nq[0];
+        if (sg.pair) ++nq[1];
+        tc_fence_after();
+        qk(0, 0, u0 + k_use(0));
+        if (sg.pair) {
+          qk(1, 1, u0 + k_use(0));
+          free_tile(u0 + k_use(0));
+          for (int j = 0; j < n; ++j) {
+            const int uv = u0 + v_use(j, n), uk = u0 + k_use(j + 1);
+            const bool more = j + 1 < n;
+            ok = wait(&bars.pfull[0], u[0]) && have_tile(uv) &&
+                 (j > 0 || k[0] == 0 || wait(&bars.ofree[0], k[0] - 1));
+            if (!ok) break;
+            tc_fence_after();
+            pv(0, uv, j == 0);
+            ++u[0];
+            if (more) {
+              ok = have_tile(uk);
+              if (!ok) break;
+              tc_fence_after();
+              qk(0, 0, uk);
+            }
+            ok = wait(&bars.pfull[1], u[1]) &&
+                 (j > 0 || k[1] == 0 || wait(&bars.ofree[1], k[1] - 1));
+            if (!ok) break;
+            tc_fence_after();
+            pv(1, uv, j == 0);
+            ++u[1];
+            free_tile(uv);
+            if (more) {
+              qk(1, 1, uk);
+              free_tile(uk);
+            }
+          }
+        } else {  // the pipes take the tile's steps in turn
+          free_tile(u0 + k_use(0));
+          if (n > 1) {
+            ok = have_tile(u0 + k_use(1));
+            if (!ok) break;
+            tc_fence_after();
+            qk(1, 0, u0 + k_use(1));
+            free_tile(u0 + k_use(1));
+          }
+          for (int j = 0; j < n; ++j) {
+            const int e = j & 1, uv = u0 + v_use(j, n);
+            ok = wait(&bars.pfull[e], u[e]) && have_tile(uv) &&
+                 (j > 1 || k[e] == 0 || wait(&bars.ofree[e], k[e] - 1));
+            if (!ok) break;
+            tc_fence_after();
+            pv(e, uv, j < 2);
+            ++u[e];
+            free_tile(uv);
+            if (j + 2 < n) {
+              const int uk = u0 + k_use(j + 2);
+              ok = have_tile(uk);
+              if (!ok) break;
+              tc_fence_after();
+              qk(e, 0, uk);
+              free_tile(uk);
+            }
+          }
+        }
+        if (!ok) break;
+        u0 += 2 * n;
+        // a pipe's O is complete once every MMA issued so far is
+        mma_commit(&bars.segdone[0]);
+        ++k[0];
+        if (sg.pair || n > 1) {
+          mma_commit(&bars.segdone[1]);
+          ++k[1];
+        }
+      }
+      if (!ok) {
+        set_err(p.err, KVQ_DEVERR_TIMEOUT);
+        atomicExch(&abort_flag, 1);
+      }
+      // drain: every MMA this thread issued has finished (TMEM is freed after it)
+      mma_commit(&bars.drain);
+      mbar_wait_bounded(&bars.drain, 0, nullptr, 100000000ull);
+    }
+  } else if (warp < kDequantWarp) {
+    // ---------------- softmax pipe e: thread = query row
+    const int e = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tms = tm_s[e] + lane_off, tmo = tm_o[e] + lane_off;
+    const bool rot_k = p.codec[0] == KVQ_TURBO4, rot_v = p.codec[1] == KVQ_TURBO4;
+    float *exchange = reinterpret_cast<float *>(sq + kTileBytes);  // [64][128]: Q tile 1's place
+    auto mine = [&](const Segment &g) { return e == 0 || g.pair || g.j_hi - g.j_lo > 1; };
+    auto next_mine = [&](Segment &g) {
+      while (it.next(p, g))
+        if (mine(g)) return true;
+      return false;
+    };
+    // This pipe's query tile of a segment, as fp16 in K's order of dims, a warp
+    // 32 rows of it; then tell the MMA thread.  (Pipe 1 of a single tile: pipe 0's.)
+    auto load_q = [&](const Segment &g) {
+      if (e == 1 && !g.pair) return;
+      uint8_t *dst = sq + e * kTileBytes;
+      const int64_t R0 = g.row0 + e * kTile + quad * 32;
+      int64_t tok = R0 / p.G;
+      int head = static_cast<int>(R0 - tok * p.G);
+      const uint8_t *base = p.q + g.first * p.q_row + static_cast<int64_t>(g.kvh) * p.G * p.q_head +
+                            lane * 8;
+      constexpr int kAhead = 8;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32; i0 += kAhead) {
+        uint2 x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          x[i] = make_uint2(0u, 0u);
+          if (R0 + i0 + i < g.R)
+            x[i] = *reinterpret_cast<const uint2 *>(base + tok * p.q_row + head * p.q_head);
+          if (++head == p.G) {
+            head = 0;
+            ++tok;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (p.q_bf16 || rot_k) {
+            float f[4];
+            if (p.q_bf16) load4<KVQ_T_BF16>(&x[i], f);
+            else load4<KVQ_T_F16>(&x[i], f);
+            if (rot_k) {  // H (s q) / 16
+              turbo_flip_lane(f, lane);
+              fwht128_warp(f, lane);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) f[c] *= 0.0625f;
+            }
+            x[i] = make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
+          }
+          // dims 4 lane ..: block b, half h, w of K's order
+          *reinterpret_cast<uint2 *>(
+              dst + tile_offset(quad * 32 + i0 + i, 32 * (lane >> 3) + 8 * (lane & 3) +
+                                                        4 * ((lane >> 2) & 1))) = x[i];
+        }
+      }
+      fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.qready[e]);
+    };
+    int u = 0, kseg = 0;  // tiles and segments of this pipe
+    bool ok = true;
+    bool have = next_mine(sg);
+    if (have) load_q(sg);
+    while (have) {
+      const int n = sg.j_hi - sg.j_lo;
+      const int64_t row0 = sg.row0 + (sg.pair ? e * kTile : 0);
+      const bool idle = row0 + quad * 32 >= sg.R;  // no row in this warp
+      float m = -INFINITY, l = 0.0f;
+      // After an abort (ok false) the segments still run to the end without waits,
+      // so that both pipes meet at the same barriers.
+      for (int j = sg.pair ? 0 : e; j < n && ok; j += sg.pair ? 1 : 2, ++u) {
+        ok = mbar_wait_bounded(&bars.sfull[e], static_cast<uint32_t>(u) & 1u, &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) atomicExch(&abort_flag, 1);
+          break;
+        }
+        tc_fence_after();
+        if (!idle) {
+          const int left = sg.len - (sg.j_lo + j) * kTile;  // keys from the tile's first on
+          // Pass 1: the row's maximum.  In the last tile the scores of places past
+          // the length are overwritten with -inf, so that pass 2 needs no mask.
+          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(tms + c * 32, v);
+            tmem_wait_ld();
+            if (left < kTile) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + (i & 16) + token_of(i) >= left) v[i] = -INFINITY;
+              tmem_st32f(tms + c * 32, v);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[i], v[i + 1]);
+          }
+          if (left < kTile) tmem_wait_st();
+          const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
+          // A row's running maximum is raised only when it grew by more than the
+          // threshold; O is rescaled for the whole warp when one of its rows is.
+          const bool raise = mx > m + kRaise || m == -INFINITY;
+          const float mnew = raise ? fmaxf(mx, m) : m;
+          const float a = (raise && m != -INFINITY) ? fast_exp2(m - mnew) : 1.0f;
+          if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
+            bool got = mbar_wait_bounded(&bars.odone[e], static_cast<uint32_t>(u - 1) & 1u, &abort_flag);
+            got = __all_sync(0xffffffffu, got);
+            if (!got) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              tmem_ld32(tmo + c * 32, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] *= a;
+              tmem_st32f(tmo + c * 32, v);
+            }
+            tmem_wait_st();
+          }
+          l *= a;
+          m = mnew;
+          // Pass 2: P = exp2(s * scale_log2 - m + lift) as fp16 pairs over the first
+          // 64 columns (a chunk lands on columns already read), and the row's sum.
+          const float nm = m == -INFINITY ? 0.0f : kLift - m;
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            uint32_t pk[16];
+            tmem_ld32(tms + c * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 tt = fma2(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
+              const float2 x = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
+              sum[i & 1] = add2(sum[i & 1], x);
+              pk[i] = pack_half2(x.x, x.y);
+            }
+            tmem_st16(tms + c * 16, pk);
+          }
+          const float2 s2 = add2(sum[0], sum[1]);
+          l += s2.x + s2.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.pfull[e]);
+      }
+      // The next segment's query tile: in a pair this pipe's last S has been read,
+      // so its tile is free now; a single tile's is once every product is done.
+      Segment nsg;
+      const bool have_next = next_mine(nsg);
+      if (sg.pair && have_next) load_q(nsg);
+      if (ok) ok = mbar_wait_bounded(&bars.segdone[e], static_cast<uint32_t>(kseg) & 1u, &abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      ++kseg;
+      tc_fence_after();
+      if (!sg.pair && e == 0 && have_next) load_q(nsg);
+      const bool joined = !sg.pair && n > 1;  // the other pipe has the odd key tiles
+      float w0 = 1.0f, w1 = 0.0f;
+      if (joined && e == 1) {
+        pipe1_ml[r] = make_float2(m, l);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (half) pipes_sync();  // the first half has been read
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            tmem_ld32(tmo + half * 64 + c * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) exchange[(c * 32 + i) * kTile + r] = v[i];
+          }
+          pipes_sync();  // written
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.ofree[1]);
+        pipes_sync();  // the second half has been read
+        if (have_next) load_q(nsg);
+        sg = nsg;
+        have = have_next;
+        continue;
+      }
+      // The row's place: out (whole items), xo, or this CTA's partial slot.
+      const bool whole = sg.j_lo == 0 && sg.j_hi == sg.nt;
+      const int64_t R = row0 + r, tok = R / p.G;
+      const bool valid = R < sg.R;
+      const int head = sg.kvh * p.G + static_cast<int>(R - tok * p.G);
+      const int64_t row = valid ? sg.first + tok : 0, at = row * p.n_q + head;
+      RowOut ro;
+      ro.half = nullptr;
+      ro.full = nullptr;
+      ro.bf16 = p.q_bf16;
+      if (!whole)
+        ro.full = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (sg.inside ? 1 : 0)) * kSlotFloats +
+                  static_cast<int64_t>((sg.pair ? e : 0) * kTile + r) * kPartStride;
+      else if (p.out.xo)
+        ro.full = p.out.xo + at * kD;
+      else
+        ro.half = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head;
+      if (joined) {
+        pipes_sync();  // pipe 1's first half and (m, l) are written
+        const float2 y = pipe1_ml[r];
+        const float top = fmaxf(m, y.x);
+        w0 = m == -INFINITY ? 0.0f : fast_exp2(m - top);
+        w1 = y.x == -INFINITY ? 0.0f : fast_exp2(y.x - top);
+        l = fmaf(w1, y.y, w0 * l);
+        m = top;
+      }
+      ro.inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        if (joined && c == 2) {
+          pipes_sync();  // the first half has been read
+          pipes_sync();  // the second is written
+        }
+        float v[32];
+        tmem_ld32(tmo + c * 32, v);
+        tmem_wait_ld();
+        if (joined) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = fmaf(w1, exchange[((c & 1) * 32 + i) * kTile + r], w0 * v[i]);
+        }
+        if (rot_v) {  // the stages inside 32 columns
+          fwht32(v);
+          tmem_st32f(tmo + c * 32, v);
+        } else if (valid) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ro.put(c * 32 + 8 * i, reinterpret_cast<const float(&)[8]>(v[8 * i]));
+        }
+      }
+      if (joined) pipes_sync();  // the second half has been read
+      if (rot_v) {  // the stages across them, and x = s H y / 16
+        tmem_wait_st();
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          float v[4][8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld8(tmo + c * 32 + 8 * g, v[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = v[0][i] + v[1][i], b = v[0][i] - v[1][i];
+            const float c = v[2][i] + v[3][i], d = v[2][i] - v[3][i];
+            v[0][i] = a + c;
+            v[1][i] = b + d;
+            v[2][i] = a - c;
+            v[3][i] = b - d;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t signs = turbo_signs(c) >> (8 * g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] *= (signs >> i) & 1u ? -0.0625f : 0.0625f;
+            if (valid) ro.put(c * 32 + 8 * g, v[c]);
+          }
+        }
+      }
+      tc_fence_before();  // O read: the next segment's first product may overwrite it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.ofree[e]);
+      // weights were lifted: sums of 2^(s - (m - lift))
+      const float ml = m == -INFINITY ? m : m - kLift;
+      if (!whole) {
+        *reinterpret_cast<float2 *>(ro.full + kD) = make_float2(ml, l);
+      } else if (valid) {
+        if (p.out.xo) p.out.xml[at] = make_float2(ml, l);
+        else if (p.out.lse)
+          p.out.lse[at] = l > 0.0f ? (ml + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+      sg = nsg;
+      have = have_next;
+    }
+    if (!ok && lane == 0) {
+      set_err(p.err, KVQ_DEVERR_TIMEOUT);
+      atomicExch(&abort_flag, 1);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ joining the pieces
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = kJoinThreads / 16;
+
+struct JoinParams {
+  CrossParams c;
+  int grid;  // the attention kernel's CTAs
+};
+
+// The items that the attention kernel split over several CTAs: o = sum_c
+// 2^(m_c - M) o_c over the pieces in order, 16 threads per row (8 dims each), the
+// pieces' rows requested eight at a time.  Rows of sequences without keys are
+// written here too; all others are left to the attention kernel.
+__global__ void __launch_bounds__(kJoinThreads)
+    cross_join_kernel(const __grid_constant__ JoinParams jp) {
+  const CrossParams &p = jp.c;
+  __shared__ int64_t pfx[kCrossMaxSeqs + 1];
+  __shared__ int64_t warp_sum[kJoinThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (lengths and rows are final once the attention kernel has started)
+  int64_t carry = 0;
+  for (int base = 0; base < p.rows.n_seqs; base += kJoinThreads) {
+    const int s = base + tid;
+    const int64_t n = s < p.rows.n_seqs ? seq_work(p, s).per_head() * p.n_kv : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+    int64_t all = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) all += warp_sum[w];
+    if (s < p.rows.n_seqs) pfx[s + 1] = carry + incl;
+    carry += all;
+    __syncthreads();
+  }
+  grid_dependency_wait();  // the partials are complete
+  grid_launch_dependents();
+  const int64_t W = carry, P = cross_ctas(W, jp.grid);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kJoinRows + (tid >> 4);
+  const int t16 = tid & 15;
+  if (id >= p.rows.n_rows * p.n_q) return;
+  const int64_t row = id / p.n_q;
+  const int head = static_cast<int>(id - row * p.n_q), kvh = head / p.G;
   int s;
   int64_t i;
   if (!packed_find(p.rows, row, s, i)) return;
-  int len = p.seq_lens[s];
-  if (len > p.max_len) {
-    set_err(p.err, KVQ_DEVERR_MAXLEN);
-    len = p.max_len;
-  }
-  float q[4];
-  const uint8_t *qr = p.q + row * p.q_row + head * p.q_head + 8 * lane;
-  if (p.q_type == KVQ_T_BF16) load4<KVQ_T_BF16>(qr, q);
-  else load4<KVQ_T_F16>(qr, q);
-  float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int t = 0; t < len; ++t) {
-    const int j = t / kUnitTokens, r = t % kUnitTokens;
-    int64_t unit = (static_cast<int64_t>(s) * p.n_kv + kvh) * (p.capacity / kUnitTokens) + j;
-    if (p.table) {
-      int pg = page_of(p.table, p.pages_per_seq, p.n_pages, s, j / kPageUnits);
-      if (pg < 0) {
-        set_err(p.err, KVQ_DEVERR_PAGE);
-        pg = 0;  // read pool page 0 in its place
+  const SeqWork w = seq_work(p, s);
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  float M = -INFINITY, L = 0.0f;
+  if (w.nt > 0) {
+    const int64_t R = i * p.G + (head - kvh * p.G);
+    const int blk = static_cast<int>(R / (2 * kTile)), wt = w.weight(blk);
+    const int in = static_cast<int>(R % (2 * kTile));  // tile and row of the block
+    const int64_t at = (s ? pfx[s] : 0) + kvh * w.per_head() + static_cast<int64_t>(blk) * 2 * w.nt;
+    const int64_t c0 = owner_of(at, W, P);
+    const int n = static_cast<int>(
+        owner_of(at + static_cast<int64_t>(w.nt - 1) * wt, W, P) - c0 + 1);
+    if (n == 1) return;
+    // the item begins inside its first CTA's slice, and before every other's
+    auto part = [&](int j) {
+      const int64_t c = c0 + j;
+      const int64_t slot = 2 * c + (at >= W * c / P ? 1 : 0);
+      return p.part + slot * kSlotFloats + static_cast<int64_t>(in) * kPartStride;
+    };
+    for (int j = t16; j < n; j += 16) M = fmaxf(M, __ldcg(part(j) + kD));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)  // (the other half of the warp may have returned)
+      M = fmaxf(M, __shfl_xor_sync(0xffffu << (lane & 16), M, o, 16));
+    constexpr int kAhead = 8;
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
+      float4 x[kAhead][2];
+      float2 y[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float *pr = part(min(j0 + k, n - 1));
+        y[k] = __ldcg(reinterpret_cast<const float2 *>(pr + kD));
+        x[k][0] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16));
+        x[k][1] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16) + 1);
       }
-      unit = (static_cast<int64_t>(pg) * p.n_kv + kvh) * kPageUnits + j % kPageUnits;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (j0 + k >= n || y[k].x == -INFINITY) continue;
+        const float f = fast_exp2(y[k].x - M);
+        L = fmaf(f, y[k].y, L);
+        const float z[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w,
+                            x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+#pragma unroll
+        for (int d = 0; d < 8; ++d) acc[d] = fmaf(f, z[d], acc[d]);
+      }
     }
-    float x[4];
-    decode_row_lane<0>(p.codec[0], p.cache[0] + unit * unit_bytes(p.codec[0]), r, lane, x);
-    float a = q[0] * x[0] + q[1] * x[1] + q[2] * x[2] + q[3] * x[3];
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) a += __shfl_xor_sync(0xffffffffu, a, k);
-    a *= p.scale_log2;
-    const float mn = fmaxf(m, a), f = m == -INFINITY ? 0.0f : exp2f(m - mn);
-    const float e = mn == -INFINITY ? 0.0f : exp2f(a - mn);
-    decode_row_lane<1>(p.codec[1], p.cache[1] + unit * unit_bytes(p.codec[1]), r, lane, x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = fmaf(o[k], f, e * x[k]);
-    l = fmaf(l, f, e);
-    m = mn;
   }
   const int64_t at = row * p.n_q + head;
-  if (p.out.xo) {  // unnormalised, for a merge
-    *reinterpret_cast<float4 *>(p.out.xo + at * kD + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
-    if (lane == 0) p.out.xml[at] = make_float2(m, l);
-    return;
+  RowOut ro;
+  ro.inv = L > 0.0f ? 1.0f / L : 0.0f;
+  ro.bf16 = p.q_bf16;
+  ro.full = p.out.xo ? p.out.xo + at * kD : nullptr;
+  ro.half = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head;
+  ro.put(8 * t16, acc);
+  if (t16 == 0) {
+    if (p.out.xo) p.out.xml[at] = make_float2(M, L);
+    else if (p.out.lse)
+      p.out.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] *= inv;
-  uint8_t *y = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head + 8 * lane;
-  if (p.out_type == KVQ_T_BF16) store4<KVQ_T_BF16>(y, o);
-  else store4<KVQ_T_F16>(y, o);
-  if (p.out.lse && lane == 0)
-    p.out.lse[at] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
 
 CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms) {
   CrossPlan pl;
-  pl.ws_bytes = 16;
+  pl.grid = num_sms > 0 ? num_sms : 148;
+  pl.ws_bytes = 2 * static_cast<int64_t>(pl.grid) * kSlotFloats * 4;
   return pl;
 }
 
 cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows &q,
                          int64_t n_rows, const int32_t *n_new, const int32_t *row_start,
                          float scale, const CrossOut &out, int64_t out_row, int64_t out_head,
-                         int out_type, int max_len, void *workspace, cudaStream_t stream) {
+                         int max_len, void *workspace, cudaStream_t stream) {
   CrossParams p;
   p.cache[0] = static_cast<const uint8_t *>(L.k_cache);
   p.cache[1] = static_cast<const uint8_t *>(L.v_cache);
@@ -117,11 +1149,11 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.q = static_cast<const uint8_t *>(q.data);
   p.q_row = q.row_stride * type_bytes(q.type);
   p.q_head = q.head_stride * type_bytes(q.type);
-  p.q_type = q.type;
+  p.q_bf16 = q.type == KVQ_T_BF16;
   p.out = out;
   p.out_row = out_row * 2;
   p.out_head = out_head * 2;
-  p.out_type = out_type;
+  p.part = static_cast<float *>(workspace);
   p.rows = {row_start, n_new, n_rows, n_rows / L.n_seqs, L.n_seqs};
   p.seq_lens = L.seq_lens;
   p.table = L.pages_per_seq > 0 ? L.block_table : nullptr;
@@ -133,11 +1165,20 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.max_len = max_len;
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
+  p.slot_bytes = kSlotUnits * std::max(unit_bytes(L.codec_k), unit_bytes(L.codec_v));
+  p.slots = std::min(kMaxSlots, kRingBytes / p.slot_bytes);
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int64_t blocks = (n_rows * L.n_q_heads + kCrossWarps - 1) / kCrossWarps;
+  static std::atomic<uint64_t> optin{0};
+  cudaError_t e = smem_optin(cross_attn_kernel, kSmemBytes, optin);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(cross_attn_kernel, dim3(static_cast<unsigned>(pl.grid)), dim3(kThreads), kSmemBytes,
+                 stream, p);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (n_rows * L.n_q_heads + kJoinRows - 1) / kJoinRows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_pdl(cross_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kCrossWarps * 32), 0,
-                    stream, p);
+  const JoinParams jp = {p, pl.grid};
+  return launch_pdl(cross_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), 0,
+                    stream, jp);
 }
 
 }  // namespace kvq

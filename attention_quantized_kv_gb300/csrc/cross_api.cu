@@ -128,8 +128,8 @@ int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows, const 
   if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
   const kvq::CrossOut to = {out->data, lse, nullptr, nullptr};
   const cudaError_t e = kvq::launch_cross(*layer, pl, *q, n_rows, n_new, row_start, scale, to,
-                                          out->row_stride, out->head_stride, out->type, max_len,
-                                          workspace, static_cast<cudaStream_t>(stream));
+                                          out->row_stride, out->head_stride, max_len, workspace,
+                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
 }
 
@@ -169,8 +169,8 @@ int attn_decode_prefix(const kvq_layer *layer, const kvq_layer *prefix,
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   // one prefix without group_start: its rows are the batch (padded form, all of it)
   cudaError_t e = kvq::launch_cross(*prefix, pl.shared, qr, layer->n_seqs, nullptr, group_start,
-                                    scale, {nullptr, nullptr, xo, xml}, 0, 0, KVQ_T_F16,
-                                    max_prefix, ws + pl.cross_off, st_);
+                                    scale, {nullptr, nullptr, xo, xml}, 0, 0, max_prefix,
+                                    ws + pl.cross_off, st_);
   if (e == cudaSuccess) {
     const kvq::PrefixPart part = {xo, xml, group_start, prefix->n_seqs};
     e = kvq::launch_decode(*layer, pl.own, q, scale, out, lse, max_len, workspace, st_, nullptr,

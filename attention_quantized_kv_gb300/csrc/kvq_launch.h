@@ -89,7 +89,8 @@ cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32
 // Query rows against every key of their sequence (cross.cu).
 constexpr int kCrossMaxSeqs = 1024;  // key sequences per call
 struct CrossPlan {
-  int64_t ws_bytes = 0;
+  int grid = 1;          // CTAs, at most one per SM
+  int64_t ws_bytes = 0;  // partial slots, two per CTA
 };
 // Where the rows go: out and lse (optional), or, for a merge, xo fp32
 // [n_rows][n_q][128] unnormalised and xml [n_rows][n_q] (max in log2 units, sum).
@@ -104,7 +105,7 @@ CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms);
 cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows &q,
                          int64_t n_rows, const int32_t *n_new, const int32_t *row_start,
                          float scale, const CrossOut &out, int64_t out_row, int64_t out_head,
-                         int out_type, int max_len, void *workspace, cudaStream_t stream);
+                         int max_len, void *workspace, cudaStream_t stream);
 
 // Cached rows as values (read_rows.cu).
 cudaError_t launch_read_rows(const kvq_layer &L, const kvq_rows *k, const kvq_rows *v,

@@ -4,15 +4,21 @@ With u = 2^-11 / sqrt 3 the root mean square of an fp16 rounding's relative erro
 (uniform in +-2^-11 where it is largest), a kernel that takes
   K^ = RN16(k)  (f16 keys: exact; turbo4: in the rotated space, the query too)
   P  = RN16(p),  V^ = RN16(v)   (decode: RN16(RN16(p) d) c, two roundings too)
-moves a score by ds_t of variance (scale u)^2 sum_i (q_i k_ti)^2 (turbo4: twice
-that), hence an output by sum_t (p_t / L) ((v_tj - o_j) ds_t + v_tj (e_t + e'_t)),
+moves a score by ds_t of variance (scale u)^2 sum_i (q_i k_ti)^2, hence an output by sum_t (p_t / L) ((v_tj - o_j) ds_t + v_tj (e_t + e'_t)),
 of variance sum_t (p_t / L)^2 ((v_tj - o_j)^2 var(ds_t) + 2 u^2 v_tj^2), and the
-log-sum-exp by sum_t (p_t / L) ds_t.  Eight of these standard deviations hold for
+log-sum-exp by sum_t (p_t / L) ds_t.  turbo4's rotated query r is rounded once for
+all keys: its errors e_i r_i add scale sum_i e_i r_i y_ti to every score, so they do
+not average over t but move the log-sum-exp by scale sum_i e_i r_i m_i, m the weighted
+mean of the y_t, and an output by scale sum_i e_i r_i c_ij, c the weighted covariance
+of y_ti and v_tj.  Eight of these standard deviations hold for
 sums of few terms (at most sqrt 3 deviations each) and of many.  Absolute parts:
 values below 2^-14 are multiples of 2^-24, 2^-25 off; weights are held as 2^6 p or
 more (decode: p), so 2^-25 sum |v| / L covers them.  fp32 sums of T terms: partial
 sums of 256, T / 256 + 64 roundings of 2^-24, of L relative to itself (and so of the
 log-sum-exp, its logarithm) and of sum p v relative to sum p |v|, both in o.
+A score is summed in fp32 too, 16 products at a time, cut at 2^-23 of the largest or of
+the sum so far: within e = 16 2^-23 scale max_t sum_i |q_i k_ti|, which moves the
+log-sum-exp by e and an output by 2 e sum p |v| / L at most.
 turbo4 values: the same in the rotated space y, x_j = sum_i +-y_i / 16.
 """
 import numpy as np
@@ -70,7 +76,7 @@ def attend(q, parts, scale):
         if ck == F16:
             d = torch.zeros_like(a[..., at:at + t])
         elif ck == T4:
-            d = 2 * (rot ** 2) @ ((((k * signs) @ h / 8) ** 2).transpose(1, 2))
+            d = (rot ** 2) @ ((((k * signs) @ h / 8) ** 2).transpose(1, 2))
         else:
             d = (qh ** 2) @ (k ** 2).transpose(1, 2)
         ds.append(d * (scale * U) ** 2)
@@ -79,6 +85,18 @@ def attend(q, parts, scale):
     w2 = w ** 2
     # (v - o)^2 ds = v^2 ds - 2 v o ds + o^2 ds
     var = (w2 * ds) @ v ** 2 - 2 * ref * ((w2 * ds) @ v) + ref ** 2 * (w2 * ds).sum(-1, keepdim=True)
+    lvar = (w2 * ds).sum(-1, keepdim=True)
+    at = 0
+    for ck, cv, k, vv in parts:
+        if ck == T4 and k.shape[1]:
+            y, part = (k * signs) @ h / 8, w[..., at:at + k.shape[1]]
+            mean = part @ y
+            lvar = lvar + (scale * U) ** 2 * ((rot * mean) ** 2).sum(-1, keepdim=True)
+            for i in range(0, rot.shape[1], 64):  # c_ij, 64 rows at a time
+                c = torch.einsum("hrt,hti,htj->hrij", part[:, i:i + 64], y, vv) - \
+                    mean[:, i:i + 64, :, None] * ref[:, i:i + 64, None, :]
+                var[:, i:i + 64] += (scale * U) ** 2 * ((rot[:, i:i + 64, :, None] * c) ** 2).sum(-2)
+        at += k.shape[1]
     at = 0
     for ck, cv, k, vv in parts:
         part = w2[..., at:at + k.shape[1]]
@@ -91,10 +109,15 @@ def attend(q, parts, scale):
     size = w @ v.abs()
     if any(p[1] == T4 for p in parts):
         size = torch.maximum(size, (w @ v.abs()).amax(-1, keepdim=True))
-    bound = 8 * var.clamp(min=0).sqrt() + 2.0 ** -24 + 2.0 ** -25 * (v.abs().sum(1, keepdim=True) + 8) / L + \
+    e = torch.zeros_like(L)
+    for ck, cv, k, vv in parts:
+        if k.shape[1]:
+            x, y = (rot, (k * signs) @ h / 8) if ck == T4 else (qh, k)
+            e = torch.maximum(e, 16 * 2.0 ** -23 * scale * (x.abs() @ y.abs().transpose(1, 2)).amax(-1, keepdim=True))
+    bound = 2 * e * size + 8 * var.clamp(min=0).sqrt() + 2.0 ** -24 + 2.0 ** -25 * (v.abs().sum(1, keepdim=True) + 8) / L + \
         2 * (T / 256 + 64) * 2.0 ** -24 * size
     back = lambda x: x.reshape(n_kv, n, -1, x.shape[-1]).transpose(0, 1).reshape(n, n_q, -1)
-    err = 8 * (w2 * ds).sum(-1, keepdim=True).sqrt() + 2.0 ** -20 + (T / 256 + 64) * 2.0 ** -24
+    err = e + 8 * lvar.sqrt() + 2.0 ** -20 + (T / 256 + 64) * 2.0 ** -24
     total = top + torch.log(L)
     return back(ref), back(bound), back(total)[..., 0], back(err + 2.0 ** -22 * total.abs())[..., 0]
 
