@@ -74,6 +74,8 @@ struct CrossParams {
   const int32_t *seq_lens, *table;
   int32_t *err;
   int n_q, n_kv, G, capacity, max_len, pages_per_seq, n_pages, slots, slot_bytes;
+  int key_tile;  // keys of a step: 128, or 64 where a side is split
+  int singles;   // no pairs: the second query tile's place holds the rest of a turbo4 query
   float scale_log2;
 };
 
@@ -83,11 +85,17 @@ struct CrossParams {
 struct SeqWork {
   int64_t first, R;  // first row (token); rows per kv head: tokens * G
   int len, nt;       // keys, key tiles (0: nothing to do)
-  int blocks;        // pairs, and the single tile if there is one
-  bool odd;          // the last block is a single tile
-  __device__ __forceinline__ int weight(int blk) const { return odd && blk == blocks - 1 ? 1 : 2; }
+  int blocks, full;  // pairs and the single tile if there is one (singles: tiles); weight
+  bool odd;          // the last block is a single tile among pairs
+  __device__ __forceinline__ int weight(int blk) const {
+    return odd && blk == blocks - 1 ? 1 : full;
+  }
   __device__ __forceinline__ int64_t per_head() const {
-    return static_cast<int64_t>(nt) * (2 * static_cast<int64_t>(blocks) - (odd ? 1 : 0));
+    return static_cast<int64_t>(nt) * (full * static_cast<int64_t>(blocks) - (odd ? 1 : 0));
+  }
+  // position of block blk of kv head kvh, from the sequence's
+  __device__ __forceinline__ int64_t at(int kvh, int blk) const {
+    return kvh * per_head() + static_cast<int64_t>(blk) * full * nt;
   }
 };
 __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
@@ -96,11 +104,19 @@ __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
   const int64_t n = packed_rows(p.rows, s, w.first, bad);
   w.len = max(0, min(p.seq_lens[s], p.max_len));
   w.R = n * p.G;
-  w.nt = n > 0 ? (w.len + kTile - 1) / kTile : 0;
+  w.nt = n > 0 ? (w.len + p.key_tile - 1) / p.key_tile : 0;
   const int64_t tiles = (w.R + kTile - 1) / kTile;
-  w.blocks = static_cast<int>((tiles + 1) / 2);
-  w.odd = (tiles & 1) != 0;
+  w.full = p.singles ? 1 : 2;
+  w.blocks = static_cast<int>(p.singles ? tiles : (tiles + 1) / 2);
+  w.odd = !p.singles && (tiles & 1) != 0;
   return w;
+}
+// The kv head and block at offset `off` of a sequence's work.
+__device__ __forceinline__ void block_at(const SeqWork &w, int64_t off, int &kvh, int &blk) {
+  const int64_t head = w.per_head();
+  kvh = static_cast<int>(off / head);
+  blk = static_cast<int>(min((off % head) / (static_cast<int64_t>(w.full) * w.nt),
+                             static_cast<int64_t>(w.blocks - 1)));
 }
 // CTAs that get a slice: each at least as long as a step, so that every CTA
 // between an item's first and last has a step of it.
@@ -128,10 +144,8 @@ struct SegIter {
     s1 = b;
     s = seq;
     w = seq_work(p, s);
-    const int64_t head = w.per_head(), off = a - seq_at;
-    kvh = static_cast<int>(off / head);
-    blk = static_cast<int>(min((off % head) / (2 * w.nt), static_cast<int64_t>(w.blocks - 1)));
-    at = seq_at + kvh * head + static_cast<int64_t>(blk) * 2 * w.nt;
+    block_at(w, a - seq_at, kvh, blk);
+    at = seq_at + w.at(kvh, blk);
   }
   __device__ __forceinline__ bool next(const CrossParams &p, Segment &g) {
     while (at < s1) {
@@ -140,7 +154,7 @@ struct SegIter {
       const int64_t hi = min(static_cast<int64_t>(w.nt), (s1 - at + wt - 1) / wt);
       g.first = w.first;
       g.R = w.R;
-      g.row0 = static_cast<int64_t>(blk) * (2 * kTile);
+      g.row0 = static_cast<int64_t>(blk) * (w.full * kTile);
       g.s = s;
       g.kvh = kvh;
       g.len = w.len;
@@ -183,6 +197,15 @@ __device__ __forceinline__ void sts128(uint8_t *p, uint32_t a, uint32_t b, uint3
 __device__ __forceinline__ void sts64(uint8_t *p, uint32_t a, uint32_t b) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
 }
+// c d as hi = RN16(c d) and the rest, which is exact.
+struct Parts {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Parts scaled(uint32_t c, uint32_t d) {
+  const __half2 x = *reinterpret_cast<__half2 *>(&c), y = *reinterpret_cast<__half2 *>(&d);
+  const __half2 h = __hmul2(x, y), l = __hfma2(x, y, __hneg2(h));
+  return {*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l)};
+}
 __device__ __forceinline__ uint32_t twice(uint32_t half) { return half * 0x10001u; }
 // Four signed bytes as fp16 pairs (0, 1) and (2, 3), exact: the byte plus 128 in
 // the mantissa of 1024, less 1152.
@@ -196,6 +219,12 @@ __device__ __forceinline__ void u4_quad(uint32_t w, uint32_t &lo, uint32_t &hi) 
   lo = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4140), 0x64086408u);
   hi = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4342), 0x64086408u);
 }
+
+// Quantized sides are split: x^ = d c has up to 18 bits, an operand 11, so a tile
+// holds 64 keys twice, RN16(x^) and the rest.  (Rounded once, 128 keys to a tile,
+// outputs over q8_0 sides were 4.1e-4 off, relative to their own rounding of
+// 2.1e-4 and that of the weights, 1.7e-4; split they are 2.7e-4 off, as over f16.)
+constexpr int kLoRows = 64;  // K: the rests' first row; V: their columns' half
 
 // One unit of K into rows 16 u .. of the tile (all 32 lanes).  A lane takes the
 // 16-byte pieces (g, w) of row g and row g + 8; the order of g over the lanes
@@ -239,6 +268,13 @@ __device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int r
         d[rh][b] = twice((b & 1) ? z >> 16 : z & 0xffffu);
       }
   }
+  auto put = [&](int rh, int b, const uint32_t (&c)[4]) {
+    const Parts a0 = scaled(c[0], d[rh][b]), a1 = scaled(c[1], d[rh][b]);
+    const Parts a2 = scaled(c[2], d[rh][b]), a3 = scaled(c[3], d[rh][b]);
+    uint8_t *to = at(rh, b);
+    sts128(to, a0.hi, a1.hi, a2.hi, a3.hi);
+    sts128(to + kLoRows * 128, a0.lo, a1.lo, a2.lo, a3.lo);
+  };
   if (CODEC == KVQ_Q8_0) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -249,8 +285,7 @@ __device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int r
         uint32_t o[4];
         s8_quad(y[2 * rh], o[0], o[1]);
         s8_quad(y[2 * rh + 1], o[2], o[3]);
-        sts128(at(rh, b), hmul2_bits(o[0], d[rh][b]), hmul2_bits(o[1], d[rh][b]),
-               hmul2_bits(o[2], d[rh][b]), hmul2_bits(o[3], d[rh][b]));
+        put(rh, b, o);
       }
     }
   } else {
@@ -264,8 +299,7 @@ __device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int r
         uint32_t o[4];
         u4_quad(y[i] & 0x0f0f0f0fu, o[0], o[1]);
         u4_quad((y[i] >> 4) & 0x0f0f0f0fu, o[2], o[3]);
-        sts128(at(rh, b), hmul2_bits(o[0], d[rh][b]), hmul2_bits(o[1], d[rh][b]),
-               hmul2_bits(o[2], d[rh][b]), hmul2_bits(o[3], d[rh][b]));
+        put(rh, b, o);
       }
     }
   }
@@ -281,7 +315,7 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
                                           int lane) {
   const int q8 = lane >> 2, tig = lane & 3;
   const int gq = nibble_codec(CODEC) ? (0x65217430 >> (4 * q8)) & 7 : q8;
-  uint8_t *col = tile + (unit >> 2) * kHalfBytes + (tig & 1) * 8;
+  uint8_t *col = tile + (unit >> 2) * kHalfBytes + (tig & 1) * 8;  // (split: units 0..3)
   const int piece = 2 * (unit & 3) + (tig >> 1);
   uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // tokens 2 tig, + 1; + 8, + 9
   if (TAIL) {
@@ -297,6 +331,13 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
       b &= m1;
     }
     sts64(col + dim * 128 + ((piece ^ (dim & 7)) << 4), a, b);
+  };
+  auto put_split = [&](int dim, uint32_t a, uint32_t b, uint2 d) {
+    const Parts x = scaled(a, d.x), y = scaled(b, d.y);
+    put(dim, x.hi, y.hi);
+    col += kHalfBytes;
+    put(dim, x.lo, y.lo);
+    col -= kHalfBytes;
   };
   const uint8_t *src = u + (4 * gq + tig) * 16;
   if (CODEC == KVQ_F16) {
@@ -315,9 +356,8 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int dim = 32 * b + 16 * m + 2 * gq;
-        put(dim, hmul2_bits(s8_pair_02(y[2 * m]), d.x), hmul2_bits(s8_pair_02(y[2 * m + 1]), d.y));
-        put(dim + 1, hmul2_bits(s8_pair_13(y[2 * m]), d.x),
-            hmul2_bits(s8_pair_13(y[2 * m + 1]), d.y));
+        put_split(dim, s8_pair_02(y[2 * m]), s8_pair_02(y[2 * m + 1]), d);
+        put_split(dim + 1, s8_pair_13(y[2 * m]), s8_pair_13(y[2 * m + 1]), d);
       }
     }
   } else {
@@ -332,9 +372,8 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
         const int b = 2 * h + (i >> 1), dim = 32 * b + 8 * (i & 1) + gq;
         if (CODEC == KVQ_Q4_0 && (i & 1) == 0) d = lds64(u + 1024 + tig * 32 + b * 8);
         const uint32_t z = y[i] >> 8;
-        put(dim, hmul2_bits(u4_pair_minus8(y[i]), d.x), hmul2_bits(u4_pair_minus8(z), d.y));
-        put(dim + 16, hmul2_bits(u4_pair_minus8_hi(y[i]), d.x),
-            hmul2_bits(u4_pair_minus8_hi(z), d.y));
+        put_split(dim, u4_pair_minus8(y[i]), u4_pair_minus8(z), d);
+        put_split(dim + 16, u4_pair_minus8_hi(y[i]), u4_pair_minus8_hi(z), d);
       }
     }
   }
@@ -425,8 +464,12 @@ __device__ __forceinline__ void pipes_sync() {
   asm volatile("bar.sync 1, 256;\n" ::: "memory");
 }
 
+// SPLIT: a side is quantized, a step is 64 keys; else 128 keys of f16.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_attn_kernel(const __grid_constant__ CrossParams p) {
+  constexpr int KT = SPLIT ? 64 : 128;
+  constexpr int kSlotsPerTile = KT / (kSlotUnits * kUnitTokens);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ CrossBars bars;
   __shared__ uint32_t tmem_base_sh;
@@ -503,6 +546,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_mbar_init();
     }
   }
+  if (warp > kMmaWarp) {  // rows of sequences without keys
+    for (int s = blockIdx.x; s < p.rows.n_seqs; s += gridDim.x) {
+      const SeqWork w = seq_work(p, s);
+      if (w.len > 0) continue;
+      const int64_t n = w.R * p.n_kv;  // rows x query heads
+      for (int64_t i = warp - kMmaWarp - 1; i < n; i += kThreads / 32 - kMmaWarp - 1) {
+        const int64_t row = w.first + i / p.n_q;
+        const int head = static_cast<int>(i % p.n_q);
+        const int64_t at = row * p.n_q + head;
+        if (p.out.xo) {
+          if (lane == 0) p.out.xml[at] = make_float2(-INFINITY, 0.0f);
+        } else {
+          reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out.out) + row * p.out_row +
+                                    head * p.out_head)[lane] = make_uint2(0u, 0u);
+          if (p.out.lse && lane == 0) p.out.lse[at] = -INFINITY;
+        }
+      }
+    }
+  }
   __syncthreads();
   const int64_t s0 = slice[0], s1 = slice[1];
   if (s0 >= s1) return;  // whole CTA: no work
@@ -527,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2 * n && ok; ++i) {
           int side, j;
           use_at(i, n, side, j);
-          const int u0 = (sg.j_lo + j) * (kTile / kUnitTokens);
+          const int u0 = (sg.j_lo + j) * (KT / kUnitTokens);
           const int ub = unit_bytes(p.codec[side]);
           int64_t unit = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) *
                              (p.capacity / kUnitTokens) + u0;
@@ -540,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unit = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits + u0 % kPageUnits;
           }
           const uint8_t *src = p.cache[side] + unit * ub;
-          for (int h = 0; h < 2; ++h, ++t) {
+          for (int h = 0; h < kSlotsPerTile; ++h, ++t) {
             const int slot = t % p.slots;
             if (t >= p.slots &&
                 !mbar_wait_bounded(&bars.raw_empty[slot],
@@ -578,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_bounded(&bars.tile_empty[buf], static_cast<uint32_t>(use / kBufs - 1) & 1u,
                                  &abort_flag);
         ok = __all_sync(0xffffffffu, ok);
-        for (int h = 0; h < 2 && ok; ++h, ++t) {
+        for (int h = 0; h < kSlotsPerTile && ok; ++h, ++t) {
           const int slot = t % p.slots;
           ok = mbar_wait_bounded(&bars.raw_full[slot], static_cast<uint32_t>(t / p.slots) & 1u,
                                  &abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int unit = h * kSlotUnits + dw;  // of the tile
-          const int live = sg.len - (sg.j_lo + j) * kTile - unit * kUnitTokens;
+          const int live = sg.len - (sg.j_lo + j) * KT - unit * kUnitTokens;
           unit_to_tile(side, p.codec[side],
                        ring + slot * p.slot_bytes + dw * unit_bytes(p.codec[side]),
                        tiles + buf * kTileBytes, unit, live, lane);
@@ -605,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issuer (one thread)
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16(0);
+      const bool split_k = SPLIT && p.codec[0] != KVQ_F16, split_v = SPLIT && p.codec[1] != KVQ_F16;
+      const uint32_t idesc_k = idesc_f16(0, SPLIT && !split_k ? 64 : 128), idesc_v = idesc_f16(0);
       // 16 columns kk of a 128-row tile
       auto desc = [](uint32_t base, int kk) {
         return smem_desc(base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
@@ -613,20 +676,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](uint64_t *bar, int phase) {
         return mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u, &abort_flag);
       };
-      // S_e = Q K^T of the operand tile of use u
+      // S_e = Q K^T of the operand tile of use u; split keys: their rests' scores
+      // in columns 64 ..; turbo4: the rest of Q too
       auto qk = [&](int e, int qtile, int u) {
         const uint32_t a = smem_u32(sq + qtile * kTileBytes);
         const uint32_t b = smem_u32(tiles + (u % kBufs) * kTileBytes);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_ss(tm_s[e], desc(a, kk), desc(b, kk), idesc, kk > 0);
+        for (int kk = 0; kk < 8; ++kk) mma_ss(tm_s[e], desc(a, kk), desc(b, kk), idesc_k, kk > 0);
+        if (SPLIT && p.singles) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(tm_s[e], desc(a + kTileBytes, kk), desc(b, kk), idesc_k, 1u);
+        }
         mma_commit(&bars.sfull[e]);
       };
-      // O_e (+)= P_e V
+      // O_e (+)= P_e V; split values: the same P for the rests, columns 64 .. of V
       auto pv = [&](int e, int u, bool first) {
         const uint32_t b = smem_u32(tiles + (u % kBufs) * kTileBytes);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tm_o[e], tm_s[e] + kk * 8, desc(b, kk), idesc, (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk) {
+          if (SPLIT && kk >= 4 && !split_v) break;
+          mma_ts(tm_o[e], tm_s[e] + (SPLIT ? kk & 3 : kk) * 8, desc(b, kk), idesc_v,
+                 (!first || kk > 0) ? 1u : 0u);
+        }
         mma_commit(&bars.odone[e]);
       };
       auto free_tile = [&](int u) { mma_commit(&bars.tile_empty[u % kBufs]); };
@@ -726,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int e = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tms = tm_s[e] + lane_off, tmo = tm_o[e] + lane_off;
-    const bool rot_k = p.codec[0] == KVQ_TURBO4, rot_v = p.codec[1] == KVQ_TURBO4;
+    const bool rot_k = SPLIT && p.codec[0] == KVQ_TURBO4, rot_v = SPLIT && p.codec[1] == KVQ_TURBO4;
+    const bool split_k = SPLIT && p.codec[0] != KVQ_F16;
     float *exchange = reinterpret_cast<float *>(sq + kTileBytes);  // [64][128]: Q tile 1's place
     auto mine = [&](const Segment &g) { return e == 0 || g.pair || g.j_hi - g.j_lo > 1; };
     auto next_mine = [&](Segment &g) {
@@ -744,6 +817,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int head = static_cast<int>(R0 - tok * p.G);
       const uint8_t *base = p.q + g.first * p.q_row + static_cast<int64_t>(g.kvh) * p.G * p.q_head +
                             lane * 8;
+      // dims 4 lane ..: block b, half h, w of K's order
+      auto place = [&](int i) {
+        return tile_offset(quad * 32 + i, 32 * (lane >> 3) + 8 * (lane & 3) + 4 * ((lane >> 2) & 1));
+      };
       constexpr int kAhead = 8;
 #pragma unroll 1
       for (int i0 = 0; i0 < 32; i0 += kAhead) {
@@ -771,11 +848,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 4; ++c) f[c] *= 0.0625f;
             }
             x[i] = make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
+            if (rot_k) {  // what the rounding leaves, in the second tile's place
+              const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].x));
+              const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].y));
+              *reinterpret_cast<uint2 *>(dst + kTileBytes + place(i0 + i)) = make_uint2(
+                  pack_half2(f[0] - a.x, f[1] - a.y), pack_half2(f[2] - b.x, f[3] - b.y));
+            }
           }
-          // dims 4 lane ..: block b, half h, w of K's order
-          *reinterpret_cast<uint2 *>(
-              dst + tile_offset(quad * 32 + i0 + i, 32 * (lane >> 3) + 8 * (lane & 3) +
-                                                        4 * ((lane >> 2) & 1))) = x[i];
+          *reinterpret_cast<uint2 *>(dst + place(i0 + i)) = x[i];
         }
       }
       fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
@@ -802,25 +882,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (!idle) {
-          const int left = sg.len - (sg.j_lo + j) * kTile;  // keys from the tile's first on
-          // Pass 1: the row's maximum.  In the last tile the scores of places past
-          // the length are overwritten with -inf, so that pass 2 needs no mask.
+          const int left = sg.len - (sg.j_lo + j) * KT;  // keys from the tile's first on
+          // Pass 1: the row's maximum; scores of places past the length become -inf.
+          // Split: the 64 scores stay in registers.  Else 128 are read again in pass 2
+          // (those of the last tile overwritten in TMEM, so that it needs no mask).
           float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float sc[SPLIT ? 2 : 1][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
+          for (int c = 0; c < KT / 32; ++c) {
+            float(&v)[32] = sc[SPLIT ? c : 0];
             tmem_ld32(tms + c * 32, v);
-            tmem_wait_ld();
-            if (left < kTile) {
+            if (split_k) {
+              float x[32];
+              tmem_ld32(tms + 64 + c * 32, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = add2(make_float2(v[i], v[i + 1]), make_float2(x[i], x[i + 1]));
+                v[i] = y.x;
+                v[i + 1] = y.y;
+              }
+            } else {
+              tmem_wait_ld();
+            }
+            if (left < KT) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (c * 32 + (i & 16) + token_of(i) >= left) v[i] = -INFINITY;
-              tmem_st32f(tms + c * 32, v);
+              if (!SPLIT) tmem_st32f(tms + c * 32, v);
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 2) mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[i], v[i + 1]);
           }
-          if (left < kTile) tmem_wait_st();
+          if (!SPLIT && left < KT) tmem_wait_st();
           const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
           // A row's running maximum is raised only when it grew by more than the
           // threshold; O is rescaled for the whole warp when one of its rows is.
@@ -849,16 +943,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= a;
           m = mnew;
           // Pass 2: P = exp2(s * scale_log2 - m + lift) as fp16 pairs over the first
-          // 64 columns (a chunk lands on columns already read), and the row's sum.
+          // columns of S (a chunk lands on columns already read), and the row's sum.
           const float nm = m == -INFINITY ? 0.0f : kLift - m;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
+          for (int c = 0; c < KT / 32; ++c) {
+            float(&v)[32] = sc[SPLIT ? c : 0];
             uint32_t pk[16];
-            tmem_ld32(tms + c * 32, v);
-            tmem_wait_ld();
+            if (!SPLIT) {
+              tmem_ld32(tms + c * 32, v);
+              tmem_wait_ld();
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 tt = fma2(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
@@ -885,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       ++kseg;
       tc_fence_after();
-      if (!sg.pair && e == 0 && have_next) load_q(nsg);
+      if (!sg.pair && e == 0 && have_next && !rot_k) load_q(nsg);
       const bool joined = !sg.pair && n > 1;  // the other pipe has the odd key tiles
       float w0 = 1.0f, w1 = 0.0f;
       if (joined && e == 1) {
@@ -992,6 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();  // O read: the next segment's first product may overwrite it
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.ofree[e]);
+      if (rot_k && have_next) load_q(nsg);  // (its second tile's place was the exchange's)
       // weights were lifted: sums of 2^(s - (m - lift))
       const float ml = m == -INFINITY ? m : m - kLift;
       if (!whole) {
@@ -1029,103 +1126,118 @@ struct JoinParams {
 };
 
 // The items that the attention kernel split over several CTAs: o = sum_c
-// 2^(m_c - M) o_c over the pieces in order, 16 threads per row (8 dims each), the
-// pieces' rows requested eight at a time.  Rows of sequences without keys are
-// written here too; all others are left to the attention kernel.
+// 2^(m_c - M) o_c over the pieces in order.  Block (c, rows): the item that the
+// slices c and c + 1 share, where c is the first slice that holds a part of it; 16
+// threads per row (8 dims each), the pieces' rows requested eight at a time.
 __global__ void __launch_bounds__(kJoinThreads)
     cross_join_kernel(const __grid_constant__ JoinParams jp) {
   const CrossParams &p = jp.c;
-  __shared__ int64_t pfx[kCrossMaxSeqs + 1];
-  __shared__ int64_t warp_sum[kJoinThreads / 32];
+  __shared__ int64_t warp_sum[kJoinThreads / 32], seq_at;
+  __shared__ int seq;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // (lengths and rows are final once the attention kernel has started)
-  int64_t carry = 0;
-  for (int base = 0; base < p.rows.n_seqs; base += kJoinThreads) {
-    const int s = base + tid;
-    const int64_t n = s < p.rows.n_seqs ? seq_work(p, s).per_head() * p.n_kv : 0;
-    int64_t incl = n;
+  auto scan = [&](bool find, int64_t x) {  // all work, or the sequence at position x
+    int64_t carry = 0;
+    for (int base = 0; base < p.rows.n_seqs; base += kJoinThreads) {
+      const int s = base + tid;
+      const int64_t n = s < p.rows.n_seqs ? seq_work(p, s).per_head() * p.n_kv : 0;
+      int64_t incl = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      incl += carry;
+      for (int w = 0; w < kJoinThreads / 32; ++w) {
+        if (w < warp) incl += warp_sum[w];
+        carry += warp_sum[w];
+      }
+      if (find && x >= incl - n && x < incl) {
+        seq = s;
+        seq_at = incl - n;
+      }
+      __syncthreads();
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-    int64_t all = 0;
-    for (int w = 0; w < kJoinThreads / 32; ++w) all += warp_sum[w];
-    if (s < p.rows.n_seqs) pfx[s + 1] = carry + incl;
-    carry += all;
-    __syncthreads();
+    return carry;
+  };
+  const int64_t W = scan(false, 0), P = cross_ctas(W, jp.grid), c = blockIdx.x;
+  if (c + 1 >= P) {
+    grid_dependency_wait();  // (this grid must not end before the attention kernel)
+    return;
   }
+  const int64_t x = W * (c + 1) / P - 1;  // the last position of slice c
+  scan(true, x);
+  const SeqWork w = seq_work(p, seq);
+  int kvh, blk;
+  block_at(w, x - seq_at, kvh, blk);
+  const int64_t at = seq_at + w.at(kvh, blk);
+  const int wt = w.weight(blk);
+  const int64_t c0 = owner_of(at, W, P);
+  const int n = static_cast<int>(owner_of(at + static_cast<int64_t>(w.nt - 1) * wt, W, P) - c0 + 1);
   grid_dependency_wait();  // the partials are complete
   grid_launch_dependents();
-  const int64_t W = carry, P = cross_ctas(W, jp.grid);
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kJoinRows + (tid >> 4);
-  const int t16 = tid & 15;
-  if (id >= p.rows.n_rows * p.n_q) return;
-  const int64_t row = id / p.n_q;
-  const int head = static_cast<int>(id - row * p.n_q), kvh = head / p.G;
-  int s;
-  int64_t i;
-  if (!packed_find(p.rows, row, s, i)) return;
-  const SeqWork w = seq_work(p, s);
+  if (c0 != c || n == 1) return;
+  const int in = blockIdx.y * kJoinRows + (tid >> 4), t16 = tid & 15;  // row of the block
+  const int64_t R = static_cast<int64_t>(blk) * (w.full * kTile) + in;
+  if (in >= wt * kTile || R >= w.R) return;
+  const int64_t tok = R / p.G, row = w.first + tok;
+  const int head = kvh * p.G + static_cast<int>(R - tok * p.G);
+  // the item begins inside its first CTA's slice, and before every other's
+  auto part = [&](int j) {
+    return p.part + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlotFloats +
+           static_cast<int64_t>(in) * kPartStride;
+  };
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   float M = -INFINITY, L = 0.0f;
-  if (w.nt > 0) {
-    const int64_t R = i * p.G + (head - kvh * p.G);
-    const int blk = static_cast<int>(R / (2 * kTile)), wt = w.weight(blk);
-    const int in = static_cast<int>(R % (2 * kTile));  // tile and row of the block
-    const int64_t at = (s ? pfx[s] : 0) + kvh * w.per_head() + static_cast<int64_t>(blk) * 2 * w.nt;
-    const int64_t c0 = owner_of(at, W, P);
-    const int n = static_cast<int>(
-        owner_of(at + static_cast<int64_t>(w.nt - 1) * wt, W, P) - c0 + 1);
-    if (n == 1) return;
-    // the item begins inside its first CTA's slice, and before every other's
-    auto part = [&](int j) {
-      const int64_t c = c0 + j;
-      const int64_t slot = 2 * c + (at >= W * c / P ? 1 : 0);
-      return p.part + slot * kSlotFloats + static_cast<int64_t>(in) * kPartStride;
-    };
-    for (int j = t16; j < n; j += 16) M = fmaxf(M, __ldcg(part(j) + kD));
+  for (int j = t16; j < n; j += 16) M = fmaxf(M, __ldcg(part(j) + kD));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)  // (the other half of the warp may have returned)
-      M = fmaxf(M, __shfl_xor_sync(0xffffu << (lane & 16), M, o, 16));
-    constexpr int kAhead = 8;
-    for (int j0 = 0; j0 < n; j0 += kAhead) {
-      float4 x[kAhead][2];
-      float2 y[kAhead];
+  for (int o = 8; o > 0; o >>= 1)  // (the other half of the warp may have returned)
+    M = fmaxf(M, __shfl_xor_sync(0xffffu << (lane & 16), M, o, 16));
+  constexpr int kAhead = 8;
+  for (int j0 = 0; j0 < n; j0 += kAhead) {
+    float4 v[kAhead][2];
+    float2 y[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const float *pr = part(min(j0 + k, n - 1));
-        y[k] = __ldcg(reinterpret_cast<const float2 *>(pr + kD));
-        x[k][0] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16));
-        x[k][1] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16) + 1);
-      }
+    for (int k = 0; k < kAhead; ++k) {
+      const float *pr = part(min(j0 + k, n - 1));
+      y[k] = __ldcg(reinterpret_cast<const float2 *>(pr + kD));
+      v[k][0] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16));
+      v[k][1] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16) + 1);
+    }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (j0 + k >= n || y[k].x == -INFINITY) continue;
-        const float f = fast_exp2(y[k].x - M);
-        L = fmaf(f, y[k].y, L);
-        const float z[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w,
-                            x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+    for (int k = 0; k < kAhead; ++k) {
+      if (j0 + k >= n || y[k].x == -INFINITY) continue;
+      const float f = fast_exp2(y[k].x - M);
+      L = fmaf(f, y[k].y, L);
+      const float z[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                          v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
-        for (int d = 0; d < 8; ++d) acc[d] = fmaf(f, z[d], acc[d]);
-      }
+      for (int d = 0; d < 8; ++d) acc[d] = fmaf(f, z[d], acc[d]);
     }
   }
-  const int64_t at = row * p.n_q + head;
+  const int64_t to = row * p.n_q + head;
   RowOut ro;
   ro.inv = L > 0.0f ? 1.0f / L : 0.0f;
   ro.bf16 = p.q_bf16;
-  ro.full = p.out.xo ? p.out.xo + at * kD : nullptr;
+  ro.full = p.out.xo ? p.out.xo + to * kD : nullptr;
   ro.half = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head;
   ro.put(8 * t16, acc);
   if (t16 == 0) {
-    if (p.out.xo) p.out.xml[at] = make_float2(M, L);
+    if (p.out.xo) p.out.xml[to] = make_float2(M, L);
     else if (p.out.lse)
-      p.out.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      p.out.lse[to] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
   }
+}
+
+template <bool SPLIT>
+cudaError_t launch_attn(const CrossParams &p, int grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> optin{0};
+  const cudaError_t e = smem_optin(cross_attn_kernel<SPLIT>, kSmemBytes, optin);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(cross_attn_kernel<SPLIT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                    kSmemBytes, stream, p);
 }
 
 }  // namespace
@@ -1167,18 +1279,19 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.n_pages = L.n_pages;
   p.slot_bytes = kSlotUnits * std::max(unit_bytes(L.codec_k), unit_bytes(L.codec_v));
   p.slots = std::min(kMaxSlots, kRingBytes / p.slot_bytes);
+  const bool split = L.codec_k != KVQ_F16 || L.codec_v != KVQ_F16;
+  p.key_tile = split ? 64 : 128;
+  p.singles = L.codec_k == KVQ_TURBO4;
   p.scale_log2 = scale * 1.4426950408889634f;
-  static std::atomic<uint64_t> optin{0};
-  cudaError_t e = smem_optin(cross_attn_kernel, kSmemBytes, optin);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(cross_attn_kernel, dim3(static_cast<unsigned>(pl.grid)), dim3(kThreads), kSmemBytes,
-                 stream, p);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = (n_rows * L.n_q_heads + kJoinRows - 1) / kJoinRows;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = split ? launch_attn<true>(p, pl.grid, stream) : launch_attn<false>(p, pl.grid, stream);
+  if (e != cudaSuccess || pl.grid < 2) return e;
   const JoinParams jp = {p, pl.grid};
-  return launch_pdl(cross_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), 0,
-                    stream, jp);
+  // at most this many rows of a block (fewer: short batches need fewer blocks)
+  const int64_t rows = std::min<int64_t>(p.singles ? kTile : 2 * kTile, n_rows * p.G);
+  return launch_pdl(cross_join_kernel,
+                    dim3(static_cast<unsigned>(pl.grid - 1),
+                         static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)),
+                    dim3(kJoinThreads), 0, stream, jp);
 }
 
 }  // namespace kvq

@@ -35,10 +35,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
          (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
-// Instruction descriptor, kind::f16: fp16 A and B, fp32 D, M = 128, N = 128.
-__host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major) {
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 D, M = 128, N = 128 (or n).
+__host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int n = 128) {
   return (1u << 4) | (0u << 7) | (0u << 10) | (0u << 15) |
-         (static_cast<uint32_t>(b_mn_major) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+         (static_cast<uint32_t>(b_mn_major) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate) {
