@@ -18,16 +18,16 @@
 // Inside a CTA (16 warps) nothing is written to HBM but the results: codes are
 // copied in as they lie in the cache, turned into tensor-core operand tiles in
 // shared memory and used there.
-//  * Warp 12 copies the codes of 64 keys of one side at a time into a ring
+//  * Warp 14 copies the codes of 64 keys of one side at a time into a ring
 //    (1-D bulk copies); K and V tiles alternate.
-//  * Warps 8-11 turn them into fp16 operand tiles (x^ = d q rounded once; three
-//    32 KB buffers).  The cache's order is kept where the operands leave the
+//  * Warps 8-13 turn them into fp16 operand tiles (three 32 KB buffers), half a
+//    16-token unit at a time.  The cache's order is kept where the operands leave the
 //    choice, so that 16 bytes of codes become whole 8- or 16-byte pieces of a tile
 //    without an exchange between lanes: a key's place in its tile is 4 tig + 2 rh
 //    + par (include/kvq.h), the same for K's rows and V's columns, and K's dims
 //    stand in the order 32 b + 8 w + 4 h + i, as Q's do.  turbo4 stays in its
 //    rotated space: Q is rotated, O rotated back.
-//  * One thread of warp 13 issues tcgen05.mma: S = Q K^T into TMEM, O += P V with
+//  * One thread of warp 15 issues tcgen05.mma: S = Q K^T into TMEM, O += P V with
 //    P read from TMEM.
 //  * Warps 0-3 and 4-7 are two softmax pipes, one query row per thread.  In a
 //    pair they hold the two tiles; with a single tile they take its even and odd
@@ -47,12 +47,14 @@
 namespace kvq {
 namespace {
 
-constexpr int kTile = 128;                        // query rows, and keys, of a tile
-constexpr int kSlotUnits = 4;                     // units per ring slot: half a key tile
+constexpr int kTile = 128;                        // query rows of a tile
+constexpr int kKeys = 64;                         // keys of a step
+constexpr int kUnits = kKeys / kUnitTokens;       // units of a step, and of a ring slot
 constexpr int kBufs = 3;                          // operand tiles of K and V
 constexpr int kMaxSlots = 14;
 constexpr int kThreads = 512;
-constexpr int kDequantWarp = 8, kDequantWarps = 4, kCopyWarp = 12, kMmaWarp = 13;
+// warps 0-3, 4-7: softmax pipes; 8-13: operand tiles; 14: copies; 15: MMA
+constexpr int kDequantWarp = 8, kDequantWarps = 6, kCopyWarp = 14, kMmaWarp = 15;
 constexpr int kRingBytes = 65536;                 // four slots of f16 units
 constexpr int kSmemBytes = (2 + kBufs) * kTileBytes + kRingBytes + 1024;
 constexpr float kRaise = 8.0f;                    // log2 units, as in the prefill
@@ -74,7 +76,6 @@ struct CrossParams {
   const int32_t *seq_lens, *table;
   int32_t *err;
   int n_q, n_kv, G, capacity, max_len, pages_per_seq, n_pages, slots, slot_bytes;
-  int key_tile;  // keys of a step: 128, or 64 where a side is split
   int singles;   // no pairs: the second query tile's place holds the rest of a turbo4 query
   float scale_log2;
 };
@@ -104,7 +105,7 @@ __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
   const int64_t n = packed_rows(p.rows, s, w.first, bad);
   w.len = max(0, min(p.seq_lens[s], p.max_len));
   w.R = n * p.G;
-  w.nt = n > 0 ? (w.len + p.key_tile - 1) / p.key_tile : 0;
+  w.nt = n > 0 ? (w.len + kKeys - 1) / kKeys : 0;
   const int64_t tiles = (w.R + kTile - 1) / kTile;
   w.full = p.singles ? 1 : 2;
   w.blocks = static_cast<int>(p.singles ? tiles : (tiles + 1) / 2);
@@ -226,47 +227,44 @@ __device__ __forceinline__ void u4_quad(uint32_t w, uint32_t &lo, uint32_t &hi) 
 // 2.1e-4 and that of the weights, 1.7e-4; split they are 2.7e-4 off, as over f16.)
 constexpr int kLoRows = 64;  // K: the rests' first row; V: their columns' half
 
-// One unit of K into rows 16 u .. of the tile (all 32 lanes).  A lane takes the
+// One unit of K into rows 16 u .. of the tile (all 32 lanes): its dims 64 half ...  A lane takes the
 // 16-byte pieces (g, w) of row g and row g + 8; the order of g over the lanes
 // keeps loads (pieces 4 g + w) and stores (piece w ^ place of g) of eight lanes on
 // distinct banks.
 template <int CODEC>
-__device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int row0, int lane) {
+__device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int row0, int half,
+                                          int lane) {
   const int q8 = lane >> 2, w = lane & 3;
   const int g = (q8 & 4) | ((0x2130 >> (4 * (q8 & 3))) & 3);
   const int place = row0 + 4 * (g >> 1) + (g & 1);
   uint8_t *row[2] = {tile + place * 128, tile + (place + 2) * 128};
   const int sw[2] = {place & 7, (place + 2) & 7};
   const uint8_t *src = u + (4 * g + w) * 16;
+  // (b: the block, 0 or 1, of the half)
   auto at = [&](int rh, int b) {
-    return row[rh] + (b >> 1) * kHalfBytes + (((4 * (b & 1) + w) ^ sw[rh]) << 4);
+    return row[rh] + half * kHalfBytes + (((4 * b + w) ^ sw[rh]) << 4);
   };
   if (CODEC == KVQ_F16) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh)
-        *reinterpret_cast<uint4 *>(at(rh, b)) = lds128(src + (2 * b + rh) * 512);
+        *reinterpret_cast<uint4 *>(at(rh, b)) = lds128(src + (4 * half + 2 * b + rh) * 512);
     return;
   }
-  uint32_t d[2][4];  // scales by row and block, as pairs
+  uint32_t d[2][2];  // scales by row and block, as pairs
   if (CODEC == KVQ_TURBO4) {
     const uint32_t x = *reinterpret_cast<const uint32_t *>(u + 1024 + g * 4);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      d[0][b] = twice(x & 0xffffu);
-      d[1][b] = twice(x >> 16);
-    }
+    d[0][0] = d[0][1] = twice(x & 0xffffu);
+    d[1][0] = d[1][1] = twice(x >> 16);
   } else {
-    const uint4 x = lds128(u + unit_scale_offset(CODEC) + g * 16);
-    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int rh = 0; rh < 2; ++rh) {
-        const uint32_t z = y[2 * rh + (b >> 1)];
-        d[rh][b] = twice((b & 1) ? z >> 16 : z & 0xffffu);
-      }
+    for (int rh = 0; rh < 2; ++rh) {
+      const uint32_t z = *reinterpret_cast<const uint32_t *>(u + unit_scale_offset(CODEC) + g * 16 +
+                                                             rh * 8 + half * 4);
+      d[rh][0] = twice(z & 0xffffu);
+      d[rh][1] = twice(z >> 16);
+    }
   }
   auto put = [&](int rh, int b, const uint32_t (&c)[4]) {
     const Parts a0 = scaled(c[0], d[rh][b]), a1 = scaled(c[1], d[rh][b]);
@@ -277,8 +275,8 @@ __device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int r
   };
   if (CODEC == KVQ_Q8_0) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint4 x = lds128(src + b * 512);
+    for (int b = 0; b < 2; ++b) {
+      const uint4 x = lds128(src + (2 * half + b) * 512);
       const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (rh, h)
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh) {
@@ -289,30 +287,26 @@ __device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int r
       }
     }
   } else {
+    const uint4 x = lds128(src + half * 512);
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (b, rh)
 #pragma unroll
-    for (int bp = 0; bp < 2; ++bp) {
-      const uint4 x = lds128(src + bp * 512);
-      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (b & 1, rh)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = 2 * bp + (i >> 1), rh = i & 1;
-        uint32_t o[4];
-        u4_quad(y[i] & 0x0f0f0f0fu, o[0], o[1]);
-        u4_quad((y[i] >> 4) & 0x0f0f0f0fu, o[2], o[3]);
-        put(rh, b, o);
-      }
+    for (int i = 0; i < 4; ++i) {
+      uint32_t o[4];
+      u4_quad(y[i] & 0x0f0f0f0fu, o[0], o[1]);
+      u4_quad((y[i] >> 4) & 0x0f0f0f0fu, o[2], o[3]);
+      put(i & 1, i >> 1, o);
     }
   }
 }
 
 // One unit of V into columns 16 u .. of the tile, whose rows are dims (all 32
-// lanes).  A lane takes the pieces (gq, tig): two to eight dims of four tokens,
+// lanes): its dims 64 half ..  A lane takes the pieces (gq, tig): two to eight dims of four tokens,
 // eight bytes in each dim's row.  TAIL: of the unit only `live` tokens (any
 // number, none and more than 16 included) are the sequence's; the others'
 // columns are zeros, whatever lies there.
 template <int CODEC, bool TAIL>
-__device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int unit, int live,
-                                          int lane) {
+__device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int unit, int half,
+                                          int live, int lane) {
   const int q8 = lane >> 2, tig = lane & 3;
   const int gq = nibble_codec(CODEC) ? (0x65217430 >> (4 * q8)) & 7 : q8;
   uint8_t *col = tile + (unit >> 2) * kHalfBytes + (tig & 1) * 8;  // (split: units 0..3)
@@ -342,14 +336,16 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
   const uint8_t *src = u + (4 * gq + tig) * 16;
   if (CODEC == KVQ_F16) {
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
+    for (int m = 0; m < 4; ++m) {
+      const int mt = 4 * half + m;
       const uint4 x = lds128(src + mt * 512);  // (rh, s)
       put(16 * mt + 2 * gq, x.x, x.z);
       put(16 * mt + 2 * gq + 1, x.y, x.w);
     }
   } else if (CODEC == KVQ_Q8_0) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int k = 0; k < 2; ++k) {
+      const int b = 2 * half + k;
       const uint2 d = lds64(u + 2048 + tig * 32 + b * 8);
       const uint4 x = lds128(src + b * 512);
       const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (mt & 1, rh)
@@ -363,39 +359,36 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
   } else {
     uint2 d = make_uint2(0u, 0u);
     if (CODEC == KVQ_TURBO4) d = lds64(u + 1024 + tig * 8);
+    const uint4 x = lds128(src + half * 512);
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // mt = 4 half + i; bytes (par, rh)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 x = lds128(src + h * 512);
-      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // mt = 4 h + i; bytes (par, rh)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = 2 * h + (i >> 1), dim = 32 * b + 8 * (i & 1) + gq;
-        if (CODEC == KVQ_Q4_0 && (i & 1) == 0) d = lds64(u + 1024 + tig * 32 + b * 8);
-        const uint32_t z = y[i] >> 8;
-        put_split(dim, u4_pair_minus8(y[i]), u4_pair_minus8(z), d);
-        put_split(dim + 16, u4_pair_minus8_hi(y[i]), u4_pair_minus8_hi(z), d);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int b = 2 * half + (i >> 1), dim = 32 * b + 8 * (i & 1) + gq;
+      if (CODEC == KVQ_Q4_0 && (i & 1) == 0) d = lds64(u + 1024 + tig * 32 + b * 8);
+      const uint32_t z = y[i] >> 8;
+      put_split(dim, u4_pair_minus8(y[i]), u4_pair_minus8(z), d);
+      put_split(dim + 16, u4_pair_minus8_hi(y[i]), u4_pair_minus8_hi(z), d);
     }
   }
 }
 
 __device__ __forceinline__ void unit_to_tile(int side, int codec, const uint8_t *u, uint8_t *tile,
-                                             int unit, int live, int lane) {
+                                             int unit, int half, int live, int lane) {
   if (side == 0) {  // (rows past the length: their scores are masked)
-    if (codec == KVQ_F16) unit_to_k<KVQ_F16>(u, tile, 16 * unit, lane);
-    else if (codec == KVQ_Q8_0) unit_to_k<KVQ_Q8_0>(u, tile, 16 * unit, lane);
-    else if (codec == KVQ_Q4_0) unit_to_k<KVQ_Q4_0>(u, tile, 16 * unit, lane);
-    else unit_to_k<KVQ_TURBO4>(u, tile, 16 * unit, lane);
+    if (codec == KVQ_F16) unit_to_k<KVQ_F16>(u, tile, 16 * unit, half, lane);
+    else if (codec == KVQ_Q8_0) unit_to_k<KVQ_Q8_0>(u, tile, 16 * unit, half, lane);
+    else if (codec == KVQ_Q4_0) unit_to_k<KVQ_Q4_0>(u, tile, 16 * unit, half, lane);
+    else unit_to_k<KVQ_TURBO4>(u, tile, 16 * unit, half, lane);
   } else if (live >= kUnitTokens) {
-    if (codec == KVQ_F16) unit_to_v<KVQ_F16, false>(u, tile, unit, live, lane);
-    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, false>(u, tile, unit, live, lane);
-    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, false>(u, tile, unit, live, lane);
-    else unit_to_v<KVQ_TURBO4, false>(u, tile, unit, live, lane);
+    if (codec == KVQ_F16) unit_to_v<KVQ_F16, false>(u, tile, unit, half, live, lane);
+    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, false>(u, tile, unit, half, live, lane);
+    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, false>(u, tile, unit, half, live, lane);
+    else unit_to_v<KVQ_TURBO4, false>(u, tile, unit, half, live, lane);
   } else {
-    if (codec == KVQ_F16) unit_to_v<KVQ_F16, true>(u, tile, unit, live, lane);
-    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, true>(u, tile, unit, live, lane);
-    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, true>(u, tile, unit, live, lane);
-    else unit_to_v<KVQ_TURBO4, true>(u, tile, unit, live, lane);
+    if (codec == KVQ_F16) unit_to_v<KVQ_F16, true>(u, tile, unit, half, live, lane);
+    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, true>(u, tile, unit, half, live, lane);
+    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, true>(u, tile, unit, half, live, lane);
+    else unit_to_v<KVQ_TURBO4, true>(u, tile, unit, half, live, lane);
   }
 }
 // The token, within a unit, of column c of a tile (mod 16).
@@ -405,6 +398,18 @@ __device__ __forceinline__ constexpr int token_of(int c) {
 
 // ------------------------------------------------------------------ TMEM pieces
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   uint32_t r[8];
   asm volatile(
@@ -459,17 +464,30 @@ struct __align__(8) CrossBars {
 
 // ------------------------------------------------------------------ attention
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(x));
+  return x != 0;
+}
+// D += A B with A in TMEM, B's descriptor as its low word and the constant HI.
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
+
 // Both softmax pipes (256 threads).
 __device__ __forceinline__ void pipes_sync() {
   asm volatile("bar.sync 1, 256;\n" ::: "memory");
 }
 
-// SPLIT: a side is quantized, a step is 64 keys; else 128 keys of f16.
-template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_attn_kernel(const __grid_constant__ CrossParams p) {
-  constexpr int KT = SPLIT ? 64 : 128;
-  constexpr int kSlotsPerTile = KT / (kSlotUnits * kUnitTokens);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ CrossBars bars;
   __shared__ uint32_t tmem_base_sh;
@@ -528,10 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       abort_flag = 0;
       for (int i = 0; i < p.slots; ++i) {
         mbar_init(&bars.raw_full[i], 1);
-        mbar_init(&bars.raw_empty[i], kDequantWarps);
+        mbar_init(&bars.raw_empty[i], 2 * kUnits);  // one arrival per half unit
       }
       for (int i = 0; i < kBufs; ++i) {
-        mbar_init(&bars.tile_full[i], kDequantWarps);
+        mbar_init(&bars.tile_full[i], 2 * kUnits);
         mbar_init(&bars.tile_empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -546,12 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_mbar_init();
     }
   }
-  if (warp > kMmaWarp) {  // rows of sequences without keys
+  if (warp > 0) {  // rows of sequences without keys
     for (int s = blockIdx.x; s < p.rows.n_seqs; s += gridDim.x) {
       const SeqWork w = seq_work(p, s);
       if (w.len > 0) continue;
       const int64_t n = w.R * p.n_kv;  // rows x query heads
-      for (int64_t i = warp - kMmaWarp - 1; i < n; i += kThreads / 32 - kMmaWarp - 1) {
+      for (int64_t i = warp - 1; i < n; i += kThreads / 32 - 1) {
         const int64_t row = w.first + i / p.n_q;
         const int head = static_cast<int>(i % p.n_q);
         const int64_t at = row * p.n_q + head;
@@ -573,36 +591,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 384};
+  // columns: each pipe's scores (64 keys), query tiles, outputs
+  const uint32_t tm_s[2] = {tmem, tmem + 64}, tm_q[2] = {tmem + 128, tmem + 192};
+  const uint32_t tm_o[2] = {tmem + 256, tmem + 384};
 
   SegIter it;
   it.init(p, s0, s1, first_seq, slice[2]);
   Segment sg;
 
-  if (warp == kCopyWarp) {
-    // ---------------- codes into the ring, half a tile of one side at a time
-    if (lane == 0) {
-      int t = 0;  // slots filled
-      bool ok = true;
-      while (ok && it.next(p, sg)) {
-        const int n = sg.j_hi - sg.j_lo, units = (sg.len + kUnitTokens - 1) / kUnitTokens;
-        for (int i = 0; i < 2 * n && ok; ++i) {
-          int side, j;
-          use_at(i, n, side, j);
-          const int u0 = (sg.j_lo + j) * (KT / kUnitTokens);
-          const int ub = unit_bytes(p.codec[side]);
-          int64_t unit = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) *
-                             (p.capacity / kUnitTokens) + u0;
-          if (p.table) {  // a tile lies inside one page
-            int pg = page_of(p.table, p.pages_per_seq, p.n_pages, sg.s, u0 / kPageUnits);
-            if (pg < 0) {
-              set_err(p.err, KVQ_DEVERR_PAGE);
-              pg = 0;  // read pool page 0 in its place
+  if (warp >= kCopyWarp) {
+    if (warp == kCopyWarp) {
+      // ---------------- codes into the ring, a step of one side at a time
+      if (lane == 0) {
+        int t = 0;  // slots filled
+        bool ok = true;
+        while (ok && it.next(p, sg)) {
+          const int n = sg.j_hi - sg.j_lo, units = (sg.len + kUnitTokens - 1) / kUnitTokens;
+          for (int i = 0; i < 2 * n && ok; ++i) {
+            int side, j;
+            use_at(i, n, side, j);
+            const int u0 = (sg.j_lo + j) * kUnits;
+            const int ub = unit_bytes(p.codec[side]);
+            int64_t unit = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) *
+                               (p.capacity / kUnitTokens) + u0;
+            if (p.table) {  // a step lies inside one page
+              int pg = page_of(p.table, p.pages_per_seq, p.n_pages, sg.s, u0 / kPageUnits);
+              if (pg < 0) {
+                set_err(p.err, KVQ_DEVERR_PAGE);
+                pg = 0;  // read pool page 0 in its place
+              }
+              unit = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits + u0 % kPageUnits;
             }
-            unit = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits + u0 % kPageUnits;
-          }
-          const uint8_t *src = p.cache[side] + unit * ub;
-          for (int h = 0; h < kSlotsPerTile; ++h, ++t) {
+            const uint8_t *src = p.cache[side] + unit * ub;
             const int slot = t % p.slots;
             if (t >= p.slots &&
                 !mbar_wait_bounded(&bars.raw_empty[slot],
@@ -610,98 +630,76 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            const int nu = max(0, min(kSlotUnits, units - u0 - h * kSlotUnits));
-            const uint32_t bytes = static_cast<uint32_t>(nu * ub);
+            const uint32_t bytes = static_cast<uint32_t>(min(kUnits, units - u0) * ub);
             mbar_arrive_expect_tx(&bars.raw_full[slot], bytes);
-            if (bytes)
-              bulk_copy_g2s(ring + slot * p.slot_bytes, src + h * kSlotUnits * ub, bytes,
-                            &bars.raw_full[slot]);
+            bulk_copy_g2s(ring + slot * p.slot_bytes, src, bytes, &bars.raw_full[slot]);
+            ++t;
           }
         }
+        // after an abort, wait (bounded) for the copies still landing in the ring
+        if (!ok || *reinterpret_cast<volatile int *>(&abort_flag))
+          for (int u = max(0, t - p.slots); u < t; ++u)
+            mbar_wait_bounded(&bars.raw_full[u % p.slots], static_cast<uint32_t>(u / p.slots) & 1u,
+                              nullptr, 100000000ull);
       }
-      // after an abort, wait (bounded) for the copies still landing in the ring
-      if (!ok || *reinterpret_cast<volatile int *>(&abort_flag))
-        for (int u = max(0, t - p.slots); u < t; ++u)
-          mbar_wait_bounded(&bars.raw_full[u % p.slots], static_cast<uint32_t>(u / p.slots) & 1u,
-                            nullptr, 100000000ull);
-    }
-  } else if (warp >= kDequantWarp && warp < kDequantWarp + kDequantWarps) {
-    // ---------------- codes into operand tiles
-    const int dw = warp - kDequantWarp;
-    int t = 0, use = 0;  // slots and tiles so far
-    bool ok = true;
-    while (ok && it.next(p, sg)) {
-      const int n = sg.j_hi - sg.j_lo;
-      for (int i = 0; i < 2 * n && ok; ++i, ++use) {
-        int side, j;
-        use_at(i, n, side, j);
-        const int buf = use % kBufs;
-        if (use >= kBufs)
-          ok = mbar_wait_bounded(&bars.tile_empty[buf], static_cast<uint32_t>(use / kBufs - 1) & 1u,
-                                 &abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        for (int h = 0; h < kSlotsPerTile && ok; ++h, ++t) {
-          const int slot = t % p.slots;
-          ok = mbar_wait_bounded(&bars.raw_full[slot], static_cast<uint32_t>(t / p.slots) & 1u,
-                                 &abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const int unit = h * kSlotUnits + dw;  // of the tile
-          const int live = sg.len - (sg.j_lo + j) * KT - unit * kUnitTokens;
-          unit_to_tile(side, p.codec[side],
-                       ring + slot * p.slot_bytes + dw * unit_bytes(p.codec[side]),
-                       tiles + buf * kTileBytes, unit, live, lane);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.raw_empty[slot]);
-        }
-        if (!ok) break;
-        fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.tile_full[buf]);
-      }
-    }
-    if (!ok && lane == 0) {
-      set_err(p.err, KVQ_DEVERR_TIMEOUT);
-      atomicExch(&abort_flag, 1);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---------------- MMA issuer (one thread)
-    if (lane == 0) {
-      const bool split_k = SPLIT && p.codec[0] != KVQ_F16, split_v = SPLIT && p.codec[1] != KVQ_F16;
-      const uint32_t idesc_k = idesc_f16(0, SPLIT && !split_k ? 64 : 128), idesc_v = idesc_f16(0);
-      // 16 columns kk of a 128-row tile
-      auto desc = [](uint32_t base, int kk) {
-        return smem_desc(base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024);
-      };
+    } else if (warp == kMmaWarp) {
+      // ---------------- MMA issuer.  The whole warp walks the steps, so that what an
+      // instruction takes is known to be uniform; one elected thread issues.
+      const bool leader = elect_one();
+      const bool split_k = p.codec[0] != KVQ_F16, split_v = p.codec[1] != KVQ_F16;
+      constexpr uint32_t idesc_k = idesc_f16(0, kKeys), idesc_v = idesc_f16(0);
+      // A tile's 16 columns kk: 32 bytes on inside 64 columns, then the next half.
+      // The low word of the descriptor is all that changes from one to the next.
+      constexpr uint32_t kLo = 1u << 16, kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+      const uint32_t tile0 = kLo | ((smem_u32(tiles) & 0x3FFFFu) >> 4);
+      auto step = [](int kk) { return ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16; };
       auto wait = [&](uint64_t *bar, int phase) {
-        return mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u, &abort_flag);
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u,
+                                                         &abort_flag)) != 0;
       };
-      // S_e = Q K^T of the operand tile of use u; split keys: their rests' scores
-      // in columns 64 ..; turbo4: the rest of Q too
+      // S_e = Q K^T of the operand tile of use u: split keys add their rests'
+      // products, turbo4 those of the rest of Q
       auto qk = [&](int e, int qtile, int u) {
-        const uint32_t a = smem_u32(sq + qtile * kTileBytes);
-        const uint32_t b = smem_u32(tiles + (u % kBufs) * kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_ss(tm_s[e], desc(a, kk), desc(b, kk), idesc_k, kk > 0);
-        if (SPLIT && p.singles) {
+        const uint32_t b = tile0 + (u % kBufs) * (kTileBytes / 16);
+        const uint32_t d = tm_s[e], a = tm_q[qtile];
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss(tm_s[e], desc(a + kTileBytes, kk), desc(b, kk), idesc_k, 1u);
-        }
-        mma_commit(&bars.sfull[e]);
-      };
-      // O_e (+)= P_e V; split values: the same P for the rests, columns 64 .. of V
-      auto pv = [&](int e, int u, bool first) {
-        const uint32_t b = smem_u32(tiles + (u % kBufs) * kTileBytes);
+            mma_ts_lo<kHi>(d, a + kk * 8, b + step(kk), idesc_k, kk > 0);
+          if (split_k) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          if (SPLIT && kk >= 4 && !split_v) break;
-          mma_ts(tm_o[e], tm_s[e] + (SPLIT ? kk & 3 : kk) * 8, desc(b, kk), idesc_v,
-                 (!first || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts_lo<kHi>(d, a + kk * 8, b + kLoRows * 8 + step(kk), idesc_k, 1u);
+          }
+          if (p.singles) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts_lo<kHi>(d, tm_q[1] + kk * 8, b + step(kk), idesc_k, 1u);
+          }
+          mma_commit(&bars.sfull[e]);
         }
-        mma_commit(&bars.odone[e]);
+        __syncwarp();
       };
-      auto free_tile = [&](int u) { mma_commit(&bars.tile_empty[u % kBufs]); };
+      // O_e (+)= P_e V; split values: the same P with the rests, columns 64 .. of V
+      auto pv = [&](int e, int u, bool first) {
+        const uint32_t b = tile0 + (u % kBufs) * (kTileBytes / 16);
+        const uint32_t d = tm_o[e], a = tm_s[e];
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts_lo<kHi>(d, a + kk * 8, b + step(kk), idesc_v, (!first || kk > 0) ? 1u : 0u);
+          if (split_v) {
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              mma_ts_lo<kHi>(d, a + (kk - 4) * 8, b + step(kk), idesc_v, 1u);
+          }
+          mma_commit(&bars.odone[e]);
+        }
+        __syncwarp();
+      };
+      auto free_tile = [&](int u) {
+        if (leader) mma_commit(&bars.tile_empty[u % kBufs]);
+      };
       auto have_tile = [&](int u) { return wait(&bars.tile_full[u % kBufs], u / kBufs); };
       int u0 = 0;         // operand tiles used by earlier segments
       int u[2] = {0, 0};  // products P V of each pipe
@@ -778,28 +776,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         u0 += 2 * n;
         // a pipe's O is complete once every MMA issued so far is
-        mma_commit(&bars.segdone[0]);
-        ++k[0];
-        if (sg.pair || n > 1) {
-          mma_commit(&bars.segdone[1]);
-          ++k[1];
+        const bool both = sg.pair || n > 1;
+        if (leader) {
+          mma_commit(&bars.segdone[0]);
+          if (both) mma_commit(&bars.segdone[1]);
         }
+        ++k[0];
+        if (both) ++k[1];
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_err(p.err, KVQ_DEVERR_TIMEOUT);
         atomicExch(&abort_flag, 1);
       }
-      // drain: every MMA this thread issued has finished (TMEM is freed after it)
-      mma_commit(&bars.drain);
+      // drain: every MMA the thread issued has finished (TMEM is freed after it)
+      if (leader) mma_commit(&bars.drain);
       mbar_wait_bounded(&bars.drain, 0, nullptr, 100000000ull);
+  }
+  } else if (warp >= kDequantWarp) {
+    // ---------------- codes into operand tiles, half a unit at a time
+    constexpr int kItems = 2 * kUnits;  // halves of units in a tile
+    int use = 0;                     // tiles (and slots) so far
+    int item = warp - kDequantWarp;  // this warp's next, counted over all tiles
+    bool ok = true;
+    while (ok && it.next(p, sg)) {
+      const int n = sg.j_hi - sg.j_lo;
+      for (int i = 0; i < 2 * n && ok; ++i, ++use) {
+        int side, j;
+        use_at(i, n, side, j);
+        const int buf = use % kBufs, slot = use % p.slots, ub = unit_bytes(p.codec[side]);
+        if (use >= kBufs)
+          ok = mbar_wait_bounded(&bars.tile_empty[buf], static_cast<uint32_t>(use / kBufs - 1) & 1u,
+                                 &abort_flag);
+        if (ok)
+          ok = mbar_wait_bounded(&bars.raw_full[slot], static_cast<uint32_t>(use / p.slots) & 1u,
+                                 &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        for (; ok && item < (use + 1) * kItems; item += kDequantWarps) {
+          const int unit = (item % kItems) >> 1;
+          const int live = sg.len - (sg.j_lo + j) * kKeys - unit * kUnitTokens;
+          unit_to_tile(side, p.codec[side], ring + slot * p.slot_bytes + unit * ub,
+                       tiles + buf * kTileBytes, unit, item & 1, live, lane);
+          fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars.raw_empty[slot]);
+            mbar_arrive(&bars.tile_full[buf]);
+          }
+        }
+      }
     }
-  } else if (warp < kDequantWarp) {
+    if (!ok && lane == 0) {
+      set_err(p.err, KVQ_DEVERR_TIMEOUT);
+      atomicExch(&abort_flag, 1);
+    }
+  } else {
     // ---------------- softmax pipe e: thread = query row
     const int e = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tms = tm_s[e] + lane_off, tmo = tm_o[e] + lane_off;
-    const bool rot_k = SPLIT && p.codec[0] == KVQ_TURBO4, rot_v = SPLIT && p.codec[1] == KVQ_TURBO4;
-    const bool split_k = SPLIT && p.codec[0] != KVQ_F16;
+    const bool rot_k = p.codec[0] == KVQ_TURBO4, rot_v = p.codec[1] == KVQ_TURBO4;
     float *exchange = reinterpret_cast<float *>(sq + kTileBytes);  // [64][128]: Q tile 1's place
     auto mine = [&](const Segment &g) { return e == 0 || g.pair || g.j_hi - g.j_lo > 1; };
     auto next_mine = [&](Segment &g) {
@@ -858,7 +893,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint2 *>(dst + place(i0 + i)) = x[i];
         }
       }
-      fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
+      // a thread's own row into TMEM, where the products take it from (both operands
+      // of a product from shared memory take it twice as long)
+      __syncwarp();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && !rot_k) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 x = lds128(dst + t * kTileBytes + tile_offset(r, 32 * c + 8 * k));
+            w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+          }
+          tmem_st16(tm_q[rot_k ? t : e] + lane_off + 16 * c, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.qready[e]);
     };
@@ -882,39 +935,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (!idle) {
-          const int left = sg.len - (sg.j_lo + j) * KT;  // keys from the tile's first on
-          // Pass 1: the row's maximum; scores of places past the length become -inf.
-          // Split: the 64 scores stay in registers.  Else 128 are read again in pass 2
-          // (those of the last tile overwritten in TMEM, so that it needs no mask).
+          const int left = sg.len - (sg.j_lo + j) * kKeys;  // keys from the step's first on
+          // The row's scores stay in registers; those of places past the length are
+          // -inf.
           float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          float sc[SPLIT ? 2 : 1][32];
+          float v[kKeys / 32][32];
 #pragma unroll
-          for (int c = 0; c < KT / 32; ++c) {
-            float(&v)[32] = sc[SPLIT ? c : 0];
-            tmem_ld32(tms + c * 32, v);
-            if (split_k) {
-              float x[32];
-              tmem_ld32(tms + 64 + c * 32, x);
-              tmem_wait_ld();
+          for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(tms + c * 32, v[c]);
+          tmem_wait_ld();
+          if (left < kKeys) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = add2(make_float2(v[i], v[i + 1]), make_float2(x[i], x[i + 1]));
-                v[i] = y.x;
-                v[i + 1] = y.y;
-              }
-            } else {
-              tmem_wait_ld();
-            }
-            if (left < KT) {
+            for (int c = 0; c < kKeys / 32; ++c)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (c * 32 + (i & 16) + token_of(i) >= left) v[i] = -INFINITY;
-              if (!SPLIT) tmem_st32f(tms + c * 32, v);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[i], v[i + 1]);
+                if (c * 32 + (i & 16) + token_of(i) >= left) v[c][i] = -INFINITY;
           }
-          if (!SPLIT && left < KT) tmem_wait_st();
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[c][i], v[c][i + 1]);
           const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
           // A row's running maximum is raised only when it grew by more than the
           // threshold; O is rescaled for the whole warp when one of its rows is.
@@ -930,34 +970,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tmem_ld32(tmo + c * 32, v);
+            for (int c = 0; c < 8; ++c) {
+              float x[16];
+              tmem_ld16(tmo + c * 16, x);
               tmem_wait_ld();
+              uint32_t y[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= a;
-              tmem_st32f(tmo + c * 32, v);
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * a);
+              tmem_st16(tmo + c * 16, y);
             }
             tmem_wait_st();
           }
           l *= a;
           m = mnew;
-          // Pass 2: P = exp2(s * scale_log2 - m + lift) as fp16 pairs over the first
-          // columns of S (a chunk lands on columns already read), and the row's sum.
+          // P = exp2(s * scale_log2 - m + lift) as fp16 pairs over S, and the row's sum.
           const float nm = m == -INFINITY ? 0.0f : kLift - m;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-          for (int c = 0; c < KT / 32; ++c) {
-            float(&v)[32] = sc[SPLIT ? c : 0];
+          for (int c = 0; c < kKeys / 32; ++c) {
             uint32_t pk[16];
-            if (!SPLIT) {
-              tmem_ld32(tms + c * 32, v);
-              tmem_wait_ld();
-            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 tt = fma2(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
+              const float2 tt = fma2(make_float2(v[c][2 * i], v[c][2 * i + 1]), sc2, nm2);
               const float2 x = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
               sum[i & 1] = add2(sum[i & 1], x);
               pk[i] = pack_half2(x.x, x.y);
@@ -1231,15 +1266,6 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-template <bool SPLIT>
-cudaError_t launch_attn(const CrossParams &p, int grid, cudaStream_t stream) {
-  static std::atomic<uint64_t> optin{0};
-  const cudaError_t e = smem_optin(cross_attn_kernel<SPLIT>, kSmemBytes, optin);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(cross_attn_kernel<SPLIT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                    kSmemBytes, stream, p);
-}
-
 }  // namespace
 
 CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms) {
@@ -1277,13 +1303,15 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.max_len = max_len;
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
-  p.slot_bytes = kSlotUnits * std::max(unit_bytes(L.codec_k), unit_bytes(L.codec_v));
+  p.slot_bytes = kUnits * std::max(unit_bytes(L.codec_k), unit_bytes(L.codec_v));
   p.slots = std::min(kMaxSlots, kRingBytes / p.slot_bytes);
-  const bool split = L.codec_k != KVQ_F16 || L.codec_v != KVQ_F16;
-  p.key_tile = split ? 64 : 128;
   p.singles = L.codec_k == KVQ_TURBO4;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const cudaError_t e = split ? launch_attn<true>(p, pl.grid, stream) : launch_attn<false>(p, pl.grid, stream);
+  static std::atomic<uint64_t> optin{0};
+  cudaError_t e = smem_optin(cross_attn_kernel, kSmemBytes, optin);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(cross_attn_kernel, dim3(static_cast<unsigned>(pl.grid)), dim3(kThreads), kSmemBytes,
+                 stream, p);
   if (e != cudaSuccess || pl.grid < 2) return e;
   const JoinParams jp = {p, pl.grid};
   // at most this many rows of a block (fewer: short batches need fewer blocks)
