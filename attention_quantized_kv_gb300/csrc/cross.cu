@@ -15,19 +15,19 @@
 // slot (unnormalised O, max, sum), and a second kernel joins an item's pieces by
 // log-sum-exp in a fixed order.  Lengths and row counts are read on the device.
 //
-// Inside a CTA (16 warps) nothing is written to HBM but the results: codes are
+// Inside a CTA (18 warps at work) nothing is written to HBM but the results: codes are
 // copied in as they lie in the cache, turned into tensor-core operand tiles in
 // shared memory and used there.
-//  * Warp 14 copies the codes of 64 keys of one side at a time into a ring
+//  * Warp 16 copies the codes of 64 keys of one side at a time into a ring
 //    (1-D bulk copies); K and V tiles alternate.
-//  * Warps 8-13 turn them into fp16 operand tiles (three 32 KB buffers), half a
-//    16-token unit at a time.  The cache's order is kept where the operands leave the
+//  * Warps 8-11 (K) and 12-15 (V) turn them into fp16 operand tiles (three 32 KB
+//    buffers), a 16-token unit each.  The cache's order is kept where the operands leave the
 //    choice, so that 16 bytes of codes become whole 8- or 16-byte pieces of a tile
 //    without an exchange between lanes: a key's place in its tile is 4 tig + 2 rh
 //    + par (include/kvq.h), the same for K's rows and V's columns, and K's dims
 //    stand in the order 32 b + 8 w + 4 h + i, as Q's do.  turbo4 stays in its
 //    rotated space: Q is rotated, O rotated back.
-//  * One thread of warp 15 issues tcgen05.mma: S = Q K^T into TMEM, O += P V with
+//  * One thread of warp 17 issues tcgen05.mma: S = Q K^T into TMEM, O += P V with
 //    P read from TMEM.
 //  * Warps 0-3 and 4-7 are two softmax pipes, one query row per thread.  In a
 //    pair they hold the two tiles; with a single tile they take its even and odd
@@ -50,13 +50,15 @@ namespace {
 constexpr int kTile = 128;                        // query rows of a tile
 constexpr int kKeys = 64;                         // keys of a step
 constexpr int kUnits = kKeys / kUnitTokens;       // units of a step, and of a ring slot
-constexpr int kBufs = 3;                          // operand tiles of K and V
-constexpr int kMaxSlots = 14;
-constexpr int kThreads = 512;
-// warps 0-3, 4-7: softmax pipes; 8-13: operand tiles; 14: copies; 15: MMA
-constexpr int kDequantWarp = 8, kDequantWarps = 6, kCopyWarp = 14, kMmaWarp = 15;
-constexpr int kRingBytes = 65536;                 // four slots of f16 units
-constexpr int kSmemBytes = (2 + kBufs) * kTileBytes + kRingBytes + 1024;
+constexpr int kBufs = 2;                          // operand tiles of each side
+constexpr int kMaxSlots = 8;                      // of one side
+constexpr int kThreads = 640;
+// warps 0-3, 4-7: softmax pipes; 8-11, 12-15: tiles of K, of V; 16: copies; 17: MMA;
+// two idle (registers go to a CTA in groups of four warps)
+constexpr int kTileWarp = 8, kCopyWarp = 16, kMmaWarp = 17;
+constexpr int kRingBytes = 65536;                 // K's ring, then V's: two steps of f16 each
+constexpr int kExchangeBytes = 64 * kTile * 4;   // half of pipe 1's O
+constexpr int kSmemBytes = 2 * kBufs * kTileBytes + kExchangeBytes + kRingBytes + 1024;
 constexpr float kRaise = 8.0f;                    // log2 units, as in the prefill
 // Weights are held as 2^(s - m + 6): at most 2^14 in fp16, and 2^6 further from
 // its subnormals than 2^(s - m).
@@ -75,7 +77,8 @@ struct CrossParams {
   PackedRows rows;
   const int32_t *seq_lens, *table;
   int32_t *err;
-  int n_q, n_kv, G, capacity, max_len, pages_per_seq, n_pages, slots, slot_bytes;
+  int n_q, n_kv, G, capacity, max_len, pages_per_seq, n_pages;
+  int slots[2];  // ring slots of K and V codes
   int singles;   // no pairs: the second query tile's place holds the rest of a turbo4 query
   float scale_log2;
 };
@@ -181,11 +184,9 @@ struct SegIter {
     return false;
   }
 };
-// The order in which a segment of n steps uses its 2 n operand tiles: K_0, then
-// K_{j+1}, V_j in turn, the last V alone.
-__device__ __forceinline__ int k_use(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int v_use(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
-__device__ __forceinline__ void use_at(int i, int n, int &side, int &j) {
+// The order in which a segment of n steps takes its 2 n copies: K_0, then K_{j+1},
+// V_j in turn, the last V alone.
+__device__ __forceinline__ void copy_at(int i, int n, int &side, int &j) {
   side = i == 0 || ((i & 1) && i < 2 * n - 1) ? 0 : 1;
   j = side == 0 ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1;
 }
@@ -227,56 +228,51 @@ __device__ __forceinline__ void u4_quad(uint32_t w, uint32_t &lo, uint32_t &hi) 
 // 2.1e-4 and that of the weights, 1.7e-4; split they are 2.7e-4 off, as over f16.)
 constexpr int kLoRows = 64;  // K: the rests' first row; V: their columns' half
 
-// One unit of K into rows 16 u .. of the tile (all 32 lanes): its dims 64 half ...  A lane takes the
+// One unit of K into rows 16 u .. of the tile (all 32 lanes).  A lane takes the
 // 16-byte pieces (g, w) of row g and row g + 8; the order of g over the lanes
 // keeps loads (pieces 4 g + w) and stores (piece w ^ place of g) of eight lanes on
 // distinct banks.
 template <int CODEC>
-__device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int row0, int half,
-                                          int lane) {
+__device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int row0, int lane) {
   const int q8 = lane >> 2, w = lane & 3;
   const int g = (q8 & 4) | ((0x2130 >> (4 * (q8 & 3))) & 3);
   const int place = row0 + 4 * (g >> 1) + (g & 1);
   uint8_t *row[2] = {tile + place * 128, tile + (place + 2) * 128};
   const int sw[2] = {place & 7, (place + 2) & 7};
   const uint8_t *src = u + (4 * g + w) * 16;
-  // (b: the block, 0 or 1, of the half)
   auto at = [&](int rh, int b) {
-    return row[rh] + half * kHalfBytes + (((4 * b + w) ^ sw[rh]) << 4);
+    return row[rh] + (b >> 1) * kHalfBytes + (((4 * (b & 1) + w) ^ sw[rh]) << 4);
   };
   if (CODEC == KVQ_F16) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh)
-        *reinterpret_cast<uint4 *>(at(rh, b)) = lds128(src + (4 * half + 2 * b + rh) * 512);
+        *reinterpret_cast<uint4 *>(at(rh, b)) = lds128(src + (2 * b + rh) * 512);
     return;
   }
-  uint32_t d[2][2];  // scales by row and block, as pairs
+  uint32_t d[4];  // scales by (row, pair of blocks); turbo4: by row
   if (CODEC == KVQ_TURBO4) {
     const uint32_t x = *reinterpret_cast<const uint32_t *>(u + 1024 + g * 4);
-    d[0][0] = d[0][1] = twice(x & 0xffffu);
-    d[1][0] = d[1][1] = twice(x >> 16);
+    d[0] = d[1] = twice(x & 0xffffu);
+    d[2] = d[3] = twice(x >> 16);
   } else {
-#pragma unroll
-    for (int rh = 0; rh < 2; ++rh) {
-      const uint32_t z = *reinterpret_cast<const uint32_t *>(u + unit_scale_offset(CODEC) + g * 16 +
-                                                             rh * 8 + half * 4);
-      d[rh][0] = twice(z & 0xffffu);
-      d[rh][1] = twice(z >> 16);
-    }
+    const uint4 x = lds128(u + unit_scale_offset(CODEC) + g * 16);
+    d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
   }
   auto put = [&](int rh, int b, const uint32_t (&c)[4]) {
-    const Parts a0 = scaled(c[0], d[rh][b]), a1 = scaled(c[1], d[rh][b]);
-    const Parts a2 = scaled(c[2], d[rh][b]), a3 = scaled(c[3], d[rh][b]);
+    const uint32_t z = d[2 * rh + (b >> 1)];
+    const uint32_t y = __byte_perm(z, z, (b & 1) ? 0x3232 : 0x1010);
+    const Parts a0 = scaled(c[0], y), a1 = scaled(c[1], y);
+    const Parts a2 = scaled(c[2], y), a3 = scaled(c[3], y);
     uint8_t *to = at(rh, b);
     sts128(to, a0.hi, a1.hi, a2.hi, a3.hi);
     sts128(to + kLoRows * 128, a0.lo, a1.lo, a2.lo, a3.lo);
   };
   if (CODEC == KVQ_Q8_0) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const uint4 x = lds128(src + (2 * half + b) * 512);
+    for (int b = 0; b < 4; ++b) {
+      const uint4 x = lds128(src + b * 512);
       const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (rh, h)
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh) {
@@ -287,26 +283,29 @@ __device__ __forceinline__ void unit_to_k(const uint8_t *u, uint8_t *tile, int r
       }
     }
   } else {
-    const uint4 x = lds128(src + half * 512);
-    const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (b, rh)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t o[4];
-      u4_quad(y[i] & 0x0f0f0f0fu, o[0], o[1]);
-      u4_quad((y[i] >> 4) & 0x0f0f0f0fu, o[2], o[3]);
-      put(i & 1, i >> 1, o);
+    for (int bp = 0; bp < 2; ++bp) {
+      const uint4 x = lds128(src + bp * 512);
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (b & 1, rh)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
+        u4_quad(y[i] & 0x0f0f0f0fu, o[0], o[1]);
+        u4_quad((y[i] >> 4) & 0x0f0f0f0fu, o[2], o[3]);
+        put(i & 1, 2 * bp + (i >> 1), o);
+      }
     }
   }
 }
 
 // One unit of V into columns 16 u .. of the tile, whose rows are dims (all 32
-// lanes): its dims 64 half ..  A lane takes the pieces (gq, tig): two to eight dims of four tokens,
+// lanes).  A lane takes the pieces (gq, tig): two to eight dims of four tokens,
 // eight bytes in each dim's row.  TAIL: of the unit only `live` tokens (any
 // number, none and more than 16 included) are the sequence's; the others'
 // columns are zeros, whatever lies there.
 template <int CODEC, bool TAIL>
-__device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int unit, int half,
-                                          int live, int lane) {
+__device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int unit, int live,
+                                          int lane) {
   const int q8 = lane >> 2, tig = lane & 3;
   const int gq = nibble_codec(CODEC) ? (0x65217430 >> (4 * q8)) & 7 : q8;
   uint8_t *col = tile + (unit >> 2) * kHalfBytes + (tig & 1) * 8;  // (split: units 0..3)
@@ -336,16 +335,14 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
   const uint8_t *src = u + (4 * gq + tig) * 16;
   if (CODEC == KVQ_F16) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int mt = 4 * half + m;
+    for (int mt = 0; mt < 8; ++mt) {
       const uint4 x = lds128(src + mt * 512);  // (rh, s)
       put(16 * mt + 2 * gq, x.x, x.z);
       put(16 * mt + 2 * gq + 1, x.y, x.w);
     }
   } else if (CODEC == KVQ_Q8_0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int b = 2 * half + k;
+    for (int b = 0; b < 4; ++b) {
       const uint2 d = lds64(u + 2048 + tig * 32 + b * 8);
       const uint4 x = lds128(src + b * 512);
       const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // (mt & 1, rh)
@@ -359,36 +356,39 @@ __device__ __forceinline__ void unit_to_v(const uint8_t *u, uint8_t *tile, int u
   } else {
     uint2 d = make_uint2(0u, 0u);
     if (CODEC == KVQ_TURBO4) d = lds64(u + 1024 + tig * 8);
-    const uint4 x = lds128(src + half * 512);
-    const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // mt = 4 half + i; bytes (par, rh)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = 2 * half + (i >> 1), dim = 32 * b + 8 * (i & 1) + gq;
-      if (CODEC == KVQ_Q4_0 && (i & 1) == 0) d = lds64(u + 1024 + tig * 32 + b * 8);
-      const uint32_t z = y[i] >> 8;
-      put_split(dim, u4_pair_minus8(y[i]), u4_pair_minus8(z), d);
-      put_split(dim + 16, u4_pair_minus8_hi(y[i]), u4_pair_minus8_hi(z), d);
+    for (int h = 0; h < 2; ++h) {
+      const uint4 x = lds128(src + h * 512);
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};  // mt = 4 h + i; bytes (par, rh)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 2 * h + (i >> 1), dim = 32 * b + 8 * (i & 1) + gq;
+        if (CODEC == KVQ_Q4_0 && (i & 1) == 0) d = lds64(u + 1024 + tig * 32 + b * 8);
+        const uint32_t z = y[i] >> 8;
+        put_split(dim, u4_pair_minus8(y[i]), u4_pair_minus8(z), d);
+        put_split(dim + 16, u4_pair_minus8_hi(y[i]), u4_pair_minus8_hi(z), d);
+      }
     }
   }
 }
 
 __device__ __forceinline__ void unit_to_tile(int side, int codec, const uint8_t *u, uint8_t *tile,
-                                             int unit, int half, int live, int lane) {
+                                             int unit, int live, int lane) {
   if (side == 0) {  // (rows past the length: their scores are masked)
-    if (codec == KVQ_F16) unit_to_k<KVQ_F16>(u, tile, 16 * unit, half, lane);
-    else if (codec == KVQ_Q8_0) unit_to_k<KVQ_Q8_0>(u, tile, 16 * unit, half, lane);
-    else if (codec == KVQ_Q4_0) unit_to_k<KVQ_Q4_0>(u, tile, 16 * unit, half, lane);
-    else unit_to_k<KVQ_TURBO4>(u, tile, 16 * unit, half, lane);
+    if (codec == KVQ_F16) unit_to_k<KVQ_F16>(u, tile, 16 * unit, lane);
+    else if (codec == KVQ_Q8_0) unit_to_k<KVQ_Q8_0>(u, tile, 16 * unit, lane);
+    else if (codec == KVQ_Q4_0) unit_to_k<KVQ_Q4_0>(u, tile, 16 * unit, lane);
+    else unit_to_k<KVQ_TURBO4>(u, tile, 16 * unit, lane);
   } else if (live >= kUnitTokens) {
-    if (codec == KVQ_F16) unit_to_v<KVQ_F16, false>(u, tile, unit, half, live, lane);
-    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, false>(u, tile, unit, half, live, lane);
-    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, false>(u, tile, unit, half, live, lane);
-    else unit_to_v<KVQ_TURBO4, false>(u, tile, unit, half, live, lane);
+    if (codec == KVQ_F16) unit_to_v<KVQ_F16, false>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, false>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, false>(u, tile, unit, live, lane);
+    else unit_to_v<KVQ_TURBO4, false>(u, tile, unit, live, lane);
   } else {
-    if (codec == KVQ_F16) unit_to_v<KVQ_F16, true>(u, tile, unit, half, live, lane);
-    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, true>(u, tile, unit, half, live, lane);
-    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, true>(u, tile, unit, half, live, lane);
-    else unit_to_v<KVQ_TURBO4, true>(u, tile, unit, half, live, lane);
+    if (codec == KVQ_F16) unit_to_v<KVQ_F16, true>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q8_0) unit_to_v<KVQ_Q8_0, true>(u, tile, unit, live, lane);
+    else if (codec == KVQ_Q4_0) unit_to_v<KVQ_Q4_0, true>(u, tile, unit, live, lane);
+    else unit_to_v<KVQ_TURBO4, true>(u, tile, unit, live, lane);
   }
 }
 // The token, within a unit, of column c of a tile (mod 16).
@@ -409,6 +409,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   uint32_t r[8];
@@ -434,6 +447,19 @@ __device__ __forceinline__ void fwht32(float (&v)[32]) {
       }
 }
 
+// The stages across four groups of 32 (v[c]: 8 of group c's), and a factor.
+__device__ __forceinline__ void across32(float (&v)[4][8], float f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = v[0][i] + v[1][i], b = v[0][i] - v[1][i];
+    const float c = v[2][i] + v[3][i], d = v[2][i] - v[3][i];
+    v[0][i] = (a + c) * f;
+    v[1][i] = (b + d) * f;
+    v[2][i] = (a - c) * f;
+    v[3][i] = (b - d) * f;
+  }
+}
+
 // Where a finished row goes: its place in out (fp16 or bf16, normalised), or
 // fp32 (unnormalised) in xo or a partial slot.
 struct RowOut {
@@ -457,8 +483,8 @@ struct RowOut {
 };
 
 struct __align__(8) CrossBars {
-  uint64_t raw_full[kMaxSlots], raw_empty[kMaxSlots];
-  uint64_t tile_full[kBufs], tile_empty[kBufs];
+  uint64_t raw_full[2][kMaxSlots], raw_empty[2][kMaxSlots];
+  uint64_t tile_full[2][kBufs], tile_empty[2][kBufs];
   uint64_t sfull[2], pfull[2], odone[2], segdone[2], qready[2], ofree[2], drain;
 };
 
@@ -496,7 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float2 pipe1_ml[kTile];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t *sq = smem, *tiles = smem + 2 * kTileBytes, *ring = tiles + kBufs * kTileBytes;
+  // operand tiles of K, of V, the exchange, codes
+  uint8_t *tiles = smem, *ring = smem + 2 * kBufs * kTileBytes + kExchangeBytes;
+  float *exchange = reinterpret_cast<float *>(smem + 2 * kBufs * kTileBytes);  // [64][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   grid_dependency_wait();
@@ -544,13 +572,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       slice[0] = s0;
       slice[1] = s1;
       abort_flag = 0;
-      for (int i = 0; i < p.slots; ++i) {
-        mbar_init(&bars.raw_full[i], 1);
-        mbar_init(&bars.raw_empty[i], 2 * kUnits);  // one arrival per half unit
+      for (int i = 0; i < 2 * kMaxSlots; ++i) {
+        mbar_init(&bars.raw_full[0][i], 1);
+        mbar_init(&bars.raw_empty[0][i], kUnits);  // one arrival per unit
       }
-      for (int i = 0; i < kBufs; ++i) {
-        mbar_init(&bars.tile_full[i], 2 * kUnits);
-        mbar_init(&bars.tile_empty[i], 1);
+      for (int i = 0; i < 2 * kBufs; ++i) {
+        mbar_init(&bars.tile_full[0][i], kUnits);
+        mbar_init(&bars.tile_empty[0][i], 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bars.sfull[i], 1);
@@ -603,13 +631,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
       // ---------------- codes into the ring, a step of one side at a time
       if (lane == 0) {
-        int t = 0;  // slots filled
+        int slot[2] = {0, 0};  // each ring's next slot
+        uint32_t turn[2] = {0, 0};
         bool ok = true;
         while (ok && it.next(p, sg)) {
           const int n = sg.j_hi - sg.j_lo, units = (sg.len + kUnitTokens - 1) / kUnitTokens;
           for (int i = 0; i < 2 * n && ok; ++i) {
             int side, j;
-            use_at(i, n, side, j);
+            copy_at(i, n, side, j);
             const int u0 = (sg.j_lo + j) * kUnits;
             const int ub = unit_bytes(p.codec[side]);
             int64_t unit = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) *
@@ -623,24 +652,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               unit = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits + u0 % kPageUnits;
             }
             const uint8_t *src = p.cache[side] + unit * ub;
-            const int slot = t % p.slots;
-            if (t >= p.slots &&
-                !mbar_wait_bounded(&bars.raw_empty[slot],
-                                   static_cast<uint32_t>(t / p.slots - 1) & 1u, &abort_flag)) {
+            const int at = slot[side];
+            uint64_t *full = &bars.raw_full[side][at];
+            if (turn[side] > 0 && !mbar_wait_bounded(&bars.raw_empty[side][at], (turn[side] - 1) & 1u,
+                                                     &abort_flag)) {
               ok = false;
               break;
             }
             const uint32_t bytes = static_cast<uint32_t>(min(kUnits, units - u0) * ub);
-            mbar_arrive_expect_tx(&bars.raw_full[slot], bytes);
-            bulk_copy_g2s(ring + slot * p.slot_bytes, src, bytes, &bars.raw_full[slot]);
-            ++t;
+            mbar_arrive_expect_tx(full, bytes);
+            bulk_copy_g2s(ring + (side ? p.slots[0] * kUnits * unit_bytes(p.codec[0]) : 0) +
+                              at * kUnits * ub,
+                          src, bytes, full);
+            if (++slot[side] == p.slots[side]) {
+              slot[side] = 0;
+              ++turn[side];
+            }
           }
         }
-        // after an abort, wait (bounded) for the copies still landing in the ring
+        // after an abort, wait (bounded) for the copies still landing in the rings: each
+        // slot's last one
         if (!ok || *reinterpret_cast<volatile int *>(&abort_flag))
-          for (int u = max(0, t - p.slots); u < t; ++u)
-            mbar_wait_bounded(&bars.raw_full[u % p.slots], static_cast<uint32_t>(u / p.slots) & 1u,
-                              nullptr, 100000000ull);
+          for (int side = 0; side < 2; ++side)
+            for (int i = 0; i < p.slots[side]; ++i) {
+              const uint32_t n = turn[side] + (i < slot[side] ? 1u : 0u);  // copies into it
+              if (n > 0)
+                mbar_wait_bounded(&bars.raw_full[side][i], (n - 1) & 1u, nullptr, 100000000ull);
+            }
       }
     } else if (warp == kMmaWarp) {
       // ---------------- MMA issuer.  The whole warp walks the steps, so that what an
@@ -657,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u,
                                                          &abort_flag)) != 0;
       };
-      // S_e = Q K^T of the operand tile of use u: split keys add their rests'
+      // S_e = Q K^T of K's tile u: split keys add their rests'
       // products, turbo4 those of the rest of Q
       auto qk = [&](int e, int qtile, int u) {
         const uint32_t b = tile0 + (u % kBufs) * (kTileBytes / 16);
@@ -680,9 +718,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      // O_e (+)= P_e V; split values: the same P with the rests, columns 64 .. of V
+      // O_e (+)= P_e V of V's tile u; split values: the same P with the rests, columns 64 .. of V
       auto pv = [&](int e, int u, bool first) {
-        const uint32_t b = tile0 + (u % kBufs) * (kTileBytes / 16);
+        const uint32_t b = tile0 + (kBufs + u % kBufs) * (kTileBytes / 16);
         const uint32_t d = tm_o[e], a = tm_s[e];
         if (leader) {
 #pragma unroll
@@ -697,84 +735,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      auto free_tile = [&](int u) {
-        if (leader) mma_commit(&bars.tile_empty[u % kBufs]);
+      // tiles of a side are numbered over all segments
+      auto free_tile = [&](int side, int u) {
+        if (leader) mma_commit(&bars.tile_empty[side][u % kBufs]);
       };
-      auto have_tile = [&](int u) { return wait(&bars.tile_full[u % kBufs], u / kBufs); };
-      int u0 = 0;         // operand tiles used by earlier segments
-      int u[2] = {0, 0};  // products P V of each pipe
-      int k[2] = {0, 0};  // segments of each pipe
+      auto have_tile = [&](int side, int u) {
+        return wait(&bars.tile_full[side][u % kBufs], u / kBufs);
+      };
+      int u0 = 0;          // steps of earlier segments
+      int u[2] = {0, 0};   // products P V of each pipe
+      int k[2] = {0, 0};   // segments of each pipe
       int nq[2] = {0, 0};  // query tiles taken
       bool ok = true;
       while (ok && it.next(p, sg)) {
         const int n = sg.j_hi - sg.j_lo;
         ok = wait(&bars.qready[0], nq[0]) && (!sg.pair || wait(&bars.qready[1], nq[1])) &&
-             have_tile(u0 + k_use(0));
+             have_tile(0, u0);
         if (!ok) break;
         ++nq[0];
         if (sg.pair) ++nq[1];
         tc_fence_after();
-        qk(0, 0, u0 + k_use(0));
+        qk(0, 0, u0);
         if (sg.pair) {
-          qk(1, 1, u0 + k_use(0));
-          free_tile(u0 + k_use(0));
+          qk(1, 1, u0);
+          free_tile(0, u0);
           for (int j = 0; j < n; ++j) {
-            const int uv = u0 + v_use(j, n), uk = u0 + k_use(j + 1);
             const bool more = j + 1 < n;
-            ok = wait(&bars.pfull[0], u[0]) && have_tile(uv) &&
+            ok = wait(&bars.pfull[0], u[0]) && have_tile(1, u0 + j) &&
                  (j > 0 || k[0] == 0 || wait(&bars.ofree[0], k[0] - 1));
             if (!ok) break;
             tc_fence_after();
-            pv(0, uv, j == 0);
+            pv(0, u0 + j, j == 0);
             ++u[0];
             if (more) {
-              ok = have_tile(uk);
+              ok = have_tile(0, u0 + j + 1);
               if (!ok) break;
               tc_fence_after();
-              qk(0, 0, uk);
+              qk(0, 0, u0 + j + 1);
             }
             ok = wait(&bars.pfull[1], u[1]) &&
                  (j > 0 || k[1] == 0 || wait(&bars.ofree[1], k[1] - 1));
             if (!ok) break;
             tc_fence_after();
-            pv(1, uv, j == 0);
+            pv(1, u0 + j, j == 0);
             ++u[1];
-            free_tile(uv);
+            free_tile(1, u0 + j);
             if (more) {
-              qk(1, 1, uk);
-              free_tile(uk);
+              qk(1, 1, u0 + j + 1);
+              free_tile(0, u0 + j + 1);
             }
           }
         } else {  // the pipes take the tile's steps in turn
-          free_tile(u0 + k_use(0));
+          free_tile(0, u0);
           if (n > 1) {
-            ok = have_tile(u0 + k_use(1));
+            ok = have_tile(0, u0 + 1);
             if (!ok) break;
             tc_fence_after();
-            qk(1, 0, u0 + k_use(1));
-            free_tile(u0 + k_use(1));
+            qk(1, 0, u0 + 1);
+            free_tile(0, u0 + 1);
           }
           for (int j = 0; j < n; ++j) {
-            const int e = j & 1, uv = u0 + v_use(j, n);
-            ok = wait(&bars.pfull[e], u[e]) && have_tile(uv) &&
+            const int e = j & 1;
+            ok = wait(&bars.pfull[e], u[e]) && have_tile(1, u0 + j) &&
                  (j > 1 || k[e] == 0 || wait(&bars.ofree[e], k[e] - 1));
             if (!ok) break;
             tc_fence_after();
-            pv(e, uv, j < 2);
+            pv(e, u0 + j, j < 2);
             ++u[e];
-            free_tile(uv);
+            free_tile(1, u0 + j);
             if (j + 2 < n) {
-              const int uk = u0 + k_use(j + 2);
-              ok = have_tile(uk);
+              ok = have_tile(0, u0 + j + 2);
               if (!ok) break;
               tc_fence_after();
-              qk(e, 0, uk);
-              free_tile(uk);
+              qk(e, 0, u0 + j + 2);
+              free_tile(0, u0 + j + 2);
             }
           }
         }
         if (!ok) break;
-        u0 += 2 * n;
+        u0 += n;
         // a pipe's O is complete once every MMA issued so far is
         const bool both = sg.pair || n > 1;
         if (leader) {
@@ -792,36 +831,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) mma_commit(&bars.drain);
       mbar_wait_bounded(&bars.drain, 0, nullptr, 100000000ull);
   }
-  } else if (warp >= kDequantWarp) {
-    // ---------------- codes into operand tiles, half a unit at a time
-    constexpr int kItems = 2 * kUnits;  // halves of units in a tile
-    int use = 0;                     // tiles (and slots) so far
-    int item = warp - kDequantWarp;  // this warp's next, counted over all tiles
+  } else if (warp >= kTileWarp) {
+    // ---------------- codes into operand tiles: warp w of a side takes unit w of each
+    const int side = (warp - kTileWarp) >> 2, unit = warp & 3;
+    const int codec = p.codec[side];
+    const int slot_bytes = kUnits * unit_bytes(codec), slots = p.slots[side];
+    const uint8_t *src = ring + (side ? p.slots[0] * kUnits * unit_bytes(p.codec[0]) : 0) +
+                         unit * unit_bytes(codec);
+    int u = 0, slot = 0;  // this side's tiles so far; its next ring slot
+    uint32_t turn = 0;
     bool ok = true;
     while (ok && it.next(p, sg)) {
       const int n = sg.j_hi - sg.j_lo;
-      for (int i = 0; i < 2 * n && ok; ++i, ++use) {
-        int side, j;
-        use_at(i, n, side, j);
-        const int buf = use % kBufs, slot = use % p.slots, ub = unit_bytes(p.codec[side]);
-        if (use >= kBufs)
-          ok = mbar_wait_bounded(&bars.tile_empty[buf], static_cast<uint32_t>(use / kBufs - 1) & 1u,
-                                 &abort_flag);
-        if (ok)
-          ok = mbar_wait_bounded(&bars.raw_full[slot], static_cast<uint32_t>(use / p.slots) & 1u,
-                                 &abort_flag);
+      for (int j = 0; j < n; ++j, ++u) {
+        const int buf = u % kBufs;
+        ok = mbar_wait_bounded(&bars.raw_full[side][slot], turn & 1u, &abort_flag) &&
+             (u < kBufs || mbar_wait_bounded(&bars.tile_empty[side][buf],
+                                             static_cast<uint32_t>(u / kBufs - 1) & 1u, &abort_flag));
         ok = __all_sync(0xffffffffu, ok);
-        for (; ok && item < (use + 1) * kItems; item += kDequantWarps) {
-          const int unit = (item % kItems) >> 1;
-          const int live = sg.len - (sg.j_lo + j) * kKeys - unit * kUnitTokens;
-          unit_to_tile(side, p.codec[side], ring + slot * p.slot_bytes + unit * ub,
-                       tiles + buf * kTileBytes, unit, item & 1, live, lane);
-          fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars.raw_empty[slot]);
-            mbar_arrive(&bars.tile_full[buf]);
-          }
+        if (!ok) break;
+        const int live = sg.len - (sg.j_lo + j) * kKeys - unit * kUnitTokens;
+        unit_to_tile(side, codec, src + slot * slot_bytes,
+                     tiles + (side * kBufs + buf) * kTileBytes, unit, live, lane);
+        fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.raw_empty[side][slot]);
+          mbar_arrive(&bars.tile_full[side][buf]);
+        }
+        if (++slot == slots) {
+          slot = 0;
+          ++turn;
         }
       }
     }
@@ -835,79 +875,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tms = tm_s[e] + lane_off, tmo = tm_o[e] + lane_off;
     const bool rot_k = p.codec[0] == KVQ_TURBO4, rot_v = p.codec[1] == KVQ_TURBO4;
-    float *exchange = reinterpret_cast<float *>(sq + kTileBytes);  // [64][128]: Q tile 1's place
     auto mine = [&](const Segment &g) { return e == 0 || g.pair || g.j_hi - g.j_lo > 1; };
     auto next_mine = [&](Segment &g) {
       while (it.next(p, g))
         if (mine(g)) return true;
       return false;
     };
-    // This pipe's query tile of a segment, as fp16 in K's order of dims, a warp
-    // 32 rows of it; then tell the MMA thread.  (Pipe 1 of a single tile: pipe 0's.)
+    // This pipe's query tile of a segment, a thread its own row, as fp16 in K's order
+    // of dims into TMEM, where the products take it from (with both operands in
+    // shared memory they took twice as long); then tell the MMA thread.  (Pipe 1 of a
+    // single tile: pipe 0's.)
     auto load_q = [&](const Segment &g) {
       if (e == 1 && !g.pair) return;
-      uint8_t *dst = sq + e * kTileBytes;
-      const int64_t R0 = g.row0 + e * kTile + quad * 32;
-      int64_t tok = R0 / p.G;
-      int head = static_cast<int>(R0 - tok * p.G);
-      const uint8_t *base = p.q + g.first * p.q_row + static_cast<int64_t>(g.kvh) * p.G * p.q_head +
-                            lane * 8;
-      // dims 4 lane ..: block b, half h, w of K's order
-      auto place = [&](int i) {
-        return tile_offset(quad * 32 + i, 32 * (lane >> 3) + 8 * (lane & 3) + 4 * ((lane >> 2) & 1));
+      const int64_t R = g.row0 + e * kTile + r, tok = R / p.G;
+      const bool have = R < g.R;
+      const uint8_t *src = p.q + (g.first + (have ? tok : 0)) * p.q_row +
+                           (static_cast<int64_t>(g.kvh) * p.G + (have ? R - tok * p.G : 0)) * p.q_head;
+      auto eight = [&](int d) {  // dims d ..
+        return have ? *reinterpret_cast<const uint4 *>(src + 2 * d) : make_uint4(0u, 0u, 0u, 0u);
       };
-      constexpr int kAhead = 8;
+      if (rot_k) {
+        // H (s q) / 16 by way of this pipe's columns of O, which are free: the stages
+        // inside 32 dims, then those across; two parts, the second in tile 1's place
 #pragma unroll 1
-      for (int i0 = 0; i0 < 32; i0 += kAhead) {
-        uint2 x[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          x[i] = make_uint2(0u, 0u);
-          if (R0 + i0 + i < g.R)
-            x[i] = *reinterpret_cast<const uint2 *>(base + tok * p.q_row + head * p.q_head);
-          if (++head == p.G) {
-            head = 0;
-            ++tok;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (p.q_bf16 || rot_k) {
-            float f[4];
-            if (p.q_bf16) load4<KVQ_T_BF16>(&x[i], f);
-            else load4<KVQ_T_F16>(&x[i], f);
-            if (rot_k) {  // H (s q) / 16
-              turbo_flip_lane(f, lane);
-              fwht128_warp(f, lane);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) f[c] *= 0.0625f;
-            }
-            x[i] = make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
-            if (rot_k) {  // what the rounding leaves, in the second tile's place
-              const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].x));
-              const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].y));
-              *reinterpret_cast<uint2 *>(dst + kTileBytes + place(i0 + i)) = make_uint2(
-                  pack_half2(f[0] - a.x, f[1] - a.y), pack_half2(f[2] - b.x, f[3] - b.y));
-            }
-          }
-          *reinterpret_cast<uint2 *>(dst + place(i0 + i)) = x[i];
-        }
-      }
-      // a thread's own row into TMEM, where the products take it from (both operands
-      // of a product from shared memory take it twice as long)
-      __syncwarp();
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t == 1 && !rot_k) break;
-#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          float v[32];
+          const uint32_t signs = turbo_signs(c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 x = lds128(dst + t * kTileBytes + tile_offset(r, 32 * c + 8 * k));
-            w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+            Eight<KVQ_T_F16> x;
+            x.w[0] = eight(32 * c + 8 * k);
+            float(&f)[8] = reinterpret_cast<float(&)[8]>(v[8 * k]);
+            if (p.q_bf16) eight_values<KVQ_T_BF16>(*reinterpret_cast<Eight<KVQ_T_BF16> *>(&x), f);
+            else eight_values<KVQ_T_F16>(x, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = (signs >> (8 * k + i)) & 1u ? -f[i] : f[i];
           }
-          tmem_st16(tm_q[rot_k ? t : e] + lane_off + 16 * c, w);
+          fwht32(v);
+          tmem_st32f(tmo + c * 32, v);
+        }
+        tmem_wait_st();
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {  // dims 32 c + 4 m .., + 16: columns 16 c + 4 m .. of Q
+          float v[4][8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld4(tmo + c * 32 + 4 * m, reinterpret_cast<float(&)[4]>(v[c][0]));
+            tmem_ld4(tmo + c * 32 + 4 * m + 16, reinterpret_cast<float(&)[4]>(v[c][4]));
+          }
+          tmem_wait_ld();
+          across32(v, 0.0625f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hi[i] = pack_half2(v[c][2 * i], v[c][2 * i + 1]);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
+              lo[i] = pack_half2(v[c][2 * i] - f.x, v[c][2 * i + 1] - f.y);
+            }
+            tmem_st4(tm_q[0] + lane_off + 16 * c + 4 * m, hi);
+            tmem_st4(tm_q[1] + lane_off + 16 * c + 4 * m, lo);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = eight(32 * b + 8 * k);
+          if (p.q_bf16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t *y = reinterpret_cast<uint32_t *>(&x[k]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = pack_half2(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xffff0000u));
+            }
+          }
+          const uint32_t w[16] = {x[0].x, x[0].y, x[2].x, x[2].y, x[0].z, x[0].w, x[2].z, x[2].w,
+                                  x[1].x, x[1].y, x[3].x, x[3].y, x[1].z, x[1].w, x[3].z, x[3].w};
+          tmem_st16(tm_q[e] + lane_off + 16 * b, w);
         }
       }
       tmem_wait_st();
@@ -936,25 +984,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (!idle) {
           const int left = sg.len - (sg.j_lo + j) * kKeys;  // keys from the step's first on
-          // The row's scores stay in registers; those of places past the length are
-          // -inf.
-          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          float v[kKeys / 32][32];
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(tms + c * 32, v[c]);
-          tmem_wait_ld();
-          if (left < kKeys) {
-#pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c)
+          // 32 scores at a time, read twice (registers); places past the length -inf.
+          auto scores = [&](int c, float(&v)[32]) {
+            tmem_ld32(tms + c * 32, v);
+            tmem_wait_ld();
+            if (left < kKeys) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (c * 32 + (i & 16) + token_of(i) >= left) v[c][i] = -INFINITY;
+                if (c * 32 + (i & 16) + token_of(i) >= left) v[i] = -INFINITY;
+            }
+          };
+          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) {
+            float v[32];
+            scores(c, v);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[i], v[i + 1]);
           }
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[c][i], v[c][i + 1]);
           const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
           // A row's running maximum is raised only when it grew by more than the
           // threshold; O is rescaled for the whole warp when one of its rows is.
@@ -983,16 +1030,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l *= a;
           m = mnew;
-          // P = exp2(s * scale_log2 - m + lift) as fp16 pairs over S, and the row's sum.
+          // P = exp2(s * scale_log2 - m + lift) as fp16 pairs over S (32 of them on
+          // columns already read), and the row's sum.
           const float nm = m == -INFINITY ? 0.0f : kLift - m;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int c = 0; c < kKeys / 32; ++c) {
+            float v[32];
             uint32_t pk[16];
+            scores(c, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 tt = fma2(make_float2(v[c][2 * i], v[c][2 * i + 1]), sc2, nm2);
+              const float2 tt = fma2(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
               const float2 x = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
               sum[i & 1] = add2(sum[i & 1], x);
               pk[i] = pack_half2(x.x, x.y);
@@ -1102,28 +1152,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld8(tmo + c * 32 + 8 * g, v[c]);
           tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = v[0][i] + v[1][i], b = v[0][i] - v[1][i];
-            const float c = v[2][i] + v[3][i], d = v[2][i] - v[3][i];
-            v[0][i] = a + c;
-            v[1][i] = b + d;
-            v[2][i] = a - c;
-            v[3][i] = b - d;
-          }
+          across32(v, 0.0625f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t signs = turbo_signs(c) >> (8 * g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] *= (signs >> i) & 1u ? -0.0625f : 0.0625f;
+            for (int i = 0; i < 8; ++i) v[c][i] = (signs >> i) & 1u ? -v[c][i] : v[c][i];
             if (valid) ro.put(c * 32 + 8 * g, v[c]);
           }
         }
       }
+      if (rot_k && have_next) load_q(nsg);  // (its way leads through O)
       tc_fence_before();  // O read: the next segment's first product may overwrite it
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.ofree[e]);
-      if (rot_k && have_next) load_q(nsg);  // (its second tile's place was the exchange's)
       // weights were lifted: sums of 2^(s - (m - lift))
       const float ml = m == -INFINITY ? m : m - kLift;
       if (!whole) {
@@ -1303,8 +1345,15 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.max_len = max_len;
   p.pages_per_seq = L.pages_per_seq;
   p.n_pages = L.n_pages;
-  p.slot_bytes = kUnits * std::max(unit_bytes(L.codec_k), unit_bytes(L.codec_v));
-  p.slots = std::min(kMaxSlots, kRingBytes / p.slot_bytes);
+  // as many steps of each side as fit, and what is left to the side that it fits
+  const int kb = kUnits * unit_bytes(L.codec_k), vb = kUnits * unit_bytes(L.codec_v);
+  int n = std::min(kMaxSlots, kRingBytes / (kb + vb)), left = kRingBytes - n * (kb + vb);
+  p.slots[0] = p.slots[1] = n;
+  for (int side = 1; side >= 0; --side)
+    while (p.slots[side] < kMaxSlots && left >= (side ? vb : kb)) {
+      ++p.slots[side];
+      left -= side ? vb : kb;
+    }
   p.singles = L.codec_k == KVQ_TURBO4;
   p.scale_log2 = scale * 1.4426950408889634f;
   static std::atomic<uint64_t> optin{0};
