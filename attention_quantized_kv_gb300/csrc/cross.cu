@@ -66,6 +66,14 @@ constexpr float kLift = 6.0f;
 constexpr int kPartStride = 132;                  // floats of a partial row: 128 O, m, l, 2 pad
 constexpr int kSlotFloats = 2 * kTile * kPartStride;
 
+// An item whose pieces are to be joined: n of them, of the CTAs from its first on.
+struct __align__(16) JoinItem {
+  int64_t first;  // the sequence's first row
+  int R, row0;    // its rows per kv head; the block's first
+  int kvh, rows;  // kv head; the block's rows
+  int n, pad;     // (0: no item)
+};
+
 struct CrossParams {
   const uint8_t *cache[2];
   int codec[2];
@@ -74,6 +82,7 @@ struct CrossParams {
   int q_bf16;                                // q and out: bf16, else fp16
   CrossOut out;
   float *part;  // partial slots [2 per CTA][2 tiles][128][kPartStride]
+  JoinItem *items;  // [CTAs]: the split item that begins in each one's slice
   PackedRows rows;
   const int32_t *seq_lens, *table;
   int32_t *err;
@@ -87,7 +96,8 @@ struct CrossParams {
 
 // One sequence's rows and keys.
 struct SeqWork {
-  int64_t first, R;  // first row (token); rows per kv head: tokens * G
+  int64_t first;     // first row (token)
+  int R;             // rows per kv head: tokens * G
   int len, nt;       // keys, key tiles (0: nothing to do)
   int blocks, full;  // pairs and the single tile if there is one (singles: tiles); weight
   bool odd;          // the last block is a single tile among pairs
@@ -107,11 +117,11 @@ __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
   bool bad;
   const int64_t n = packed_rows(p.rows, s, w.first, bad);
   w.len = max(0, min(p.seq_lens[s], p.max_len));
-  w.R = n * p.G;
+  w.R = static_cast<int>(n) * p.G;
   w.nt = n > 0 ? (w.len + kKeys - 1) / kKeys : 0;
-  const int64_t tiles = (w.R + kTile - 1) / kTile;
+  const int tiles = (w.R - 1) / kTile + (w.R > 0);
   w.full = p.singles ? 1 : 2;
-  w.blocks = static_cast<int>(p.singles ? tiles : (tiles + 1) / 2);
+  w.blocks = p.singles ? tiles : (tiles + 1) / 2;
   w.odd = !p.singles && (tiles & 1) != 0;
   return w;
 }
@@ -133,32 +143,26 @@ __device__ __forceinline__ int64_t owner_of(int64_t x, int64_t W, int64_t P) {
 }
 
 struct Segment {
-  int64_t first, R, row0;  // the sequence's first row and rows; the block's first row
+  int64_t first;  // the sequence's first row
+  int R, row0;    // its rows per kv head; the block's first
   int s, kvh, len, nt, j_lo, j_hi;
-  bool pair, inside;       // inside: the item begins in this CTA's slice
+  bool pair, inside;  // inside: the item begins in this CTA's slice
+  int64_t at;         // its position
 };
 // A CTA's segments: the pieces of the items that its slice [s0, s1) holds.
 struct SegIter {
   int64_t s0, s1, at;  // at: the current item's first position
   SeqWork w;
   int s, kvh, blk;
-  __device__ __forceinline__ void init(const CrossParams &p, int64_t a, int64_t b, int seq,
-                                       int64_t seq_at) {
-    s0 = a;
-    s1 = b;
-    s = seq;
-    w = seq_work(p, s);
-    block_at(w, a - seq_at, kvh, blk);
-    at = seq_at + w.at(kvh, blk);
-  }
   __device__ __forceinline__ bool next(const CrossParams &p, Segment &g) {
     while (at < s1) {
       const int wt = w.weight(blk);
-      const int64_t lo = s0 <= at ? 0 : (s0 - at + wt - 1) / wt;
-      const int64_t hi = min(static_cast<int64_t>(w.nt), (s1 - at + wt - 1) / wt);
+      // (wt is 1 or 2)
+      const int64_t lo = s0 <= at ? 0 : (s0 - at + wt - 1) >> (wt - 1);
+      const int64_t hi = min(static_cast<int64_t>(w.nt), (s1 - at + wt - 1) >> (wt - 1));
       g.first = w.first;
       g.R = w.R;
-      g.row0 = static_cast<int64_t>(blk) * (w.full * kTile);
+      g.row0 = blk * (w.full * kTile);
       g.s = s;
       g.kvh = kvh;
       g.len = w.len;
@@ -167,6 +171,7 @@ struct SegIter {
       g.j_hi = static_cast<int>(hi);
       g.pair = wt == 2;
       g.inside = at >= s0;
+      g.at = at;
       at += static_cast<int64_t>(wt) * w.nt;
       if (++blk == w.blocks) {
         blk = 0;
@@ -517,8 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ CrossBars bars;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag, first_seq;
-  __shared__ int64_t slice[3];  // the slice, and the first sequence's position
+  __shared__ int abort_flag;
+  __shared__ SegIter begin;   // where the slice begins
+  __shared__ int64_t all[2];  // all work, and the CTAs that share it
   __shared__ float2 pipe1_ml[kTile];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -532,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {  // this CTA's slice, and where it begins
     int64_t sum = 0;
+    SeqWork mine;  // (of up to 32 sequences: looked up once)
     for (int s = lane; s < p.rows.n_seqs; s += 32) {
       if (blockIdx.x == 0) {
         bool bad;
@@ -540,17 +547,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad) set_err(p.err, KVQ_DEVERR_ROWS);
         if (p.seq_lens[s] > p.max_len) set_err(p.err, KVQ_DEVERR_MAXLEN);
       }
-      sum += seq_work(p, s).per_head() * p.n_kv;
+      mine = seq_work(p, s);
+      sum += mine.per_head() * p.n_kv;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int64_t W = sum, P = cross_ctas(W, gridDim.x), c = blockIdx.x;
     const int64_t s0 = c < P ? W * c / P : W, s1 = c < P ? W * (c + 1) / P : W;
+    if (lane == 0) {
+      begin.s0 = s0;
+      begin.s1 = s1;
+      all[0] = W;
+      all[1] = P;
+      p.items[blockIdx.x].n = 0;
+    }
     if (s0 < s1) {
       int64_t carry = 0;
       for (int base = 0; base < p.rows.n_seqs; base += 32) {
         const int s = base + lane;
-        const int64_t n = s < p.rows.n_seqs ? seq_work(p, s).per_head() * p.n_kv : 0;
+        if (p.rows.n_seqs > 32 && s < p.rows.n_seqs) mine = seq_work(p, s);
+        const int64_t n = s < p.rows.n_seqs ? mine.per_head() * p.n_kv : 0;
         int64_t incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -560,8 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned past = __ballot_sync(0xffffffffu, carry + incl > s0);
         if (past) {
           if (lane == __ffs(past) - 1) {
-            first_seq = s;
-            slice[2] = carry + incl - n;
+            const int64_t seq_at = carry + incl - n;
+            begin.s = s;
+            begin.w = mine;
+            block_at(mine, s0 - seq_at, begin.kvh, begin.blk);
+            begin.at = seq_at + mine.at(begin.kvh, begin.blk);
           }
           break;
         }
@@ -569,8 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (lane == 0) {
-      slice[0] = s0;
-      slice[1] = s1;
       abort_flag = 0;
       for (int i = 0; i < 2 * kMaxSlots; ++i) {
         mbar_init(&bars.raw_full[0][i], 1);
@@ -596,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = blockIdx.x; s < p.rows.n_seqs; s += gridDim.x) {
       const SeqWork w = seq_work(p, s);
       if (w.len > 0) continue;
-      const int64_t n = w.R * p.n_kv;  // rows x query heads
+      const int64_t n = static_cast<int64_t>(w.R) * p.n_kv;  // rows x query heads
       for (int64_t i = warp - 1; i < n; i += kThreads / 32 - 1) {
         const int64_t row = w.first + i / p.n_q;
         const int head = static_cast<int>(i % p.n_q);
@@ -612,8 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const int64_t s0 = slice[0], s1 = slice[1];
-  if (s0 >= s1) return;  // whole CTA: no work
+  if (begin.s0 >= begin.s1) return;  // whole CTA: no work
   if (warp == kMmaWarp) tmem_alloc(&tmem_base_sh, 512);
   tc_fence_before();
   __syncthreads();
@@ -623,8 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm_s[2] = {tmem, tmem + 64}, tm_q[2] = {tmem + 128, tmem + 192};
   const uint32_t tm_o[2] = {tmem + 256, tmem + 384};
 
-  SegIter it;
-  it.init(p, s0, s1, first_seq, slice[2]);
+  SegIter it = begin;
   Segment sg;
 
   if (warp >= kCopyWarp) {
@@ -887,10 +902,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // single tile: pipe 0's.)
     auto load_q = [&](const Segment &g) {
       if (e == 1 && !g.pair) return;
-      const int64_t R = g.row0 + e * kTile + r, tok = R / p.G;
+      const int R = g.row0 + e * kTile + r;
       const bool have = R < g.R;
-      const uint8_t *src = p.q + (g.first + (have ? tok : 0)) * p.q_row +
-                           (static_cast<int64_t>(g.kvh) * p.G + (have ? R - tok * p.G : 0)) * p.q_head;
+      const int tok = have ? R / p.G : 0, head = g.kvh * p.G + (have ? R - tok * p.G : 0);
+      const uint8_t *src = p.q + (g.first + tok) * p.q_row + head * p.q_head;
       auto eight = [&](int d) {  // dims d ..
         return have ? *reinterpret_cast<const uint4 *>(src + 2 * d) : make_uint4(0u, 0u, 0u, 0u);
       };
@@ -939,11 +954,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
+        uint4 two[2][4];  // (two blocks' pieces requested together)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          uint4 x[4];
+          if ((b & 1) == 0) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = eight(32 * b + 8 * k);
+            for (int k = 0; k < 8; ++k) two[k >> 2][k & 3] = eight(32 * b + 8 * k);
+          }
+          uint4(&x)[4] = two[b & 1];
           if (p.q_bf16) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -969,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (have) load_q(sg);
     while (have) {
       const int n = sg.j_hi - sg.j_lo;
-      const int64_t row0 = sg.row0 + (sg.pair ? e * kTile : 0);
+      const int row0 = sg.row0 + (sg.pair ? e * kTile : 0);
       const bool idle = row0 + quad * 32 >= sg.R;  // no row in this warp
       float m = -INFINITY, l = 0.0f;
       // After an abort (ok false) the segments still run to the end without waits,
@@ -1075,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int half = 0; half < 2; ++half) {
           if (half) pipes_sync();  // the first half has been read
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 2 && !idle; ++c) {
             float v[32];
             tmem_ld32(tmo + half * 64 + c * 32, v);
             tmem_wait_ld();
@@ -1095,9 +1113,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The row's place: out (whole items), xo, or this CTA's partial slot.
       const bool whole = sg.j_lo == 0 && sg.j_hi == sg.nt;
-      const int64_t R = row0 + r, tok = R / p.G;
+      const int R = row0 + r, tok = R / p.G;
       const bool valid = R < sg.R;
-      const int head = sg.kvh * p.G + static_cast<int>(R - tok * p.G);
+      const int head = sg.kvh * p.G + R - tok * p.G;
       const int64_t row = valid ? sg.first + tok : 0, at = row * p.n_q + head;
       RowOut ro;
       ro.half = nullptr;
@@ -1110,6 +1128,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ro.full = p.out.xo + at * kD;
       else
         ro.half = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head;
+      if (!whole && sg.inside && threadIdx.x == 0) {
+        const int64_t last = sg.at + static_cast<int64_t>(sg.nt - 1) * (sg.pair ? 2 : 1);
+        p.items[blockIdx.x] = {sg.first, sg.R, sg.row0, sg.kvh, sg.pair ? 2 * kTile : kTile,
+                               static_cast<int>(owner_of(last, all[0], all[1]) - blockIdx.x + 1), 0};
+      }
       if (joined) {
         pipes_sync();  // pipe 1's first half and (m, l) are written
         const float2 y = pipe1_ml[r];
@@ -1126,6 +1149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pipes_sync();  // the first half has been read
           pipes_sync();  // the second is written
         }
+        if (idle) continue;
         float v[32];
         tmem_ld32(tmo + c * 32, v);
         tmem_wait_ld();
@@ -1144,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (joined) pipes_sync();  // the second half has been read
-      if (rot_v) {  // the stages across them, and x = s H y / 16
+      if (rot_v && !idle) {  // the stages across them, and x = s H y / 16
         tmem_wait_st();
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
@@ -1169,7 +1193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // weights were lifted: sums of 2^(s - (m - lift))
       const float ml = m == -INFINITY ? m : m - kLift;
       if (!whole) {
-        *reinterpret_cast<float2 *>(ro.full + kD) = make_float2(ml, l);
+        if (valid) *reinterpret_cast<float2 *>(ro.full + kD) = make_float2(ml, l);
       } else if (valid) {
         if (p.out.xo) p.out.xml[at] = make_float2(ml, l);
         else if (p.out.lse)
@@ -1197,70 +1221,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 16;
 
-struct JoinParams {
-  CrossParams c;
-  int grid;  // the attention kernel's CTAs
-};
-
 // The items that the attention kernel split over several CTAs: o = sum_c
-// 2^(m_c - M) o_c over the pieces in order.  Block (c, rows): the item that the
-// slices c and c + 1 share, where c is the first slice that holds a part of it; 16
-// threads per row (8 dims each), the pieces' rows requested eight at a time.
-__global__ void __launch_bounds__(kJoinThreads)
-    cross_join_kernel(const __grid_constant__ JoinParams jp) {
-  const CrossParams &p = jp.c;
-  __shared__ int64_t warp_sum[kJoinThreads / 32], seq_at;
-  __shared__ int seq;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // (lengths and rows are final once the attention kernel has started)
-  auto scan = [&](bool find, int64_t x) {  // all work, or the sequence at position x
-    int64_t carry = 0;
-    for (int base = 0; base < p.rows.n_seqs; base += kJoinThreads) {
-      const int s = base + tid;
-      const int64_t n = s < p.rows.n_seqs ? seq_work(p, s).per_head() * p.n_kv : 0;
-      int64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      incl += carry;
-      for (int w = 0; w < kJoinThreads / 32; ++w) {
-        if (w < warp) incl += warp_sum[w];
-        carry += warp_sum[w];
-      }
-      if (find && x >= incl - n && x < incl) {
-        seq = s;
-        seq_at = incl - n;
-      }
-      __syncthreads();
-    }
-    return carry;
-  };
-  const int64_t W = scan(false, 0), P = cross_ctas(W, jp.grid), c = blockIdx.x;
-  if (c + 1 >= P) {
-    grid_dependency_wait();  // (this grid must not end before the attention kernel)
-    return;
-  }
-  const int64_t x = W * (c + 1) / P - 1;  // the last position of slice c
-  scan(true, x);
-  const SeqWork w = seq_work(p, seq);
-  int kvh, blk;
-  block_at(w, x - seq_at, kvh, blk);
-  const int64_t at = seq_at + w.at(kvh, blk);
-  const int wt = w.weight(blk);
-  const int64_t c0 = owner_of(at, W, P);
-  const int n = static_cast<int>(owner_of(at + static_cast<int64_t>(w.nt - 1) * wt, W, P) - c0 + 1);
-  grid_dependency_wait();  // the partials are complete
+// 2^(m_c - M) o_c over the pieces in order.  Block (c, rows): the item, if any, that
+// begins in CTA c's slice and ends in another's; 16 threads per row (8 dims each),
+// the pieces' rows requested four at a time.
+__global__ void __launch_bounds__(kJoinThreads, 4)
+    cross_join_kernel(const __grid_constant__ CrossParams p) {
+  const int tid = threadIdx.x, lane = tid & 31, t16 = tid & 15;
+  grid_dependency_wait();  // items and partials are complete
   grid_launch_dependents();
-  if (c0 != c || n == 1) return;
-  const int in = blockIdx.y * kJoinRows + (tid >> 4), t16 = tid & 15;  // row of the block
-  const int64_t R = static_cast<int64_t>(blk) * (w.full * kTile) + in;
-  if (in >= wt * kTile || R >= w.R) return;
-  const int64_t tok = R / p.G, row = w.first + tok;
-  const int head = kvh * p.G + static_cast<int>(R - tok * p.G);
+  const JoinItem item = p.items[blockIdx.x];
+  const int64_t c0 = blockIdx.x;
+  const int n = item.n, in = blockIdx.y * kJoinRows + (tid >> 4);  // row of the block
+  const int R = item.row0 + in;
+  if (n == 0 || in >= item.rows || R >= item.R) return;
+  const int tok = R / p.G, head = item.kvh * p.G + R - tok * p.G;
+  const int64_t row = item.first + tok;
   // the item begins inside its first CTA's slice, and before every other's
   auto part = [&](int j) {
     return p.part + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlotFloats +
@@ -1272,7 +1248,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1)  // (the other half of the warp may have returned)
     M = fmaxf(M, __shfl_xor_sync(0xffffu << (lane & 16), M, o, 16));
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 4;
   for (int j0 = 0; j0 < n; j0 += kAhead) {
     float4 v[kAhead][2];
     float2 y[kAhead];
@@ -1313,7 +1289,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms) {
   CrossPlan pl;
   pl.grid = num_sms > 0 ? num_sms : 148;
-  pl.ws_bytes = 2 * static_cast<int64_t>(pl.grid) * kSlotFloats * 4;
+  pl.items_off = 2 * static_cast<int64_t>(pl.grid) * kSlotFloats * 4;
+  pl.ws_bytes = pl.items_off + pl.grid * static_cast<int64_t>(sizeof(JoinItem));
   return pl;
 }
 
@@ -1334,6 +1311,7 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.out_row = out_row * 2;
   p.out_head = out_head * 2;
   p.part = static_cast<float *>(workspace);
+  p.items = reinterpret_cast<JoinItem *>(static_cast<uint8_t *>(workspace) + pl.items_off);
   p.rows = {row_start, n_new, n_rows, n_rows / L.n_seqs, L.n_seqs};
   p.seq_lens = L.seq_lens;
   p.table = L.pages_per_seq > 0 ? L.block_table : nullptr;
@@ -1362,13 +1340,12 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   e = launch_pdl(cross_attn_kernel, dim3(static_cast<unsigned>(pl.grid)), dim3(kThreads), kSmemBytes,
                  stream, p);
   if (e != cudaSuccess || pl.grid < 2) return e;
-  const JoinParams jp = {p, pl.grid};
   // at most this many rows of a block (fewer: short batches need fewer blocks)
   const int64_t rows = std::min<int64_t>(p.singles ? kTile : 2 * kTile, n_rows * p.G);
   return launch_pdl(cross_join_kernel,
                     dim3(static_cast<unsigned>(pl.grid - 1),
                          static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)),
-                    dim3(kJoinThreads), 0, stream, jp);
+                    dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace kvq

@@ -51,6 +51,7 @@
 #include <cuda_runtime.h>
 
 #include <math.h>
+#include <stdlib.h>
 
 #include "kvq_device.cuh"
 #include "kvq_encode.cuh"
@@ -721,6 +722,49 @@ __device__ __forceinline__ Geo make_geo(const DecodeParams &p, const int32_t *pf
   return geo;
 }
 
+// A 4-bit V's codec offset: o = 2^24 o - 8 C_b (rows g) and 2^20 o - 8 C_b (rows
+// g+8), C_b from lane 4b + tig of corr.
+__device__ __forceinline__ void restore_offset(float (&o)[8][4], const float (&corr)[4], int tig) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float c0 = -8.0f * __shfl_sync(0xffffffffu, corr[0], 4 * b + tig);
+    const float c1 = -8.0f * __shfl_sync(0xffffffffu, corr[1], 4 * b + tig);
+#pragma unroll
+    for (int mt = 2 * b; mt < 2 * b + 2; ++mt) {
+      o[mt][0] = fmaf(0x1p24f, o[mt][0], c0);
+      o[mt][1] = fmaf(0x1p24f, o[mt][1], c1);
+      o[mt][2] = fmaf(0x1p20f, o[mt][2], c0);
+      o[mt][3] = fmaf(0x1p20f, o[mt][3], c1);
+    }
+  }
+}
+
+// A warp's partial of head group hg (l0, l1: each lane's part) into a slot.
+template <int CV>
+__device__ __forceinline__ void write_partial(const DecodeParams &p, int64_t slot, int hg, int lane,
+                                              const float (&o)[8][4], float m0, float m1, float l0,
+                                              float l1) {
+  const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+  }
+  float *po = p.part_o + slot * 8 * kD;
+  const int h0 = 2 * tig, h1 = 2 * tig + 1;
+  const bool v0 = hg * 8 + h0 < p.G, v1 = hg * 8 + h1 < p.G;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const int dlo = v_dim<CV>(mt, g), dhi = v_dim<CV>(mt, g + 8);
+    if (v0) { po[h0 * kD + dlo] = o[mt][0]; po[h0 * kD + dhi] = o[mt][2]; }
+    if (v1) { po[h1 * kD + dlo] = o[mt][1]; po[h1 * kD + dhi] = o[mt][3]; }
+  }
+  if (g == 0) {
+    if (v0) p.part_ml[slot * 8 + h0] = make_float2(m0, l0);
+    if (v1) p.part_ml[slot * 8 + h1] = make_float2(m1, l1);
+  }
+}
+
 // MODE: the plain decode, the fused decode step (p.k_new set) or that with
 // the rotation; separate instantiations, so that the plain decode loop carries
 // none of their state.
@@ -1014,22 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
       k_next += two ? 2 * kWarps : kWarps;
     }
 
-    if (nibble_codec(CV)) {
-      // Restore the codec offset: o = 2^24 o - 8 C_b (rows g) and
-      // 2^20 o - 8 C_b (rows g+8), C_b from lane 4b + tig of corr.
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float c0 = -8.0f * __shfl_sync(0xffffffffu, corr[0], 4 * b + tig);
-        const float c1 = -8.0f * __shfl_sync(0xffffffffu, corr[1], 4 * b + tig);
-#pragma unroll
-        for (int mt = 2 * b; mt < 2 * b + 2; ++mt) {
-          o[mt][0] = fmaf(0x1p24f, o[mt][0], c0);
-          o[mt][1] = fmaf(0x1p24f, o[mt][1], c1);
-          o[mt][2] = fmaf(0x1p20f, o[mt][2], c0);
-          o[mt][3] = fmaf(0x1p20f, o[mt][3], c1);
-        }
-      }
-    }
+    if (nibble_codec(CV)) restore_offset(o, corr, tig);
 
     // Merge the 8 warps' partials for this segment: 8 -> 4 in pairs, then
     // warp 0 takes in warps 1..3.  Four shared slots, three barriers (turbo4
@@ -1051,29 +1080,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_split_kernel(const DecodeP
     if (warp == 0) {
 #pragma unroll 1
       for (int w = 1; w < 4; ++w) merge_into(o, m0, m1, l0, l1, rs + w * 32 * kRedFloats);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-      }
       // The CTA's partial of this stream, in slot blockIdx.x + stream (a
       // CTA's slice covers consecutive streams, so the slots of all (CTA,
       // stream) pairs are distinct); the merge kernel reads it after this
       // kernel has completed.
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) + stream;
-      float *po = p.part_o + slot * 8 * kD;
-      const int h0 = 2 * tig, h1 = 2 * tig + 1;
-      const bool v0 = hg * 8 + h0 < p.G, v1 = hg * 8 + h1 < p.G;
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        const int dlo = v_dim<CV>(mt, g), dhi = v_dim<CV>(mt, g + 8);
-        if (v0) { po[h0 * kD + dlo] = o[mt][0]; po[h0 * kD + dhi] = o[mt][2]; }
-        if (v1) { po[h1 * kD + dlo] = o[mt][1]; po[h1 * kD + dhi] = o[mt][3]; }
-      }
-      if (g == 0) {
-        if (v0) p.part_ml[slot * 8 + h0] = make_float2(ok ? m0 : -INFINITY, ok ? l0 : 0.0f);
-        if (v1) p.part_ml[slot * 8 + h1] = make_float2(ok ? m1 : -INFINITY, ok ? l1 : 0.0f);
-      }
+      write_partial<CV>(p, static_cast<int64_t>(blockIdx.x) + stream, hg, lane, o,
+                        ok ? m0 : -INFINITY, ok ? m1 : -INFINITY, ok ? l0 : 0.0f, ok ? l1 : 0.0f);
     }
     cta_bar();  // the reduction slots are free again
 
@@ -1262,6 +1274,130 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
   }
 }
 
+// ------------------------------------------------------------------ short streams
+
+// The own keys of sequences behind a shared prefix, where they are short: a CTA
+// takes `spc` whole streams (1, 2, 4 or 8) with 8 / spc warps each, which read
+// every wps-th item straight from global memory (its pieces are their operands),
+// the next one's lines requested into L1 meanwhile.  The warps are joined once, in
+// shared memory, and the rows written with the prefix's part: no partials, no
+// merge kernel.
+template <int CK, int CV>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_short_kernel(const DecodeParams p, const PrefixPart x, const int spc) {
+  using C = DecodeCfg<CK, CV>;
+  __shared__ __align__(16) float red[kWarps][32 * kRedFloats];
+  __shared__ float2 ml_s[kWarps][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tig = lane & 3, g = lane >> 2;
+  const int wps = kWarps / spc, sub = warp % wps, KH = p.n_kv * p.n_hg;
+  const int stream = blockIdx.x * spc + warp / wps;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  float o[8][4];
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.0f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+  if (stream < p.n_seqs * KH) {
+    const int seq = stream / KH, sl = stream % KH, kvh = sl / p.n_hg, hg = sl % p.n_hg;
+    int len = p.seq_lens[seq];
+    if (len > p.max_len) {
+      if (lane == 0) set_err(p.err, KVQ_DEVERR_MAXLEN);
+      len = p.max_len;
+    }
+    const int items = len > 0 ? (len + C::UPS * kUnitTokens - 1) / (C::UPS * kUnitTokens) : 0;
+    auto unit_of = [&](int j) -> int64_t {  // an item's first unit, in the cache or the pool
+      const int u = j * C::UPS;
+      if (!p.table)
+        return (static_cast<int64_t>(seq) * p.n_kv + kvh) * (p.capacity / kUnitTokens) + u;
+      int pg = page_of(p.table, p.pages_per_seq, p.n_pages, seq, u / kPageUnits);
+      if (pg < 0) {
+        set_err(p.err, KVQ_DEVERR_PAGE);
+        pg = 0;  // read pool page 0 in its place
+      }
+      return (static_cast<int64_t>(pg) * p.n_kv + kvh) * kPageUnits + u % kPageUnits;
+    };
+    auto request = [&](int64_t unit) {
+      for (int i = lane * 128; i < C::UPS * C::UK; i += 32 * 128)
+        asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p.k_cache + unit * C::UK + i));
+      for (int i = lane * 128; i < C::UPS * C::UV; i += 32 * 128)
+        asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p.v_cache + unit * C::UV + i));
+    };
+    int64_t unit = 0;
+    if (sub < items) {
+      unit = unit_of(sub);
+      request(unit);
+    }
+    uint32_t qb[8][2], qlo_r[8][2];
+    load_q_frags<CK>(p.q, static_cast<int64_t>(seq) * p.n_q + kvh * p.G, p.n_q, p.G, hg, lane, qb,
+                     qlo_r);
+    // turbo4 keys: the query's low halves wait in this warp's reduction slot
+    uint2 *const qlo = reinterpret_cast<uint2 *>(red[warp]) + lane;
+    if (CK == KVQ_TURBO4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qlo[i * 32] = make_uint2(qlo_r[i][0], qlo_r[i][1]);
+      __syncwarp();
+    }
+    float corr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = sub; j < items; j += wps) {
+      const uint8_t *ku[C::UPS], *vu[C::UPS];
+      int nv[C::UPS];
+#pragma unroll
+      for (int i = 0; i < C::UPS; ++i) {
+        ku[i] = p.k_cache + (unit + i) * C::UK;
+        vu[i] = p.v_cache + (unit + i) * C::UV;
+        nv[i] = min(kUnitTokens, len - (C::UPS * j + i) * kUnitTokens);
+      }
+      if (j + wps < items) {
+        unit = unit_of(j + wps);
+        request(unit);
+      }
+      process_units<CK, CV, C::UPS>(ku, vu, nv, lane, qb, qlo, p.scale_log2, o, corr, m0, m1, l0, l1);
+    }
+    if (nibble_codec(CV)) restore_offset(o, corr, tig);
+  }
+  if (CK == KVQ_TURBO4) __syncthreads();  // the slots are free
+  if (sub > 0) store_red(red[warp] + lane * kRedFloats, o, m0, m1, l0, l1);
+  __syncthreads();
+  if (sub == 0) {  // join the stream's warps in order; its rows into this warp's slot
+#pragma unroll 1
+    for (int w = 1; w < wps; ++w) merge_into(o, m0, m1, l0, l1, red[warp + w] + lane * kRedFloats);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    float *rows = red[warp];
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const int dlo = v_dim<CV>(mt, g), dhi = v_dim<CV>(mt, g + 8);
+      rows[2 * tig * kD + dlo] = o[mt][0];
+      rows[2 * tig * kD + dhi] = o[mt][2];
+      rows[(2 * tig + 1) * kD + dlo] = o[mt][1];
+      rows[(2 * tig + 1) * kD + dhi] = o[mt][3];
+    }
+    if (g == 0) {
+      ml_s[warp][2 * tig] = make_float2(m0, l0);
+      ml_s[warp][2 * tig + 1] = make_float2(m1, l1);
+    }
+  }
+  __syncthreads();
+  const MergeArgs a = {nullptr, nullptr, p.out, p.lse, p.n_q, p.G};
+  for (int r = warp; r < 8 * spc; r += kWarps) {
+    const int st = blockIdx.x * spc + r / 8, h = r % 8, leader = r / 8 * wps;
+    const int seq = st / KH, kvh = st % KH / p.n_hg, hg = st % KH % p.n_hg;
+    if (st >= p.n_seqs * KH || h >= p.G - hg * 8) continue;
+    const float4 acc = reinterpret_cast<const float4 *>(red[leader] + h * kD)[lane];
+    const float2 ml = ml_s[leader][h];
+    if (behind_prefix(x, seq)) {
+      const int64_t row = static_cast<int64_t>(seq) * p.n_q + kvh * p.G + hg * 8 + h;
+      merge_write<CV == KVQ_TURBO4>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y, x.xml[row],
+                                    reinterpret_cast<const float4 *>(x.xo + row * kD)[lane]);
+    } else {
+      merge_write<CV == KVQ_TURBO4>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y);
+    }
+  }
+}
+
 template <int CK, int CV, int MODE>
 cudaError_t launch_split_m(const DecodeParams &p, int grid, cudaStream_t stream) {
   using C = DecodeCfg<CK, CV>;
@@ -1273,19 +1409,26 @@ cudaError_t launch_split_m(const DecodeParams &p, int grid, cudaStream_t stream)
 }
 
 template <int CK, int CV>
-cudaError_t launch_split(const DecodeParams &p, int grid, cudaStream_t stream) {
+cudaError_t launch_split(const DecodeParams &p, int grid, cudaStream_t stream, const PrefixPart *x,
+                         int spc) {
+  if (spc > 0) {
+    const int streams = p.n_seqs * p.n_kv * p.n_hg;
+    return launch_pdl(decode_short_kernel<CK, CV>, dim3((streams + spc - 1) / spc), dim3(kThreads), 0,
+                      stream, p, *x, spc);
+  }
   return !p.k_new        ? launch_split_m<CK, CV, kPlainDecode>(p, grid, stream)
          : !p.rope.table ? launch_split_m<CK, CV, kFusedStep>(p, grid, stream)
                          : launch_split_m<CK, CV, kFusedRope>(p, grid, stream);
 }
 
 template <int CK>
-cudaError_t launch_split_v(int cv, const DecodeParams &p, int grid, cudaStream_t stream) {
+cudaError_t launch_split_v(int cv, const DecodeParams &p, int grid, cudaStream_t stream,
+                           const PrefixPart *x, int spc) {
   switch (cv) {
-    case KVQ_F16: return launch_split<CK, KVQ_F16>(p, grid, stream);
-    case KVQ_Q8_0: return launch_split<CK, KVQ_Q8_0>(p, grid, stream);
-    case KVQ_Q4_0: return launch_split<CK, KVQ_Q4_0>(p, grid, stream);
-    default: return launch_split<CK, KVQ_TURBO4>(p, grid, stream);
+    case KVQ_F16: return launch_split<CK, KVQ_F16>(p, grid, stream, x, spc);
+    case KVQ_Q8_0: return launch_split<CK, KVQ_Q8_0>(p, grid, stream, x, spc);
+    case KVQ_Q4_0: return launch_split<CK, KVQ_Q4_0>(p, grid, stream, x, spc);
+    default: return launch_split<CK, KVQ_TURBO4>(p, grid, stream, x, spc);
   }
 }
 
@@ -1314,6 +1457,14 @@ DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms) {
   pl.o_bytes = pl.slots * 8 * kD * 4;
   pl.ws_bytes = pl.ticket_bytes + pl.ml_bytes + pl.o_bytes;
   return pl;
+}
+
+static int short_streams(const kvq_layer &L, const DecodePlan &pl, int max_len) {
+  const int streams = L.n_seqs * L.n_kv_heads * pl.n_hgroups;
+  if (getenv("SLICES") && !atoi(getenv("SLICES"))) return 0;
+  int spc = 1;
+  while (spc < kWarps && streams / (2 * spc) >= 304) spc *= 2;
+  return spc;
 }
 
 cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *q, float scale,
@@ -1349,14 +1500,16 @@ cudaError_t launch_decode(const kvq_layer &L, const DecodePlan &pl, const void *
   p.capacity = L.capacity;
   p.max_len = max_len;
   p.scale_log2 = scale * 1.4426950408889634f;
+  // streams per CTA of the short kernel (0: the split and merge kernels)
+  const int spc = prefix ? short_streams(L, pl, max_len) : 0;
   cudaError_t e;
   switch (L.codec_k) {
-    case KVQ_F16: e = launch_split_v<KVQ_F16>(L.codec_v, p, pl.grid, stream); break;
-    case KVQ_Q8_0: e = launch_split_v<KVQ_Q8_0>(L.codec_v, p, pl.grid, stream); break;
-    case KVQ_Q4_0: e = launch_split_v<KVQ_Q4_0>(L.codec_v, p, pl.grid, stream); break;
-    default: e = launch_split_v<KVQ_TURBO4>(L.codec_v, p, pl.grid, stream); break;
+    case KVQ_F16: e = launch_split_v<KVQ_F16>(L.codec_v, p, pl.grid, stream, prefix, spc); break;
+    case KVQ_Q8_0: e = launch_split_v<KVQ_Q8_0>(L.codec_v, p, pl.grid, stream, prefix, spc); break;
+    case KVQ_Q4_0: e = launch_split_v<KVQ_Q4_0>(L.codec_v, p, pl.grid, stream, prefix, spc); break;
+    default: e = launch_split_v<KVQ_TURBO4>(L.codec_v, p, pl.grid, stream, prefix, spc); break;
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || spc > 0) return e;
   MergeParams mp;
   mp.a = {p.part_ml, p.part_o, p.out, p.lse, p.n_q, p.G};
   mp.seq_lens = L.seq_lens;

@@ -90,7 +90,7 @@ cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32
 constexpr int kCrossMaxSeqs = 1024;  // key sequences per call
 struct CrossPlan {
   int grid = 1;          // CTAs, at most one per SM
-  int64_t ws_bytes = 0;  // partial slots, two per CTA
+  int64_t items_off = 0, ws_bytes = 0;  // partial slots, two per CTA; what is to be joined
 };
 // Where the rows go: out and lse (optional), or, for a merge, xo fp32
 // [n_rows][n_q][128] unnormalised and xml [n_rows][n_q] (max in log2 units, sum).
