@@ -8,31 +8,37 @@
 // token R / G, head R % G) in tiles of 128, and two tiles (a pair) share every
 // key tile that is read; a last odd tile stands alone.
 //
-// Work.  An item is (sequence, kv head, pair or single tile): a run of key-tile
-// steps, one per 128 keys.  All items' steps are laid end to end, a pair's
-// counting twice, and the CTAs (one per SM) take equal contiguous slices: whole
-// items, and pieces of at most two more.  The rows of a piece go to a partial
-// slot (unnormalised O, max, sum), and a second kernel joins an item's pieces by
-// log-sum-exp in a fixed order.  Lengths and row counts are read on the device.
+// Work.  An item is (sequence, kv head, pair or single tile): a run of steps, one
+// per 64 keys.  All items' steps are laid end to end, a pair's counting twice and
+// every item's start a few more, and the CTAs (one per SM) take equal contiguous
+// slices: whole items, and pieces of at most two more.  The rows of a piece go to a
+// partial slot (unnormalised O, max, sum), and a second kernel joins an item's pieces
+// by log-sum-exp in a fixed order.  Lengths and row counts are read on the device.
 //
-// Inside a CTA (18 warps at work) nothing is written to HBM but the results: codes are
+// Inside a CTA (19 warps at work) nothing is written to HBM but the results: codes are
 // copied in as they lie in the cache, turned into tensor-core operand tiles in
 // shared memory and used there.
-//  * Warp 16 copies the codes of 64 keys of one side at a time into a ring
+//  * Warp 16 copies the codes of 64 keys of one side at a time into that side's ring
 //    (1-D bulk copies); K and V tiles alternate.
-//  * Warps 8-11 (K) and 12-15 (V) turn them into fp16 operand tiles (three 32 KB
-//    buffers), a 16-token unit each.  The cache's order is kept where the operands leave the
-//    choice, so that 16 bytes of codes become whole 8- or 16-byte pieces of a tile
-//    without an exchange between lanes: a key's place in its tile is 4 tig + 2 rh
-//    + par (include/kvq.h), the same for K's rows and V's columns, and K's dims
-//    stand in the order 32 b + 8 w + 4 h + i, as Q's do.  turbo4 stays in its
+//  * Warps 8-11 (K) and 12-15 (V) turn them into fp16 operand tiles (two 32 KB
+//    buffers a side), a 16-token unit each.  The cache's order is kept where the
+//    operands leave the choice, so that 16 bytes of codes become whole 8- or 16-byte
+//    pieces of a tile without an exchange between lanes: a key's place in its tile is
+//    4 tig + 2 rh + par (include/kvq.h), the same for K's rows and V's columns, and
+//    K's dims stand in the order 32 b + 8 w + 4 h + i, as Q's do.  turbo4 stays in its
 //    rotated space: Q is rotated, O rotated back.
-//  * One thread of warp 17 issues tcgen05.mma: S = Q K^T into TMEM, O += P V with
-//    P read from TMEM.
-//  * Warps 0-3 and 4-7 are two softmax pipes, one query row per thread.  In a
-//    pair they hold the two tiles; with a single tile they take its even and odd
-//    key tiles and are joined through shared memory at the end, so that one
-//    pipe's softmax overlaps the other's products either way.
+//  * Warps 17 and 18 issue tcgen05.mma for a pipe each: S = Q K^T into TMEM, O += P V
+//    with P read from TMEM.
+//  * Warps 0-3 and 4-7 are two softmax pipes, one query row per thread, 32 keys at a
+//    time in two score buffers.  In a pair they hold the two tiles; with a single tile
+//    they take the first and second half of its every key tile and are joined through
+//    shared memory at the end.
+//
+// Bound: the tensor cores, from two rows tiles per byte on: a pair's 64 keys cost
+// 2050 cycles of products over split sides (1290 over f16), and took 4600 by one
+// issuing warp, 3450 by one for each pipe and 3000 with the waits and the issue as
+// they are now.  2048 rows x 32 heads over 32768 states (q8_0): 1.27 ms, the tensor pipe
+// busy for 69 % of it.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,12 +55,13 @@ namespace {
 
 constexpr int kTile = 128;                        // query rows of a tile
 constexpr int kKeys = 64;                         // keys of a step
+constexpr int kHalf = kKeys / 2;                  // keys of a score buffer
 constexpr int kUnits = kKeys / kUnitTokens;       // units of a step, and of a ring slot
 constexpr int kBufs = 2;                          // operand tiles of each side
 constexpr int kMaxSlots = 8;                      // of one side
 constexpr int kThreads = 640;
-// warps 0-3, 4-7: softmax pipes; 8-11, 12-15: tiles of K, of V; 16: copies; 17: MMA;
-// two idle (registers go to a CTA in groups of four warps)
+// warps 0-3, 4-7: softmax pipes; 8-11, 12-15: tiles of K, of V; 16: copies; 17, 18:
+// products of each pipe; one idle (registers go to a CTA in groups of four warps)
 constexpr int kTileWarp = 8, kCopyWarp = 16, kMmaWarp = 17;
 constexpr int kRingBytes = 65536;                 // K's ring, then V's: two steps of f16 each
 constexpr int kExchangeBytes = 64 * kTile * 4;   // half of pipe 1's O
@@ -63,8 +70,14 @@ constexpr float kRaise = 8.0f;                    // log2 units, as in the prefi
 // Weights are held as 2^(s - m + 6): at most 2^14 in fp16, and 2^6 further from
 // its subnormals than 2^(s - m).
 constexpr float kLift = 6.0f;
-constexpr int kPartStride = 132;                  // floats of a partial row: 128 O, m, l, 2 pad
-constexpr int kSlotFloats = 2 * kTile * kPartStride;
+// A partial tile: O as [32 groups of 4 dims][128 rows], so that a warp's rows are
+// written and read as whole lines (row by row the lines' parts took 8000 cycles), then
+// (m, l) of every row.
+constexpr int kPartFloats = kTile * kD + 2 * kTile;
+constexpr int kSlotFloats = 2 * kPartFloats;
+// What an item costs besides its steps (queries, results, the pipeline's fill), in
+// steps of a single tile.
+constexpr int kItemCost = 8;
 
 // An item whose pieces are to be joined: n of them, of the CTAs from its first on.
 struct __align__(16) JoinItem {
@@ -81,7 +94,7 @@ struct CrossParams {
   int64_t q_row, q_head, out_row, out_head;  // strides in bytes
   int q_bf16;                                // q and out: bf16, else fp16
   CrossOut out;
-  float *part;  // partial slots [2 per CTA][2 tiles][128][kPartStride]
+  float *part;  // partial slots [2 per CTA][2 tiles][kPartFloats]
   JoinItem *items;  // [CTAs]: the split item that begins in each one's slice
   PackedRows rows;
   const int32_t *seq_lens, *table;
@@ -94,6 +107,12 @@ struct CrossParams {
 
 // ------------------------------------------------------------------ work
 
+// a / b of numbers that are not negative, mostly small.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                              : a / b;
+}
+
 // One sequence's rows and keys.
 struct SeqWork {
   int64_t first;     // first row (token)
@@ -105,11 +124,12 @@ struct SeqWork {
     return odd && blk == blocks - 1 ? 1 : full;
   }
   __device__ __forceinline__ int64_t per_head() const {
-    return static_cast<int64_t>(nt) * (full * static_cast<int64_t>(blocks) - (odd ? 1 : 0));
+    return nt == 0 ? 0 : static_cast<int64_t>(nt) * (full * blocks - (odd ? 1 : 0)) +
+                             static_cast<int64_t>(blocks) * kItemCost;
   }
   // position of block blk of kv head kvh, from the sequence's
   __device__ __forceinline__ int64_t at(int kvh, int blk) const {
-    return kvh * per_head() + static_cast<int64_t>(blk) * full * nt;
+    return kvh * per_head() + static_cast<int64_t>(blk) * (full * nt + kItemCost);
   }
 };
 __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
@@ -128,8 +148,8 @@ __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
 // The kv head and block at offset `off` of a sequence's work.
 __device__ __forceinline__ void block_at(const SeqWork &w, int64_t off, int &kvh, int &blk) {
   const int64_t head = w.per_head();
-  kvh = static_cast<int>(off / head);
-  blk = static_cast<int>(min((off % head) / (static_cast<int64_t>(w.full) * w.nt),
+  kvh = static_cast<int>(quotient(off, head));
+  blk = static_cast<int>(min(quotient(off - kvh * head, w.full * w.nt + kItemCost),
                              static_cast<int64_t>(w.blocks - 1)));
 }
 // CTAs that get a slice: each at least as long as a step, so that every CTA
@@ -139,15 +159,15 @@ __device__ __forceinline__ int64_t cross_ctas(int64_t W, int grid) {
 }
 // The CTA whose slice [W c / P, W (c + 1) / P) holds position x.
 __device__ __forceinline__ int64_t owner_of(int64_t x, int64_t W, int64_t P) {
-  return ((x + 1) * P - 1) / W;
+  return quotient((x + 1) * P - 1, W);
 }
 
 struct Segment {
   int64_t first;  // the sequence's first row
   int R, row0;    // its rows per kv head; the block's first
   int s, kvh, len, nt, j_lo, j_hi;
-  bool pair, inside;  // inside: the item begins in this CTA's slice
-  int64_t at;         // its position
+  bool pair, inside;  // inside: the item's first step is in this CTA's slice
+  int64_t at;         // and its position
 };
 // A CTA's segments: the pieces of the items that its slice [s0, s1) holds.
 struct SegIter {
@@ -157,9 +177,10 @@ struct SegIter {
   __device__ __forceinline__ bool next(const CrossParams &p, Segment &g) {
     while (at < s1) {
       const int wt = w.weight(blk);
-      // (wt is 1 or 2)
-      const int64_t lo = s0 <= at ? 0 : (s0 - at + wt - 1) >> (wt - 1);
-      const int64_t hi = min(static_cast<int64_t>(w.nt), (s1 - at + wt - 1) >> (wt - 1));
+      // its steps follow its cost (wt is 1 or 2)
+      const int64_t from = at + kItemCost;
+      const int64_t lo = s0 <= from ? 0 : min(static_cast<int64_t>(w.nt), (s0 - from + wt - 1) >> (wt - 1));
+      const int64_t hi = s1 <= from ? 0 : min(static_cast<int64_t>(w.nt), (s1 - from + wt - 1) >> (wt - 1));
       g.first = w.first;
       g.R = w.R;
       g.row0 = blk * (w.full * kTile);
@@ -170,9 +191,9 @@ struct SegIter {
       g.j_lo = static_cast<int>(lo);
       g.j_hi = static_cast<int>(hi);
       g.pair = wt == 2;
-      g.inside = at >= s0;
-      g.at = at;
-      at += static_cast<int64_t>(wt) * w.nt;
+      g.inside = from >= s0;
+      g.at = from;
+      at = from + static_cast<int64_t>(wt) * w.nt;
       if (++blk == w.blocks) {
         blk = 0;
         if (++kvh == p.n_kv) {
@@ -470,13 +491,15 @@ __device__ __forceinline__ void across32(float (&v)[4][8], float f) {
 struct RowOut {
   uint8_t *half;
   float *full;
+  int step;  // floats between groups of 4 dims in full
   float inv;
   int bf16;
   // 8 values at dims d ..
   __device__ __forceinline__ void put(int d, const float (&x)[8]) const {
     if (full) {
-      reinterpret_cast<float4 *>(full + d)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4 *>(full + d)[1] = make_float4(x[4], x[5], x[6], x[7]);
+      float *y = full + (d >> 2) * step;
+      *reinterpret_cast<float4 *>(y) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4 *>(y + step) = make_float4(x[4], x[5], x[6], x[7]);
       return;
     }
     float y[8];
@@ -490,7 +513,8 @@ struct RowOut {
 struct __align__(8) CrossBars {
   uint64_t raw_full[2][kMaxSlots], raw_empty[2][kMaxSlots];
   uint64_t tile_full[2][kBufs], tile_empty[2][kBufs];
-  uint64_t sfull[2], pfull[2], odone[2], segdone[2], qready[2], ofree[2], drain;
+  uint64_t sfull[2][2], pfull[2][2];  // by pipe and score buffer
+  uint64_t odone[2], segdone[2], qready[2], ofree[2], drain[2];
 };
 
 // ------------------------------------------------------------------ attention
@@ -503,12 +527,22 @@ __device__ __forceinline__ bool elect_one() {
 }
 // D += A B with A in TMEM, B's descriptor as its low word and the constant HI.
 template <uint32_t HI>
-__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                          uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts_lo(bool leader, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " mov.b64 b, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(bool leader, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
 
@@ -523,16 +557,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ CrossBars bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  __shared__ SegIter begin;   // where the slice begins
-  __shared__ int64_t all[2];  // all work, and the CTAs that share it
+  __shared__ SegIter begin;      // the slice, behind its first segment
+  __shared__ Segment first_seg;
+  __shared__ int have_first;
+  __shared__ int64_t all[2];     // all work, and the CTAs that share it
   __shared__ float2 pipe1_ml[kTile];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // operand tiles of K, of V, the exchange, codes
   uint8_t *tiles = smem, *ring = smem + 2 * kBufs * kTileBytes + kExchangeBytes;
   float *exchange = reinterpret_cast<float *>(smem + 2 * kBufs * kTileBytes);  // [64][128]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);  // (uniform)
+  const int lane = threadIdx.x & 31;
 
+  // What needs no other kernel's results
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_base_sh, 512);
+  } else if (warp == kCopyWarp) {
+    if (lane == 0) {
+      abort_flag = 0;
+      for (int i = 0; i < 2 * kMaxSlots; ++i) {
+        mbar_init(&bars.raw_full[0][i], 1);
+        mbar_init(&bars.raw_empty[0][i], kUnits);  // one arrival per unit
+      }
+      for (int i = 0; i < 2 * kBufs; ++i) {
+        mbar_init(&bars.tile_full[0][i], kUnits);
+        mbar_init(&bars.tile_empty[0][i], 2);  // both pipes' products
+      }
+      for (int i = 0; i < 2; ++i) {
+        for (int b = 0; b < 2; ++b) {
+          mbar_init(&bars.sfull[i][b], 1);
+          mbar_init(&bars.pfull[i][b], 4);  // one arrival per softmax warp
+        }
+        mbar_init(&bars.odone[i], 1);
+        mbar_init(&bars.segdone[i], 1);
+        mbar_init(&bars.qready[i], 4);
+        mbar_init(&bars.ofree[i], 4);
+        mbar_init(&bars.drain[i], 1);
+      }
+      fence_mbar_init();
+    }
+  }
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -553,14 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int64_t W = sum, P = cross_ctas(W, gridDim.x), c = blockIdx.x;
-    const int64_t s0 = c < P ? W * c / P : W, s1 = c < P ? W * (c + 1) / P : W;
+    const int64_t s0 = c < P ? quotient(W * c, P) : W, s1 = c < P ? quotient(W * (c + 1), P) : W;
     if (lane == 0) {
-      begin.s0 = s0;
-      begin.s1 = s1;
+      have_first = 0;
       all[0] = W;
       all[1] = P;
       p.items[blockIdx.x].n = 0;
     }
+    __syncwarp();
     if (s0 < s1) {
       int64_t carry = 0;
       for (int base = 0; base < p.rows.n_seqs; base += 32) {
@@ -577,39 +642,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (past) {
           if (lane == __ffs(past) - 1) {
             const int64_t seq_at = carry + incl - n;
-            begin.s = s;
-            begin.w = mine;
-            block_at(mine, s0 - seq_at, begin.kvh, begin.blk);
-            begin.at = seq_at + mine.at(begin.kvh, begin.blk);
+            SegIter it;
+            it.s0 = s0;
+            it.s1 = s1;
+            it.s = s;
+            it.w = mine;
+            block_at(mine, s0 - seq_at, it.kvh, it.blk);
+            it.at = seq_at + mine.at(it.kvh, it.blk);
+            Segment g;
+            have_first = it.next(p, g);
+            first_seg = g;
+            begin = it;
           }
           break;
         }
         carry += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    if (lane == 0) {
-      abort_flag = 0;
-      for (int i = 0; i < 2 * kMaxSlots; ++i) {
-        mbar_init(&bars.raw_full[0][i], 1);
-        mbar_init(&bars.raw_empty[0][i], kUnits);  // one arrival per unit
-      }
-      for (int i = 0; i < 2 * kBufs; ++i) {
-        mbar_init(&bars.tile_full[0][i], kUnits);
-        mbar_init(&bars.tile_empty[0][i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&bars.sfull[i], 1);
-        mbar_init(&bars.pfull[i], 4);  // one arrival per softmax warp
-        mbar_init(&bars.odone[i], 1);
-        mbar_init(&bars.segdone[i], 1);
-        mbar_init(&bars.qready[i], 4);
-        mbar_init(&bars.ofree[i], 4);
-      }
-      mbar_init(&bars.drain, 1);
-      fence_mbar_init();
-    }
-  }
-  if (warp > 0) {  // rows of sequences without keys
+  } else {  // rows of sequences without keys
     for (int s = blockIdx.x; s < p.rows.n_seqs; s += gridDim.x) {
       const SeqWork w = seq_work(p, s);
       if (w.len > 0) continue;
@@ -628,28 +678,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  __syncthreads();
-  if (begin.s0 >= begin.s1) return;  // whole CTA: no work
-  if (warp == kMmaWarp) tmem_alloc(&tmem_base_sh, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  // columns: each pipe's scores (64 keys), query tiles, outputs
+  if (!have_first) {  // whole CTA: no work
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
+  // columns: each pipe's two score buffers (32 keys each), query tiles, outputs
   const uint32_t tm_s[2] = {tmem, tmem + 64}, tm_q[2] = {tmem + 128, tmem + 192};
   const uint32_t tm_o[2] = {tmem + 256, tmem + 384};
-
   SegIter it = begin;
-  Segment sg;
+  Segment sg = first_seg;
+  bool have = true;
 
   if (warp >= kCopyWarp) {
     if (warp == kCopyWarp) {
-      // ---------------- codes into the ring, a step of one side at a time
+      // ---------------- codes into the rings, a step of one side at a time
       if (lane == 0) {
         int slot[2] = {0, 0};  // each ring's next slot
         uint32_t turn[2] = {0, 0};
         bool ok = true;
-        while (ok && it.next(p, sg)) {
+        for (; ok && have; have = it.next(p, sg)) {
           const int n = sg.j_hi - sg.j_lo, units = (sg.len + kUnitTokens - 1) / kUnitTokens;
           for (int i = 0; i < 2 * n && ok; ++i) {
             int side, j;
@@ -695,12 +746,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait_bounded(&bars.raw_full[side][i], (n - 1) & 1u, nullptr, 100000000ull);
             }
       }
-    } else if (warp == kMmaWarp) {
-      // ---------------- MMA issuer.  The whole warp walks the steps, so that what an
-      // instruction takes is known to be uniform; one elected thread issues.
+    } else if (warp < kMmaWarp + 2) {
+      // ---------------- MMA issuer of pipe e.  The whole warp walks the steps, so that what an
+      // instruction takes is known to be uniform; one elected thread issues.  (By one
+      // thread of a diverged warp, with descriptors put together for each, an
+      // instruction took about 96 cycles whatever its size; the tensor core takes
+      // 16 for 32 keys of K and 64 for 16 keys of V.  Turns, one warp waiting while the
+      // other issues, took 8 % longer than both at will.)
+      const int e = warp - kMmaWarp;
       const bool leader = elect_one();
       const bool split_k = p.codec[0] != KVQ_F16, split_v = p.codec[1] != KVQ_F16;
-      constexpr uint32_t idesc_k = idesc_f16(0, kKeys), idesc_v = idesc_f16(0);
+      constexpr uint32_t idesc_k = idesc_f16(0, kHalf), idesc_v = idesc_f16(0);
       // A tile's 16 columns kk: 32 bytes on inside 64 columns, then the next half.
       // The low word of the descriptor is all that changes from one to the next.
       constexpr uint32_t kLo = 1u << 16, kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -710,142 +766,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u,
                                                          &abort_flag)) != 0;
       };
-      // S_e = Q K^T of K's tile u: split keys add their rests'
-      // products, turbo4 those of the rest of Q
-      auto qk = [&](int e, int qtile, int u) {
-        const uint32_t b = tile0 + (u % kBufs) * (kTileBytes / 16);
-        const uint32_t d = tm_s[e], a = tm_q[qtile];
-        if (leader) {
+      // S = Q K^T of half h of K's tile u into score buffer b: split keys add their rests'
+      // products, turbo4 those of the rest of Q (at a: the query tile)
+      auto qk = [&](uint32_t a, int u, int h, int b) {
+        const uint32_t k = tile0 + (u % kBufs) * (kTileBytes / 16) + h * (kHalf * 128 / 16);
+        const uint32_t d = tm_s[e] + b * kHalf;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_lo<kHi>(leader, d, a + kk * 8, k + step(kk), idesc_k, kk > 0);
+        if (split_k) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts_lo<kHi>(d, a + kk * 8, b + step(kk), idesc_k, kk > 0);
-          if (split_k) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts_lo<kHi>(d, a + kk * 8, b + kLoRows * 8 + step(kk), idesc_k, 1u);
-          }
-          if (p.singles) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts_lo<kHi>(d, tm_q[1] + kk * 8, b + step(kk), idesc_k, 1u);
-          }
-          mma_commit(&bars.sfull[e]);
+            mma_ts_lo<kHi>(leader, d, a + kk * 8, k + kLoRows * 8 + step(kk), idesc_k, 1u);
         }
-        __syncwarp();
+        if (p.singles) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_lo<kHi>(leader, d, tm_q[1] + kk * 8, k + step(kk), idesc_k, 1u);
+        }
+        commit_if(leader, &bars.sfull[e][b]);
       };
-      // O_e (+)= P_e V of V's tile u; split values: the same P with the rests, columns 64 .. of V
-      auto pv = [&](int e, int u, bool first) {
-        const uint32_t b = tile0 + (kBufs + u % kBufs) * (kTileBytes / 16);
-        const uint32_t d = tm_o[e], a = tm_s[e];
-        if (leader) {
+      // O (+)= P V of half h of V's tile u, P from score buffer b; split values: the
+      // same P with the rests, columns 64 .. of V
+      auto pv = [&](int u, int h, int b, bool first) {
+        const uint32_t v = tile0 + (kBufs + u % kBufs) * (kTileBytes / 16) + h * (kHalf * 2 / 16);
+        const uint32_t d = tm_o[e], a = tm_s[e] + b * kHalf;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts_lo<kHi>(d, a + kk * 8, b + step(kk), idesc_v, (!first || kk > 0) ? 1u : 0u);
-          if (split_v) {
+        for (int kk = 0; kk < 2; ++kk)
+          mma_ts_lo<kHi>(leader, d, a + kk * 8, v + step(kk), idesc_v, (!first || kk > 0) ? 1u : 0u);
+        if (split_v) {
 #pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              mma_ts_lo<kHi>(d, a + (kk - 4) * 8, b + step(kk), idesc_v, 1u);
-          }
-          mma_commit(&bars.odone[e]);
+          for (int kk = 0; kk < 2; ++kk)
+            mma_ts_lo<kHi>(leader, d, a + kk * 8, v + step(4 + kk), idesc_v, 1u);
         }
-        __syncwarp();
+        commit_if(leader, &bars.odone[e]);
       };
       // tiles of a side are numbered over all segments
       auto free_tile = [&](int side, int u) {
-        if (leader) mma_commit(&bars.tile_empty[side][u % kBufs]);
+        commit_if(leader, &bars.tile_empty[side][u % kBufs]);
       };
       auto have_tile = [&](int side, int u) {
         return wait(&bars.tile_full[side][u % kBufs], u / kBufs);
       };
-      int u0 = 0;          // steps of earlier segments
-      int u[2] = {0, 0};   // products P V of each pipe
-      int k[2] = {0, 0};   // segments of each pipe
-      int nq[2] = {0, 0};  // query tiles taken
+      // a barrier, and tiles of V and K where they are asked for
+      auto wait3 = [&](uint64_t *bar, int phase, bool need_v, int uv, bool need_k, int uk) {
+        uint64_t *const v = need_v ? &bars.tile_full[1][uv % kBufs] : bar;
+        uint64_t *const x = need_k ? &bars.tile_full[0][uk % kBufs] : bar;
+        const int vp = need_v ? uv / kBufs : phase, xp = need_k ? uk / kBufs : phase;
+        const bool a = mbar_try_wait(bar, static_cast<uint32_t>(phase) & 1u);
+        const bool b = mbar_try_wait(v, static_cast<uint32_t>(vp) & 1u);
+        const bool c = mbar_try_wait(x, static_cast<uint32_t>(xp) & 1u);
+        if (__all_sync(0xffffffffu, a & b & c)) return true;
+        return wait(bar, phase) && wait(v, vp) && wait(x, xp);
+      };
+      int u0 = 0;  // tiles of earlier segments
+      int c0 = 0;  // halves that the pipe has taken in earlier segments
+      int k = 0;   // segments
       bool ok = true;
-      while (ok && it.next(p, sg)) {
+      for (; ok && have; have = it.next(p, sg)) {
         const int n = sg.j_hi - sg.j_lo;
-        ok = wait(&bars.qready[0], nq[0]) && (!sg.pair || wait(&bars.qready[1], nq[1])) &&
-             have_tile(0, u0);
+        const bool pair = sg.pair;
+        // The pipe's halves i: of a pair both of every tile, of a single tile's the
+        // pipe's own of every tile.
+        const int cnt = pair ? 2 * n : n;
+        const uint32_t q = tm_q[pair ? e : 0];
+        auto scores = [&](int i) {  // of half i
+          const int t = pair ? i >> 1 : i;
+          qk(q, u0 + t, pair ? i & 1 : e, (c0 + i) & 1);
+          if (!pair || (i & 1)) free_tile(0, u0 + t);
+        };
+        ok = wait(&bars.qready[e], k) && have_tile(0, u0) &&
+             (pair || cnt == 1 || have_tile(0, u0 + 1)) &&
+             (k == 0 || wait(&bars.ofree[e], k - 1));
         if (!ok) break;
-        ++nq[0];
-        if (sg.pair) ++nq[1];
         tc_fence_after();
-        qk(0, 0, u0);
-        if (sg.pair) {
-          qk(1, 1, u0);
-          free_tile(0, u0);
-          for (int j = 0; j < n; ++j) {
-            const bool more = j + 1 < n;
-            ok = wait(&bars.pfull[0], u[0]) && have_tile(1, u0 + j) &&
-                 (j > 0 || k[0] == 0 || wait(&bars.ofree[0], k[0] - 1));
-            if (!ok) break;
-            tc_fence_after();
-            pv(0, u0 + j, j == 0);
-            ++u[0];
-            if (more) {
-              ok = have_tile(0, u0 + j + 1);
-              if (!ok) break;
-              tc_fence_after();
-              qk(0, 0, u0 + j + 1);
-            }
-            ok = wait(&bars.pfull[1], u[1]) &&
-                 (j > 0 || k[1] == 0 || wait(&bars.ofree[1], k[1] - 1));
-            if (!ok) break;
-            tc_fence_after();
-            pv(1, u0 + j, j == 0);
-            ++u[1];
-            free_tile(1, u0 + j);
-            if (more) {
-              qk(1, 1, u0 + j + 1);
-              free_tile(0, u0 + j + 1);
-            }
-          }
-        } else {  // the pipes take the tile's steps in turn
-          free_tile(0, u0);
-          if (n > 1) {
-            ok = have_tile(0, u0 + 1);
-            if (!ok) break;
-            tc_fence_after();
-            qk(1, 0, u0 + 1);
-            free_tile(0, u0 + 1);
-          }
-          for (int j = 0; j < n; ++j) {
-            const int e = j & 1;
-            ok = wait(&bars.pfull[e], u[e]) && have_tile(1, u0 + j) &&
-                 (j > 1 || k[e] == 0 || wait(&bars.ofree[e], k[e] - 1));
-            if (!ok) break;
-            tc_fence_after();
-            pv(e, u0 + j, j < 2);
-            ++u[e];
-            free_tile(1, u0 + j);
-            if (j + 2 < n) {
-              ok = have_tile(0, u0 + j + 2);
-              if (!ok) break;
-              tc_fence_after();
-              qk(e, 0, u0 + j + 2);
-              free_tile(0, u0 + j + 2);
-            }
-          }
+        scores(0);
+        if (cnt > 1) scores(1);
+        for (int i = 0; i < cnt; ++i) {
+          const int t = pair ? i >> 1 : i, b = (c0 + i) & 1;
+          // P of half i, V's tile, and K's of half i + 2, asked for together: one wait
+          // after the other the tensor core ran dry between them (100 cycles each)
+          const int tk = pair ? t + 1 : t + 2;
+          const bool fresh = !pair || (i & 1) == 0;  // not asked for with the half before
+          ok = wait3(&bars.pfull[e][b], (c0 + i) >> 1, fresh, u0 + t, fresh && tk < n, u0 + tk);
+          if (!ok) break;
+          tc_fence_after();
+          pv(u0 + t, pair ? i & 1 : e, b, i == 0);
+          if (!pair || (i & 1)) free_tile(1, u0 + t);
+          if (i + 2 < cnt) scores(i + 2);
         }
         if (!ok) break;
         u0 += n;
-        // a pipe's O is complete once every MMA issued so far is
-        const bool both = sg.pair || n > 1;
-        if (leader) {
-          mma_commit(&bars.segdone[0]);
-          if (both) mma_commit(&bars.segdone[1]);
-        }
-        ++k[0];
-        if (both) ++k[1];
+        c0 += cnt;
+        ++k;
+        commit_if(leader, &bars.segdone[e]);  // the pipe's O is complete
       }
       if (!ok && lane == 0) {
         set_err(p.err, KVQ_DEVERR_TIMEOUT);
         atomicExch(&abort_flag, 1);
       }
       // drain: every MMA the thread issued has finished (TMEM is freed after it)
-      if (leader) mma_commit(&bars.drain);
-      mbar_wait_bounded(&bars.drain, 0, nullptr, 100000000ull);
-  }
+      commit_if(leader, &bars.drain[e]);
+      mbar_wait_bounded(&bars.drain[e], 0, nullptr, 100000000ull);
+    }
   } else if (warp >= kTileWarp) {
     // ---------------- codes into operand tiles: warp w of a side takes unit w of each
     const int side = (warp - kTileWarp) >> 2, unit = warp & 3;
@@ -856,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int u = 0, slot = 0;  // this side's tiles so far; its next ring slot
     uint32_t turn = 0;
     bool ok = true;
-    while (ok && it.next(p, sg)) {
+    for (; ok && have; have = it.next(p, sg)) {
       const int n = sg.j_hi - sg.j_lo;
       for (int j = 0; j < n; ++j, ++u) {
         const int buf = u % kBufs;
@@ -890,16 +913,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tms = tm_s[e] + lane_off, tmo = tm_o[e] + lane_off;
     const bool rot_k = p.codec[0] == KVQ_TURBO4, rot_v = p.codec[1] == KVQ_TURBO4;
-    auto mine = [&](const Segment &g) { return e == 0 || g.pair || g.j_hi - g.j_lo > 1; };
-    auto next_mine = [&](Segment &g) {
-      while (it.next(p, g))
-        if (mine(g)) return true;
-      return false;
-    };
     // This pipe's query tile of a segment, a thread its own row, as fp16 in K's order
     // of dims into TMEM, where the products take it from (with both operands in
-    // shared memory they took twice as long); then tell the MMA thread.  (Pipe 1 of a
-    // single tile: pipe 0's.)
+    // shared memory they took twice as long); then tell the pipe's issuer.  A single
+    // tile is pipe 0's, for both issuers.
     auto load_q = [&](const Segment &g) {
       if (e == 1 && !g.pair) return;
       const int R = g.row0 + e * kTile + r;
@@ -979,21 +996,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.qready[e]);
+      if (lane == 0) {
+        mbar_arrive(&bars.qready[e]);
+        if (!g.pair) mbar_arrive(&bars.qready[1]);
+      }
     };
-    int u = 0, kseg = 0;  // tiles and segments of this pipe
+    int c0 = 0, kseg = 0;  // halves and segments of this pipe so far
     bool ok = true;
-    bool have = next_mine(sg);
     if (have) load_q(sg);
     while (have) {
-      const int n = sg.j_hi - sg.j_lo;
+      const int n = sg.j_hi - sg.j_lo, cnt = sg.pair ? 2 * n : n;
       const int row0 = sg.row0 + (sg.pair ? e * kTile : 0);
       const bool idle = row0 + quad * 32 >= sg.R;  // no row in this warp
       float m = -INFINITY, l = 0.0f;
       // After an abort (ok false) the segments still run to the end without waits,
       // so that both pipes meet at the same barriers.
-      for (int j = sg.pair ? 0 : e; j < n && ok; j += sg.pair ? 1 : 2, ++u) {
-        ok = mbar_wait_bounded(&bars.sfull[e], static_cast<uint32_t>(u) & 1u, &abort_flag);
+      for (int i = 0; i < cnt && ok; ++i) {
+        const int b = (c0 + i) & 1;
+        ok = mbar_wait_bounded(&bars.sfull[e][b], static_cast<uint32_t>((c0 + i) >> 1) & 1u,
+                               &abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) atomicExch(&abort_flag, 1);
@@ -1001,33 +1022,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (!idle) {
-          const int left = sg.len - (sg.j_lo + j) * kKeys;  // keys from the step's first on
-          // 32 scores at a time, read twice (registers); places past the length -inf.
-          auto scores = [&](int c, float(&v)[32]) {
-            tmem_ld32(tms + c * 32, v);
-            tmem_wait_ld();
-            if (left < kKeys) {
+          // keys from the half's first on
+          const int left = sg.len - (sg.pair ? (2 * sg.j_lo + i) * kHalf
+                                             : (2 * (sg.j_lo + i) + e) * kHalf);
+          float v[kHalf];
+          tmem_ld32(tms + b * kHalf, v);
+          tmem_wait_ld();
+          if (left < kHalf) {  // places past the length
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + (i & 16) + token_of(i) >= left) v[i] = -INFINITY;
-            }
-          };
+            for (int c = 0; c < kHalf; ++c)
+              if ((c & 16) + token_of(c) >= left) v[c] = -INFINITY;
+          }
           float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            float v[32];
-            scores(c, v);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mp[(i >> 1) & 3] = fmax3(mp[(i >> 1) & 3], v[i], v[i + 1]);
-          }
-          const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
+          for (int c = 0; c < kHalf; c += 2) mp[(c >> 1) & 3] = fmax3(mp[(c >> 1) & 3], v[c], v[c + 1]);
+          const float mx = fmaxf(fmax3(mp[0], mp[1], mp[2]), mp[3]) * p.scale_log2;
           // A row's running maximum is raised only when it grew by more than the
           // threshold; O is rescaled for the whole warp when one of its rows is.
           const bool raise = mx > m + kRaise || m == -INFINITY;
           const float mnew = raise ? fmaxf(mx, m) : m;
           const float a = (raise && m != -INFINITY) ? fast_exp2(m - mnew) : 1.0f;
           if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
-            bool got = mbar_wait_bounded(&bars.odone[e], static_cast<uint32_t>(u - 1) & 1u, &abort_flag);
+            // every product of the halves before is in O: the one before the last was
+            // done before these scores were, the last is waited for
+            bool got = mbar_wait_bounded(&bars.odone[e], static_cast<uint32_t>(c0 + i - 1) & 1u,
+                                         &abort_flag);
             got = __all_sync(0xffffffffu, got);
             if (!got) {
               ok = false;
@@ -1041,53 +1060,47 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld();
               uint32_t y[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * a);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(x[k] * a);
               tmem_st16(tmo + c * 16, y);
             }
             tmem_wait_st();
           }
           l *= a;
           m = mnew;
-          // P = exp2(s * scale_log2 - m + lift) as fp16 pairs over S (32 of them on
-          // columns already read), and the row's sum.
+          // P = exp2(s * scale_log2 - m + lift) as fp16 pairs over S, and the row's sum.
           const float nm = m == -INFINITY ? 0.0f : kLift - m;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          uint32_t pk[kHalf / 2];
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            float v[32];
-            uint32_t pk[16];
-            scores(c, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 tt = fma2(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
-              const float2 x = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
-              sum[i & 1] = add2(sum[i & 1], x);
-              pk[i] = pack_half2(x.x, x.y);
-            }
-            tmem_st16(tms + c * 16, pk);
+          for (int c = 0; c < kHalf / 2; ++c) {
+            const float2 tt = fma2(make_float2(v[2 * c], v[2 * c + 1]), sc2, nm2);
+            const float2 x = make_float2(fast_exp2(tt.x), fast_exp2(tt.y));
+            sum[c & 1] = add2(sum[c & 1], x);
+            pk[c] = pack_half2(x.x, x.y);
           }
+          tmem_st16(tms + b * kHalf, pk);
           const float2 s2 = add2(sum[0], sum[1]);
           l += s2.x + s2.y;
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.pfull[e]);
+        if (lane == 0) mbar_arrive(&bars.pfull[e][b]);
       }
-      // The next segment's query tile: in a pair this pipe's last S has been read,
-      // so its tile is free now; a single tile's is once every product is done.
+      c0 += cnt;
+      // Once both pipes have read their last scores the query tiles are free, and no
+      // pipe is further than that ahead of the other.
+      pipes_sync();
       Segment nsg;
-      const bool have_next = next_mine(nsg);
-      if (sg.pair && have_next) load_q(nsg);
+      const bool have_next = it.next(p, nsg);
+      if (have_next && !rot_k) load_q(nsg);
       if (ok) ok = mbar_wait_bounded(&bars.segdone[e], static_cast<uint32_t>(kseg) & 1u, &abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       ++kseg;
       tc_fence_after();
-      if (!sg.pair && e == 0 && have_next && !rot_k) load_q(nsg);
-      const bool joined = !sg.pair && n > 1;  // the other pipe has the odd key tiles
       float w0 = 1.0f, w1 = 0.0f;
-      if (joined && e == 1) {
+      if (!sg.pair && e == 1) {  // to pipe 0, half of O at a time
         pipe1_ml[r] = make_float2(m, l);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -1106,7 +1119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.ofree[1]);
         pipes_sync();  // the second half has been read
-        if (have_next) load_q(nsg);
         sg = nsg;
         have = have_next;
         continue;
@@ -1121,9 +1133,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ro.half = nullptr;
       ro.full = nullptr;
       ro.bf16 = p.q_bf16;
+      float *const slot = p.part +
+                          (2 * static_cast<int64_t>(blockIdx.x) + (sg.inside ? 1 : 0)) * kSlotFloats +
+                          (sg.pair ? e : 0) * kPartFloats;
+      ro.step = whole ? 4 : 4 * kTile;
       if (!whole)
-        ro.full = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (sg.inside ? 1 : 0)) * kSlotFloats +
-                  static_cast<int64_t>((sg.pair ? e : 0) * kTile + r) * kPartStride;
+        ro.full = slot + 4 * r;
       else if (p.out.xo)
         ro.full = p.out.xo + at * kD;
       else
@@ -1133,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.items[blockIdx.x] = {sg.first, sg.R, sg.row0, sg.kvh, sg.pair ? 2 * kTile : kTile,
                                static_cast<int>(owner_of(last, all[0], all[1]) - blockIdx.x + 1), 0};
       }
-      if (joined) {
+      if (!sg.pair) {
         pipes_sync();  // pipe 1's first half and (m, l) are written
         const float2 y = pipe1_ml[r];
         const float top = fmaxf(m, y.x);
@@ -1145,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ro.inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        if (joined && c == 2) {
+        if (!sg.pair && c == 2) {
           pipes_sync();  // the first half has been read
           pipes_sync();  // the second is written
         }
@@ -1153,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
         tmem_ld32(tmo + c * 32, v);
         tmem_wait_ld();
-        if (joined) {
+        if (!sg.pair) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             v[i] = fmaf(w1, exchange[((c & 1) * 32 + i) * kTile + r], w0 * v[i]);
@@ -1167,7 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ro.put(c * 32 + 8 * i, reinterpret_cast<const float(&)[8]>(v[8 * i]));
         }
       }
-      if (joined) pipes_sync();  // the second half has been read
+      if (!sg.pair) pipes_sync();  // the second half has been read
       if (rot_v && !idle) {  // the stages across them, and x = s H y / 16
         tmem_wait_st();
 #pragma unroll 1
@@ -1193,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // weights were lifted: sums of 2^(s - (m - lift))
       const float ml = m == -INFINITY ? m : m - kLift;
       if (!whole) {
-        if (valid) *reinterpret_cast<float2 *>(ro.full + kD) = make_float2(ml, l);
+        if (valid) reinterpret_cast<float2 *>(slot + kTile * kD)[r] = make_float2(ml, l);
       } else if (valid) {
         if (p.out.xo) p.out.xml[at] = make_float2(ml, l);
         else if (p.out.lse)
@@ -1223,31 +1238,26 @@ constexpr int kJoinRows = kJoinThreads / 16;
 
 // The items that the attention kernel split over several CTAs: o = sum_c
 // 2^(m_c - M) o_c over the pieces in order.  Block (c, rows): the item, if any, that
-// begins in CTA c's slice and ends in another's; 16 threads per row (8 dims each),
-// the pieces' rows requested four at a time.
+// begins in CTA c's slice and ends in another's; 16 threads per row (8 dims each), a
+// warp 16 rows wide, four pieces requested at a time.
 __global__ void __launch_bounds__(kJoinThreads, 4)
     cross_join_kernel(const __grid_constant__ CrossParams p) {
-  const int tid = threadIdx.x, lane = tid & 31, t16 = tid & 15;
-  grid_dependency_wait();  // items and partials are complete
+  const int tid = threadIdx.x, g8 = tid >> 4;  // dims 8 g8 ..
+  grid_dependency_wait();                      // items and partials are complete
   grid_launch_dependents();
   const JoinItem item = p.items[blockIdx.x];
   const int64_t c0 = blockIdx.x;
-  const int n = item.n, in = blockIdx.y * kJoinRows + (tid >> 4);  // row of the block
+  const int n = item.n, in = blockIdx.y * kJoinRows + (tid & 15);  // row of the block
   const int R = item.row0 + in;
   if (n == 0 || in >= item.rows || R >= item.R) return;
   const int tok = R / p.G, head = item.kvh * p.G + R - tok * p.G;
   const int64_t row = item.first + tok;
   // the item begins inside its first CTA's slice, and before every other's
   auto part = [&](int j) {
-    return p.part + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlotFloats +
-           static_cast<int64_t>(in) * kPartStride;
+    return p.part + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlotFloats + (in / kTile) * kPartFloats;
   };
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   float M = -INFINITY, L = 0.0f;
-  for (int j = t16; j < n; j += 16) M = fmaxf(M, __ldcg(part(j) + kD));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1)  // (the other half of the warp may have returned)
-    M = fmaxf(M, __shfl_xor_sync(0xffffu << (lane & 16), M, o, 16));
   constexpr int kAhead = 4;
   for (int j0 = 0; j0 < n; j0 += kAhead) {
     float4 v[kAhead][2];
@@ -1255,13 +1265,21 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const float *pr = part(min(j0 + k, n - 1));
-      y[k] = __ldcg(reinterpret_cast<const float2 *>(pr + kD));
-      v[k][0] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16));
-      v[k][1] = __ldcg(reinterpret_cast<const float4 *>(pr + 8 * t16) + 1);
+      const int r = in % kTile;
+      y[k] = __ldcg(reinterpret_cast<const float2 *>(pr + kTile * kD) + r);
+      v[k][0] = __ldcg(reinterpret_cast<const float4 *>(pr) + 2 * g8 * kTile + r);
+      v[k][1] = __ldcg(reinterpret_cast<const float4 *>(pr) + (2 * g8 + 1) * kTile + r);
+      if (j0 + k >= n) y[k].x = -INFINITY;
     }
+    const float top = fmaxf(fmaxf(M, fmaxf(y[0].x, y[1].x)), fmaxf(y[2].x, y[3].x));
+    const float f0 = M == -INFINITY ? 0.0f : fast_exp2(M - top);
+    L *= f0;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) acc[d] *= f0;
+    M = top;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (j0 + k >= n || y[k].x == -INFINITY) continue;
+      if (y[k].x == -INFINITY) continue;
       const float f = fast_exp2(y[k].x - M);
       L = fmaf(f, y[k].y, L);
       const float z[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
@@ -1275,9 +1293,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   ro.inv = L > 0.0f ? 1.0f / L : 0.0f;
   ro.bf16 = p.q_bf16;
   ro.full = p.out.xo ? p.out.xo + to * kD : nullptr;
+  ro.step = 4;
   ro.half = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head;
-  ro.put(8 * t16, acc);
-  if (t16 == 0) {
+  ro.put(8 * g8, acc);
+  if (g8 == 0) {
     if (p.out.xo) p.out.xml[to] = make_float2(M, L);
     else if (p.out.lse)
       p.out.lse[to] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;

@@ -326,19 +326,19 @@ def test_graphs_share_a_workspace():
 def test_two_streams_at_once():
     """Calls on two streams over workspaces of their own, behind work that fills their inputs."""
     lens = [3000, 2000]
-    L, table = _filled(2, 2, 8, 3072, F16, Q8, False, lens, 18)
+    L, table = _filled(2, 2, 8, 3328, F16, Q8, False, lens, 18)
     values = _values(L, table, lens)
     streams = [torch.cuda.Stream() for _ in "ab"]
     qs = [torch.zeros((60, 8, 128), dtype=torch.float16, device="cuda") for _ in "ab"]
     fresh = [_queries(60, 8, 40 + i) for i in (0, 1)]
-    outs, wss = [torch.empty_like(q) for q in qs], [_cross_ws(L, 60, 3072) for _ in "ab"]
+    outs, wss = [torch.empty_like(q) for q in qs], [_cross_ws(L, 60, 3328) for _ in "ab"]
     start = _i32([0, 25, 60])
     torch.cuda.synchronize()
     for _ in range(5):
         for i, st in enumerate(streams):
             with torch.cuda.stream(st):
                 qs[i].copy_(fresh[i])
-            kvq.attn_cross(L, qs[i], SCALE, outs[i], None, 3072, wss[i], row_start=start, stream=st)
+            kvq.attn_cross(L, qs[i], SCALE, outs[i], None, 3328, wss[i], row_start=start, stream=st)
     torch.cuda.synchronize()
     for i in (0, 1):
         _check_rows(L, values, fresh[i], outs[i], None, [25, 35])
