@@ -235,19 +235,6 @@ __device__ __forceinline__ Parts scaled(uint32_t c, uint32_t d) {
   return {*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l)};
 }
 __device__ __forceinline__ uint32_t twice(uint32_t half) { return half * 0x10001u; }
-// Four signed bytes as fp16 pairs (0, 1) and (2, 3), exact: the byte plus 128 in
-// the mantissa of 1024, less 1152.
-__device__ __forceinline__ void s8_quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  const uint32_t t = w ^ 0x80808080u;
-  lo = hsub2_bits(__byte_perm(t, 0x64646464u, 0x4140), 0x64806480u);
-  hi = hsub2_bits(__byte_perm(t, 0x64646464u, 0x4342), 0x64806480u);
-}
-// Four nibbles (one in each byte's low half) less 8, likewise.
-__device__ __forceinline__ void u4_quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  lo = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4140), 0x64086408u);
-  hi = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4342), 0x64086408u);
-}
-
 // Quantized sides are split: x^ = d c has up to 18 bits, an operand 11, so a tile
 // holds 64 keys twice, RN16(x^) and the rest.  (Rounded once, 128 keys to a tile,
 // outputs over q8_0 sides were 4.1e-4 off, relative to their own rounding of

@@ -83,7 +83,9 @@ int kv_read_rows(const kvq_layer *layer, const kvq_rows *k, const kvq_rows *v, i
       overlap(k->data, span_bytes(*k, n_rows, heads), v->data, span_bytes(*v, n_rows, heads)) &&
       !kvq::interleaved(*k, *v, n_rows, heads))
     return KVQ_EINVAL;
-  const cudaError_t e = kvq::launch_read_rows(*layer, k, v, n_rows, n_read, row_start, first,
+  const int sms = kvq::device_sms();
+  if (sms <= 0) return KVQ_ECUDA;
+  const cudaError_t e = kvq::launch_read_rows(*layer, k, v, n_rows, n_read, row_start, first, sms,
                                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
 }

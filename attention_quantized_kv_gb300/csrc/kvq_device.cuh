@@ -276,6 +276,19 @@ __device__ __forceinline__ uint32_t u4_pair_minus8_hi(uint32_t w) {
   return r;
 }
 
+// Four signed bytes as fp16 pairs (0, 1) and (2, 3), exact: the byte plus 128 in
+// the mantissa of 1024, less 1152.
+__device__ __forceinline__ void s8_quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t t = w ^ 0x80808080u;
+  lo = hsub2_bits(__byte_perm(t, 0x64646464u, 0x4140), 0x64806480u);
+  hi = hsub2_bits(__byte_perm(t, 0x64646464u, 0x4342), 0x64806480u);
+}
+// Four nibbles (one in each byte's low half) less 8, likewise.
+__device__ __forceinline__ void u4_quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  lo = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4140), 0x64086408u);
+  hi = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4342), 0x64086408u);
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&h);

@@ -110,7 +110,7 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
 // Cached rows as values (read_rows.cu).
 cudaError_t launch_read_rows(const kvq_layer &L, const kvq_rows *k, const kvq_rows *v,
                              int64_t n_rows, const int32_t *n_read, const int32_t *row_start,
-                             const int32_t *first, cudaStream_t stream);
+                             const int32_t *first, int sms, cudaStream_t stream);
 
 // Rotary positions (rope.cu, append_rope.cu).
 

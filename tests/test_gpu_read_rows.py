@@ -98,6 +98,69 @@ def test_padded_views(ck, cv):
     assert (fused[:, :, 2 * n_kv:] == 5).all()
 
 
+def _equal(a, b):
+    return bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+@pytest.mark.parametrize("ck,cv", [(F16, F16), (Q8, Q4), (Q4, T4), (T4, Q8)])
+@pytest.mark.parametrize("kinds", [("float16", "float16"), ("float32", "bfloat16"), ("bfloat16", "float32")])
+@pytest.mark.parametrize("paged", [False, True])
+def test_many_rows(ck, cv, kinds, paged):
+    """A large call gives what small ones give, which the other tests compare with the decoders:
+    runs of every length and place in a unit, pages that two sequences share, sides of two types."""
+    n_kv, cap = 3, 1536
+    L, _ = _layer(6, n_kv, n_kv, cap, ck, cv, paged, 3, unmapped=[(2, 1)] if paged else [])
+    _noise(L, 31 + ck)
+    if paged:  # sequence 1 ends, and sequence 3 begins, in one page
+        L.block_table[3, 0] = L.block_table[1, 4]
+    L.seq_lens.copy_(_i32([1536, 1100, 900, 40, 1, 700]))
+    counts, first = [1500, 1024 + 13, 850, 23, 1, 530], [36, 1037 - 974, 11, 3, 0, 170]
+    counts[5] += 20  # behind the sequence
+    total = sum(counts)
+    start = np.cumsum([0] + counts)
+    got = [torch.full((total + 3, n_kv, 128), 3, dtype=KINDS[t], device="cuda") for t in kinds]
+    kvq.kv_read_rows(L, *got, row_start=_i32(start), first=_i32(first))
+    bits = kvq.KVQ_DEVERR_SEQLEN | (kvq.KVQ_DEVERR_PAGE if paged else 0)
+    assert L.err.item() == bits
+    want = [torch.full_like(t, 3) for t in got]
+    for s, n in enumerate(counts):
+        for at in range(0, n, 500):
+            m = min(500, n - at)
+            rows = [t[start[s] + at:start[s] + at + m] for t in want]
+            begin = [0] * 6
+            begin[s] = first[s] + at
+            kvq.kv_read_rows(L, *rows, row_start=_i32([0] * (s + 1) + [m] * (6 - s)), first=_i32(begin))
+    for a, b in zip(got, want):
+        assert _equal(a, b)
+    pad = torch.full((6, 1600, 2 * n_kv, 128), 3, dtype=KINDS[kinds[0]], device="cuda")  # views, padded
+    kvq.kv_read_rows(L, pad[:, :, :n_kv], n_read=_i32(counts), first=_i32(first))
+    for s, n in enumerate(counts):
+        assert _equal(pad[s, :n, :n_kv], want[0][start[s]:start[s + 1]])
+        assert (pad[s, n:] == 3).all() and (pad[s, :, n_kv:] == 3).all()
+
+
+def test_many_sequences():
+    """More sequences than a block keeps the starts of, empty ones among them."""
+    n_seqs, n_kv = 300, 4
+    L, _ = _layer(n_seqs, n_kv, n_kv, 256, Q8, T4, False, 3)
+    _noise(L, 77)
+    L.seq_lens.fill_(100)
+    counts = [(7 * s) % 26 for s in range(n_seqs)]
+    first = [s % 75 for s in range(n_seqs)]
+    start = np.cumsum([0] + counts)
+    total = int(start[-1])
+    assert total >= 8 * n_seqs and total * 2 * n_kv >= 16384
+    got = [torch.full((total, n_kv, 128), 3, dtype=torch.float32, device="cuda") for _ in "kv"]
+    kvq.kv_read_rows(L, *got, row_start=_i32(start), first=_i32(first))
+    assert L.err.item() == 0
+    want = [torch.full_like(t, 3) for t in got]
+    for lo in range(0, n_seqs, 75):
+        rows = [t[start[lo]:start[lo + 75]] for t in want]
+        part = np.clip(start, start[lo], start[lo + 75]) - start[lo]
+        kvq.kv_read_rows(L, *rows, row_start=_i32(part), first=_i32(first))
+    assert all(_equal(a, b) for a, b in zip(got, want))
+
+
 def test_conditions():
     """Tokens outside a sequence, bad counts and unmapped pages: their bits, their rows untouched."""
     L, table = _layer(2, 2, 2, 512, Q8, Q8, True, 4, unmapped=[(1, 1)])
