@@ -15,11 +15,11 @@
 // partial slot (unnormalised O, max, sum), and a second kernel joins an item's pieces
 // by log-sum-exp in a fixed order.  Lengths and row counts are read on the device.
 //
-// Inside a CTA (19 warps at work) nothing is written to HBM but the results: codes are
+// Inside a CTA (20 warps) nothing is written to HBM but the results: codes are
 // copied in as they lie in the cache, turned into tensor-core operand tiles in
 // shared memory and used there.
-//  * Warp 16 copies the codes of 64 keys of one side at a time into that side's ring
-//    (1-D bulk copies); K and V tiles alternate.
+//  * Warps 16 (K) and 19 (V) copy the codes of 64 keys at a time into their side's ring
+//    (1-D bulk copies).
 //  * Warps 8-11 (K) and 12-15 (V) turn them into fp16 operand tiles (two 32 KB
 //    buffers a side), a 16-token unit each.  The cache's order is kept where the
 //    operands leave the choice, so that 16 bytes of codes become whole 8- or 16-byte
@@ -31,8 +31,8 @@
 //    with P read from TMEM.
 //  * Warps 0-3 and 4-7 are two softmax pipes, one query row per thread, 32 keys at a
 //    time in two score buffers.  In a pair they hold the two tiles; with a single tile
-//    they take the first and second half of its every key tile and are joined through
-//    shared memory at the end.
+//    they take the first and second half of its every key tile, and each joins and writes
+//    half of the dims at the end.
 //
 // Bound: the tensor cores, from two rows tiles per byte on: a pair's 64 keys cost
 // 2050 cycles of products over split sides (1290 over f16), and took 4600 by one
@@ -60,12 +60,13 @@ constexpr int kUnits = kKeys / kUnitTokens;       // units of a step, and of a r
 constexpr int kBufs = 2;                          // operand tiles of each side
 constexpr int kMaxSlots = 8;                      // of one side
 constexpr int kThreads = 640;
-// warps 0-3, 4-7: softmax pipes; 8-11, 12-15: tiles of K, of V; 16: copies; 17, 18:
-// products of each pipe; one idle (registers go to a CTA in groups of four warps)
-constexpr int kTileWarp = 8, kCopyWarp = 16, kMmaWarp = 17;
-constexpr int kRingBytes = 65536;                 // K's ring, then V's: two steps of f16 each
-constexpr int kExchangeBytes = 64 * kTile * 4;   // half of pipe 1's O
-constexpr int kSmemBytes = 2 * kBufs * kTileBytes + kExchangeBytes + kRingBytes + 1024;
+// warps 0-3, 4-7: softmax pipes; 8-11, 12-15: tiles of K, of V; 16, 19: copies of K's
+// codes, of V's; 17, 18: products of each pipe
+constexpr int kTileWarp = 8, kCopyWarp = 16, kMmaWarp = 17, kCopyWarpV = 19;
+// K's ring, then V's.  What is in flight is what it holds: 24 beams of f16 and q8_0
+// states took 73 us with 64 KB of it and one warp for both sides' copies.
+constexpr int kRingBytes = 98304;
+constexpr int kSmemBytes = 2 * kBufs * kTileBytes + kRingBytes;
 constexpr float kRaise = 8.0f;                    // log2 units, as in the prefill
 // Weights are held as 2^(s - m + 6): at most 2^14 in fp16, and 2^6 further from
 // its subnormals than 2^(s - m).
@@ -210,13 +211,6 @@ struct SegIter {
     return false;
   }
 };
-// The order in which a segment of n steps takes its 2 n copies: K_0, then K_{j+1},
-// V_j in turn, the last V alone.
-__device__ __forceinline__ void copy_at(int i, int n, int &side, int &j) {
-  side = i == 0 || ((i & 1) && i < 2 * n - 1) ? 0 : 1;
-  j = side == 0 ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1;
-}
-
 // ------------------------------------------------------------------ codes to operand tiles
 
 __device__ __forceinline__ void sts128(uint8_t *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -540,7 +534,7 @@ __device__ __forceinline__ void pipes_sync() {
 
 __global__ void __launch_bounds__(kThreads, 1)
     cross_attn_kernel(const __grid_constant__ CrossParams p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ CrossBars bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
@@ -548,14 +542,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Segment first_seg;
   __shared__ int have_first;
   __shared__ int64_t all[2];     // all work, and the CTAs that share it
-  __shared__ float2 pipe1_ml[kTile];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  // operand tiles of K, of V, the exchange, codes
-  uint8_t *tiles = smem, *ring = smem + 2 * kBufs * kTileBytes + kExchangeBytes;
-  float *exchange = reinterpret_cast<float *>(smem + 2 * kBufs * kTileBytes);  // [64][128]
+  __shared__ float2 pipe_ml[2][kTile];  // of a single tile's pipes
+  uint8_t *tiles = smem, *ring = smem + 2 * kBufs * kTileBytes;  // operand tiles of K, of V; codes
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);  // (uniform)
   const int lane = threadIdx.x & 31;
+
+  // (swizzled tiles lie at multiples of 1024 bytes, as this memory is declared; there is
+  // none left to round up in)
+  if ((smem_u32(smem) & 1023u) != 0) {
+    grid_dependency_wait();
+    set_err(p.err, KVQ_DEVERR_TIMEOUT);
+    return;
+  }
 
   // What needs no other kernel's results
   if (warp == kMmaWarp) {
@@ -681,59 +679,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool have = true;
 
   if (warp >= kCopyWarp) {
-    if (warp == kCopyWarp) {
-      // ---------------- codes into the rings, a step of one side at a time
+    if (warp == kCopyWarp || warp == kCopyWarpV) {
+      // ---------------- codes into a side's ring, a step at a time
       if (lane == 0) {
-        int slot[2] = {0, 0};  // each ring's next slot
-        uint32_t turn[2] = {0, 0};
+        const int side = warp == kCopyWarp ? 0 : 1, slots = p.slots[side];
+        const int ub = unit_bytes(p.codec[side]);
+        uint8_t *const to = ring + (side ? p.slots[0] * kUnits * unit_bytes(p.codec[0]) : 0);
+        int slot = 0;
+        uint32_t turn = 0;
         bool ok = true;
         for (; ok && have; have = it.next(p, sg)) {
-          const int n = sg.j_hi - sg.j_lo, units = (sg.len + kUnitTokens - 1) / kUnitTokens;
-          for (int i = 0; i < 2 * n && ok; ++i) {
-            int side, j;
-            copy_at(i, n, side, j);
-            const int u0 = (sg.j_lo + j) * kUnits;
-            const int ub = unit_bytes(p.codec[side]);
-            int64_t unit = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) *
-                               (p.capacity / kUnitTokens) + u0;
-            if (p.table) {  // a step lies inside one page
+          const int units = (sg.len + kUnitTokens - 1) / kUnitTokens;
+          // the units of the sequence's kv head; in pages, those of the current page
+          int64_t base = (static_cast<int64_t>(sg.s) * p.n_kv + sg.kvh) * (p.capacity / kUnitTokens);
+          for (int j = sg.j_lo; j < sg.j_hi; ++j) {
+            const int u0 = j * kUnits;
+            if (p.table && (j == sg.j_lo || u0 % kPageUnits == 0)) {  // (a step lies inside one page)
               int pg = page_of(p.table, p.pages_per_seq, p.n_pages, sg.s, u0 / kPageUnits);
               if (pg < 0) {
                 set_err(p.err, KVQ_DEVERR_PAGE);
                 pg = 0;  // read pool page 0 in its place
               }
-              unit = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits + u0 % kPageUnits;
+              base = (static_cast<int64_t>(pg) * p.n_kv + sg.kvh) * kPageUnits -
+                     u0 / kPageUnits * kPageUnits;
             }
-            const uint8_t *src = p.cache[side] + unit * ub;
-            const int at = slot[side];
-            uint64_t *full = &bars.raw_full[side][at];
-            if (turn[side] > 0 && !mbar_wait_bounded(&bars.raw_empty[side][at], (turn[side] - 1) & 1u,
-                                                     &abort_flag)) {
+            uint64_t *full = &bars.raw_full[side][slot];
+            if (turn > 0 && !mbar_wait_bounded(&bars.raw_empty[side][slot], (turn - 1) & 1u, &abort_flag)) {
               ok = false;
               break;
             }
             const uint32_t bytes = static_cast<uint32_t>(min(kUnits, units - u0) * ub);
             mbar_arrive_expect_tx(full, bytes);
-            bulk_copy_g2s(ring + (side ? p.slots[0] * kUnits * unit_bytes(p.codec[0]) : 0) +
-                              at * kUnits * ub,
-                          src, bytes, full);
-            if (++slot[side] == p.slots[side]) {
-              slot[side] = 0;
-              ++turn[side];
+            bulk_copy_g2s(to + slot * kUnits * ub, p.cache[side] + (base + u0) * ub, bytes, full);
+            if (++slot == slots) {
+              slot = 0;
+              ++turn;
             }
           }
         }
-        // after an abort, wait (bounded) for the copies still landing in the rings: each
+        // after an abort, wait (bounded) for the copies still landing in the ring: each
         // slot's last one
         if (!ok || *reinterpret_cast<volatile int *>(&abort_flag))
-          for (int side = 0; side < 2; ++side)
-            for (int i = 0; i < p.slots[side]; ++i) {
-              const uint32_t n = turn[side] + (i < slot[side] ? 1u : 0u);  // copies into it
-              if (n > 0)
-                mbar_wait_bounded(&bars.raw_full[side][i], (n - 1) & 1u, nullptr, 100000000ull);
-            }
+          for (int i = 0; i < slots; ++i) {
+            const uint32_t n = turn + (i < slot ? 1u : 0u);  // copies into it
+            if (n > 0)
+              mbar_wait_bounded(&bars.raw_full[side][i], (n - 1) & 1u, nullptr, 100000000ull);
+          }
       }
-    } else if (warp < kMmaWarp + 2) {
+    } else {
       // ---------------- MMA issuer of pipe e.  The whole warp walks the steps, so that what an
       // instruction takes is known to be uniform; one elected thread issues.  (By one
       // thread of a diverged warp, with descriptors put together for each, an
@@ -1086,30 +1079,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       ++kseg;
       tc_fence_after();
-      float w0 = 1.0f, w1 = 0.0f;
-      if (!sg.pair && e == 1) {  // to pipe 0, half of O at a time
-        pipe1_ml[r] = make_float2(m, l);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (half) pipes_sync();  // the first half has been read
-#pragma unroll 1
-          for (int c = 0; c < 2 && !idle; ++c) {
-            float v[32];
-            tmem_ld32(tmo + half * 64 + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) exchange[(c * 32 + i) * kTile + r] = v[i];
-          }
-          pipes_sync();  // written
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.ofree[1]);
-        pipes_sync();  // the second half has been read
-        sg = nsg;
-        have = have_next;
-        continue;
-      }
       // The row's place: out (whole items), xo, or this CTA's partial slot.
       const bool whole = sg.j_lo == 0 && sg.j_hi == sg.nt;
       const int R = row0 + r, tok = R / p.G;
@@ -1135,48 +1104,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.items[blockIdx.x] = {sg.first, sg.R, sg.row0, sg.kvh, sg.pair ? 2 * kTile : kTile,
                                static_cast<int>(owner_of(last, all[0], all[1]) - blockIdx.x + 1), 0};
       }
+      // A single tile's O is both pipes' (the same lanes of TMEM), and each writes half
+      // of the dims.
+      float w0 = 1.0f, w1 = 0.0f;
       if (!sg.pair) {
-        pipes_sync();  // pipe 1's first half and (m, l) are written
-        const float2 y = pipe1_ml[r];
-        const float top = fmaxf(m, y.x);
-        w0 = m == -INFINITY ? 0.0f : fast_exp2(m - top);
-        w1 = y.x == -INFINITY ? 0.0f : fast_exp2(y.x - top);
-        l = fmaf(w1, y.y, w0 * l);
-        m = top;
+        pipe_ml[e][r] = make_float2(m, l);
+        tc_fence_before();
+        pipes_sync();  // both pipes' products are done
+        tc_fence_after();
+        const float2 x = pipe_ml[0][r], y = pipe_ml[1][r];
+        m = fmaxf(x.x, y.x);
+        w0 = x.x == -INFINITY ? 0.0f : fast_exp2(x.x - m);
+        w1 = y.x == -INFINITY ? 0.0f : fast_exp2(y.x - m);
+        l = fmaf(w1, y.y, w0 * x.y);
       }
+      const int lo = sg.pair ? 0 : 2 * e, hi = sg.pair ? 4 : lo + 2;
+      const uint32_t o0 = (sg.pair ? tm_o[e] : tm_o[0]) + lane_off, o1 = tm_o[1] + lane_off;
       ro.inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        if (!sg.pair && c == 2) {
-          pipes_sync();  // the first half has been read
-          pipes_sync();  // the second is written
-        }
-        if (idle) continue;
+      for (int c = lo; c < hi && !idle; ++c) {
         float v[32];
-        tmem_ld32(tmo + c * 32, v);
+        tmem_ld32(o0 + c * 32, v);
         tmem_wait_ld();
         if (!sg.pair) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = fmaf(w1, exchange[((c & 1) * 32 + i) * kTile + r], w0 * v[i]);
+          for (int h = 0; h < 2; ++h) {
+            float y[16];
+            tmem_ld16(o1 + c * 32 + 16 * h, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[16 * h + i] = fmaf(w1, y[i], w0 * v[16 * h + i]);
+          }
         }
         if (rot_v) {  // the stages inside 32 columns
           fwht32(v);
-          tmem_st32f(tmo + c * 32, v);
+          tmem_st32f(o0 + c * 32, v);
         } else if (valid) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             ro.put(c * 32 + 8 * i, reinterpret_cast<const float(&)[8]>(v[8 * i]));
         }
       }
-      if (!sg.pair) pipes_sync();  // the second half has been read
-      if (rot_v && !idle) {  // the stages across them, and x = s H y / 16
+      if (rot_v) {  // the stages across them, and x = s H y / 16
         tmem_wait_st();
+        if (!sg.pair) {
+          tc_fence_before();
+          pipes_sync();
+          tc_fence_after();
+        }
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
+        for (int g = lo; g < hi && !idle; ++g) {
           float v[4][8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld8(tmo + c * 32 + 8 * g, v[c]);
+          for (int c = 0; c < 4; ++c) tmem_ld8(o0 + c * 32 + 8 * g, v[c]);
           tmem_wait_ld();
           across32(v, 0.0625f);
 #pragma unroll
@@ -1188,16 +1168,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (rot_k && have_next) load_q(nsg);  // (its way leads through O)
       tc_fence_before();  // O read: the next segment's first product may overwrite it
-      __syncwarp();
+      if (sg.pair) __syncwarp();
+      else pipes_sync();
+      if (rot_k && have_next) {  // (its way leads through O)
+        tc_fence_after();
+        load_q(nsg);
+        tc_fence_before();
+        __syncwarp();
+      }
       if (lane == 0) mbar_arrive(&bars.ofree[e]);
       // weights were lifted: sums of 2^(s - (m - lift))
       const float ml = m == -INFINITY ? m : m - kLift;
-      if (!whole) {
-        if (valid) reinterpret_cast<float2 *>(slot + kTile * kD)[r] = make_float2(ml, l);
-      } else if (valid) {
-        if (p.out.xo) p.out.xml[at] = make_float2(ml, l);
+      if (valid && (sg.pair || e == 0)) {
+        if (!whole)
+          reinterpret_cast<float2 *>(slot + kTile * kD)[r] = make_float2(ml, l);
+        else if (p.out.xo)
+          p.out.xml[at] = make_float2(ml, l);
         else if (p.out.lse)
           p.out.lse[at] = l > 0.0f ? (ml + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
