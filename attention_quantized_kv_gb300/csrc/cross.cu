@@ -78,7 +78,7 @@ constexpr int kPartFloats = kTile * kD + 2 * kTile;
 constexpr int kSlotFloats = 2 * kPartFloats;
 // What an item costs besides its steps (queries, results, the pipeline's fill), in
 // steps of a single tile.
-constexpr int kItemCost = 8;
+constexpr int kItemCost = 12;
 
 // An item whose pieces are to be joined: n of them, of the CTAs from its first on.
 struct __align__(16) JoinItem {

@@ -51,7 +51,6 @@
 #include <cuda_runtime.h>
 
 #include <math.h>
-#include <stdlib.h>
 
 #include "kvq_device.cuh"
 #include "kvq_encode.cuh"
@@ -1459,9 +1458,19 @@ DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms) {
   return pl;
 }
 
+// Own keys behind a prefix: streams (sequence, kv head, head group) per CTA of the
+// short kernel, or 0 for the split and merge kernels.  Whole streams need no second
+// kernel and no partials, but leave SMs idle where few of them are long.  Measured, both
+// with the prefix's own kernels for 64 keys (split and short, f16, in us): 8 streams of 255
+// keys 18.6 and 14.0, of 1023 18.6 and 19.2; 32 of 1023 21.8 and 19.0, of 2047 22.6 and
+// 25.6; 128 of 2047 38 and 30, of 4095 48 and 56; 512 of 2047 124 and 65, of 8191 212 and
+// 185 (turbo4 193 and 107); 64 of 2047 38 and 35, of 4095 40 and 52.
 static int short_streams(const kvq_layer &L, const DecodePlan &pl, int max_len) {
-  const int streams = L.n_seqs * L.n_kv_heads * pl.n_hgroups;
-  if (getenv("SLICES") && !atoi(getenv("SLICES"))) return 0;
+  const int64_t streams = static_cast<int64_t>(L.n_seqs) * L.n_kv_heads * pl.n_hgroups;
+  if (max_len > 1024 + 20 * streams) return 0;
+  // Two CTAs of eight warps an SM first, then fewer warps a stream (q8_0, 1, 2, 4 and 8
+  // streams a CTA): 1024 streams of 255 keys 37.5, 32.9, 33.0 and 41.7 us, of 1023 59, 53,
+  // 68 and 106; 1280 of 255 42, 37, 33 and 42; 4096 of 511 118, 97, 90 and 85.
   int spc = 1;
   while (spc < kWarps && streams / (2 * spc) >= 304) spc *= 2;
   return spc;

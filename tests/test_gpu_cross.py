@@ -240,6 +240,39 @@ def test_one_prefix_for_all(n_seqs, plen, group, pk, pv):
     _check_prefix(L, P, _values(L, table, lens), _values(P, ptable, [plen]), [0] * n_seqs, q, out, None)
 
 
+@pytest.mark.parametrize("ck,cv", [(F16, F16), (Q8, Q4), (F16, T4), (T4, Q8)])
+@pytest.mark.parametrize("group", [4, 12])
+def test_long_own_keys(ck, cv, group):
+    """Few sequences of many own keys, which are split; one of none, one behind no prefix."""
+    lens, plens = [2304, 0, 700, 1], [300, 9]
+    L, table = _filled(4, 1, group, 2304, ck, cv, ck == Q8, lens, 23)
+    P, ptable = _filled(2, 1, group, 512, Q4, F16, False, plens, 24)
+    q = _queries(4, group, 15)
+    out, lse = torch.empty_like(q), torch.empty((4, group), device="cuda")
+    kvq.attn_decode_prefix(L, P, q, SCALE, out, lse, 2304, 512, _prefix_ws(L, P, 2304, 512), group_start=_i32([0, 2, 3]))
+    assert L.err.item() == 0 and P.err.item() == 0
+    _check_prefix(L, P, _values(L, table, lens), _values(P, ptable, plens), [0, 0, 1, None], q, out, lse)
+
+
+@pytest.mark.parametrize("n_seqs,n_kv", [(160, 4), (321, 4), (1024, 3)])
+def test_many_sequences(n_seqs, n_kv):
+    """So many that a block takes two, four or eight of them (the last one less)."""
+    lens = [(11 * s) % 70 for s in range(n_seqs)]
+    L, table = _filled(n_seqs, n_kv, 2 * n_kv, 256, Q8, T4, False, lens, 25)
+    P, ptable = _filled(2, n_kv, 2 * n_kv, 256, Q8, Q8, False, [200, 31], 26)
+    q = _queries(n_seqs, 2 * n_kv, 16)
+    out, lse = torch.empty_like(q), torch.empty((n_seqs, 2 * n_kv), device="cuda")
+    cut = n_seqs // 3
+    kvq.attn_decode_prefix(L, P, q, SCALE, out, lse, 256, 256, _prefix_ws(L, P, 256, 256),
+                           group_start=_i32([0, cut, n_seqs - 1]))
+    assert L.err.item() == 0 and P.err.item() == 0
+    own, shared = _values(L, table, lens), _values(P, ptable, [200, 31])
+    some = sorted({0, 1, 2, 7, 8, 9, cut - 1, cut, cut + 1, n_seqs // 2, n_seqs - 9, n_seqs - 2, n_seqs - 1})
+    for s in some:
+        parts = [(Q8, T4) + own[s]] + ([(Q8, Q8) + shared[int(s >= cut)]] if s < n_seqs - 1 else [])
+        C.check(out[s:s + 1], lse[s:s + 1], C.attend(q[s:s + 1].double(), parts, SCALE), EPS[torch.float16], s)
+
+
 def test_views_of_one_pool():
     """Sequences whose block tables share their first pages: the prefix a view over the shared
     pages, the rest a view behind them; the result is attn_decode's over the whole tables."""
