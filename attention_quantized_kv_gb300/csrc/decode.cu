@@ -1290,7 +1290,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tig = lane & 3, g = lane >> 2;
   const int wps = kWarps / spc, sub = warp % wps, KH = p.n_kv * p.n_hg;
   const int stream = blockIdx.x * spc + warp / wps;
-  grid_dependency_wait();
+  // The kernel before this one joins the prefix's pieces.  It waits for all before
+  // itself and then lets this one start, so that only its own results, wanted at the
+  // end, are still to be waited for.
   grid_launch_dependents();
   float o[8][4];
 #pragma unroll
@@ -1379,6 +1381,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ml_s[warp][2 * tig + 1] = make_float2(m1, l1);
     }
   }
+  grid_dependency_wait();
   __syncthreads();
   const MergeArgs a = {nullptr, nullptr, p.out, p.lse, p.n_q, p.G};
   for (int r = warp; r < 8 * spc; r += kWarps) {
