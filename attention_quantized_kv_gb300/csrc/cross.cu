@@ -77,7 +77,8 @@ constexpr float kLift = 6.0f;
 constexpr int kPartFloats = kTile * kD + 2 * kTile;
 constexpr int kSlotFloats = 2 * kPartFloats;
 // What an item costs besides its steps (queries, results, the pipeline's fill), in
-// steps of a single tile.
+// steps of a single tile.  With 2, 8, 14 and 22 in its place 24 beams over f16 and q8_0
+// states took 65, 53, 57 and 60 us, 3011 rows of eight targets 125, 94, 87 and 90.
 constexpr int kItemCost = 12;
 
 // An item whose pieces are to be joined: n of them, of the CTAs from its first on.
