@@ -547,7 +547,8 @@ KVQ_API int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope
  * without a causal mask.  The pages name none of these; the definitions below
  * are this library's.  Which rows belong to which sequence is said as for
  * kv_append_rope, by row_start (packed) or n_new (padded); an entry out of
- * range sets KVQ_DEVERR_ROWS and that sequence's rows are unspecified.
+ * range sets KVQ_DEVERR_ROWS and that sequence's rows are unspecified.  A call
+ * has at most 2^31 - 1 rows times query heads.
  * ------------------------------------------------------------------------ */
 
 /* kv_append_rope without the rotation: k and v rows (one type; strided) are
@@ -585,7 +586,11 @@ KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t
  * that belong to no sequence are left as they were; a sequence of length 0 gives
  * out = 0 and lse = -inf.  scale > 0.  max_len bounds every seq_lens[s].
  * workspace: device, 16-byte aligned, of any contents; calls that may run
- * concurrently need separate ones.  At most 1024 sequences. */
+ * concurrently need separate ones.  At most 1024 sequences.
+ * Keys and values go through the products as fp16 (quantized ones as a pair of
+ * fp16 numbers that add up to them exactly), softmax weights as fp16, sums as
+ * fp32: a cached value (turbo4: a rotated one) beyond fp16's range makes the
+ * results over it NaN. */
 KVQ_API int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows,
                        const int32_t *n_new, const int32_t *row_start, float scale,
                        const kvq_rows *out, float *lse, int32_t max_len, void *workspace,

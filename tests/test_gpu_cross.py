@@ -315,6 +315,41 @@ def test_prefix_conditions():
         assert P.err.item() & kvq.KVQ_DEVERR_ROWS, bad
 
 
+# ------------------------------------------------------------------ far places
+
+@pytest.mark.parametrize("ck,cv", [(F16, F16), (Q8, F16)])
+def test_pages_past_four_gigabytes(ck, cv):
+    """Pages whose bytes lie past 2^32: the results of the same pages near the pool's start."""
+    n_kv, far = 2, 70000 if ck == Q8 else 36000
+    lens, pages = [600, 256], [[far - 1, 3, far - 7], [far - 2, 0, 0]]
+    near = [[0, 1, 2], [3, 0, 0]]
+    layers = []
+    for n_pages, table in ((far, pages), (4, near)):
+        L = kvq.KVLayer(2, n_kv, 8, 768, ck, cv, n_pages=n_pages, block_table=torch.tensor(table, dtype=torch.int32, device="cuda"))
+        g = torch.Generator(device="cuda").manual_seed(4)
+        x = torch.randn((sum(lens), 2 * n_kv, 128), generator=g, device="cuda").half()
+        kvq.kv_append_rows(L, x[:, :n_kv], x[:, n_kv:], row_start=_i32([0, 600, 856]))
+        assert L.k_cache.numel() > 2 ** 32 or n_pages == 4
+        layers.append(L)
+    got = []
+    for L in layers:
+        q = _queries(9, 8, 3)
+        out, lse = torch.empty_like(q), torch.empty((9, 8), device="cuda")
+        kvq.attn_cross(L, q, SCALE, out, lse, 768, _cross_ws(L, 9, 768), row_start=_i32([0, 4, 9]))
+        one, P = torch.empty_like(q[:2]), kvq.KVLayer(1, n_kv, 8, 768, ck, cv, n_pages=L.n_pages, k_cache=L.k_cache,
+                                                      v_cache=L.v_cache, block_table=L.block_table[:1].contiguous())
+        P.seq_lens.fill_(600)
+        kvq.attn_decode_prefix(L, P, q[:2].contiguous(), SCALE, one, None, 768, 768, _prefix_ws(L, P, 768, 768))
+        rows = [torch.empty((856, n_kv, 128), dtype=torch.float32, device="cuda") for _ in "kv"]
+        kvq.kv_read_rows(L, *rows, row_start=_i32([0, 600, 856]))
+        few = [torch.empty((9, n_kv, 128), dtype=torch.float16, device="cuda") for _ in "kv"]
+        kvq.kv_read_rows(L, *few, row_start=_i32([0, 4, 9]), first=_i32([590, 250]))
+        got.append([out, lse, one, *rows, *few])
+        assert L.err.item() == 0 and P.err.item() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ streams and graphs
 
 def test_graphs_share_a_workspace():
