@@ -34,11 +34,12 @@
 //    they take the first and second half of its every key tile, and each joins and writes
 //    half of the dims at the end.
 //
-// Bound: the tensor cores, from two rows tiles per byte on: a pair's 64 keys cost
-// 2050 cycles of products over split sides (1290 over f16), and took 4600 by one
-// issuing warp, 3450 by one for each pipe and 3000 with the waits and the issue as
-// they are now.  2048 rows x 32 heads over 32768 states (q8_0): 1.27 ms, the tensor pipe
-// busy for 69 % of it.
+// Bound: the tensor cores, where a pair's rows fill its tiles: its 64 keys cost 2050
+// cycles of products over split sides (1290 over f16) and take 2700 to 3000 (4600 by one
+// issuing warp for both pipes).  2048 rows x 32 heads over 32768 states, K q8_0 and V q4_0:
+// 1.18 ms; over 8192 the tensor pipe is busy for 75 % of 0.32 ms.  Where rows are few the
+// codes' conversion, about 1000 cycles for 64 keys of q8_0: 120 beams x 40 heads over 24 inputs
+// of up to 4096 states, K f16 and V q8_0, 48 us (24 at the copy rate).
 #include <cuda_runtime.h>
 
 #include <algorithm>
