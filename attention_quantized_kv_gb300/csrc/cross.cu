@@ -9,11 +9,11 @@
 // key tile that is read; a last odd tile stands alone.
 //
 // Work.  An item is (sequence, kv head, pair or single tile): a run of steps, one
-// per 64 keys.  All items' steps are laid end to end, a pair's counting twice and
-// every item's start a few more, and the CTAs (one per SM) take equal contiguous
-// slices: whole items, and pieces of at most two more.  The rows of a piece go to a
-// partial slot (unnormalised O, max, sum), and a second kernel joins an item's pieces
-// by log-sum-exp in a fixed order.  Lengths and row counts are read on the device.
+// per 64 keys.  All items' steps are laid end to end by what they cost, every item's
+// start with a cost of its own, and the CTAs (one per SM) take equal contiguous slices:
+// whole items, and pieces of at most two more.  The rows of a piece go to a partial slot
+// (unnormalised O, max, sum), and a second kernel joins an item's pieces by log-sum-exp
+// in a fixed order.  Lengths and row counts are read on the device.
 //
 // Inside a CTA (20 warps) nothing is written to HBM but the results: codes are
 // copied in as they lie in the cache, turned into tensor-core operand tiles in
@@ -37,7 +37,7 @@
 // Bound: the tensor cores, where a pair's rows fill its tiles: its 64 keys cost 2050
 // cycles of products over split sides (1290 over f16) and take 2700 to 3000 (4600 by one
 // issuing warp for both pipes).  2048 rows x 32 heads over 32768 states, K q8_0 and V q4_0:
-// 1.18 ms; over 8192 the tensor pipe is busy for 75 % of 0.32 ms.  Where rows are few the
+// 1.13 ms; over 8192 the tensor pipe is busy for 75 % of 0.32 ms.  Where rows are few the
 // codes' conversion, about 1000 cycles for 64 keys of q8_0: 120 beams x 40 heads over 24 inputs
 // of up to 4096 states, K f16 and V q8_0, 48 us (24 at the copy rate).
 #include <cuda_runtime.h>
@@ -77,10 +77,13 @@ constexpr float kLift = 6.0f;
 // (m, l) of every row.
 constexpr int kPartFloats = kTile * kD + 2 * kTile;
 constexpr int kSlotFloats = 2 * kPartFloats;
-// What an item costs besides its steps (queries, results, the pipeline's fill), in
-// steps of a single tile.  With 2, 8, 14 and 22 in its place 24 beams over f16 and q8_0
-// states took 65, 53, 57 and 60 us, 3011 rows of eight targets 125, 94, 87 and 90.
-constexpr int kItemCost = 12;
+// Work: what a step of a single tile and of a pair count (cycle counters: 1300 to 1550
+// and 1900 to 2900), and what an item counts besides its steps (queries, results, the
+// pipeline's fill).  With 10, 13, 16, 20 and 26 for the latter 24 x 5 beams over f16 and
+// q8_0 states took 51, 51, 49, 50 and 52 us, 3011 rows of eight targets 89, 82, 79, 77, 79;
+// other short items gain up to 26.
+constexpr int kSingle = 2, kPair = 3;
+constexpr int kItemCost = 24;
 
 // An item whose pieces are to be joined: n of them, of the CTAs from its first on.
 struct __align__(16) JoinItem {
@@ -116,6 +119,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
                               : a / b;
 }
 
+// x work as steps of weight w, rounded up.
+__device__ __forceinline__ int64_t steps_in(int64_t x, int w) {
+  return w == kPair ? (x + kPair - 1) / kPair : (x + kSingle - 1) / kSingle;
+}
+
 // One sequence's rows and keys.
 struct SeqWork {
   int64_t first;     // first row (token)
@@ -124,10 +132,10 @@ struct SeqWork {
   int blocks, full;  // pairs and the single tile if there is one (singles: tiles); weight
   bool odd;          // the last block is a single tile among pairs
   __device__ __forceinline__ int weight(int blk) const {
-    return odd && blk == blocks - 1 ? 1 : full;
+    return odd && blk == blocks - 1 ? kSingle : full;
   }
   __device__ __forceinline__ int64_t per_head() const {
-    return nt == 0 ? 0 : static_cast<int64_t>(nt) * (full * blocks - (odd ? 1 : 0)) +
+    return nt == 0 ? 0 : static_cast<int64_t>(nt) * (full * blocks - (odd ? kPair - kSingle : 0)) +
                              static_cast<int64_t>(blocks) * kItemCost;
   }
   // position of block blk of kv head kvh, from the sequence's
@@ -143,7 +151,7 @@ __device__ __forceinline__ SeqWork seq_work(const CrossParams &p, int s) {
   w.R = static_cast<int>(n) * p.G;
   w.nt = n > 0 ? (w.len + kKeys - 1) / kKeys : 0;
   const int tiles = (w.R - 1) / kTile + (w.R > 0);
-  w.full = p.singles ? 1 : 2;
+  w.full = p.singles ? kSingle : kPair;
   w.blocks = p.singles ? tiles : (tiles + 1) / 2;
   w.odd = !p.singles && (tiles & 1) != 0;
   return w;
@@ -158,7 +166,7 @@ __device__ __forceinline__ void block_at(const SeqWork &w, int64_t off, int &kvh
 // CTAs that get a slice: each at least as long as a step, so that every CTA
 // between an item's first and last has a step of it.
 __device__ __forceinline__ int64_t cross_ctas(int64_t W, int grid) {
-  return max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), W / 2));
+  return max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), W / (2 * kSingle)));
 }
 // The CTA whose slice [W c / P, W (c + 1) / P) holds position x.
 __device__ __forceinline__ int64_t owner_of(int64_t x, int64_t W, int64_t P) {
@@ -180,20 +188,20 @@ struct SegIter {
   __device__ __forceinline__ bool next(const CrossParams &p, Segment &g) {
     while (at < s1) {
       const int wt = w.weight(blk);
-      // its steps follow its cost (wt is 1 or 2)
+      // its steps follow its cost
       const int64_t from = at + kItemCost;
-      const int64_t lo = s0 <= from ? 0 : min(static_cast<int64_t>(w.nt), (s0 - from + wt - 1) >> (wt - 1));
-      const int64_t hi = s1 <= from ? 0 : min(static_cast<int64_t>(w.nt), (s1 - from + wt - 1) >> (wt - 1));
+      const int64_t lo = s0 <= from ? 0 : min(static_cast<int64_t>(w.nt), steps_in(s0 - from, wt));
+      const int64_t hi = s1 <= from ? 0 : min(static_cast<int64_t>(w.nt), steps_in(s1 - from, wt));
       g.first = w.first;
       g.R = w.R;
-      g.row0 = blk * (w.full * kTile);
+      g.row0 = blk * (p.singles ? kTile : 2 * kTile);
       g.s = s;
       g.kvh = kvh;
       g.len = w.len;
       g.nt = w.nt;
       g.j_lo = static_cast<int>(lo);
       g.j_hi = static_cast<int>(hi);
-      g.pair = wt == 2;
+      g.pair = wt == kPair;
       g.inside = from >= s0;
       g.at = from;
       at = from + static_cast<int64_t>(wt) * w.nt;
@@ -1102,7 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         ro.half = static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head;
       if (!whole && sg.inside && threadIdx.x == 0) {
-        const int64_t last = sg.at + static_cast<int64_t>(sg.nt - 1) * (sg.pair ? 2 : 1);
+        const int64_t last = sg.at + static_cast<int64_t>(sg.nt - 1) * (sg.pair ? kPair : kSingle);
         p.items[blockIdx.x] = {sg.first, sg.R, sg.row0, sg.kvh, sg.pair ? 2 * kTile : kTile,
                                static_cast<int>(owner_of(last, all[0], all[1]) - blockIdx.x + 1), 0};
       }
