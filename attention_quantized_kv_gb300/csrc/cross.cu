@@ -873,11 +873,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = sg.j_hi - sg.j_lo;
       for (int j = 0; j < n; ++j, ++u) {
         const int buf = u % kBufs;
-        ok = mbar_wait_bounded(&bars.raw_full[side][slot], turn & 1u, &abort_flag) &&
-             (u < kBufs || mbar_wait_bounded(&bars.tile_empty[side][buf],
-                                             static_cast<uint32_t>(u / kBufs - 1) & 1u, &abort_flag));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        uint64_t *const raw = &bars.raw_full[side][slot], *const place = &bars.tile_empty[side][buf];
+        const uint32_t gone = static_cast<uint32_t>(u / kBufs - 1) & 1u;
+        const bool there = mbar_try_wait(raw, turn & 1u);  // asked for together: beams 50.9 -> 49.6 us
+        const bool free = u < kBufs || mbar_try_wait(place, gone);
+        if (!__all_sync(0xffffffffu, there & free)) {
+          ok = mbar_wait_bounded(raw, turn & 1u, &abort_flag) &&
+               (u < kBufs || mbar_wait_bounded(place, gone, &abort_flag));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         const int live = sg.len - (sg.j_lo + j) * kKeys - unit * kUnitTokens;
         unit_to_tile(side, codec, src + slot * slot_bytes,
                      tiles + (side * kBufs + buf) * kTileBytes, unit, live, lane);
