@@ -37,7 +37,7 @@
 // Bound: the tensor cores, where a pair's rows fill its tiles: its 64 keys cost 2050
 // cycles of products over split sides (1290 over f16) and take 2640 (4600 by one issuing
 // warp for both pipes).  2048 rows x 32 heads over 32768 states, K q8_0 and V q4_0:
-// 1.13 ms; over 8192 the tensor pipe is busy for 75 % of 0.32 ms.  Where rows are few the
+// 1.11 ms; over 8192 the tensor pipe is busy for 78 % of 0.30 ms.  Where rows are few the
 // codes' conversion, about 1000 cycles for 64 keys of q8_0: 120 beams x 40 heads over 24 inputs
 // of up to 4096 states, K f16 and V q8_0, 48 us (24 at the copy rate).
 #include <cuda_runtime.h>
