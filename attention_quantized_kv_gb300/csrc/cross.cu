@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int lo = sg.pair ? 0 : 2 * e, hi = sg.pair ? 4 : lo + 2;
       const uint32_t o0 = (sg.pair ? tm_o[e] : tm_o[0]) + lane_off, o1 = tm_o[1] + lane_off;
-      ro.inv = l > 0.0f ? 1.0f / l : 0.0f;
+      ro.inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
       for (int c = lo; c < hi && !idle; ++c) {
         float v[32];
@@ -1195,15 +1195,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(&bars.ofree[e]);
-      // weights were lifted: sums of 2^(s - (m - lift))
-      const float ml = m == -INFINITY ? m : m - kLift;
+      // Weights were lifted: sums of 2^(s - (m - lift)).  A sum that is no number, where no
+      // maximum tells of it, goes with an infinite one, so that no join leaves it out.
+      const float ml = l != l ? INFINITY : m == -INFINITY ? m : m - kLift;
       if (valid && (sg.pair || e == 0)) {
         if (!whole)
           reinterpret_cast<float2 *>(slot + kTile * kD)[r] = make_float2(ml, l);
         else if (p.out.xo)
           p.out.xml[at] = make_float2(ml, l);
         else if (p.out.lse)
-          p.out.lse[at] = l > 0.0f ? (ml + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          p.out.lse[at] = l == 0.0f ? -INFINITY : (ml + log2f(l)) * 0.69314718055994531f;
       }
       sg = nsg;
       have = have_next;
@@ -1281,7 +1282,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   }
   const int64_t to = row * p.n_q + head;
   RowOut ro;
-  ro.inv = L > 0.0f ? 1.0f / L : 0.0f;
+  ro.inv = L == 0.0f ? 0.0f : 1.0f / L;
   ro.bf16 = p.q_bf16;
   ro.full = p.out.xo ? p.out.xo + to * kD : nullptr;
   ro.step = 4;
@@ -1290,7 +1291,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   if (g8 == 0) {
     if (p.out.xo) p.out.xml[to] = make_float2(M, L);
     else if (p.out.lse)
-      p.out.lse[to] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      p.out.lse[to] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
   }
 }
 

@@ -601,21 +601,24 @@ struct MergeArgs {
 };
 
 // One head's merged row: o = acc / L (rotated back for turbo4 V), fp16, and
-// its natural-log lse (M is in log2 units).  xml, xo: one more part, not rotated.
-template <bool ROT>
+// its natural-log lse (M is in log2 units).  SHARED: behind a prefix; xml, xo: its part,
+// not rotated.  There a sum that is no number makes the row NaN whatever its maximum (in
+// a prefix's part it comes with an infinite one).
+template <bool ROT, bool SHARED>
 __device__ __forceinline__ void merge_write(const MergeArgs &p, int seq, int kvh, int hg, int h,
                                             int lane, float4 acc, float M, float L,
                                             float2 xml = make_float2(-INFINITY, 0.0f),
                                             float4 xo = make_float4(0.0f, 0.0f, 0.0f, 0.0f)) {
   float wx = 0.0f, w = 1.0f;
-  if (xml.x != -INFINITY) {
+  if (SHARED && L != L) M = INFINITY;
+  if (SHARED && xml.x != -INFINITY) {
     const float top = fmaxf(M, xml.x);
     w = M == -INFINITY ? 0.0f : fast_exp2(M - top);
     wx = fast_exp2(xml.x - top);
     L = fmaf(wx, xml.y, w * L);
     M = top;
   }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L > 0.0f || (SHARED && L != L) ? 1.0f / L : 0.0f;
   const int64_t row = static_cast<int64_t>(seq) * p.n_q + kvh * p.G + hg * 8 + h;
   const float own = w * inv;
   float ov[4] = {acc.x * own, acc.y * own, acc.z * own, acc.w * own};
@@ -628,7 +631,9 @@ __device__ __forceinline__ void merge_write(const MergeArgs &p, int seq, int kvh
     ov[3] = fmaf(xo.w, wx, ov[3]);
   }
   const __half2 o01 = __floats2half2_rn(ov[0], ov[1]), o23 = __floats2half2_rn(ov[2], ov[3]);
-  const float lse = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  const float lse = L > 0.0f              ? (M + log2f(L)) * 0.69314718055994531f
+                    : SHARED && L != L ? L
+                                       : -INFINITY;
   __half2 *dst = reinterpret_cast<__half2 *>(p.out + row * kD) + lane * 2;
   dst[0] = o01;
   dst[1] = o23;
@@ -1210,11 +1215,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
   int64_t sa = 0, sb = 0;
   float2 mla, mlb;
   float4 x[kMergeRows];
+  // (max, sum) of a part; behind a prefix one whose sum is no number has an infinite maximum
+  auto part_ml = [&](int64_t slot) {
+    float2 y = __ldcg(ml + slot * 8);
+    if (SHARED && y.y != y.y) y.x = INFINITY;
+    return y;
+  };
   auto load_window = [&](int base) {
     sa = base + lane < n_live ? slot_of(base + lane) : 0;
     sb = base + 32 + lane < n_live ? slot_of(base + 32 + lane) : 0;
-    mla = base + lane < n_live ? __ldcg(ml + sa * 8) : make_float2(-INFINITY, 0.0f);
-    mlb = base + 32 + lane < n_live ? __ldcg(ml + sb * 8) : make_float2(-INFINITY, 0.0f);
+    mla = base + lane < n_live ? part_ml(sa) : make_float2(-INFINITY, 0.0f);
+    mlb = base + 32 + lane < n_live ? part_ml(sb) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
     for (int t = 0; t < kMergeRows; ++t) {
       const int jr = warp + kMergeWarps * t;  // window-relative part
@@ -1225,7 +1236,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
   };
   load_window(0);
   float M = fmaxf(mla.x, mlb.x);
-  for (int j = 64 + lane; j < n_live; j += 32) M = fmaxf(M, __ldcg(ml + slot_of(j) * 8).x);
+  for (int j = 64 + lane; j < n_live; j += 32) M = fmaxf(M, part_ml(slot_of(j)).x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float L = 0.0f;
@@ -1265,10 +1276,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
     if (SHARED && behind_prefix(p.prefix, seq)) {
       const int64_t row = static_cast<int64_t>(seq) * p.a.n_q + kvh * p.a.G + hg * 8 + h;
       const float2 x = p.prefix.xml[row];
-      merge_write<ROT>(p.a, seq, kvh, hg, h, lane, acc, M, L, x,
+      merge_write<ROT, SHARED>(p.a, seq, kvh, hg, h, lane, acc, M, L, x,
                        reinterpret_cast<const float4 *>(p.prefix.xo + row * kD)[lane]);
     } else {
-      merge_write<ROT>(p.a, seq, kvh, hg, h, lane, acc, M, L);
+      merge_write<ROT, SHARED>(p.a, seq, kvh, hg, h, lane, acc, M, L);
     }
   }
 }
@@ -1392,10 +1403,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float2 ml = ml_s[leader][h];
     if (behind_prefix(x, seq)) {
       const int64_t row = static_cast<int64_t>(seq) * p.n_q + kvh * p.G + hg * 8 + h;
-      merge_write<CV == KVQ_TURBO4>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y, x.xml[row],
-                                    reinterpret_cast<const float4 *>(x.xo + row * kD)[lane]);
+      merge_write<CV == KVQ_TURBO4, true>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y, x.xml[row],
+                                          reinterpret_cast<const float4 *>(x.xo + row * kD)[lane]);
     } else {
-      merge_write<CV == KVQ_TURBO4>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y);
+      merge_write<CV == KVQ_TURBO4, true>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y);
     }
   }
 }

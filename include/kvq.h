@@ -584,7 +584,8 @@ KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t
  * optional fp32 [n_rows][n_q_heads], natural log.  Rows belong to sequences by
  * n_new or row_start; both NULL: row s to sequence s (n_rows = n_seqs).  Rows
  * that belong to no sequence are left as they were; a sequence of length 0 gives
- * out = 0 and lse = -inf.  scale > 0.  max_len bounds every seq_lens[s].
+ * out = 0 and lse = -inf, a NaN in a row's query or in one of its keys NaN in
+ * both.  scale > 0.  max_len bounds every seq_lens[s].
  * workspace: device, 16-byte aligned, of any contents; calls that may run
  * concurrently need separate ones.  At most 1024 sequences.
  * Keys and values go through the products as fp16 (quantized ones as a pair of
@@ -610,7 +611,8 @@ KVQ_API int attn_decode_prefix_workspace(const kvq_layer *layer, const kvq_layer
  * paged layers may be views of one pool, the prefix's block table over the shared
  * pages, the layer's over the rest (their lengths then count those alone).
  * q, out, lse, max_len: as attn_decode (q 16-byte aligned and not meeting out;
- * scale > 0); max_prefix bounds the prefix's lengths.  workspace: as attn_cross.
+ * scale > 0) but for a NaN in a query or a key, which makes lse NaN with the row;
+ * max_prefix bounds the prefix's lengths.  workspace: as attn_cross.
  * Conditions of the prefix (and of group_start) are set in its own err word. */
 KVQ_API int attn_decode_prefix(const kvq_layer *layer, const kvq_layer *prefix,
                                const int32_t *group_start, const void *q, float scale,
