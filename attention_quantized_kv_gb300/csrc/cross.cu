@@ -34,6 +34,15 @@
 //    they take the first and second half of its every key tile, and each joins and writes
 //    half of the dims at the end.
 //
+// fp16 operands do not hold everything that a cache and fp32 do: a cached value past 65504
+// (codes and scales go to 8 * 10^6; fp16 rows reach 65532), a bf16 query or a rotated one
+// past it, scores so large (2^22 of an exponent) that a step of fp32 between them is no
+// longer small against a weight's range.  The first three give NaN (as two parts: an
+// infinity and its opposite), the last is seen in the maximum.  Where a CTA meets a row that
+// is NaN it computes that piece of it anew at its end, in fp32, a warp a row, key by key:
+// right and slow (2048 rows x 32 heads over 32768 states, one value past 65504 in a head:
+// 1.1 -> 570 ms; one such query: 19 ms; a NaN in a query ends it at the first key).
+//
 // Bound: the tensor cores, where a pair's rows fill its tiles: its 64 keys cost 2050
 // cycles of products over split sides (1290 over f16) and take 2640 (4600 by one issuing
 // warp for both pipes).  2048 rows x 32 heads over 32768 states, K q8_0 and V q4_0:
@@ -49,6 +58,7 @@
 #include "kvq_launch.h"
 #include "kvq_packed.cuh"
 #include "kvq_rope.cuh"
+#include "kvq_row_decode.cuh"
 #include "kvq_tcgen05.cuh"
 
 namespace kvq {
@@ -72,6 +82,9 @@ constexpr float kRaise = 8.0f;                    // log2 units, as in the prefi
 // Weights are held as 2^(s - m + 6): at most 2^14 in fp16, and 2^6 further from
 // its subnormals than 2^(s - m).
 constexpr float kLift = 6.0f;
+// From here on (log2 units) a maximum is too large for fp16 weights: 2^(s - m + 6 + 8) and
+// the steps of s and of m, 1 or more each from 2^24, leave fp16's range.
+constexpr float kFar = 0x1p22f;
 // A partial tile: O as [32 groups of 4 dims][128 rows], so that a warp's rows are
 // written and read as whole lines (row by row the lines' parts took 8000 cycles), then
 // (m, l) of every row.
@@ -539,6 +552,135 @@ __device__ __forceinline__ void commit_if(bool leader, uint64_t *bar) {
       : "memory");
 }
 
+// max(a, b, c), NaN if one of them is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// ------------------------------------------------------------------ rows in fp32
+
+// Where a segment's piece of a row and head lies: its fp32 O (groups of 4 dims `step` floats
+// apart) or its 16-bit row, and its (m, l) or lse.
+struct Piece {
+  float *full;
+  int step;
+  float2 *ml;
+  uint8_t *half;
+  float *lse;
+};
+__device__ __forceinline__ Piece piece_of(const CrossParams &p, const Segment &g, int in) {
+  const int R = g.row0 + in, tok = R / p.G, head = g.kvh * p.G + R - tok * p.G;
+  const int64_t row = g.first + tok, at = row * p.n_q + head;
+  if (g.j_lo > 0 || g.j_hi < g.nt) {
+    float *const part = p.part +
+                        (2 * static_cast<int64_t>(blockIdx.x) + (g.inside ? 1 : 0)) * kSlotFloats +
+                        in / kTile * kPartFloats;
+    const int r = in % kTile;
+    return {part + 4 * r, 4 * kTile, reinterpret_cast<float2 *>(part + kTile * kD) + r, nullptr, nullptr};
+  }
+  if (p.out.xo) return {p.out.xo + at * kD, 4, p.out.xml + at, nullptr, nullptr};
+  return {nullptr, 0, nullptr, static_cast<uint8_t *>(p.out.out) + row * p.out_row + head * p.out_head,
+          p.out.lse ? p.out.lse + at : nullptr};
+}
+
+// Whether the piece is NaN somewhere (all 32 lanes).
+__device__ __forceinline__ bool piece_is_nan(const CrossParams &p, const Piece &y, int lane) {
+  float x[4], l = 0.0f;
+  if (y.half) {
+    if (p.q_bf16) load4<KVQ_T_BF16>(y.half + 8 * lane, x);
+    else load4<KVQ_T_F16>(y.half + 8 * lane, x);
+  } else {
+    load4<KVQ_T_F32>(y.full + lane * y.step, x);
+    l = y.ml->y;
+  }
+  const float most = fmax3_nan(fmax3_nan(x[0], x[1], x[2]), x[3], l);
+  return __any_sync(0xffffffffu, most != most);
+}
+
+// A segment's piece of the block's row `in`, by a warp, lane l dims 4 l ..: every key as
+// kvq_row_decode.cuh has it, its weight against the running maximum, sums of 256 keys added
+// up.  A NaN among the weights ends it: nothing changes it any more.
+__device__ __forceinline__ void piece_in_fp32(const CrossParams &p, const Segment &g, int in, int lane) {
+  const int R = g.row0 + in, tok = R / p.G, head = g.kvh * p.G + R - tok * p.G;
+  const uint8_t *src = p.q + (g.first + tok) * p.q_row + head * p.q_head + 8 * lane;
+  float q[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.q_bf16) load4<KVQ_T_BF16>(src, q);
+  else load4<KVQ_T_F16>(src, q);
+  float m = -INFINITY, l = 0.0f, lp = 0.0f;
+  const int t0 = g.j_lo * kKeys, t1 = min(g.len, g.j_hi * kKeys);
+  int64_t base = (static_cast<int64_t>(g.s) * p.n_kv + g.kvh) * (p.capacity / kUnitTokens);
+#pragma unroll 1
+  for (int t = t0; t < t1 && lp == lp; ++t) {
+    constexpr int kPageTokens = kPageUnits * kUnitTokens;
+    if (t == t0 || t % kPageTokens == 0) {
+      const int page = t / kPageTokens;
+      if (p.table)  // (an unmapped page: pool page 0, as the copies have it)
+        base = (static_cast<int64_t>(max(0, page_of(p.table, p.pages_per_seq, p.n_pages, g.s, page))) *
+                    p.n_kv + g.kvh) * kPageUnits - static_cast<int64_t>(page) * kPageUnits;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] += part[i];
+        part[i] = 0.0f;
+      }
+      l += lp;
+      lp = 0.0f;
+    }
+    const int64_t unit = base + t / kUnitTokens;
+    float x[4];
+    decode_row_lane<0>(p.codec[0], p.cache[0] + unit * unit_bytes(p.codec[0]), t % kUnitTokens, lane, x);
+    float z = q[0] * x[0] + q[1] * x[1] + q[2] * x[2] + q[3] * x[3];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    z = __fmul_rn(z, p.scale_log2);  // (rounded: z - m below is then exact near it)
+    if (z > m) {
+      const float a = fast_exp2(m - z);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] *= a;
+        part[i] *= a;
+      }
+      l *= a;
+      lp *= a;
+      m = z;
+    }
+    const float w = z == -INFINITY ? 0.0f : fast_exp2(z - m);
+    lp += w;
+    decode_row_lane<1>(p.codec[1], p.cache[1] + unit * unit_bytes(p.codec[1]), t % kUnitTokens, lane, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[i] = fmaf(w, x[i], part[i]);
+  }
+  l += lp;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = l != l ? l : acc[i] + part[i];
+  if (l != l) m = INFINITY;  // (as above: no join leaves it out)
+  const Piece y = piece_of(p, g, in);
+  if (y.full) {
+    store4<KVQ_T_F32>(y.full + lane * y.step, acc);
+    if (lane == 0) *y.ml = make_float2(m, l);
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] *= inv;
+  if (p.q_bf16) store4<KVQ_T_BF16>(y.half + 8 * lane, acc);
+  else store4<KVQ_T_F16>(y.half + 8 * lane, acc);
+  if (y.lse && lane == 0)
+    *y.lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// The pieces of a CTA's rows that are NaN (all warps, once its results are written).  (A call
+// of its own in the kernel costs the loops before it registers: 3011 rows 87 -> 93 us.)
+__device__ __forceinline__ void nan_rows_in_fp32(const CrossParams &p, SegIter it, Segment g, int warp,
+                                              int lane) {
+  do {
+    const int rows = min(g.R - g.row0, g.pair ? 2 * kTile : kTile);
+    for (int in = warp; in < rows; in += kThreads / 32)
+      if (piece_is_nan(p, piece_of(p, g, in), lane)) piece_in_fp32(p, g, in, lane);
+  } while (it.next(p, g));
+}
+
 // Both softmax pipes (256 threads).
 __device__ __forceinline__ void pipes_sync() {
   asm volatile("bar.sync 1, 256;\n" ::: "memory");
@@ -555,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int have_first;
   __shared__ int64_t all[2];     // all work, and the CTAs that share it
   __shared__ float2 pipe_ml[2][kTile];  // of a single tile's pipes
+  __shared__ int any_nan;               // among the CTA's rows
   uint8_t *tiles = smem, *ring = smem + 2 * kBufs * kTileBytes;  // operand tiles of K, of V; codes
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);  // (uniform)
   const int lane = threadIdx.x & 31;
@@ -573,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kCopyWarp) {
     if (lane == 0) {
       abort_flag = 0;
+      any_nan = 0;
       for (int i = 0; i < 2 * kMaxSlots; ++i) {
         mbar_init(&bars.raw_full[0][i], 1);
         mbar_init(&bars.raw_empty[0][i], kUnits);  // one arrival per unit
@@ -981,8 +1125,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               uint32_t *y = reinterpret_cast<uint32_t *>(&x[k]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[i] = pack_half2(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xffff0000u));
+              for (int i = 0; i < 4; ++i) {
+                // (y 0 + y: an infinity, of a value past fp16's, becomes NaN)
+                const uint32_t z =
+                    pack_half2(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xffff0000u));
+                const __half2 h = *reinterpret_cast<const __half2 *>(&z);
+                const __half2 v = __hfma2(h, __float2half2_rn(0.0f), h);
+                y[i] = *reinterpret_cast<const uint32_t *>(&v);
+              }
             }
           }
           const uint32_t w[16] = {x[0].x, x[0].y, x[2].x, x[2].y, x[0].z, x[0].w, x[2].z, x[2].w,
@@ -1005,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = sg.j_hi - sg.j_lo, cnt = sg.pair ? 2 * n : n;
       const int row0 = sg.row0 + (sg.pair ? e * kTile : 0);
       const bool idle = row0 + quad * 32 >= sg.R;  // no row in this warp
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f, far = 0.0f;
       // After an abort (ok false) the segments still run to the end without waits,
       // so that both pipes meet at the same barriers.
       for (int i = 0; i < cnt && ok; ++i) {
@@ -1066,6 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mnew;
           // P = exp2(s * scale_log2 - m + lift) as fp16 pairs over S, and the row's sum.
           const float nm = m == -INFINITY ? 0.0f : kLift - m;
+          far = fmaxf(far, fabsf(nm));
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
           uint32_t pk[kHalf / 2];
@@ -1096,6 +1247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       ++kseg;
       tc_fence_after();
+      if (far >= kFar) l = NAN;
       // The row's place: out (whole items), xo, or this CTA's partial slot.
       const bool whole = sg.j_lo == 0 && sg.j_hi == sg.nt;
       const int R = row0 + r, tok = R / p.G;
@@ -1138,6 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = sg.pair ? 0 : 2 * e, hi = sg.pair ? 4 : lo + 2;
       const uint32_t o0 = (sg.pair ? tm_o[e] : tm_o[0]) + lane_off, o1 = tm_o[1] + lane_off;
       ro.inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float nan = l;
 #pragma unroll 1
       for (int c = lo; c < hi && !idle; ++c) {
         float v[32];
@@ -1152,6 +1305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[16 * h + i] = fmaf(w1, y[i], w0 * v[16 * h + i]);
           }
+        }
+        if (p.codec[1] != KVQ_F16) {  // (of split values past fp16's range)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) nan = fmax3_nan(nan, v[i], v[i + 1]);
         }
         if (rot_v) {  // the stages inside 32 columns
           fwht32(v);
@@ -1185,6 +1342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (valid && nan != nan) any_nan = 1;
       tc_fence_before();  // O read: the next segment's first product may overwrite it
       if (sg.pair) __syncwarp();
       else pipes_sync();
@@ -1221,6 +1379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (any_nan) nan_rows_in_fp32(p, begin, first_seg, warp, lane);
 }
 
 // ------------------------------------------------------------------ joining the pieces

@@ -579,8 +579,8 @@ KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t
  * head h: softmax(scale q k^T) v over the tokens t < seq_lens[s] of kv head
  * h / (n_q/n_kv); cross attention to an encoder's states, whose lengths have
  * nothing to do with the rows'.
- * q: rows [n_rows][n_q_heads][128], fp16 or bf16 (taken as fp16: rounded, and
- * infinite beyond its range); out: rows of the same type, not meeting q; lse:
+ * q: rows [n_rows][n_q_heads][128], fp16 or bf16 (rounded to fp16 first, within
+ * its range); out: rows of the same type, not meeting q; lse:
  * optional fp32 [n_rows][n_q_heads], natural log.  Rows belong to sequences by
  * n_new or row_start; both NULL: row s to sequence s (n_rows = n_seqs).  Rows
  * that belong to no sequence are left as they were; a sequence of length 0 gives
@@ -590,8 +590,9 @@ KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t
  * concurrently need separate ones.  At most 1024 sequences.
  * Keys and values go through the products as fp16 (quantized ones as a pair of
  * fp16 numbers that add up to them exactly), softmax weights as fp16, sums as
- * fp32: a cached value (turbo4: a rotated one) beyond fp16's range makes the
- * results over it NaN. */
+ * fp32.  Rows for which that does not do - a cached value (turbo4: a rotated
+ * one) or a query past 65504, scores past 2^22 - are computed in fp32 instead,
+ * key by key: many times slower. */
 KVQ_API int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows,
                        const int32_t *n_new, const int32_t *row_start, float scale,
                        const kvq_rows *out, float *lse, int32_t max_len, void *workspace,
@@ -612,6 +613,7 @@ KVQ_API int attn_decode_prefix_workspace(const kvq_layer *layer, const kvq_layer
  * pages, the layer's over the rest (their lengths then count those alone).
  * q, out, lse, max_len: as attn_decode (q 16-byte aligned and not meeting out;
  * scale > 0) but for a NaN in a query or a key, which makes lse NaN with the row;
+ * the prefix's keys and values are taken as attn_cross takes them;
  * max_prefix bounds the prefix's lengths.  workspace: as attn_cross.
  * Conditions of the prefix (and of group_start) are set in its own err word. */
 KVQ_API int attn_decode_prefix(const kvq_layer *layer, const kvq_layer *prefix,
