@@ -1459,7 +1459,8 @@ DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms) {
   // short contexts spread over enough CTAs that each warp has about one
   // unit (a 4096-key layer: 16.9 -> 14.9 us against 32 units per CTA),
   // without splitting into partials that hold less than a unit per warp.
-  int64_t grid = static_cast<int64_t>(num_sms > 0 ? num_sms : 148) * 2;
+  pl.sms = num_sms > 0 ? num_sms : 148;
+  int64_t grid = static_cast<int64_t>(pl.sms) * 2;
   const int64_t by_work = (max_items * upi + 7) / 8;
   if (grid > by_work) grid = by_work;
   if (grid < 1) grid = 1;
@@ -1474,19 +1475,30 @@ DecodePlan plan_decode(const kvq_layer &L, int max_len, int num_sms) {
 
 // Own keys behind a prefix: streams (sequence, kv head, head group) per CTA of the
 // short kernel, or 0 for the split and merge kernels.  Whole streams need no second
-// kernel and no partials, but leave SMs idle where few of them are long.  Measured, both
-// with the prefix's own kernels for 64 keys (split and short, f16, in us): 8 streams of 255
-// keys 18.6 and 14.0, of 1023 18.6 and 19.2; 32 of 1023 21.8 and 19.0, of 2047 22.6 and
-// 25.6; 128 of 2047 38 and 30, of 4095 48 and 56; 512 of 2047 124 and 65, of 8191 212 and
-// 185 (turbo4 193 and 107); 64 of 2047 38 and 35, of 4095 40 and 52.
+// kernel and no partials, and no search where each begins, but one long stream among short
+// ones holds its warps while the others are done, so a warp's share of the longest is
+// bounded.  The lengths are the device's: max_len stands for the longest.  Measured, the
+// prefix's own kernels for 64 keys with them, in us (split, short):
+//   few streams (f16): 8 of 255 keys 18.6, 14.0, of 1023 18.6, 19.2; 32 of 1023 21.8,
+//   19.0, of 2047 22.6, 25.6; 128 of 2047 38, 30, of 4095 48, 56;
+//   one of 8000 keys, the rest of 200 (q8_0): 512 streams 65, 87; 1024 104, 101; 4096 169,
+//   150; 8192 573, 202; of 20,000 keys, with up to eight streams a CTA, 1024: 110, 362; 4096:
+//   193, 1482; lengths spread evenly up to 8000: 182, 118; 344, 196; 1239, 724; 2908, 1412;
+//   all of 8000: 212, 210; 381, 386; 1339, 1385; 2896, 2711.
+constexpr int kWarpKeys = 1024;   // of the longest stream, a warp at most: 8192 for eight
+// with more than one stream a CTA (1, 2, 4 and 8; one of 2047 keys, the rest of 200): 1024
+// streams 51, 62, 90, 155 us; 4096 108, 96, 125, 187; 8192 200, 161, 162, 225
+constexpr int kSharedWarpKeys = 512;
 static int short_streams(const kvq_layer &L, const DecodePlan &pl, int max_len) {
   const int64_t streams = static_cast<int64_t>(L.n_seqs) * L.n_kv_heads * pl.n_hgroups;
-  if (max_len > 1024 + 20 * streams) return 0;
+  if (max_len > 1024 + 20 * streams || max_len > kWarps * kWarpKeys) return 0;
   // Two CTAs of eight warps an SM first, then fewer warps a stream (q8_0, 1, 2, 4 and 8
-  // streams a CTA): 1024 streams of 255 keys 37.5, 32.9, 33.0 and 41.7 us, of 1023 59, 53,
-  // 68 and 106; 1280 of 255 42, 37, 33 and 42; 4096 of 511 118, 97, 90 and 85.
+  // streams a CTA): 1024 streams of 255 keys 48, 44, 42, 49 us, of 1023 86, 82, 80, 105;
+  // 4096 of 511 154, 135, 137, 137; 8192 of 255 209, 169, 152, 156.
   int spc = 1;
-  while (spc < kWarps && streams / (2 * spc) >= 304) spc *= 2;
+  while (spc < kWarps && streams / (2 * spc) >= 2 * pl.sms &&
+         static_cast<int64_t>(max_len) * 2 * spc <= kWarps * kSharedWarpKeys)
+    spc *= 2;
   return spc;
 }
 

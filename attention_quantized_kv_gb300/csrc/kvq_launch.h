@@ -29,6 +29,7 @@ constexpr int kDecodeMaxStreams = kDecodeTicketBytes / 4 - 1;  // streams per ca
 
 struct DecodePlan {
   int n_hgroups = 1;      // groups of up to 8 query heads per kv head
+  int sms = 0;            // the device's SMs
   int grid = 1;           // CTAs, each an equal slice of the (stream, unit) space
   int64_t slots = 0;      // partial slots: grid + streams
   int64_t ticket_bytes = 0;  // workspace: the counter region (zero between calls)

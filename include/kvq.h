@@ -614,7 +614,10 @@ KVQ_API int attn_decode_prefix_workspace(const kvq_layer *layer, const kvq_layer
  * q, out, lse, max_len: as attn_decode (q 16-byte aligned and not meeting out;
  * scale > 0) but for a NaN in a query or a key, which makes lse NaN with the row;
  * the prefix's keys and values are taken as attn_cross takes them;
- * max_prefix bounds the prefix's lengths.  workspace: as attn_cross.
+ * max_prefix bounds the prefix's lengths.  max_len also chooses how the own keys
+ * are read (whole sequences up to 1024 keys and 20 more for each sequence and kv
+ * head, at most 8192; split over the GPU beyond): a bound far above the lengths
+ * makes short ones slower.  workspace: as attn_cross.
  * Conditions of the prefix (and of group_start) are set in its own err word. */
 KVQ_API int attn_decode_prefix(const kvq_layer *layer, const kvq_layer *prefix,
                                const int32_t *group_start, const void *q, float scale,
