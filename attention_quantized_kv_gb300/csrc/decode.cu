@@ -1128,9 +1128,19 @@ struct MergeParams {
   PrefixPart prefix;  // SHARED: one more part per row
 };
 
-// Whether sequence `seq` has a part from a shared prefix.
-__device__ __forceinline__ bool behind_prefix(const PrefixPart &p, int seq) {
-  return !p.group_start || (seq >= p.group_start[0] && seq < p.group_start[p.n_groups]);
+// Whether sequence `seq` of n has a part from a shared prefix (all 32 lanes): one of the
+// groups holds it whose entries are in range, as the attention kernel takes them.
+__device__ __forceinline__ bool behind_prefix(const PrefixPart &p, int seq, int n, int lane) {
+  if (!p.group_start) return true;
+  for (int base = 0; base < p.n_groups; base += 32) {
+    bool in = false;
+    if (base + lane < p.n_groups) {
+      const int a = p.group_start[base + lane], b = p.group_start[base + lane + 1];
+      in = a >= 0 && a <= seq && seq < b && b <= n;
+    }
+    if (__any_sync(0xffffffffu, in)) return true;
+  }
+  return false;
 }
 
 // The log-sum-exp merge of every stream's partials (the second kernel of a
@@ -1273,7 +1283,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const Me
       const float4 y = accs[w][lane];
       acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
     }
-    if (SHARED && behind_prefix(p.prefix, seq)) {
+    if (SHARED && behind_prefix(p.prefix, seq, p.n_seqs, lane)) {
       const int64_t row = static_cast<int64_t>(seq) * p.a.n_q + kvh * p.a.G + hg * 8 + h;
       const float2 x = p.prefix.xml[row];
       merge_write<ROT, SHARED>(p.a, seq, kvh, hg, h, lane, acc, M, L, x,
@@ -1401,7 +1411,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (st >= p.n_seqs * KH || h >= p.G - hg * 8) continue;
     const float4 acc = reinterpret_cast<const float4 *>(red[leader] + h * kD)[lane];
     const float2 ml = ml_s[leader][h];
-    if (behind_prefix(x, seq)) {
+    if (behind_prefix(x, seq, p.n_seqs, lane)) {
       const int64_t row = static_cast<int64_t>(seq) * p.n_q + kvh * p.G + hg * 8 + h;
       merge_write<CV == KVQ_TURBO4, true>(a, seq, kvh, hg, h, lane, acc, ml.x, ml.y, x.xml[row],
                                           reinterpret_cast<const float4 *>(x.xo + row * kD)[lane]);

@@ -40,7 +40,7 @@ struct DecodePlan {
 
 // What a decode step's rows have from the keys of a shared prefix: xo fp32
 // [n_seqs][n_q][128] unnormalised, xml [n_seqs][n_q] (max in log2 units, sum),
-// of sequences group_start[0] .. group_start[n_groups] - 1 (null: all).
+// of the sequences of the groups group_start[g] .. group_start[g + 1] - 1 (null: all).
 struct PrefixPart {
   const float *xo;
   const float2 *xml;

@@ -607,8 +607,8 @@ KVQ_API int attn_decode_prefix_workspace(const kvq_layer *layer, const kvq_layer
  * `prefix` and every key of its own, one softmax over both.  prefix: a layer of
  * the same heads whose sequence g is the prefix of the sequences group_start[g]
  * .. group_start[g + 1] - 1 of `layer` (device int32 [prefix n_seqs + 1],
- * non-decreasing; NULL: the one prefix of all); sequences outside the groups
- * attend their own keys alone.  Its codecs, capacity and pages are its own: two
+ * non-decreasing; NULL: the one prefix of all); sequences outside the groups, and
+ * those of a group whose entries are out of range, attend their own keys alone.  Its codecs, capacity and pages are its own: two
  * paged layers may be views of one pool, the prefix's block table over the shared
  * pages, the layer's over the rest (their lengths then count those alone).
  * q, out, lse, max_len: as attn_decode (q 16-byte aligned and not meeting out;
