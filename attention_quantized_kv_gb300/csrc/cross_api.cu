@@ -93,7 +93,7 @@ int kv_read_rows(const kvq_layer *layer, const kvq_rows *k, const kvq_rows *v, i
 int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t max_len, size_t *bytes) {
   const int st = check_layer(layer);
   if (st != KVQ_OK) return st;
-  if (!bytes || n_rows < 0 || n_rows * layer->n_q_heads > INT32_MAX || max_len <= 0 ||
+  if (!bytes || !kvq::rows_fit(layer, n_rows) || max_len <= 0 ||
       layer->n_seqs > kvq::kCrossMaxSeqs)
     return KVQ_EINVAL;
   if (max_len > layer->capacity) return KVQ_ECAPACITY;

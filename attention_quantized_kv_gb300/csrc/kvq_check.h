@@ -91,11 +91,16 @@ inline bool interleaved(const kvq_rows &a, const kvq_rows &b, int64_t n, int32_t
   return d >= wa && d + wb <= pitch;
 }
 
+// At most 2^31 - 1 rows times query heads (any n_rows: no product that could wrap).
+inline bool rows_fit(const kvq_layer *L, int64_t n_rows) {
+  return n_rows >= 0 && n_rows <= INT32_MAX / L->n_q_heads;
+}
+
 // Which rows belong to which sequence: row_start (packed), n_new (padded) or
 // neither (one row per sequence).
 inline int check_packed(const kvq_layer *L, int64_t n_rows, const int32_t *n_new,
                         const int32_t *row_start, bool one_each) {
-  if (n_rows < 0 || n_rows * L->n_q_heads > INT32_MAX) return KVQ_EINVAL;
+  if (!rows_fit(L, n_rows)) return KVQ_EINVAL;
   if (n_new && row_start) return KVQ_EINVAL;
   if (!n_new && !row_start && (!one_each || n_rows != L->n_seqs)) return KVQ_EINVAL;
   if (n_new && n_rows % L->n_seqs != 0) return KVQ_EINVAL;
