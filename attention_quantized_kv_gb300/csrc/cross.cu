@@ -707,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if ((smem_u32(smem) & 1023u) != 0) {
     grid_dependency_wait();
     set_err(p.err, KVQ_DEVERR_TIMEOUT);
+    if (threadIdx.x == 0) p.items[blockIdx.x].n = 0;  // nothing to join
     return;
   }
 
