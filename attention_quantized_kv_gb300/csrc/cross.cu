@@ -89,7 +89,6 @@ constexpr float kFar = 0x1p22f;
 // written and read as whole lines (row by row the lines' parts took 8000 cycles), then
 // (m, l) of every row.
 constexpr int kPartFloats = kTile * kD + 2 * kTile;
-constexpr int kSlotFloats = 2 * kPartFloats;
 // Work: what a step of a single tile and of a pair count (cycle counters: 1300 to 1550
 // and 1900 to 2900), and what an item counts besides its steps (queries, results, the
 // pipeline's fill).  With 10, 13, 16, 20 and 26 for the latter 24 x 5 beams over f16 and
@@ -113,7 +112,8 @@ struct CrossParams {
   int64_t q_row, q_head, out_row, out_head;  // strides in bytes
   int q_bf16;                                // q and out: bf16, else fp16
   CrossOut out;
-  float *part;  // partial slots [2 per CTA][2 tiles][kPartFloats]
+  float *part;  // partial slots [2 per CTA][slot_floats]: a tile or two of kPartFloats
+  int slot_floats;
   JoinItem *items;  // [CTAs]: the split item that begins in each one's slice
   PackedRows rows;
   const int32_t *seq_lens, *table;
@@ -575,7 +575,7 @@ __device__ __forceinline__ Piece piece_of(const CrossParams &p, const Segment &g
   const int64_t row = g.first + tok, at = row * p.n_q + head;
   if (g.j_lo > 0 || g.j_hi < g.nt) {
     float *const part = p.part +
-                        (2 * static_cast<int64_t>(blockIdx.x) + (g.inside ? 1 : 0)) * kSlotFloats +
+                        (2 * static_cast<int64_t>(blockIdx.x) + (g.inside ? 1 : 0)) * p.slot_floats +
                         in / kTile * kPartFloats;
     const int r = in % kTile;
     return {part + 4 * r, 4 * kTile, reinterpret_cast<float2 *>(part + kTile * kD) + r, nullptr, nullptr};
@@ -1260,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ro.full = nullptr;
       ro.bf16 = p.q_bf16;
       float *const slot = p.part +
-                          (2 * static_cast<int64_t>(blockIdx.x) + (sg.inside ? 1 : 0)) * kSlotFloats +
+                          (2 * static_cast<int64_t>(blockIdx.x) + (sg.inside ? 1 : 0)) * p.slot_floats +
                           (sg.pair ? e : 0) * kPartFloats;
       ro.step = whole ? 4 : 4 * kTile;
       if (!whole)
@@ -1406,7 +1406,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   const int64_t row = item.first + tok;
   // the item begins inside its first CTA's slice, and before every other's
   auto part = [&](int j) {
-    return p.part + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlotFloats + (in / kTile) * kPartFloats;
+    return p.part + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * p.slot_floats + (in / kTile) * kPartFloats;
   };
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   float M = -INFINITY, L = 0.0f;
@@ -1457,10 +1457,18 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 
 }  // namespace
 
-CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms) {
+// What a call can need: CTAs for the most work that n_rows rows over max_len keys can be
+// (cross_ctas of it), and tiles for the most rows that a sequence can have.
+CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int max_len, int num_sms) {
   CrossPlan pl;
-  pl.grid = num_sms;
-  pl.items_off = 2 * static_cast<int64_t>(pl.grid) * kSlotFloats * 4;
+  const int64_t R = n_rows * (L.n_q_heads / L.n_kv_heads);  // per kv head
+  pl.tiles = L.codec_k != KVQ_TURBO4 && R > kTile ? 2 : 1;
+  // sum ceil(R_s / tile rows) over the sequences with rows
+  const int64_t blocks = R / (pl.tiles * kTile) + std::min<int64_t>(L.n_seqs, n_rows);
+  const int64_t steps = (max_len + kKeys - 1) / kKeys;
+  const int64_t W = L.n_kv_heads * blocks * (steps * (pl.tiles == 2 ? kPair : kSingle) + kItemCost);
+  pl.grid = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(1, W / (4 * kSingle))));
+  pl.items_off = 2 * static_cast<int64_t>(pl.grid) * pl.tiles * kPartFloats * 4;
   pl.ws_bytes = pl.items_off + pl.grid * static_cast<int64_t>(sizeof(JoinItem));
   return pl;
 }
@@ -1482,6 +1490,7 @@ cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows
   p.out_row = out_row * 2;
   p.out_head = out_head * 2;
   p.part = static_cast<float *>(workspace);
+  p.slot_floats = pl.tiles * kPartFloats;
   p.items = reinterpret_cast<JoinItem *>(static_cast<uint8_t *>(workspace) + pl.items_off);
   p.rows = {row_start, n_new, n_rows, n_rows / L.n_seqs, L.n_seqs};
   p.seq_lens = L.seq_lens;

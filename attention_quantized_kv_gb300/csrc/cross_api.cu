@@ -20,11 +20,12 @@ struct PrefixPlan {
   int64_t xo_off, xml_off, cross_off, ws_bytes;
 };
 
-PrefixPlan plan_prefix(const kvq_layer &layer, const kvq_layer &prefix, int max_len, int sms) {
+PrefixPlan plan_prefix(const kvq_layer &layer, const kvq_layer &prefix, int max_len,
+                       int max_prefix, int sms) {
   PrefixPlan p;
   const int64_t rows = static_cast<int64_t>(layer.n_seqs) * layer.n_q_heads;
   p.own = kvq::plan_decode(layer, max_len, sms);
-  p.shared = kvq::plan_cross(prefix, layer.n_seqs, sms);
+  p.shared = kvq::plan_cross(prefix, layer.n_seqs, max_prefix, sms);
   p.xo_off = (p.own.ws_bytes + 15) / 16 * 16;
   p.xml_off = p.xo_off + rows * kHeadDim * 4;
   p.cross_off = (p.xml_off + rows * 8 + 15) / 16 * 16;
@@ -99,7 +100,7 @@ int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t max_len
   if (max_len > layer->capacity) return KVQ_ECAPACITY;
   const int sms = kvq::device_sms();
   if (sms <= 0) return KVQ_ECUDA;
-  *bytes = static_cast<size_t>(kvq::plan_cross(*layer, n_rows, sms).ws_bytes);
+  *bytes = static_cast<size_t>(kvq::plan_cross(*layer, n_rows, max_len, sms).ws_bytes);
   return KVQ_OK;
 }
 
@@ -126,7 +127,7 @@ int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows, const 
   if (!aligned(workspace, 16)) return KVQ_EALIGN;
   const int sms = kvq::device_sms();
   if (sms <= 0) return KVQ_ECUDA;
-  const kvq::CrossPlan pl = kvq::plan_cross(*layer, n_rows, sms);
+  const kvq::CrossPlan pl = kvq::plan_cross(*layer, n_rows, max_len, sms);
   if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
   const kvq::CrossOut to = {out->data, lse, nullptr, nullptr};
   const cudaError_t e = kvq::launch_cross(*layer, pl, *q, n_rows, n_new, row_start, scale, to,
@@ -142,7 +143,7 @@ int attn_decode_prefix_workspace(const kvq_layer *layer, const kvq_layer *prefix
   if (!bytes) return KVQ_EINVAL;
   const int sms = kvq::device_sms();
   if (sms <= 0) return KVQ_ECUDA;
-  *bytes = static_cast<size_t>(plan_prefix(*layer, *prefix, max_len, sms).ws_bytes);
+  *bytes = static_cast<size_t>(plan_prefix(*layer, *prefix, max_len, max_prefix, sms).ws_bytes);
   return KVQ_OK;
 }
 
@@ -162,7 +163,7 @@ int attn_decode_prefix(const kvq_layer *layer, const kvq_layer *prefix,
   if (!aligned(workspace, 16)) return KVQ_EALIGN;
   const int sms = kvq::device_sms();
   if (sms <= 0) return KVQ_ECUDA;
-  const PrefixPlan pl = plan_prefix(*layer, *prefix, max_len, sms);
+  const PrefixPlan pl = plan_prefix(*layer, *prefix, max_len, max_prefix, sms);
   if (ws_bytes < static_cast<size_t>(pl.ws_bytes)) return KVQ_EWORKSPACE;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const kvq_rows qr = {const_cast<void *>(q), layer->n_q_heads * d, d, KVQ_T_F16, 0};

@@ -91,6 +91,7 @@ cudaError_t launch_compact(const kvq_layer &L, const int32_t *evict, const int32
 constexpr int kCrossMaxSeqs = 1024;  // key sequences per call
 struct CrossPlan {
   int grid = 1;          // CTAs, at most one per SM
+  int tiles = 1;         // query tiles of a partial slot
   int64_t items_off = 0, ws_bytes = 0;  // partial slots, two per CTA; what is to be joined
 };
 // Where the rows go: out and lse (optional), or, for a merge, xo fp32
@@ -102,7 +103,7 @@ struct CrossOut {
   float2 *xml;
 };
 // n_new and row_start both null: n_rows / n_seqs rows per sequence.
-CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int num_sms);
+CrossPlan plan_cross(const kvq_layer &L, int64_t n_rows, int max_len, int num_sms);
 cudaError_t launch_cross(const kvq_layer &L, const CrossPlan &pl, const kvq_rows &q,
                          int64_t n_rows, const int32_t *n_new, const int32_t *row_start,
                          float scale, const CrossOut &out, int64_t out_row, int64_t out_head,

@@ -571,7 +571,8 @@ KVQ_API int kv_read_rows(const kvq_layer *layer, const kvq_rows *k, const kvq_ro
                          int64_t n_rows, const int32_t *n_read, const int32_t *row_start,
                          const int32_t *first, void *stream);
 
-/* Workspace bytes that attn_cross needs for n_rows rows and max_len. */
+/* Workspace bytes that attn_cross needs for n_rows rows and max_len: no more for
+ * fewer of either, and at most 266 KB an SM (40 MB on 152). */
 KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t max_len,
                                  size_t *bytes);
 
