@@ -701,7 +701,8 @@ def attn_cross(layer: KVLayer, q, scale: float, out, lse, max_len: int, workspac
     """Query rows against every cached key of their sequence (no causal mask).  ``q``, ``out``:
     float16 or bfloat16, strided, packed [rows, n_q, 128] with ``row_start``, padded [n_seqs,
     max_new, n_q, 128] with ``n_new``, or one row per sequence; ``lse``: fp32, contiguous, the
-    leading shape and n_q, or None.  Rows of no sequence are left as they are."""
+    leading shape and n_q, or None.  q and out may be views of one tensor beside each other.  Rows
+    of no sequence are left as they are."""
     what = "attn_cross"
     dev = _cuda_device(q, what)
     _layer_on(layer, dev, what)

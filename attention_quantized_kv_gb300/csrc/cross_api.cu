@@ -121,7 +121,8 @@ int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows, const 
   if (q->type == KVQ_T_F32 || out->type != q->type) return KVQ_EUNSUPPORTED;
   if (!aligned(lse, 4)) return KVQ_EALIGN;
   // (a row's query is read by every block that takes a part of its keys)
-  if (overlap(q->data, span_bytes(*q, n_rows, heads), out->data, span_bytes(*out, n_rows, heads)))
+  if (overlap(q->data, span_bytes(*q, n_rows, heads), out->data, span_bytes(*out, n_rows, heads)) &&
+      !kvq::interleaved(*q, *out, n_rows, heads))
     return KVQ_EINVAL;
   if (!workspace) return KVQ_EWORKSPACE;
   if (!aligned(workspace, 16)) return KVQ_EALIGN;

@@ -81,14 +81,24 @@ inline int64_t span_bytes(const kvq_rows &r, int64_t n, int32_t heads) {
   return ((n - 1) * r.row_stride + (heads - 1) * r.head_stride + kHeadDim) * type_bytes(r.type);
 }
 
-// Whether a and b are disjoint parts of the same rows (views of one tensor).
+// Whether a and b, whose ranges meet, are views of one tensor that share no place: with the
+// same strides, each lies in its own part of every period, the larger stride (rows or heads
+// of one beside those of the other) or the smaller one (beside each other in every head or row).
 inline bool interleaved(const kvq_rows &a, const kvq_rows &b, int64_t n, int32_t heads) {
-  const int64_t pitch = a.row_stride * type_bytes(a.type);
-  if (n < 2 || pitch != b.row_stride * type_bytes(b.type)) return false;
-  const int64_t wa = span_bytes(a, 1, heads), wb = span_bytes(b, 1, heads);
+  const int64_t sa = type_bytes(a.type), sb = type_bytes(b.type);
+  const int64_t row = a.row_stride * sa, head = a.head_stride * sa;
+  if ((n > 1 && row != b.row_stride * sb) || (heads > 1 && head != b.head_stride * sb)) return false;
   const int64_t at = static_cast<uint8_t *>(b.data) - static_cast<uint8_t *>(a.data);
-  const int64_t d = (at % pitch + pitch) % pitch;
-  return d >= wa && d + wb <= pitch;
+  auto apart = [&](int64_t period, int64_t inner) {  // inner: from the first to the last value's row
+    if (period <= 0) return false;
+    const int64_t d = (at % period + period) % period;
+    return d >= inner + kHeadDim * sa && d + inner + kHeadDim * sb <= period;
+  };
+  if (n == 1 || heads == 1) return apart(n > 1 ? row : heads > 1 ? head : 0, 0);
+  const bool rows_outside = row >= head;
+  const int64_t large = rows_outside ? row : head, small = rows_outside ? head : row;
+  return apart(large, ((rows_outside ? heads : n) - 1) * small) ||
+         (small > 0 && large % small == 0 && apart(small, 0));
 }
 
 // At most 2^31 - 1 rows times query heads (any n_rows: no product that could wrap).

@@ -563,7 +563,8 @@ KVQ_API int kv_append_rows(const kvq_layer *layer, const kvq_rows *k, const kvq_
  * device int32 [n_seqs], or NULL for 0), decoded exactly in fp32 and rounded
  * once to the output's type.  k, v: rows [n_rows][n_kv_heads][128] to be
  * written, either of them NULL for a side that is not read; their types and
- * strides may differ, their places may not meet.  n_read, row_start: as n_new
+ * strides may differ, their places may not meet (their ranges only as views of one
+ * tensor with the same strides).  n_read, row_start: as n_new
  * and row_start of kv_append_rope.  A token outside [0, seq_lens[s]) sets
  * KVQ_DEVERR_SEQLEN, an unmapped page KVQ_DEVERR_PAGE; such rows, and rows that
  * belong to no sequence, are left as they were. */
@@ -581,7 +582,8 @@ KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t
  * h / (n_q/n_kv); cross attention to an encoder's states, whose lengths have
  * nothing to do with the rows'.
  * q: rows [n_rows][n_q_heads][128], fp16 or bf16 (rounded to fp16 first, within
- * its range); out: rows of the same type, not meeting q; lse:
+ * its range); out: rows of the same type, not meeting q (views of one tensor may
+ * lie beside each other with the same strides); lse:
  * optional fp32 [n_rows][n_q_heads], natural log.  Rows belong to sequences by
  * n_new or row_start; both NULL: row s to sequence s (n_rows = n_seqs).  Rows
  * that belong to no sequence are left as they were; a sequence of length 0 gives
