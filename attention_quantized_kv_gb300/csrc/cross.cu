@@ -44,11 +44,15 @@
 // 1.1 -> 570 ms; one such query: 19 ms; a NaN in a query ends it at the first key).
 //
 // Bound: the tensor cores, where a pair's rows fill its tiles: its 64 keys cost 2050
-// cycles of products over split sides (1290 over f16) and take 2640 (4600 by one issuing
-// warp for both pipes).  2048 rows x 32 heads over 32768 states, K q8_0 and V q4_0:
-// 1.11 ms; over 8192 the tensor pipe is busy for 78 % of 0.30 ms.  Where rows are few the
-// codes' conversion, about 1000 cycles for 64 keys of q8_0: 120 beams x 40 heads over 24 inputs
-// of up to 4096 states, K f16 and V q8_0, 48 us (24 at the copy rate).
+// cycles of products over split sides (1290 over f16) and take 2500 (4600 by one issuing
+// warp for both pipes).  2048 rows x 32 heads over 32768 states, K q8_0 and V q4_0: the
+// kernel 1.11 ms at 1.93 GHz, calls in a row 1.12 ms and, once the power limit holds the
+// clock down, 1.21; over 8192 the tensor pipe is busy for 78 % of the kernel's 0.31 ms.  turbo4
+// keys, which leave no room for pairs: 1.43 ms (values turbo4), 1.48 (q8_0).  Where rows are few
+// the codes' conversion, about 1000 cycles for 64 keys of q8_0: 120 beams x 40 heads over 24
+// inputs of up to 4096 states, K f16 and V q8_0, the kernel 52 us, calls in a row 55 (24 at
+// the copy rate).  One row a sequence: 16 over 1500 states 15 us a call; from 64 rows over 4096
+// on attn_decode, which reads the codes as its operands, is twice as fast (110 and 197 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -91,9 +95,10 @@ constexpr float kFar = 0x1p22f;
 constexpr int kPartFloats = kTile * kD + 2 * kTile;
 // Work: what a step of a single tile and of a pair count (cycle counters: 1300 to 1550
 // and 1900 to 2900), and what an item counts besides its steps (queries, results, the
-// pipeline's fill).  With 10, 13, 16, 20 and 26 for the latter 24 x 5 beams over f16 and
-// q8_0 states took 51, 51, 49, 50 and 52 us, 3011 rows of eight targets 89, 82, 79, 77, 79;
-// other short items gain up to 26.
+// pipeline's fill).  With 8, 12, 16, 20, 24 and 28 for the latter a call took, in us: 24 chats
+// behind three prompts 52.1, 50.5, 49.2, 49.6, 48.8, 49.0; 120 beams over f16 and q8_0 states 58.1,
+// 54.0, 55.0, 55.1, 55.9, 57.2; 3011 rows of eight targets 107, 97, 89.8, 88.4, 88.2, 88.1; of
+// fourteen others none differs by more than 3% from 16 on.
 constexpr int kSingle = 2, kPair = 3;
 constexpr int kItemCost = 24;
 
@@ -177,9 +182,10 @@ __device__ __forceinline__ void block_at(const SeqWork &w, int64_t off, int &kvh
                              static_cast<int64_t>(w.blocks - 1)));
 }
 // CTAs that get a slice: each of at least four steps of a single tile (of one at least,
-// so that every CTA between an item's first and last has a step of it).  A decode step of
-// 64 rows of two kv heads behind 4096 keys: 20.7, 18.7 and 21.1 us with at least two,
-// four and eight.
+// so that every CTA between an item's first and last has a step of it).  With at least two,
+// four and eight: a decode step of 64 rows of two kv heads behind 4096 keys 21.3, 19.3 and 21.5
+// us, one row of 16 sequences over 1500 15.1, 14.9 and 15.5; where there is more work than that
+// for every CTA it makes no difference.
 __device__ __forceinline__ int64_t cross_ctas(int64_t W, int grid) {
   return max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), W / (4 * kSingle)));
 }

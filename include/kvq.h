@@ -547,8 +547,9 @@ KVQ_API int attn_decode_append_rope(const kvq_layer *layer, const kvq_rope *rope
  * without a causal mask.  The pages name none of these; the definitions below
  * are this library's.  Which rows belong to which sequence is said as for
  * kv_append_rope, by row_start (packed) or n_new (padded); an entry out of
- * range sets KVQ_DEVERR_ROWS and that sequence's rows are unspecified.  A call
- * has at most 2^31 - 1 rows times query heads.
+ * range sets KVQ_DEVERR_ROWS and that sequence's rows are unspecified (where
+ * row_start decreases, kv_append_rows and kv_read_rows may leave out rows of other
+ * sequences too).  A call has at most 2^31 - 1 rows times query heads.
  * ------------------------------------------------------------------------ */
 
 /* kv_append_rope without the rotation: k and v rows (one type; strided) are
@@ -595,7 +596,9 @@ KVQ_API int attn_cross_workspace(const kvq_layer *layer, int64_t n_rows, int32_t
  * fp16 numbers that add up to them exactly), softmax weights as fp16, sums as
  * fp32.  Rows for which that does not do - a cached value (turbo4: a rotated
  * one) or a query past 65504, scores past 2^22 - are computed in fp32 instead,
- * key by key: many times slower. */
+ * key by key: many times slower.  turbo4 keys cost a third more than the other
+ * codecs' where rows are many; for one fp16 row per sequence attn_decode is faster
+ * (16 sequences of 1500 keys 14.5 and 17.8 us, 64 of 4096 110 and 197). */
 KVQ_API int attn_cross(const kvq_layer *layer, const kvq_rows *q, int64_t n_rows,
                        const int32_t *n_new, const int32_t *row_start, float scale,
                        const kvq_rows *out, float *lse, int32_t max_len, void *workspace,
