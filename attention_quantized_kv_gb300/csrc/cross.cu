@@ -1349,7 +1349,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (valid && nan != nan) any_nan = 1;
+      // (fp16 operands hold fp16 queries and keys: a NaN sum of theirs stays)
+      if (valid && nan != nan &&
+          (l == l || p.codec[0] != KVQ_F16 || p.q_bf16 || far >= kFar))
+        any_nan = 1;
       tc_fence_before();  // O read: the next segment's first product may overwrite it
       if (sg.pair) __syncwarp();
       else pipes_sync();
