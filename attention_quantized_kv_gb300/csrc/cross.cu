@@ -51,8 +51,8 @@
 // keys, which leave no room for pairs: 1.43 ms (values turbo4), 1.48 (q8_0).  Where rows are few
 // the codes' conversion, about 1000 cycles for 64 keys of q8_0: 120 beams x 40 heads over 24
 // inputs of up to 4096 states, K f16 and V q8_0, the kernel 52 us, calls in a row 55 (24 at
-// the copy rate).  One row a sequence: 16 over 1500 states 15 us a call; from 64 rows over 4096
-// on attn_decode, which reads the codes as its operands, is twice as fast (110 and 197 us).
+// the copy rate).  One row a sequence: 16 over 1500 states 15 to 18 us a call; attn_decode, which
+// reads the codes as its operands, takes 14.5, and half for 64 rows over 4096 (110 and 197 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -91,7 +91,7 @@ def test_cached_values(ck, cv, size, side, lens, counts, paged):
 def test_prefix_values(pk, pv, cap, own):
     """The same as a prefix: the tokens give what they give as own keys."""
     L, table = _filled(3, 2, 6, cap, Q8, Q8, False, own, 8)
-    P, ptable = _two([30, 3000], 2, 6, 3072 + 256, pk, pv, False, 65504.0, 65504.0, [(1000, 0, 9), (2999, 1, 3)])
+    P, ptable = _two([30, 3000], 2, 6, 3328, pk, pv, False, 65504.0, 65504.0, [(1000, 0, 9), (2999, 1, 3)])
     q = _queries(3, 6, 8, gain=2.0 ** -12)
     out, lse = torch.full_like(q, 7), torch.full((3, 6), 7.0, device="cuda")
     kvq.attn_decode_prefix(L, P, q, SCALE, out, lse, cap, 3328, _prefix_ws(L, P, cap, 3328), group_start=_i32([0, 1, 3]))
